@@ -50,8 +50,10 @@ SINGLE_STAGES = ["one_kernel", "none_1", "none_2", "none_3"]
 
 
 def single_kernel_call(mode: str, cfg: dict) -> bool:
+    if mode != "sample":  # (the n-gram workload has no logits, hence no dtype)
+        return False
     tile = 1024 if cfg["dtype"] == "fp32" else 2048
-    return mode == "sample" and cfg["B"] == 1 and (2 * cfg["gamma"] + 1) * -(-cfg["V"] // tile) <= 256
+    return cfg["B"] == 1 and (2 * cfg["gamma"] + 1) * -(-cfg["V"] // tile) <= 256
 STAGE_STEPS = 200  # steps timed kernel by kernel (after the headline steps)
 ACCEPT_STEPS = 16  # untimed steps whose accepted lengths and re-draw counts are read back
 STAGES = {"sample": ["row_stats", "decide", "residual_mass", "draw_redraw"],

@@ -114,6 +114,13 @@ def test_single_kernel_rule_matches_the_library_constants():
                 assert not bench.single_kernel_call("sample_lazy", cfg)
 
 
+def test_single_kernel_rule_takes_every_workload():
+    """The rule answers for each workload's own configuration, the n-gram one's (no logits) too."""
+    from speculative_decoding_verify_spec_gb300 import workloads as W
+    one = {name for name, cfg in W.WORKLOADS.items() if bench.single_kernel_call(cfg["mode"], cfg)}
+    assert one == {"sample_b1"}
+
+
 def test_source_digest_ignores_comments_and_blank_lines():
     """A comment or a blank line leaves a kernel's key unchanged; code does not."""
     a = "int f(int x) {  // twice\n    return 2 * x; /* doubled */\n}\n"
