@@ -22,7 +22,8 @@ CHECKS_LIB_PATH = os.path.join(PKG, "libspecverify_checks.so")
 OBJ_DIR = os.path.join(ROOT, "_build")
 CHECKS_FLAGS = ["-DSV_CHECKS", "-rdc=true"]
 SOURCES = ["sv_api.cu", "sv_sample.cu", "sv_greedy.cu", "sv_refine.cu", "sv_tree_sample.cu", "sv_tree_refine.cu",
-           "sv_lazy.cu", "sv_ngram.cu", "sv_noalloc.cu", "sv_level.cu"]
+           "sv_lazy.cu", "sv_ngram.cu", "sv_noalloc.cu", "sv_level.cu",
+           "sv_adjust.cu", "sv_kv_append.cu", "sv_kv_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
@@ -36,7 +37,7 @@ def _nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "spec_verify.h"))
+    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     files.append(os.path.abspath(__file__))
     return files
 

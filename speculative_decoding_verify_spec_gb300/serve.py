@@ -1,0 +1,230 @@
+"""Python entry points of the operators around the verification step (``include/spec_serve.h``).
+
+``spec_logit_adjust`` applies penalties, biases and grammar masks to the verified rows' logits;
+``spec_kv_append`` and ``spec_kv_attention`` keep and read a paged key/value cache held in 4 bits.
+As in ``binding``, these only marshal: they check placement, type and shape, take strides and
+the current stream from PyTorch and call the C entry of the same name.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import binding
+from .binding import _check, _dtype_code, _ints, _logits3, _stream
+
+KV_BF16, KV_FP16 = 1, 2
+_ready = None
+
+
+def _library() -> ctypes.CDLL:
+    global _ready
+    if _ready is None:
+        lib = binding.load_library()
+        P, i64, i32, f32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+        lib.spec_logit_adjust.argtypes = [P, i64, i64, P, i64, i64, i32, i32, i32, i32, P, i64, P, P, P, P, P, P, P, P,
+                                          P, i32, P, P]
+        lib.spec_logit_adjust.restype = i32
+        lib.spec_kv_page_bytes.argtypes = [i32, i32]
+        lib.spec_kv_page_bytes.restype = sz
+        lib.spec_kv_code_offset.argtypes = [i32] * 5
+        lib.spec_kv_code_offset.restype = i64
+        lib.spec_kv_append.argtypes = [P, i64, i64, i64, P, i64, i64, i64, i32, i32, i32, i32, i32, P, i32, i32, P, i32,
+                                       P, P, P, P, i32, i32, i32, P, P, P, P]
+        lib.spec_kv_append.restype = i32
+        lib.spec_kv_attention_workspace_size.argtypes = [i32] * 5
+        lib.spec_kv_attention_workspace_size.restype = sz
+        lib.spec_kv_attention.argtypes = [P, i64, i64, i64, i32, i32, i32, i32, i32, i32, P, i32, i32, P, i32, P, P, P,
+                                          f32, P, P, i32, i32, i32, P, P, P, sz, P]
+        lib.spec_kv_attention.restype = i32
+        _ready = lib
+    return _ready
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _floats(t, name, shape, dev):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.device != dev or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be float32 of shape {tuple(shape)} on {dev}")
+    return t.contiguous()
+
+
+def _maybe_ints(t, name, shape, dev):
+    return None if t is None else _ints(t, name, shape, dev)
+
+
+def spec_logit_adjust(logits: torch.Tensor, *, history=None, lengths=None, prompt_lengths=None, draft_tokens=None,
+                      parent=None, repetition=None, frequency=None, presence=None, bias_tokens=None, bias_values=None,
+                      allowed=None, out=None) -> torch.Tensor:
+    """Penalties, biases and grammar masks on logits [B, rows, V] (bf16 or fp32); returns `out`, a new
+    contiguous tensor unless given (`out=logits` works in place).
+
+    The context of row i is the history ([B, n] int32 with `lengths` [B], the first `prompt_lengths`
+    [B] of them the prompt) and the drafts before it: `draft_tokens` [B, rows - 1] for a chain, or the path
+    to node i of the tree `parent` [rows] with `draft_tokens` [B, rows] (node 0, the root, is the history's
+    last token).  Tokens in the context have their logit divided (if positive) or multiplied by `repetition`
+    [B]; those in its output part lose `frequency` [B] per occurrence and `presence` [B] once; then
+    `bias_values` [B, n] fp32 are added to `bias_tokens` [B, n] (the last entry of a token counts, tokens outside the
+    vocabulary are unused); last, tokens whose bit in `allowed` [B, rows, ceil(V / 32)] int32 is clear become -inf."""
+    lib = _library()
+    sb, sr = _logits3(logits, "logits")
+    B, R, V = logits.shape
+    dt, dev = _dtype_code(logits), logits.device
+    if out is None:
+        out = torch.empty((B, R, V), dtype=logits.dtype, device=dev)
+    elif out.device != dev or out.dtype != logits.dtype or tuple(out.shape) != (B, R, V):
+        raise ValueError(f"out must be {logits.dtype} of shape {(B, R, V)} on {dev}")
+    ob, orow = _logits3(out, "out")
+    n = 0
+    if history is not None:
+        if history.dim() != 2 or lengths is None:
+            raise ValueError("history must be [B, n], with lengths [B]")
+        n = history.shape[1]
+        history = _ints(history, "history", (B, n), dev)
+        lengths = _ints(lengths, "lengths", (B,), dev)
+        prompt_lengths = _maybe_ints(prompt_lengths, "prompt_lengths", (B,), dev)
+    if parent is not None:
+        if draft_tokens is None:
+            raise ValueError("a tree (parent) needs draft_tokens [B, rows]")
+        parent = _ints(parent, "parent", (R,), dev)
+    if draft_tokens is not None:
+        draft_tokens = _ints(draft_tokens, "draft_tokens", (B, R if parent is not None else max(R - 1, 0)), dev)
+    k = 0
+    if (bias_tokens is None) != (bias_values is None):
+        raise ValueError("bias_tokens and bias_values belong together")
+    if bias_tokens is not None:
+        k = bias_tokens.shape[1] if bias_tokens.dim() == 2 else -1
+        bias_tokens = _ints(bias_tokens, "bias_tokens", (B, k), dev)
+        bias_values = _floats(bias_values, "bias_values", (B, k), dev)
+    repetition = _floats(repetition, "repetition", (B,), dev)
+    frequency = _floats(frequency, "frequency", (B,), dev)
+    presence = _floats(presence, "presence", (B,), dev)
+    allowed = _maybe_ints(allowed, "allowed", (B, R, (V + 31) // 32), dev)
+    st = lib.spec_logit_adjust(logits.data_ptr(), sb, sr, out.data_ptr(), ob, orow, dt, B, R, V, _ptr(history), n,
+                               _ptr(lengths), _ptr(prompt_lengths), _ptr(draft_tokens), _ptr(parent), _ptr(repetition),
+                               _ptr(frequency), _ptr(presence), _ptr(bias_tokens), _ptr(bias_values), k, _ptr(allowed),
+                               _stream(dev))
+    _check(st, "spec_logit_adjust")
+    return out
+
+
+def spec_kv_page_bytes(page_size: int, head_dim: int) -> int:
+    """Bytes of one page and head of the 4-bit cache (0 if the sizes are not supported)."""
+    return int(_library().spec_kv_page_bytes(page_size, head_dim))
+
+
+def _kv_dtype(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return KV_BF16
+    if t.dtype == torch.float16:
+        return KV_FP16
+    raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+
+
+def _heads4(t: torch.Tensor, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
+        raise ValueError(f"{name} must be [B, T, heads, head_dim] with a contiguous last axis")
+    return t.stride(0), t.stride(1), t.stride(2)
+
+
+def _cache(cache, page_table, start, new_lens, B, heads, D, dev):
+    """(num_pages, page_size, table width) of a checked cache."""
+    if cache.dtype != torch.uint8 or cache.device != dev or cache.dim() != 3 or not cache.is_contiguous():
+        raise ValueError(f"cache must be a contiguous uint8 tensor [pages, kv_heads, page bytes] on {dev}")
+    page, rest = divmod(cache.shape[2], D + 8)
+    if (heads is not None and cache.shape[1] != heads) or rest:
+        raise ValueError(f"cache of shape {tuple(cache.shape)} does not hold {heads} heads of {D} dimensions")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, pages per sequence]")
+    width = page_table.shape[1]
+    return (cache.shape[0], page, _ints(page_table, "page_table", (B, width), dev), width, _ints(start, "start", (B,), dev),
+            _maybe_ints(new_lens, "new_lens", (B,), dev))
+
+
+def _rotation(cos, sin, positions, B, T, dev):
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin belong together")
+    if cos is None:
+        return None, None, 0, 0, None
+    if cos.dim() != 2:
+        raise ValueError("cos must be [positions, pairs]")
+    cos, sin = _floats(cos, "cos", cos.shape, dev), _floats(sin, "sin", cos.shape, dev)
+    return cos, sin, cos.shape[0], cos.shape[1], _maybe_ints(positions, "positions", (B, T), dev)
+
+
+def spec_kv_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor,
+                   *, new_lens=None, cos=None, sin=None, positions=None, interleaved: bool = False,
+                   return_values: bool = False, k_values=None, v_values=None):
+    """Writes the new tokens' keys (rotated) and values [B, T, kv_heads, head_dim] into the 4-bit `cache`
+    [pages, kv_heads, spec_kv_page_bytes(page_size, head_dim)] uint8, as tokens start[b] .. of sequence b
+    (`new_lens` [B] of them, all T if None), in the pages that `page_table` [B, n] names.
+
+    cos, sin [positions, pairs] fp32 turn the first 2 * pairs dimensions by the angles of the tokens' positions
+    (`positions` [B, T], else start[b] + t).  With `return_values`, or `k_values` and `v_values` given, returns what the
+    cache now holds for the new tokens, in the inputs' type; else None."""
+    lib = _library()
+    ks, dt, dev = _heads4(k, "k"), _kv_dtype(k, "k"), k.device
+    vs = _heads4(v, "v")
+    if v.shape != k.shape or v.dtype != k.dtype or v.device != dev:
+        raise ValueError("v must have k's shape, type and device")
+    B, T, H, D = k.shape
+    pages, page, page_table, width, start, new_lens = _cache(cache, page_table, start, new_lens, B, H, D, dev)
+    cos, sin, length, pairs, positions = _rotation(cos, sin, positions, B, T, dev)
+    if return_values:
+        k_values = torch.empty((B, T, H, D), dtype=k.dtype, device=dev) if k_values is None else k_values
+        v_values = torch.empty((B, T, H, D), dtype=k.dtype, device=dev) if v_values is None else v_values
+    for name, t in (("k_values", k_values), ("v_values", v_values)):
+        if t is not None and (t.shape != k.shape or t.dtype != k.dtype or t.device != dev or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous tensor like k")
+    st = lib.spec_kv_append(k.data_ptr(), *ks, v.data_ptr(), *vs, dt, B, T, H, D, cache.data_ptr(), pages, page,
+                            page_table.data_ptr(), width, start.data_ptr(), _ptr(new_lens), _ptr(cos), _ptr(sin), length,
+                            pairs, int(interleaved), _ptr(positions), _ptr(k_values), _ptr(v_values), _stream(dev))
+    _check(st, "spec_kv_append")
+    return None if k_values is None and v_values is None else (k_values, v_values)
+
+
+def spec_kv_attention_workspace_size(B: int, T: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(_library().spec_kv_attention_workspace_size(B, T, heads, kv_heads, head_dim))
+
+
+def spec_kv_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor, *,
+                      new_lens=None, parent=None, scale=None, cos=None, sin=None, positions=None,
+                      interleaved: bool = False, workspace=None, out=None) -> torch.Tensor:
+    """Attention of the step's new tokens' queries [B, T, heads, head_dim] over the 4-bit cache, which holds
+    the new tokens already (see spec_kv_append: same cache, page_table, start, new_lens and rotation).
+
+    Token t sees the tokens before start[b], and of the new ones 0 .. t (a chain), or its ancestors and itself
+    if `parent` [T] gives a tree.  scale defaults to head_dim ** -0.5.  Returns [B, T, heads, head_dim]."""
+    lib = _library()
+    qs, dt, dev = _heads4(q, "q"), _kv_dtype(q, "q"), q.device
+    B, T, Hq, D = q.shape
+    if cache.dim() != 3 or cache.shape[1] < 1 or Hq % cache.shape[1]:
+        raise ValueError(f"{Hq} query heads do not share the cache's heads (shape {tuple(cache.shape)}) evenly")
+    H = cache.shape[1]
+    pages, page, page_table, width, start, new_lens = _cache(cache, page_table, start, new_lens, B, None, D, dev)
+    cos, sin, length, pairs, positions = _rotation(cos, sin, positions, B, T, dev)
+    parent = _maybe_ints(parent, "parent", (T,), dev)
+    if out is None:
+        out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor like q")
+    n = spec_kv_attention_workspace_size(B, T, Hq, H, D)
+    if workspace is None:
+        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    st = lib.spec_kv_attention(q.data_ptr(), *qs, dt, B, T, Hq, H, D, cache.data_ptr(), pages, page, page_table.data_ptr(),
+                               width, start.data_ptr(), _ptr(new_lens), _ptr(parent),
+                               1.0 / math.sqrt(D) if scale is None else float(scale), _ptr(cos), _ptr(sin), length, pairs,
+                               int(interleaved), _ptr(positions), out.data_ptr(), workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), _stream(dev))
+    _check(st, "spec_kv_attention")
+    return out
