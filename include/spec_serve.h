@@ -85,8 +85,8 @@ sv_status spec_logit_adjust(const void *logits, int64_t batch_stride, int64_t ro
  * One head's vector x of a token (the rotated key, or the value) is held as
  *   zero = fp16(min x), scale = max(fp16((max x - min x) / 15), 2^-24), both at most 65504,
  *   code_d = round((x_d - zero) / scale) clamped to 0 .. 15, standing for zero + scale code_d,
- * rounding to nearest even, of the exact values (the kernel settles what 32 bits leave in doubt
- * in 64).  A zero of -0 is held as +0.  A vector with a NaN or an infinity is held as NaN throughout.
+ * rounding to nearest even, of the exact values (fp16(y): y rounded to fp32, then to fp16; the kernel
+ * settles what 32 bits leave in doubt in 64).  A zero of -0 is held as +0.  A vector with a NaN or an infinity is held as NaN throughout.
  *
  * Rotation (cos, sin NULL: none): cos and sin are [table_len][pairs] fp32, pairs <= head_dim / 2;
  * pair i is dimensions (i, i + pairs), or (2 i, 2 i + 1) if interleaved; it becomes

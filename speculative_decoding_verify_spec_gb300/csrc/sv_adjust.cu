@@ -6,13 +6,14 @@
 // in fp32, rounded once to the logits' type.  One pass: every logit is read once and written
 // once (in place: only the 16-byte groups that change are written), so DRAM bounds it.
 //
-// A CTA owns TV consecutive tokens of one sequence for all its rows.  It counts the history's
-// tokens of its range once (a table in shared memory, integer atomics: the order does not
-// matter), marks them in a bitmap, then its warps take rows.  A warp adds the row's own
-// draft tokens to a copy of the bitmap; a vector of logits whose bitmap bits are all clear
-// is only masked and copied, and the few others look their counts up -- those on the row's
-// path count their occurrences there by walking it again.  The history is read once per
-// token range from L2, the price of needing no second kernel and no table in DRAM.
+// A CTA owns TV consecutive tokens of one sequence for all its rows.  It streams its part of every
+// row through registers, masked, 16 bytes a lane and eight loads in flight; meanwhile it counts
+// the history's tokens of its range (a table in shared memory, integer atomics: the order does
+// not matter).  The few tokens that the history, the drafts or the bias list touch are compacted into
+// a list, and after the stream each (row, listed token) pair is computed from its logit, one
+// thread each, and stored over the streamed one.  So the long part does no arithmetic on
+// logits, and the part with arithmetic has no idle lanes.  The history is read once per token range
+// from L2, the price of needing no second kernel and no table in DRAM.
 #include <cstdint>
 
 #include "spec_serve.h"
@@ -47,9 +48,11 @@ constexpr uint32_t kPrompt = 0x80000000u;  // table word: the prompt holds the t
 template <int TV>
 struct AdjustShared {
     uint32_t count[TV];
-    uint32_t winner[TV];  // 1 + index of the last bias entry of the token, 0: none
-    uint32_t base[TV / 32];
-    uint32_t mine[kAdjWarps][TV / 32];
+    uint32_t winner[TV];      // 1 + index of the last bias entry of the token, 0: none
+    uint32_t touched[TV / 32];  // tokens of the history, the drafts or the bias list
+    uint32_t drafted[TV / 32];  // tokens of the drafts
+    uint16_t list[TV];        // the touched tokens
+    int listed;
 };
 
 template <typename T>
@@ -57,25 +60,26 @@ struct Elem;
 template <>
 struct Elem<float> {
     static constexpr int per = 4;
-    static __device__ __forceinline__ float get(const uint4 &v, int i) { return __uint_as_float((&v.x)[i]); }
-    static __device__ __forceinline__ void set(uint4 &v, int i, float x) { (&v.x)[i] = __float_as_uint(x); }
-    static __device__ __forceinline__ float one(const float *p) { return *p; }
+    static __device__ __forceinline__ float get(float x) { return x; }
     static __device__ __forceinline__ float round(float x) { return x; }
+    // -inf where the bit of an element is clear
+    static __device__ __forceinline__ void mask(uint4 &v, uint32_t ok) {
+        v.x = ok & 1 ? v.x : 0xFF800000u, v.y = ok & 2 ? v.y : 0xFF800000u;
+        v.z = ok & 4 ? v.z : 0xFF800000u, v.w = ok & 8 ? v.w : 0xFF800000u;
+    }
 };
 template <>
 struct Elem<__nv_bfloat16> {
     static constexpr int per = 8;
-    static __device__ __forceinline__ float get(const uint4 &v, int i) {
-        const uint32_t w = (&v.x)[i >> 1];
-        return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
-    }
-    static __device__ __forceinline__ void set(uint4 &v, int i, float x) {
-        const uint32_t b = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-        uint32_t &w = (&v.x)[i >> 1];
-        w = i & 1 ? (w & 0xFFFFu) | (b << 16) : (w & 0xFFFF0000u) | b;
-    }
-    static __device__ __forceinline__ float one(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+    static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
     static __device__ __forceinline__ __nv_bfloat16 round(float x) { return __float2bfloat16_rn(x); }
+    static __device__ __forceinline__ uint32_t two(uint32_t v, uint32_t ok) {
+        const uint32_t m = (ok & 1 ? 0xFFFFu : 0u) | (ok & 2 ? 0xFFFF0000u : 0u);
+        return (v & m) | (0xFF80FF80u & ~m);
+    }
+    static __device__ __forceinline__ void mask(uint4 &v, uint32_t ok) {
+        v.x = two(v.x, ok), v.y = two(v.y, ok >> 2), v.z = two(v.z, ok >> 4), v.w = two(v.w, ok >> 6);
+    }
 };
 
 // Walks the drafts of row r's context, nearest first: f(draft index).
@@ -109,14 +113,76 @@ __global__ void __launch_bounds__(kAdjThreads)
 
     griddep_launch_next();
     for (int i = tid; i < TV; i += kAdjThreads) sh.count[i] = 0, sh.winner[i] = 0;
-    for (int i = tid; i < TV / 32; i += kAdjThreads) sh.base[i] = 0;
+    for (int i = tid; i < TV / 32; i += kAdjThreads) sh.touched[i] = 0, sh.drafted[i] = 0;
+    if (tid == 0) sh.listed = 0;
     griddep_wait();
+    const int64_t words = (int64_t(a.V) + 31) / 32;
+    const T *in = static_cast<const T *>(a.in) + b * a.in_bs + t0;
+    T *out = static_cast<T *>(a.out) + b * a.out_bs + t0;
+    const uint32_t *allowed = a.allowed ? a.allowed + b * a.rows * words : nullptr;
+    auto is_allowed = [&](int r, int k) {
+        return allowed == nullptr || (__ldg(allowed + r * words + ((t0 + k) >> 5)) >> ((t0 + k) & 31) & 1u);
+    };
+
+    // the stream: warps take (row, chunk) pairs
+    constexpr int U = 8, kChunk = 32 * U;
+    const int chunks = (TV / per + kChunk - 1) / kChunk;
+    for (int item = warp; item < a.rows * chunks; item += kAdjWarps) {
+        const int r = item / chunks, part = item % chunks;
+        const T *src = in + r * a.in_rs;
+        T *dst = out + r * a.out_rs;
+        auto scalar = [&](int k) {
+            const bool ok = is_allowed(r, k);
+            if (a.in_place && ok) return;
+            dst[k] = ok ? src[k] : E::round(-__int_as_float(0x7f800000));
+        };
+        const uintptr_t ai = reinterpret_cast<uintptr_t>(src), ao = reinterpret_cast<uintptr_t>(dst);
+        if (((ai ^ ao) & 15) != 0) {  // the two rows lie differently on the 16-byte grid
+            const int k1 = min(n, (part + 1) * kChunk * per);
+            for (int k = part * kChunk * per + lane; k < k1; k += 32) scalar(k);
+            continue;
+        }
+        const int head = min(n, int((16 - (ai & 15)) & 15) / int(sizeof(T)));
+        const int nv = (n - head) / per, tail = head + nv * per;
+        if (part == 0) {  // the row's ends off the grid
+            if (lane < head) scalar(lane);
+            if (lane < n - tail) scalar(tail + lane);
+        }
+        const uint4 *src4 = reinterpret_cast<const uint4 *>(src + head);
+        uint4 *dst4 = reinterpret_cast<uint4 *>(dst + head);
+        const uint32_t *mask = allowed ? allowed + r * words : nullptr;
+        constexpr uint32_t kAll = (1u << per) - 1;
+        uint4 x[U];
+        uint32_t ok[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int v = part * kChunk + u * 32 + lane;
+            ok[u] = kAll;
+            if (v < nv) {
+                x[u] = __ldcs(src4 + v);
+                if (mask) {
+                    const uint32_t e = uint32_t(t0 + head + v * per), s = e & 31;
+                    const uint32_t lo = __ldg(mask + (e >> 5)), hi = s + per > 32 ? __ldg(mask + (e >> 5) + 1) : 0u;
+                    ok[u] = __funnelshift_r(lo, hi, s) & kAll;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int v = part * kChunk + u * 32 + lane;
+            if (v < nv && !(a.in_place && ok[u] == kAll)) {
+                if (mask) E::mask(x[u], ok[u]);
+                dst4[v] = x[u];
+            }
+        }
+    }
+    if (!a.history && a.ndraft == 0 && a.nbias == 0) return;
+
+    // the tokens of this range that the history, the drafts and the bias list hold
     for (int i = tid; i < a.ndraft; i += kAdjThreads) draft_s[i] = a.drafts[b * a.ndraft + i];
     if (parent_s)
         for (int i = tid; i < a.rows; i += kAdjThreads) parent_s[i] = a.parent[i];
     __syncthreads();
-
-    // the history's and the bias list's tokens of this range
     if (a.history) {
         const int64_t Lr = a.lengths[b];
         const int64_t L = Lr < 0 ? 0 : (Lr > a.history_stride ? a.history_stride : Lr);
@@ -127,7 +193,7 @@ __global__ void __launch_bounds__(kAdjThreads)
             if (k < uint32_t(n)) {
                 if (i < P) atomicOr(&sh.count[k], kPrompt);
                 else atomicAdd(&sh.count[k], 1u);
-                atomicOr(&sh.base[k >> 5], 1u << (k & 31));
+                atomicOr(&sh.touched[k >> 5], 1u << (k & 31));
             }
         };
         int64_t i = 0;
@@ -145,115 +211,47 @@ __global__ void __launch_bounds__(kAdjThreads)
         const uint32_t k = uint32_t(__ldg(a.bias_tokens + b * a.nbias + i)) - uint32_t(t0);
         if (k < uint32_t(n)) {
             atomicMax(&sh.winner[k], uint32_t(i + 1));
-            atomicOr(&sh.base[k >> 5], 1u << (k & 31));
+            atomicOr(&sh.touched[k >> 5], 1u << (k & 31));
+        }
+    }
+    for (int i = tid; i < a.ndraft; i += kAdjThreads) {
+        const uint32_t k = uint32_t(draft_s[i]) - uint32_t(t0);
+        if (k < uint32_t(n)) {
+            atomicOr(&sh.drafted[k >> 5], 1u << (k & 31));
+            atomicOr(&sh.touched[k >> 5], 1u << (k & 31));
         }
     }
     __syncthreads();
+    for (int i = tid; i < TV / 32; i += kAdjThreads) {
+        uint32_t w = sh.touched[i];
+        int at = w ? atomicAdd(&sh.listed, __popc(w)) : 0;
+        for (; w; w &= w - 1) sh.list[at++] = uint16_t(i * 32 + __ffs(w) - 1);
+    }
+    __syncthreads();  // (and the streamed logits are in place for this CTA's threads)
 
     const float rep = a.repetition ? a.repetition[b] : 1.f;
     const float freq = a.frequency ? a.frequency[b] : 0.f;
     const float pres = a.presence ? a.presence[b] : 0.f;
-    const int64_t words = (int64_t(a.V) + 31) / 32;
-
-    for (int r = warp; r < a.rows; r += kAdjWarps) {
-        // this row's bitmap: the base and the drafts of its context
-        const uint32_t *bits = sh.base;
-        if (a.ndraft > 0 && r > 0) {
-            __syncwarp();
-            for (int i = lane; i < TV / 32; i += 32) sh.mine[warp][i] = sh.base[i];
-            __syncwarp();
-            auto mark = [&](int j) {
-                const uint32_t k = uint32_t(draft_s[j]) - uint32_t(t0);
-                if (k < uint32_t(n)) atomicOr(&sh.mine[warp][k >> 5], 1u << (k & 31));
-            };
-            if (parent_s) {
-                if (lane == 0) for_path(parent_s, r, mark);
-            } else {
-                for (int j = lane; j < r; j += 32) mark(j);
-            }
-            __syncwarp();
-            bits = sh.mine[warp];
-        }
-        // one touched token: k its place in the range
-        auto adjust = [&](float l, int k) {
-            if (!SV_IN(k, TV)) return l;
-            uint32_t w = sh.count[k];
-            if (a.ndraft > 0 && r > 0) {
-                int more = 0;
-                for_path(parent_s, r, [&](int j) { more += draft_s[j] == t0 + k; });
-                w += more;
-            }
+    const int listed = sh.listed;
+    // threads take listed tokens, and of each the rows in turn (four loads in flight)
+    const int groups = max(1, kAdjThreads / max(1, listed));  // threads that share a token
+    for (int e = tid; e < listed * groups; e += kAdjThreads) {
+        const int k = sh.list[e % listed], r0 = e / listed;
+        if (!SV_IN(k, n)) continue;
+        const uint32_t base = sh.count[k], won = sh.winner[k];
+        const bool drafted = sh.drafted[k >> 5] >> (k & 31) & 1u;
+        const float bias = won && SV_IN(won - 1, a.nbias) ? __ldg(a.bias_values + b * a.nbias + won - 1) : 0.f;
+#pragma unroll 4
+        for (int r = r0; r < a.rows; r += groups) {
+            if (!is_allowed(r, k)) continue;
+            uint32_t w = base;
+            if (drafted) for_path(parent_s, r, [&](int j) { w += draft_s[j] == t0 + k; });
             const uint32_t c = w & ~kPrompt;
+            float l = E::get(in[r * a.in_rs + k]);
             if (w) l = l > 0.f ? __fdiv_rn(l, rep) : __fmul_rn(l, rep);
             l = __fsub_rn(__fsub_rn(l, __fmul_rn(freq, float(c))), c ? pres : 0.f);
-            const uint32_t won = sh.winner[k];
-            if (won && SV_IN(won - 1, a.nbias)) l = __fadd_rn(l, __ldg(a.bias_values + b * a.nbias + won - 1));
-            return l;
-        };
-        const T *src = static_cast<const T *>(a.in) + b * a.in_bs + r * a.in_rs + t0;
-        T *dst = static_cast<T *>(a.out) + b * a.out_bs + r * a.out_rs + t0;
-        const uint32_t *mask = a.allowed ? a.allowed + (b * a.rows + r) * words : nullptr;
-        const float ninf = -__int_as_float(0x7f800000);
-        auto scalar = [&](int k) {
-            const bool ok = mask == nullptr || (__ldg(mask + ((t0 + k) >> 5)) >> ((t0 + k) & 31) & 1u);
-            const bool touched = bits[k >> 5] >> (k & 31) & 1u;
-            if (a.in_place && ok && !touched) return;
-            T v = src[k];
-            if (!ok) v = E::round(ninf);
-            else if (touched) v = E::round(adjust(E::one(src + k), k));
-            dst[k] = v;
-        };
-        const uintptr_t ai = reinterpret_cast<uintptr_t>(src), ao = reinterpret_cast<uintptr_t>(dst);
-        if (((ai ^ ao) & 15) != 0) {  // the two rows lie differently on the 16-byte grid
-            for (int k = lane; k < n; k += 32) scalar(k);
-            continue;
-        }
-        const int head = min(n, int((16 - (ai & 15)) & 15) / int(sizeof(T)));
-        const int nv = (n - head) / per;
-        if (lane < head) scalar(lane);
-        const int tail = head + nv * per;
-        if (lane < n - tail) scalar(tail + lane);
-        const uint4 *src4 = reinterpret_cast<const uint4 *>(src + head);
-        uint4 *dst4 = reinterpret_cast<uint4 *>(dst + head);
-        constexpr int U = 8;
-        for (int v0 = 0; v0 < nv; v0 += 32 * U) {
-            uint4 x[U];
-            uint32_t ok[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int v = v0 + u * 32 + lane;
-                ok[u] = (1u << per) - 1;
-                if (v < nv) {
-                    x[u] = __ldcs(src4 + v);
-                    if (mask) {
-                        const uint32_t e = uint32_t(t0 + head + v * per), s = e & 31;
-                        const uint32_t lo = __ldg(mask + (e >> 5));
-                        const uint32_t hi = s + per > 32 ? __ldg(mask + (e >> 5) + 1) : 0u;
-                        ok[u] &= __funnelshift_r(lo, hi, s);
-                    }
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int v = v0 + u * 32 + lane;
-                if (v >= nv) continue;
-                const int k = head + v * per;
-                const uint32_t s = uint32_t(k) & 31;
-                const uint32_t touched = __funnelshift_r(bits[k >> 5], s + per > 32 ? bits[(k >> 5) + 1] : 0u, s) &
-                                         ((1u << per) - 1);
-                if (a.in_place && touched == 0 && ok[u] == (1u << per) - 1) continue;
-                if (touched & ok[u]) {
-#pragma unroll
-                    for (int i = 0; i < per; ++i)
-                        if (touched & ok[u] & (1u << i)) E::set(x[u], i, adjust(E::get(x[u], i), k + i));
-                }
-                if (ok[u] != (1u << per) - 1) {
-#pragma unroll
-                    for (int i = 0; i < per; ++i)
-                        if (!(ok[u] & (1u << i))) E::set(x[u], i, ninf);
-                }
-                dst4[v] = x[u];
-            }
+            if (won) l = __fadd_rn(l, bias);
+            out[r * a.out_rs + k] = E::round(l);
         }
     }
 }

@@ -41,9 +41,7 @@ __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k ^
 __device__ __forceinline__ uint16_t half_sat(float x) {
     return __half_as_ushort(__float2half_rn(fminf(fmaxf(x, -65504.f), 65504.f)));
 }
-__device__ __noinline__ uint16_t half_sat_exact(double x) {
-    return __half_as_ushort(__double2half(fmin(fmax(x, -65504.0), 65504.0)));
-}
+__device__ __noinline__ uint16_t scale_exact(double x) { return half_sat(__double2float_rn(x)); }
 
 // Quantises one head vector held as hi + lo (E dimensions a lane): the lane's codes (4 bits each),
 // and the scale and zero as fp16 bits in one word (scale low).
@@ -70,18 +68,16 @@ __device__ __forceinline__ uint32_t quantise(const float (&hi)[E], const float (
         mnl = mxl = 0.f;
     }
     mnh = of_key(kn), mxh = of_key(kx);
-    // zero = fp16(min): hi's own rounding is the exact value's unless hi is a midpoint of fp16
-    // (12 low bits clear) or in fp16's subnormal range
+    // zero = fp16(fp32(min)): hi is that fp32 number
     uint16_t zb = half_sat(mnh);
-    if (mnl != 0.f && ((__float_as_uint(mnh) & 0xFFFu) == 0 || fabsf(mnh) < 6.2e-5f))
-        zb = half_sat_exact(double(mnh) + double(mnl));
-    // scale = fp16(range / 15): the fp32 quotient is off by less than 2 units of its last place
+    // scale = fp16(fp32(range / 15)): the fp32 quotient below is off by a few units of its last
+    // place at most, which matters next to a midpoint of fp16
     const float range = (mxh - mnh) + (mxl - mnl);
     const float t = range * (1.f / 15.f);
     uint16_t sb = half_sat(t);
     const int low = int(__float_as_uint(t) & 0x1FFFu) - 0x1000;
     if ((low >= -8 && low <= 8) || t < 6.2e-5f || !(t < 65000.f))
-        sb = half_sat_exact((((double(mxh) - double(mnh)) + (double(mxl) - double(mnl)))) / 15.0);
+        sb = scale_exact(((double(mxh) - double(mnh)) + (double(mxl) - double(mnl))) / 15.0);
     if (sb == 0) sb = 1;  // 2^-24
     if (zb == 0x8000u) zb = 0;
     meta = uint32_t(zb) << 16 | sb;

@@ -83,8 +83,8 @@ def quantise(x):
         bad = ~np.isfinite(x).all(-1, keepdims=True)
         y = np.where(bad, 0.0, x)
         low, high = y.min(-1, keepdims=True), y.max(-1, keepdims=True)
-        zero = np.clip(low, -65504, 65504).astype(np.float16) + np.float16(0)  # (-0 is held as +0)
-        scale = np.maximum(np.minimum((high - low) / 15, 65504).astype(np.float16), np.float16(2.0**-24))
+        zero = np.clip(low, -65504, 65504).astype(np.float32).astype(np.float16) + np.float16(0)  # (-0 is held as +0)
+        scale = np.maximum(np.minimum((high - low) / 15, 65504).astype(np.float32).astype(np.float16), np.float16(2.0**-24))
         code = np.clip(np.rint((y - zero.astype(np.float64)) / scale.astype(np.float64)), 0, 15).astype(np.uint8)
     nan = np.float16("nan")
     return np.where(bad, 0, code).astype(np.uint8), np.where(bad, nan, scale), np.where(bad, nan, zero)
