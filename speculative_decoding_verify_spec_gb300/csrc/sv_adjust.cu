@@ -6,14 +6,15 @@
 // in fp32, rounded once to the logits' type.  One pass: every logit is read once and written
 // once (in place: only the 16-byte groups that change are written), so DRAM bounds it.
 //
-// A CTA owns TV consecutive tokens of one sequence for all its rows.  It streams its part of every
-// row through registers, masked, 16 bytes a lane and eight loads in flight; meanwhile it counts
-// the history's tokens of its range (a table in shared memory, integer atomics: the order does
-// not matter).  The few tokens that the history, the drafts or the bias list touch are compacted into
-// a list, and after the stream each (row, listed token) pair is computed from its logit, one
-// thread each, and stored over the streamed one.  So the long part does no arithmetic on
-// logits, and the part with arithmetic has no idle lanes.  The history is read once per token range
-// from L2, the price of needing no second kernel and no table in DRAM.
+// A CTA owns TV consecutive tokens of one sequence for all its rows.  Its warps take 2 KB chunks of the
+// rows through a ring of buffers in shared memory, filled by asynchronous copies (and each chunk's mask
+// words with it), so that loads are under way from the first moment on.  Meanwhile the CTA counts the
+// history's tokens of its range (a table in shared memory, integer atomics: the order does not matter)
+// and lists the tokens that the history, the drafts or the bias list touch.  A chunk that has arrived is
+// adjusted in place at its listed tokens, which the lanes share out (text repeats few tokens: an
+// arithmetic branch in the stream itself would leave most lanes idle most of the time), and then
+// masked on its way from shared memory to the output.  The history is read once per token range from L2,
+// the price of needing no second kernel and no table in DRAM.
 #include <cstdint>
 
 #include "spec_serve.h"
@@ -45,15 +46,31 @@ struct AdjustArgs {
 
 constexpr uint32_t kPrompt = 0x80000000u;  // table word: the prompt holds the token; low bits: output count
 
+constexpr int kVecs = 4, kChunkVecs = 32 * kVecs;  // 16-byte vectors per lane and per chunk
+constexpr int kRing = 4;                           // chunks of a warp in shared memory
+
 template <int TV>
 struct AdjustShared {
+    uint4 chunk[kAdjWarps][kRing][kChunkVecs];
+    uint32_t mask[kAdjWarps][kRing][36];           // the chunk's words of the allowed mask
     uint32_t count[TV];
-    uint32_t winner[TV];      // 1 + index of the last bias entry of the token, 0: none
-    uint32_t touched[TV / 32];  // tokens of the history, the drafts or the bias list
-    uint32_t drafted[TV / 32];  // tokens of the drafts
-    uint16_t list[TV];        // the touched tokens
-    int listed;
+    uint32_t winner[TV / 2];                       // 16 bits each: 1 + index of the token's last bias entry, 0: none
+    uint16_t list[TV];                             // the touched tokens in order
+    uint32_t touched[TV / 32], drafted[TV / 32];   // tokens of history, drafts or bias list; of the drafts
+    int before[TV / 32];                           // listed tokens before each word of `touched`
 };
+static_assert(SV_MAX_BIAS < 65535, "");
+
+// Four bits as byte masks' top bits: bit j to bit 8 j + 7.
+__device__ __forceinline__ uint32_t spread4(uint32_t bits) { return (bits * 0x10204080u) & 0x80808080u; }
+// Bytes of v by prmt's selector: 8 + j is byte j's sign, eight times over.
+template <uint32_t S>
+__device__ __forceinline__ uint32_t pick(uint32_t v) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(v), "n"(S));
+    return r;
+}
+__device__ __forceinline__ uint32_t keep(uint32_t v, uint32_t m, uint32_t other) { return (v & m) | (other & ~m); }
 
 template <typename T>
 struct Elem;
@@ -73,14 +90,24 @@ struct Elem<__nv_bfloat16> {
     static constexpr int per = 8;
     static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
     static __device__ __forceinline__ __nv_bfloat16 round(float x) { return __float2bfloat16_rn(x); }
-    static __device__ __forceinline__ uint32_t two(uint32_t v, uint32_t ok) {
-        const uint32_t m = (ok & 1 ? 0xFFFFu : 0u) | (ok & 2 ? 0xFFFF0000u : 0u);
-        return (v & m) | (0xFF80FF80u & ~m);
-    }
     static __device__ __forceinline__ void mask(uint4 &v, uint32_t ok) {
-        v.x = two(v.x, ok), v.y = two(v.y, ok >> 2), v.z = two(v.z, ok >> 4), v.w = two(v.w, ok >> 6);
+        const uint32_t a = spread4(ok & 15), b = spread4(ok >> 4);  // a byte's sign selects a half-word
+        v.x = keep(v.x, pick<0x9988u>(a), 0xFF80FF80u), v.y = keep(v.y, pick<0xBBAAu>(a), 0xFF80FF80u);
+        v.z = keep(v.z, pick<0x9988u>(b), 0xFF80FF80u), v.w = keep(v.w, pick<0xBBAAu>(b), 0xFF80FF80u);
     }
 };
+
+__device__ __forceinline__ void copy_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async4(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Walks the drafts of row r's context, nearest first: f(draft index).
 template <typename F>
@@ -97,8 +124,7 @@ __device__ __forceinline__ void for_path(const int *parent_s, int r, F f) {
 }
 
 template <typename T, int TV>
-__global__ void __launch_bounds__(kAdjThreads)
-    adjust_kernel(const AdjustArgs a, int tiles) {
+__global__ void __launch_bounds__(kAdjThreads, 2) adjust_kernel(const AdjustArgs a, int tiles) {
     extern __shared__ __align__(16) unsigned char raw[];
     using Sh = AdjustShared<TV>;
     Sh &sh = *reinterpret_cast<Sh *>(raw);
@@ -110,73 +136,59 @@ __global__ void __launch_bounds__(kAdjThreads)
     const int n = min(TV, a.V - t0);  // tokens of this range
     using E = Elem<T>;
     constexpr int per = E::per;
+    constexpr uint32_t kAll = (1u << per) - 1;
+    constexpr int kChunks = (TV / per + kChunkVecs - 1) / kChunkVecs;
+    const int64_t words = (int64_t(a.V) + 31) / 32;
+    const int items = a.rows * kChunks;
 
     griddep_launch_next();
-    for (int i = tid; i < TV; i += kAdjThreads) sh.count[i] = 0, sh.winner[i] = 0;
+    for (int i = tid; i < TV; i += kAdjThreads) sh.count[i] = 0;
+    for (int i = tid; i < TV / 2; i += kAdjThreads) sh.winner[i] = 0;
     for (int i = tid; i < TV / 32; i += kAdjThreads) sh.touched[i] = 0, sh.drafted[i] = 0;
-    if (tid == 0) sh.listed = 0;
     griddep_wait();
-    const int64_t words = (int64_t(a.V) + 31) / 32;
-    const T *in = static_cast<const T *>(a.in) + b * a.in_bs + t0;
-    T *out = static_cast<T *>(a.out) + b * a.out_bs + t0;
-    const uint32_t *allowed = a.allowed ? a.allowed + b * a.rows * words : nullptr;
-    auto is_allowed = [&](int r, int k) {
-        return allowed == nullptr || (__ldg(allowed + r * words + ((t0 + k) >> 5)) >> ((t0 + k) & 31) & 1u);
-    };
 
-    // the stream: warps take (row, chunk) pairs
-    constexpr int U = 8, kChunk = 32 * U;
-    const int chunks = (TV / per + kChunk - 1) / kChunk;
-    for (int item = warp; item < a.rows * chunks; item += kAdjWarps) {
-        const int r = item / chunks, part = item % chunks;
-        const T *src = in + r * a.in_rs;
-        T *dst = out + r * a.out_rs;
-        auto scalar = [&](int k) {
-            const bool ok = is_allowed(r, k);
-            if (a.in_place && ok) return;
-            dst[k] = ok ? src[k] : E::round(-__int_as_float(0x7f800000));
-        };
-        const uintptr_t ai = reinterpret_cast<uintptr_t>(src), ao = reinterpret_cast<uintptr_t>(dst);
-        if (((ai ^ ao) & 15) != 0) {  // the two rows lie differently on the 16-byte grid
-            const int k1 = min(n, (part + 1) * kChunk * per);
-            for (int k = part * kChunk * per + lane; k < k1; k += 32) scalar(k);
-            continue;
-        }
-        const int head = min(n, int((16 - (ai & 15)) & 15) / int(sizeof(T)));
-        const int nv = (n - head) / per, tail = head + nv * per;
-        if (part == 0) {  // the row's ends off the grid
-            if (lane < head) scalar(lane);
-            if (lane < n - tail) scalar(tail + lane);
-        }
-        const uint4 *src4 = reinterpret_cast<const uint4 *>(src + head);
-        uint4 *dst4 = reinterpret_cast<uint4 *>(dst + head);
-        const uint32_t *mask = allowed ? allowed + r * words : nullptr;
-        constexpr uint32_t kAll = (1u << per) - 1;
-        uint4 x[U];
-        uint32_t ok[U];
+    // chunk `part` of row r: its vectors [v0, v1) after `head` elements off the 16-byte grid
+    struct Chunk {
+        const T *src;
+        T *dst;
+        const uint32_t *mask;
+        int r, part, head, nv, v0, v1;
+        bool vec;  // the two rows lie alike on the grid
+    };
+    auto chunk_of = [&](int item) {
+        Chunk c;
+        c.r = item / kChunks, c.part = item % kChunks;
+        c.src = static_cast<const T *>(a.in) + b * a.in_bs + c.r * a.in_rs + t0;
+        c.dst = static_cast<T *>(a.out) + b * a.out_bs + c.r * a.out_rs + t0;
+        c.mask = a.allowed ? a.allowed + (b * a.rows + c.r) * words : nullptr;
+        const uintptr_t ai = reinterpret_cast<uintptr_t>(c.src), ao = reinterpret_cast<uintptr_t>(c.dst);
+        c.vec = ((ai ^ ao) & 15) == 0;
+        c.head = min(n, int((16 - (ai & 15)) & 15) / int(sizeof(T)));
+        c.nv = (n - c.head) / per;
+        c.v0 = c.part * kChunkVecs, c.v1 = min(c.nv, c.v0 + kChunkVecs);
+        return c;
+    };
+    auto fetch = [&](int item, int slot) {
+        if (item < items) {
+            const Chunk c = chunk_of(item);
+            if (c.vec && c.v0 < c.v1) {
+                const uint4 *src4 = reinterpret_cast<const uint4 *>(c.src + c.head);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int v = part * kChunk + u * 32 + lane;
-            ok[u] = kAll;
-            if (v < nv) {
-                x[u] = __ldcs(src4 + v);
-                if (mask) {
-                    const uint32_t e = uint32_t(t0 + head + v * per), s = e & 31;
-                    const uint32_t lo = __ldg(mask + (e >> 5)), hi = s + per > 32 ? __ldg(mask + (e >> 5) + 1) : 0u;
-                    ok[u] = __funnelshift_r(lo, hi, s) & kAll;
+                for (int u = 0; u < kVecs; ++u) {
+                    const int v = c.v0 + u * 32 + lane;
+                    if (v < c.v1) copy_async16(&sh.chunk[warp][slot][u * 32 + lane], src4 + v);
+                }
+                if (c.mask) {  // at most 33 words
+                    const int e0 = t0 + c.head + c.v0 * per, w0 = e0 >> 5, w1 = (t0 + c.head + c.v1 * per - 1) >> 5;
+                    if (w0 + lane <= w1) copy_async4(&sh.mask[warp][slot][lane], c.mask + w0 + lane);
+                    if (lane == 0 && w0 + 32 <= w1) copy_async4(&sh.mask[warp][slot][32], c.mask + w0 + 32);
                 }
             }
         }
+        copy_commit();
+    };
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int v = part * kChunk + u * 32 + lane;
-            if (v < nv && !(a.in_place && ok[u] == kAll)) {
-                if (mask) E::mask(x[u], ok[u]);
-                dst4[v] = x[u];
-            }
-        }
-    }
-    if (!a.history && a.ndraft == 0 && a.nbias == 0) return;
+    for (int i = 0; i < kRing - 1; ++i) fetch(warp + i * kAdjWarps, i);
 
     // the tokens of this range that the history, the drafts and the bias list hold
     for (int i = tid; i < a.ndraft; i += kAdjThreads) draft_s[i] = a.drafts[b * a.ndraft + i];
@@ -199,18 +211,26 @@ __global__ void __launch_bounds__(kAdjThreads)
         int64_t i = 0;
         if ((reinterpret_cast<uintptr_t>(h) & 15) == 0) {
             const int4 *h4 = reinterpret_cast<const int4 *>(h);
+#pragma unroll 4
             for (int64_t q = tid; q < L / 4; q += kAdjThreads) {
                 const int4 v = __ldg(h4 + q);
                 note(v.x, 4 * q), note(v.y, 4 * q + 1), note(v.z, 4 * q + 2), note(v.w, 4 * q + 3);
             }
             i = L / 4 * 4;
         }
+#pragma unroll 4
         for (i += tid; i < L; i += kAdjThreads) note(__ldg(h + i), i);
     }
     for (int i = tid; i < a.nbias; i += kAdjThreads) {
         const uint32_t k = uint32_t(__ldg(a.bias_tokens + b * a.nbias + i)) - uint32_t(t0);
         if (k < uint32_t(n)) {
-            atomicMax(&sh.winner[k], uint32_t(i + 1));
+            uint32_t *word = &sh.winner[k >> 1], old = *word;
+            const uint32_t shift = 16 * (k & 1), mine = uint32_t(i + 1);
+            while ((old >> shift & 0xFFFFu) < mine) {  // the largest index stays, whatever the order
+                const uint32_t was = atomicCAS(word, old, (old & ~(0xFFFFu << shift)) | mine << shift);
+                if (was == old) break;
+                old = was;
+            }
             atomicOr(&sh.touched[k >> 5], 1u << (k & 31));
         }
     }
@@ -222,38 +242,103 @@ __global__ void __launch_bounds__(kAdjThreads)
         }
     }
     __syncthreads();
-    for (int i = tid; i < TV / 32; i += kAdjThreads) {
-        uint32_t w = sh.touched[i];
-        int at = w ? atomicAdd(&sh.listed, __popc(w)) : 0;
-        for (; w; w &= w - 1) sh.list[at++] = uint16_t(i * 32 + __ffs(w) - 1);
+    if (warp == 0) {
+        int run = 0;
+        for (int i0 = 0; i0 < TV / 32; i0 += 32) {
+            const int c = __popc(sh.touched[i0 + lane]);
+            int inc = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            sh.before[i0 + lane] = run + inc - c;
+            run += __shfl_sync(0xFFFFFFFFu, inc, 31);
+        }
     }
-    __syncthreads();  // (and the streamed logits are in place for this CTA's threads)
+    __syncthreads();
+    for (int k = tid; k < n; k += kAdjThreads) {
+        const uint32_t w = sh.touched[k >> 5], bit = 1u << (k & 31);
+        if (w & bit) sh.list[sh.before[k >> 5] + __popc(w & (bit - 1))] = uint16_t(k);
+    }
+    __syncthreads();
 
     const float rep = a.repetition ? a.repetition[b] : 1.f;
     const float freq = a.frequency ? a.frequency[b] : 0.f;
     const float pres = a.presence ? a.presence[b] : 0.f;
-    const int listed = sh.listed;
-    // threads take listed tokens, and of each the rows in turn (four loads in flight)
-    const int groups = max(1, kAdjThreads / max(1, listed));  // threads that share a token
-    for (int e = tid; e < listed * groups; e += kAdjThreads) {
-        const int k = sh.list[e % listed], r0 = e / listed;
-        if (!SV_IN(k, n)) continue;
-        const uint32_t base = sh.count[k], won = sh.winner[k];
-        const bool drafted = sh.drafted[k >> 5] >> (k & 31) & 1u;
-        const float bias = won && SV_IN(won - 1, a.nbias) ? __ldg(a.bias_values + b * a.nbias + won - 1) : 0.f;
-#pragma unroll 4
-        for (int r = r0; r < a.rows; r += groups) {
-            if (!is_allowed(r, k)) continue;
-            uint32_t w = base;
-            if (drafted) for_path(parent_s, r, [&](int j) { w += draft_s[j] == t0 + k; });
-            const uint32_t c = w & ~kPrompt;
-            float l = E::get(in[r * a.in_rs + k]);
-            if (w) l = l > 0.f ? __fdiv_rn(l, rep) : __fmul_rn(l, rep);
-            l = __fsub_rn(__fsub_rn(l, __fmul_rn(freq, float(c))), c ? pres : 0.f);
-            if (won) l = __fadd_rn(l, bias);
-            out[r * a.out_rs + k] = E::round(l);
+    // a touched token k of row r
+    auto adjust = [&](float l, int r, int k) {
+        if (!SV_IN(k, n)) return l;
+        uint32_t w = sh.count[k];
+        if (r > 0 && (sh.drafted[k >> 5] >> (k & 31) & 1u)) for_path(parent_s, r, [&](int j) { w += draft_s[j] == t0 + k; });
+        const uint32_t c = w & ~kPrompt;
+        if (w) l = l > 0.f ? __fdiv_rn(l, rep) : __fmul_rn(l, rep);
+        l = __fsub_rn(__fsub_rn(l, __fmul_rn(freq, float(c))), c ? pres : 0.f);
+        const uint32_t won = sh.winner[k >> 1] >> (16 * (k & 1)) & 0xFFFFu;
+        if (won && SV_IN(won - 1, a.nbias)) l = __fadd_rn(l, __ldg(a.bias_values + b * a.nbias + won - 1));
+        return l;
+    };
+    auto is_touched = [&](int k) { return sh.touched[k >> 5] >> (k & 31) & 1u; };
+    auto listed_before = [&](int k) { return sh.before[k >> 5] + __popc(sh.touched[k >> 5] & ((1u << (k & 31)) - 1)); };
+
+    for (int item = warp, slot = 0; item < items; item += kAdjWarps, slot = (slot + 1) % kRing) {
+        fetch(item + (kRing - 1) * kAdjWarps, (slot + kRing - 1) % kRing);
+        const Chunk c = chunk_of(item);
+        auto scalar = [&](int k) {
+            const bool ok = c.mask == nullptr || (__ldg(c.mask + ((t0 + k) >> 5)) >> ((t0 + k) & 31) & 1u), mine = is_touched(k);
+            if (a.in_place && ok && !mine) return;
+            const T v = c.src[k];
+            c.dst[k] = !ok ? E::round(-__int_as_float(0x7f800000)) : mine ? E::round(adjust(E::get(v), c.r, k)) : v;
+        };
+        copy_wait<kRing - 1>();
+        __syncwarp();
+        if (!c.vec) {
+            const int k1 = min(n, (c.part + 1) * kChunkVecs * per);
+            for (int k = c.part * kChunkVecs * per + lane; k < k1; k += 32) scalar(k);
+            continue;
         }
+        if (c.part == 0) {  // the row's ends off the grid
+            const int tail = c.head + c.nv * per;
+            if (lane < c.head) scalar(lane);
+            if (lane < n - tail) scalar(tail + lane);
+        }
+        if (c.v0 < c.v1) {
+            uint4 *mine = sh.chunk[warp][slot];
+            const int k0 = c.head + c.v0 * per, k1 = c.head + c.v1 * per;  // the chunk's tokens
+            const int e0 = listed_before(k0), e1 = listed_before(k1 - 1) + int(is_touched(k1 - 1));
+            if (e0 < e1) {
+                T *elems = reinterpret_cast<T *>(mine);
+                for (int e = e0 + lane; e < e1; e += 32) {
+                    const int k = sh.list[e];
+                    if (SV_IN(k - k0, k1 - k0)) elems[k - k0] = E::round(adjust(E::get(elems[k - k0]), c.r, k));
+                }
+                __syncwarp();
+            }
+            uint4 *dst4 = reinterpret_cast<uint4 *>(c.dst + c.head);
+            const uint32_t first = uint32_t(t0 + k0) & 31;
+#pragma unroll
+            for (int u = 0; u < kVecs; ++u) {
+                const int v = c.v0 + u * 32 + lane;
+                if (v >= c.v1) continue;
+                uint32_t ok = kAll;
+                if (c.mask) {
+                    const uint32_t e = first + (u * 32 + lane) * per;
+                    const uint32_t *m = &sh.mask[warp][slot][e >> 5];
+                    ok = __funnelshift_r(m[0], m[1], e & 31) & kAll;  // (m[1] unread bits: any)
+                }
+                if (a.in_place && ok == kAll) {  // only what changes is written
+                    const int k = c.head + v * per;
+                    const uint32_t s = uint32_t(k) & 31, hi = s + per > 32 ? sh.touched[(k >> 5) + 1] : 0u;
+                    if ((__funnelshift_r(sh.touched[k >> 5], hi, s) & kAll) == 0) continue;
+                }
+                uint4 x = mine[u * 32 + lane];
+                if (ok != kAll) E::mask(x, ok);
+                dst4[v] = x;
+            }
+        }
+        __syncwarp();  // the buffer may be filled again
     }
+    copy_wait<0>();
 }
 
 template <typename T, int TV>

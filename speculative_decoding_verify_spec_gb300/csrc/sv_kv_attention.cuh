@@ -1,0 +1,950 @@
+// sv_kv_attention.cuh -- the new tokens' attention over the 4-bit paged cache: the kernels, instantiated
+// per head dimension by the translation units sv_kv_attention*.cu.
+//
+// For a query row q (one of the T x G rows that share a kv head) and cached tokens j with key
+// k_j = z_j + s_j code_j and value likewise,
+//   x_j = scale (s_j (q . (code_j - 8)) + (z_j + 8 s_j) sum(q)),  p_j = exp(x_j - m),
+//   out = [ sum_j (p_j s'_j) (code'_j - 8) + sum_j p_j (z'_j + 8 s'_j) ] / sum_j p_j,
+// so the matrix products run on the bare codes (exact in fp16) and each token's scale and zero
+// cost a multiply-add per score instead of one per dimension.
+//
+// Work: a unit is 32 to 128 tokens for one (sequence, kv head, tile of 8 NR rows).  All units of the
+// batch form one list; each CTA takes an equal, contiguous share of it, so ragged lengths balance
+// by themselves and a long context spreads over the card.  A segment (one sequence, head, row
+// tile) that ends up whole in a CTA is written out there; the others leave partial results
+// that the join kernel adds up.
+//
+// A CTA has a warp that copies units into a ring in shared memory, and consumer warps.  Each
+// consumer scores its part of a unit's tokens for all rows, the weights go through shared
+// memory, and each warp accumulates its own 16 or 32 dimensions over all the tokens: a key or value code
+// is unpacked once (or twice) per row tile and the accumulators need no joining.  Both products have
+// the cache as the 16-row operand (tokens x dimensions, dimensions x tokens) and the queries or
+// weights as the 8-column one, so that a single token's few heads are padded to 8 rows, not 16.  A
+// unit's scores are computed before the previous unit's output product, which leaves one barrier per
+// unit and independent work on both sides of it.  The running maximum moves only when a score passes
+// it by 2^8 (the weights fit fp16 either way).
+#pragma once
+
+#include <cstdint>
+
+#include "sv_checks.cuh"
+#include "sv_device.cuh"
+#include "sv_grid.cuh"
+#include "sv_kv.cuh"
+
+namespace sv {
+
+constexpr float kLazy = 8.f;            // log2 of how far a weight may pass 1
+constexpr uint64_t kCopyLimitNs = 1000000000ull;
+constexpr int kAttSMs = 152;
+
+#ifndef CAP64
+#define CAP64 64
+#endif
+#ifndef CAP128
+#define CAP128 64
+#endif
+#ifndef NT1
+#define NT1 64
+#endif
+#ifndef OC1
+#define OC1 4
+#endif
+#ifndef MH3
+#define MH3 2
+#endif
+#ifndef NT3
+#define NT3 64
+#endif
+#ifndef OC3
+#define OC3 3
+#endif
+#ifndef OC8
+#define OC8 2
+#endif
+#ifndef NTS
+#define NTS 64
+#endif
+#ifndef OCS
+#define OCS 4
+#endif
+#ifndef STG
+#define STG 4
+#endif
+// 16-row tiles of dimensions per consumer warp.
+__host__ __device__ constexpr int att_mh(int D, int NR) { return D == 64 ? 1 : D == 128 && NR >= 3 ? MH3 : 2; }
+// Tokens per unit.
+__host__ __device__ constexpr int att_tokens(int D, int NR) {
+    return D == 256 ? 128 : D == 128 ? (NR <= 2 ? NT1 : NT3) : NTS;
+}
+// Units in the ring: one whose product runs, one whose scores run, and those on their way.
+__host__ __device__ constexpr int att_stages(int D, int NR) { return D == 256 ? 4 : STG; }
+// CTAs per SM, by registers and shared memory.
+__host__ __device__ constexpr int att_occupancy(int D, int NR) {
+    return D == 256 ? 1 : D == 128 ? (NR <= 2 ? OC1 : NR <= 5 ? OC3 : OC8) : (NR <= 4 ? OCS : OCS - 1);
+}
+// Tiles of 8 NR rows: as few as there have to be and no larger than they need be.
+inline int att_nr(int64_t rows, int D) {
+    const int64_t cap = D == 64 ? CAP64 : CAP128, tiles = (rows + cap - 1) / cap;
+    const int nr = int(((rows + tiles - 1) / tiles + 7) / 8);
+    return nr == 7 ? 8 : nr;
+}
+
+struct AttArgs {
+    const uint16_t *q;
+    int64_t q_bs, q_ts, q_hs;
+    int bf16, vec;  // vec: query rows lie on the 16-byte grid
+    int B, T, H, G;  // H kv heads, G query heads each
+    const uint8_t *cache;
+    int num_pages, page, width, granule;  // granule: tokens per copy, a power of two dividing page and a unit
+    const int32_t *table, *start, *new_lens, *parent;
+    float scale;
+    Rotation rot;
+    uint16_t *out;
+    int row_tiles;
+    int *status;
+    struct AttDesc *desc;  // [grid]
+    float2 *ml;            // [2 grid][R] running maximum (log2) and sum
+    float *acc;            // [2 grid][R][D]
+};
+
+// The first segment of a CTA's share, for the joining kernel.
+struct AttDesc {
+    int lo, hi, total;  // the segment's units, and all units
+    int b, h, rt, fresh;
+};
+
+// Where a CTA's share begins.
+__device__ __forceinline__ int share_begin(int total, int c, int n) { return int(int64_t(c) * total / n); }
+__device__ __forceinline__ int share_owner(int total, int u, int n) { return int((int64_t(u + 1) * n - 1) / total); }
+
+struct SeqWork {
+    int before, fresh, len;
+    int tiles;       // units of a live segment
+    int live;        // row tiles with a live row
+    int units;       // of the whole sequence (the host has checked that all fit 31 bits)
+};
+template <int NT>
+__device__ __forceinline__ SeqWork seq_work(const AttArgs &a, int64_t b, int R) {
+    SeqWork w;
+    const int64_t capacity = int64_t(a.width) * a.page;
+    kv_lengths(a.start, a.new_lens, b, a.T, capacity, w.before, w.fresh);
+    const int64_t len = int64_t(w.before) + w.fresh;
+    w.len = int(len < capacity ? len : capacity);
+    w.tiles = w.len > 0 ? (w.len + NT - 1) / NT : 1;
+    w.live = int((int64_t(w.fresh) * a.G + R - 1) / R);
+    w.units = a.H * (w.live * w.tiles + (a.row_tiles - w.live));
+    return w;
+}
+
+// A position in the list of units.
+template <int NT>
+struct Cursor {
+    SeqWork w;
+    int base;  // first unit of sequence b
+    int b, h, rt, tile;
+    bool live;
+    __device__ __forceinline__ void place(const AttArgs &a, int u) {  // base <= u < base + w.units
+        int i = u - base;
+        const int lives = a.H * w.live * w.tiles;
+        live = i < lives;
+        if (live) {
+            tile = i % w.tiles;
+            i /= w.tiles;
+            rt = i % w.live, h = i / w.live;
+        } else {
+            i -= lives;
+            const int dead = a.row_tiles - w.live;
+            tile = 0, rt = w.live + i % dead, h = i / dead;
+        }
+    }
+    __device__ __forceinline__ int tiles() const { return live ? w.tiles : 1; }
+    // to unit u, the one after the current
+    __device__ __forceinline__ void next(const AttArgs &a, int R, int u) {
+        if (++tile < tiles()) return;
+        if (u == base + w.units) {
+            base += w.units;
+            if (++b >= a.B) return;
+            w = seq_work<NT>(a, b, R);
+        }
+        place(a, u);
+    }
+};
+
+// What the consumers know of a unit; written by the copying warp.
+struct Unit {
+    int b, h, rt, tile, tiles;
+    int before, len, fresh;   // tokens before the step; all; new ones (0: no live row)
+    uint32_t have;            // bit 4 g: granule g was loaded
+    int masked;               // not every token is seen by every row
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void mbar_init(uint32_t bar, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Waits for a phase; false after kCopyLimitNs.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+    if (mbar_try(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t i = 0;; ++i) {
+        if (mbar_try(bar, parity)) return true;
+        if ((i & 63) == 63 && global_ns() - t0 > kCopyLimitNs) return false;
+    }
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldmatrix2_trans(uint32_t &r0, uint32_t &r1, uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The codes in half-bytes 0 and 4 of w, less 8, as fp16 (1024 + code has its code in the low bits), and
+// 16 times those in half-bytes 1 and 5: all exact.  (The factor is in the queries, or taken out of the
+// output.)  Centred, so that sums over thousands of tokens do not cancel against the zeros' part.
+__device__ __forceinline__ uint32_t codes_even(uint32_t w) {
+    uint32_t r;  // (w & 0x000F000F) | 0x64006400 in one instruction
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(0x000F000Fu), "r"(0x64006400u));
+    asm("sub.f16x2 %0, %0, %1;" : "+r"(r) : "r"(0x64086408u));
+    return r;
+}
+__device__ __forceinline__ uint32_t codes_odd(uint32_t w) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(0x00F000F0u), "r"(0x64006400u));
+    asm("sub.f16x2 %0, %0, %1;" : "+r"(r) : "r"(0x64806480u));
+    return r;
+}
+
+__host__ __device__ constexpr int att_threads(int D, int NR) { return D * 2 / att_mh(D, NR) + 32; }
+
+template <int D, int NR>
+struct AttShared {
+    static constexpr int R = 8 * NR, NW = D / 16 / att_mh(D, NR), kConsumers = 32 * NW;
+    static constexpr int NT = att_tokens(D, NR), kStages = att_stages(D, NR);
+    static constexpr int kStageBytes = NT * (D + 8);
+    static constexpr int kQStride = D + 8;        // halves; 16 bytes past a multiple of 128: no bank conflicts
+    static constexpr int kPStride = 8 * (NR | 1);  // an odd number of 16-byte columns: none here either
+    alignas(128) uint8_t stage[kStages][kStageBytes];
+    alignas(16) __half q[R * kQStride];
+    alignas(16) __half p[2][NT * kPStride];       // [token][row]
+    // per pair of rows: their queries' sums and the scores that move the maximum (-inf until a score was
+    // seen); log2 scales of their scores and the maxima in log2 (0 until then)
+    alignas(16) float row_y[R / 2][4];
+    alignas(16) float row_p[R / 2][4];
+    alignas(16) float alpha[R];
+    float red[2][NW][R];
+    uint32_t redv[NW];
+    int row_node[R];  // the row's new token, -1: no live row
+    alignas(8) uint64_t full[kStages], empty[kStages];
+    Unit unit[kStages];
+};
+
+__device__ __forceinline__ float power2(int e) { return __int_as_float((127 + e) << 23); }  // -126 <= e <= 127
+// Barriers of the D consumer threads.
+template <int N>
+__device__ __forceinline__ void consumers_sync() {
+    asm volatile("barrier.cta.sync 1, %0;" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ bool consumers_or(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(uint32_t(x)), "n"(N)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Eight 16-bit numbers from p (vec: 16-byte aligned) as floats.
+__device__ __forceinline__ void load8(const uint16_t *p, bool vec, bool bf16, float (&x)[8]) {
+    if (vec) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p));
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = kv_to_float(uint16_t(u[i / 2] >> (16 * (i & 1))), bf16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = kv_to_float(__ldg(p + i), bf16);
+    }
+}
+
+// The queries of a segment's rows into shared memory: rotated, scaled by a power of two into fp16's
+// range (exact for 16-bit inputs but for values 2^-25 of the row's largest; a rotated value is
+// rounded to 11 bits), columns in the order in which the codes unpack.  Eight dimensions a thread.
+template <int D, int NR>
+__device__ __forceinline__ void load_queries(const AttArgs &a, AttShared<D, NR> &sh, const Unit &un, int tid) {
+    using Sh = AttShared<D, NR>;
+    constexpr int R = Sh::R, L = D / 8, P = Sh::kConsumers / L;  // lanes of a row, rows at a time
+    const int c = tid % L, d0 = c * 8;
+#pragma unroll 2
+    for (int r0 = 0; r0 < R; r0 += P) {
+        const int r = r0 + tid / L;
+        const int row = un.rt * R + r;
+        const int node = row / a.G, head = un.h * a.G + row % a.G;
+        const bool on = r < R && node < un.fresh;
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+        if (on) {
+            const uint16_t *qp = a.q + un.b * a.q_bs + node * a.q_ts + head * a.q_hs;
+            load8(qp + d0, a.vec, a.bf16, x);
+            if (a.rot.cos && d0 < 2 * a.rot.pairs) {
+                const int64_t arow = kv_rotation_row(a.rot, int64_t(un.b) * a.T + node, un.before + node);
+                const float *cp = a.rot.cos + arow, *sp = a.rot.sin + arow;
+                float y[8], cs[8], sn[8];
+                if (!a.rot.interleaved && a.rot.pairs % 8 == 0) {  // the chunk lies within one half
+                    const int e0 = d0 < a.rot.pairs ? d0 : d0 - a.rot.pairs;
+                    load8(qp + (d0 < a.rot.pairs ? d0 + a.rot.pairs : e0), a.vec, a.bf16, y);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        cs[i] = __ldg(cp + e0 + i);
+                        sn[i] = d0 < a.rot.pairs ? -__ldg(sp + e0 + i) : __ldg(sp + e0 + i);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        int partner, angle;
+                        float sign;
+                        if (kv_partner(a.rot, d0 + i, partner, angle, sign)) {
+                            y[i] = kv_to_float(__ldg(qp + partner), a.bf16);
+                            cs[i] = __ldg(cp + angle), sn[i] = sign * __ldg(sp + angle);
+                        } else {
+                            y[i] = 0.f, cs[i] = 1.f, sn[i] = 0.f;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], cs[i], y[i] * sn[i]);
+            }
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(fabsf(x[i])));
+#pragma unroll
+        for (int o = L / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        const int e2 = top == 0 ? 0 : int(top >> 23) - 127 - 10;  // the largest becomes 2^10 .. 2^11
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float v = a.scale < 0.f ? -x[i] : (a.scale == 0.f ? 0.f : x[i]);
+            x[i] = __half2float(__float2half_rn(ldexpf(v, -e2)));
+            sum += x[i];
+        }
+#pragma unroll
+        for (int o = L / 2; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (R % P != 0 && r >= R) continue;
+        // dimension 8 w + n of quad's quarter: k-step 2 w + (n % 4) / 2, the odd n scaled by 1 / 16
+        __half *dst = &sh.q[r * Sh::kQStride + 2 * (d0 / (D / 4)) + 2 * (d0 % (D / 4) / 8) * 16];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const float f = n & 1 ? 0.0625f : 1.f;
+            *reinterpret_cast<__half2 *>(dst + (n >> 1) * 16 + (n & 1) * 8) = __floats2half2_rn(x[n] * f, x[n + 4] * f);
+        }
+        if (c == 0) {
+            const float c2 = a.scale == 0.f ? 1.f : fmaxf(ldexpf(fabsf(a.scale) * 1.4426950408889634f, e2), 1.2e-38f);
+            sh.row_y[r / 2][r & 1] = sum, sh.row_y[r / 2][2 + (r & 1)] = -INFINITY;
+            sh.row_p[r / 2][r & 1] = c2, sh.row_p[r / 2][2 + (r & 1)] = 0.f;
+            sh.row_node[r] = on ? node : -1;
+        }
+    }
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_attention_kernel(const AttArgs a) {
+    using Sh = AttShared<D, NR>;
+    constexpr int R = Sh::R, NW = Sh::NW, NT = Sh::NT, TW = NT / NW, NG = TW / 16, kStages = Sh::kStages, KS = D / 16, E = D / 32;
+    constexpr int MH = att_mh(D, NR), kThreads = att_threads(D, NR), C = Sh::kConsumers;
+    constexpr bool kQRegs = NR * KS <= 16;  // the queries' fragments stay in registers
+    static_assert(NG >= 1 && TW % 16 == 0 && NT <= 128 && NT % 32 == 0 && NG * NR <= 8, "");
+    extern __shared__ __align__(128) unsigned char raw[];
+    Sh &sh = *reinterpret_cast<Sh *>(raw);
+    int *parent_s = reinterpret_cast<int *>(raw + sizeof(Sh));
+    const int anc_words = (a.T + 31) / 32;
+    uint32_t *anc_s = reinterpret_cast<uint32_t *>(parent_s + (a.parent ? a.T : 0));  // [R][anc_words]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+    const int ncta = int(gridDim.x), cta = int(blockIdx.x);
+
+    griddep_launch_next();
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&sh.full[i]), 1), mbar_init(smem_u32(&sh.empty[i]), NW);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    griddep_wait();
+    if (cta == 0 && tid == 0) *a.status = SV_OK;
+    if (a.parent)
+        for (int i = tid; i < a.T; i += kThreads) parent_s[i] = a.parent[i];
+
+    // all units, then the sequence where this CTA's share begins (every warp for itself)
+    int total = 0;
+    for (int b = lane; b < a.B; b += 32) total += seq_work<NT>(a, b, R).units;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+    const int ubegin = share_begin(total, cta, ncta), uend = share_begin(total, cta + 1, ncta);
+    if (ubegin >= uend) return;
+    Cursor<NT> cur;
+    {
+        int run = 0;
+        for (int b0 = 0;; b0 += 32) {  // (ubegin < total: some sequence holds it)
+            const int b = b0 + lane;
+            const int u = b < a.B ? seq_work<NT>(a, b, R).units : 0;
+            int inc = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            const int lo = run + inc - u;
+            const uint32_t hit = __ballot_sync(0xFFFFFFFFu, ubegin >= lo && ubegin < lo + u);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                cur.b = b0 + l;
+                cur.base = __shfl_sync(0xFFFFFFFFu, lo, l);
+                break;
+            }
+            run += __shfl_sync(0xFFFFFFFFu, inc, 31);
+            if (b0 + 32 >= a.B) return;  // never
+        }
+    }
+    cur.w = seq_work<NT>(a, cur.b, R);
+    cur.place(a, ubegin);
+    __syncthreads();
+
+    if (warp == NW) {
+        // the copies, up to kStages units ahead of the consumers
+        const int64_t page_bytes = kv_page_bytes(a.page, D);
+        const int gi = lane >> 2, piece = lane & 3;
+        const uint32_t all_granules = NT / a.granule == 8 ? 0x11111111u : 0x11111111u & ((1u << (4 * (NT / a.granule))) - 1);
+        for (int u = ubegin; u < uend; ++u) {
+            const int it = u - ubegin, stage = it % kStages;
+            const int tok = cur.tile * NT + gi * a.granule;
+            const uint8_t *src = nullptr;
+            int slot = 0;
+            if (gi * a.granule < NT && cur.live && tok < cur.w.len) {
+                const int pi = tok / a.page, pg = __ldg(a.table + int64_t(cur.b) * a.width + pi);
+                slot = tok - pi * a.page;
+                if (pg >= 0 && pg < a.num_pages && SV_IN(slot + a.granule - 1, a.page))
+                    src = a.cache + (int64_t(pg) * a.H + cur.h) * page_bytes;
+            }
+            const uint32_t bytes = src == nullptr ? 0 : piece < 2 ? a.granule * (D / 2) : a.granule * 4;
+            const uint32_t sum = __reduce_add_sync(0xFFFFFFFFu, bytes);
+            const uint32_t have = __ballot_sync(0xFFFFFFFFu, src != nullptr && piece == 0);
+            if (it >= kStages && !mbar_wait(smem_u32(&sh.empty[stage]), uint32_t(it / kStages - 1) & 1)) {
+                atomicExch(a.status, int(SV_ERR_TIMEOUT));
+                return;  // (the consumers' waits give up too)
+            }
+            const uint32_t bar = smem_u32(&sh.full[stage]);
+            if (lane == 0) {
+                sh.unit[stage] = Unit{cur.b, cur.h, cur.rt, cur.tile, cur.tiles(), cur.w.before, cur.w.len, cur.live ? cur.w.fresh : 0, have,
+                                      int((cur.tile + 1) * NT > cur.w.before || have != all_granules)};
+                mbar_expect(bar, sum);
+            }
+            __syncwarp();
+            if (src) {
+                const uint32_t dst = smem_u32(sh.stage[stage]);
+                if (piece < 2)
+                    bulk_load(dst + (piece * NT + gi * a.granule) * (D / 2), src + (piece * a.page + slot) * (D / 2), bytes, bar);
+                else
+                    bulk_load(dst + NT * D + ((piece - 2) * NT + gi * a.granule) * 4,
+                              src + a.page * D + ((piece - 2) * a.page + slot) * 4, bytes, bar);
+            }
+            if (u + 1 < uend) cur.next(a, R, u + 1);
+        }
+        return;
+    }
+
+    // MH 16-row tiles of dimensions x R rows: dimension 4 g + 2 h (+ 1, times 16) of the slice, rows 2 t4, 2 t4 + 1
+    float acc[MH][NR][4];
+    float l[NR][2], z[NR][2];
+    float s[NG][NR][4];   // scores of tokens g, g + 8 of each group, rows 2 t4, 2 t4 + 1
+    float vs[NG][2], vz[NG][2];
+    uint32_t qf[kQRegs ? KS : 2][kQRegs ? NR : 1][2];
+    int vexp = 0;         // values' scales are divided by 2^vexp: all are below 1 then
+    bool waits = true;
+    int stage = 0;
+    uint32_t phase = 0;
+    const int units = uend - ubegin;
+    const int slice = warp % (D / 32), part = warp / (D / 32);  // this warp's dimensions
+
+    auto wait_unit = [&](int st, uint32_t ph) {
+        if (waits && !mbar_wait(smem_u32(&sh.full[st]), ph)) {
+            waits = false;  // reported; no further waits
+            atomicExch(a.status, int(SV_ERR_TIMEOUT));
+        }
+    };
+    // The scores of this warp's tokens of a unit; whether they move a maximum.
+    auto score = [&](int st) -> bool {
+        const Unit &un = sh.unit[st];
+        const uint8_t *kc = sh.stage[st];
+        const uint32_t *km = reinterpret_cast<const uint32_t *>(kc + NT * D) + warp * TW + g, *vm = km + NT;
+        uint32_t kw[NG][2][E];
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t *p = kc + (warp * TW + i * 16 + h * 8 + g) * (D / 2) + t4 * (D / 8);
+                if constexpr (E == 2) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+                    kw[i][h][0] = v.x, kw[i][h][1] = v.y;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E / 4; ++e) {
+                        const uint4 v = reinterpret_cast<const uint4 *>(p)[e];
+                        kw[i][h][4 * e] = v.x, kw[i][h][4 * e + 1] = v.y, kw[i][h][4 * e + 2] = v.z, kw[i][h][4 * e + 3] = v.w;
+                    }
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[i][n][k] = 0.f;
+        // few independent sums: the odd k-steps have their own, so that products do not wait for one another
+        constexpr bool kTwo = NG * NR <= 2;
+        float s2[kTwo ? NG : 1][kTwo ? NR : 1][4] = {};
+#pragma unroll
+        for (int w = 0; w < E; ++w) {  // a word of codes: two k-steps
+            uint32_t af[2][NG][4];
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t x = kw[i][h][w], y = x >> 8;
+                    af[0][i][h] = codes_even(x), af[0][i][2 + h] = codes_odd(x);
+                    af[1][i][h] = codes_even(y), af[1][i][2 + h] = codes_odd(y);
+                }
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                uint32_t b[4];
+                if constexpr (kQRegs) {
+                    b[0] = qf[2 * w][n][0], b[1] = qf[2 * w][n][1], b[2] = qf[2 * w + 1][n][0], b[3] = qf[2 * w + 1][n][1];
+                } else {
+                    ldmatrix4(b, smem_u32(&sh.q[(n * 8 + (lane & 7)) * Sh::kQStride + w * 32 + (lane >> 3) * 8]));
+                }
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    mma16816(s[i][n], af[0][i], b[0], b[1]);
+                    if constexpr (kTwo) mma16816(s2[i][n], af[1][i], b[2], b[3]);
+                    else mma16816(s[i][n], af[1][i], b[2], b[3]);
+                }
+            }
+        }
+        if constexpr (kTwo) {
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) s[i][n][k] += s2[i][n][k];
+        }
+        // y = s_j (q . (code_j - 8)) + (z_j + 8 s_j) sum(q)
+        float ks[NG][2], kz[NG][2], top = 0.f;
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t kk = km[i * 16 + h * 8], vv = vm[i * 16 + h * 8];
+                const float2 kf = __half22float2(*reinterpret_cast<const __half2 *>(&kk)), vf = __half22float2(*reinterpret_cast<const __half2 *>(&vv));
+                ks[i][h] = kf.x, kz[i][h] = fmaf(8.f, kf.x, kf.y);
+                vs[i][h] = vf.x, vz[i][h] = fmaf(8.f, vf.x, vf.y);
+            }
+        uint32_t see = 0xFFFFFFFFu;
+        if (un.masked) {
+            const int tok0 = un.tile * NT;  // (fits: a table spans less than 2^31 tokens)
+            auto loaded = [&](int col) { return tok0 + col < un.len && (un.have >> (4 * (col / a.granule)) & 1u); };
+            // bit (i NR + n) 4 + k: that score's token is seen by its row
+            see = 0;
+#pragma unroll 1
+            for (int e = 0; e < NG * NR * 4; ++e) {
+                const int k = e & 3, n = (e >> 2) % NR, i = (e >> 2) / NR;
+                const int r = n * 8 + 2 * t4 + (k & 1), node = sh.row_node[r];
+                const int col = warp * TW + i * 16 + (k >> 1) * 8 + g;
+                const int idx = tok0 + col - un.before;  // below 0: before the new tokens
+                bool v = node >= 0 && loaded(col);
+                if (v && idx >= 0 && SV_IN(idx, a.T)) v = a.parent ? anc_s[r * anc_words + (idx >> 5)] >> (idx & 31) & 1u : idx <= node;
+                see |= uint32_t(v) << e;
+            }
+            // A masked token's weight is 0, and its scale and zero must not matter, whatever they are.  A
+            // NaN value reaches the rows that see it by their score instead.
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bool here = loaded(warp * TW + i * 16 + h * 8 + g);
+                    if (!here || !(fabsf(vs[i][h]) < INFINITY && fabsf(vz[i][h]) < INFINITY)) {
+                        vs[i][h] = vz[i][h] = 0.f;
+                        ks[i][h] = NAN;
+                    }
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < NG; ++i) top = fmaxf(top, fmaxf(vs[i][0], vs[i][1]));
+        bool need = !(top < power2(vexp));
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const float4 ry = *reinterpret_cast<const float4 *>(sh.row_y[n * 4 + t4]);
+            float y0 = -INFINITY, y1 = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                float *y = s[i][n];
+                y[0] = fmaf(y[0], ks[i][0], ry.x * kz[i][0]), y[1] = fmaf(y[1], ks[i][0], ry.y * kz[i][0]);
+                y[2] = fmaf(y[2], ks[i][1], ry.x * kz[i][1]), y[3] = fmaf(y[3], ks[i][1], ry.y * kz[i][1]);
+            }
+            if (un.masked) {
+#pragma unroll
+                for (int i = 0; i < NG; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (!(see >> ((i * NR + n) * 4 + k) & 1u)) s[i][n][k] = -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < NG; ++i) y0 = fmaxf(y0, fmaxf(s[i][n][0], s[i][n][2])), y1 = fmaxf(y1, fmaxf(s[i][n][1], s[i][n][3]));
+            need |= y0 > ry.z || y1 > ry.w;
+        }
+        return need;
+    };
+    // Some row's maximum moves (the first unit's always does), or the values' exponent.
+    auto update = [&]() {
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) top = fmaxf(top, fmaxf(vs[i][0], vs[i][1]));
+        const uint32_t wtop = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
+        if (lane == 0) sh.redv[warp] = wtop;
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float y = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < NG; ++i) y = fmaxf(y, fmaxf(s[i][n][k], s[i][n][2 + k]));
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, o));
+                if (g == 0) sh.red[0][warp][n * 8 + 2 * t4 + k] = y;
+            }
+        consumers_sync<C>();
+        for (int r = tid; r < R; r += C) {
+            float y = sh.red[0][0][r];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) y = fmaxf(y, sh.red[0][w][r]);
+            const float c = sh.row_p[r / 2][r & 1];
+            const float seen = sh.row_y[r / 2][2 + (r & 1)] == -INFINITY ? -INFINITY : sh.row_p[r / 2][2 + (r & 1)], mn = fmaxf(seen, y * c);
+            sh.alpha[r] = seen == -INFINITY ? 0.f : ex2(seen - mn);
+            if (mn != -INFINITY) sh.row_p[r / 2][2 + (r & 1)] = mn, sh.row_y[r / 2][2 + (r & 1)] = (mn + kLazy) / c;
+        }
+        uint32_t all = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) all = max(all, sh.redv[w]);
+        const int vnew = max(vexp, int(all >> 23) - 126);
+        const float kfac = power2(vexp - vnew);
+        vexp = vnew;
+        consumers_sync<C>();
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const float2 al = *reinterpret_cast<const float2 *>(&sh.alpha[n * 8 + 2 * t4]);
+            l[n][0] *= al.x, z[n][0] *= al.x, l[n][1] *= al.y, z[n][1] *= al.y;
+#pragma unroll
+            for (int h = 0; h < MH; ++h) {
+                acc[h][n][0] *= al.x * kfac, acc[h][n][1] *= al.y * kfac;
+                acc[h][n][2] *= al.x * kfac, acc[h][n][3] *= al.y * kfac;
+            }
+        }
+    };
+    // Weights: p for the sums (this warp's tokens), p s' for the product, rounded to fp16.
+    auto weigh = [&](int buf) {
+        const float down = power2(-vexp);
+        float vd[NG][2];
+#pragma unroll
+        for (int i = 0; i < NG; ++i) vd[i][0] = vs[i][0] * down, vd[i][1] = vs[i][1] * down;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const float4 rp = *reinterpret_cast<const float4 *>(sh.row_p[n * 4 + t4]);
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                const float p0 = ex2(fmaf(s[i][n][0], rp.x, -rp.z)), p1 = ex2(fmaf(s[i][n][1], rp.y, -rp.w));
+                const float p2 = ex2(fmaf(s[i][n][2], rp.x, -rp.z)), p3 = ex2(fmaf(s[i][n][3], rp.y, -rp.w));
+                l[n][0] += p0 + p2, l[n][1] += p1 + p3;
+                z[n][0] = fmaf(p0, vz[i][0], fmaf(p2, vz[i][1], z[n][0]));
+                z[n][1] = fmaf(p1, vz[i][0], fmaf(p3, vz[i][1], z[n][1]));
+                __half *dst = &sh.p[buf][(warp * TW + i * 16 + g) * Sh::kPStride + n * 8 + 2 * t4];
+                *reinterpret_cast<__half2 *>(dst) = __floats2half2_rn(p0 * vd[i][0], p1 * vd[i][0]);
+                *reinterpret_cast<__half2 *>(dst + 8 * Sh::kPStride) = __floats2half2_rn(p2 * vd[i][1], p3 * vd[i][1]);
+            }
+        }
+    };
+    // This warp's dimensions of a unit's product.
+    auto product = [&](int st, int buf) {
+        const uint8_t *vc = sh.stage[st] + NT * (D / 2) + slice * 256 + lane * 8;
+#pragma unroll
+        for (int kk = 0; kk < NT / 16; ++kk) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(vc + kk * 8 * D);
+            uint32_t af[MH][4];
+#pragma unroll
+            for (int h = 0; h < MH; ++h) {
+                const int shift = MH == 2 ? 8 * h : 8 * part;
+                const uint32_t x = w.x >> shift, y = w.y >> shift;
+                af[h][0] = codes_even(x), af[h][1] = codes_odd(x), af[h][2] = codes_even(y), af[h][3] = codes_odd(y);
+            }
+            const uint32_t row = smem_u32(&sh.p[buf][(kk * 16 + (lane & 15)) * Sh::kPStride]);
+#pragma unroll
+            for (int n = 0; n < NR; n += 2) {
+                if (n + 1 < NR) {
+                    uint32_t b[4];
+                    ldmatrix4_trans(b, row + (n * 8 + (lane >> 4) * 8) * 2);
+#pragma unroll
+                    for (int h = 0; h < MH; ++h) mma16816(acc[h][n], af[h], b[0], b[1]), mma16816(acc[h][n + 1], af[h], b[2], b[3]);
+                } else {
+                    uint32_t b0, b1;
+                    ldmatrix2_trans(b0, b1, row + n * 16);
+#pragma unroll
+                    for (int h = 0; h < MH; ++h) mma16816(acc[h][n], af[h], b0, b1);
+                }
+            }
+        }
+    };
+
+    for (int it = 0; it < units;) {  // segments
+        wait_unit(stage, phase);
+        const Unit seg = sh.unit[stage];
+        const int last = min(units, it + seg.tiles - seg.tile);  // past the segment's last unit here
+        consumers_sync<C>();
+        load_queries<D, NR>(a, sh, seg, tid);
+        if (a.parent)
+            for (int r = tid; r < R; r += C) {
+                uint32_t *anc = anc_s + r * anc_words;
+                for (int i = 0; i < anc_words; ++i) anc[i] = 0;
+                const int node = (seg.rt * R + r) / a.G;
+                for (int v = node < seg.fresh ? node : -1; v >= 0;) {
+                    anc[v >> 5] |= 1u << (v & 31);
+                    const int up = parent_s[v];
+                    v = up < v ? up : -1;
+                }
+            }
+        consumers_sync<C>();
+        if constexpr (kQRegs) {
+#pragma unroll
+            for (int w = 0; w < E; ++w)
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    uint32_t b[4];
+                    ldmatrix4(b, smem_u32(&sh.q[(n * 8 + (lane & 7)) * Sh::kQStride + w * 32 + (lane >> 3) * 8]));
+                    qf[2 * w][n][0] = b[0], qf[2 * w][n][1] = b[1], qf[2 * w + 1][n][0] = b[2], qf[2 * w + 1][n][1] = b[3];
+                }
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            l[n][0] = l[n][1] = z[n][0] = z[n][1] = 0.f;
+#pragma unroll
+            for (int h = 0; h < MH; ++h)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[h][n][k] = 0.f;
+        }
+        vexp = -24;
+        const int seg_lo = ubegin + it - seg.tile;
+        const bool whole = it >= seg.tile && it + seg.tiles - seg.tile <= units;
+
+        bool need = score(stage);
+        if (consumers_or<C>(need)) update();
+        weigh(0);
+        for (int buf = 0; it < last; ++it, buf ^= 1) {
+            const int here = stage;
+            if (++stage == kStages) stage = 0, phase ^= 1;
+            const bool more = it + 1 < last;
+            need = false;
+            if (more) {
+                wait_unit(stage, phase);
+                need = score(stage);
+            }
+            need = consumers_or<C>(need);  // and this unit's weights are in place
+            product(here, buf);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.empty[here]));
+            if (more) {
+                if (need) update();
+                weigh(buf ^ 1);
+            }
+        }
+
+        // the rows' sums over lanes and warps
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float x = l[n][k], y = z[n][k];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o), y += __shfl_xor_sync(0xFFFFFFFFu, y, o);
+                if (g == 0) sh.red[0][warp][n * 8 + 2 * t4 + k] = x, sh.red[1][warp][n * 8 + 2 * t4 + k] = y;
+            }
+        consumers_sync<C>();
+        const int64_t slot = 2 * cta + (seg_lo > ubegin ? 1 : 0);
+        const float up = power2(vexp), up16 = up * 0.0625f;
+        const int d0 = slice * 32 + 4 * g + 2 * part;
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int r = n * 8 + 2 * t4 + k;
+                float sl = 0.f, sz = 0.f;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) sl += sh.red[0][w][r], sz += sh.red[1][w][r];
+                float o[2 * MH];
+#pragma unroll
+                for (int h = 0; h < MH; ++h) o[2 * h] = fmaf(acc[h][n][k], up, sz), o[2 * h + 1] = fmaf(acc[h][n][2 + k], up16, sz);
+                if (whole) {
+                    const int row = seg.rt * R + r, node = row / a.G;
+                    if (node < a.T) {
+                        const float inv = sh.row_node[r] < 0 || sl == 0.f ? 0.f : 1.f / sl;
+                        const int64_t head = seg.h * a.G + row % a.G;
+                        uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + ((seg.b * int64_t(a.T) + node) * a.H * a.G + head) * D + d0);
+#pragma unroll
+                        for (int h = 0; h < MH; ++h) {
+                            const float x = inv == 0.f ? 0.f : o[2 * h] * inv, y = inv == 0.f ? 0.f : o[2 * h + 1] * inv;
+                            dst[h] = uint32_t(kv_from_float(x, a.bf16)) | uint32_t(kv_from_float(y, a.bf16)) << 16;
+                        }
+                    }
+                } else if (SV_IN(slot, 2 * ncta)) {
+                    float2 *dst = reinterpret_cast<float2 *>(a.acc + (slot * R + r) * D + d0);
+#pragma unroll
+                    for (int h = 0; h < MH; ++h) dst[h] = make_float2(o[2 * h], o[2 * h + 1]);
+                    if (warp == 0 && g == 0)
+                        a.ml[slot * R + r] = make_float2(sh.row_y[r / 2][2 + k] == -INFINITY ? -INFINITY : sh.row_p[r / 2][2 + k], sl);
+                }
+            }
+        if (tid == 0 && seg_lo <= ubegin)  // the share's first segment
+            a.desc[cta] = AttDesc{seg_lo, seg_lo + seg.tiles, total, seg.b, seg.h, seg.rt, seg.fresh};
+    }
+}
+
+// Joins a segment that several CTAs share: out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c.
+// Block (c, y) acts if CTA c's share begins inside a segment whose previous owner held its start;
+// y takes four of the segment's rows.
+constexpr int kJoinThreads = 128, kJoinRows = 4;
+
+template <int D, int NR>
+__global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const AttArgs a, int ncta) {
+    constexpr int R = 8 * NR;
+    __shared__ float weight[kJoinRows][kAttSMs * 8 + 8];
+    __shared__ float inv_s[kJoinRows];
+    griddep_launch_next();
+    griddep_wait();
+    const int c = int(blockIdx.x) / (R / kJoinRows) + 1;
+    const int r0 = int(blockIdx.x % (R / kJoinRows)) * kJoinRows;
+    if (c >= ncta) return;
+    // (CTA 0's share is empty only if all are; a CTA with an empty share wrote no descriptor)
+    const int total = a.desc[ncta - 1].total;  // the last share is never empty
+    const int begin = share_begin(total, c, ncta);
+    if (begin >= share_begin(total, c + 1, ncta)) return;
+    const AttDesc d = a.desc[c];
+    if (begin <= d.lo) return;
+    const int c0 = share_owner(total, d.lo, ncta), c1 = share_owner(total, d.hi - 1, ncta);
+    // the first non-empty share after the start's owner joins the segment
+    if (share_owner(total, begin - 1, ncta) != c0) return;
+    if (d.fresh <= 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // c0's part lies in its second slot unless its share begins with the segment
+    auto slot_of = [&](int k) { return int64_t(2) * k + (k == c0 && share_begin(total, c0, ncta) != d.lo ? 1 : 0); };
+    for (int q = warp; q < kJoinRows; q += kJoinThreads / 32) {
+        const int r = r0 + q;
+        float big = -INFINITY;
+        for (int k = c0 + lane; k <= c1; k += 32)
+            if (share_begin(total, k, ncta) < share_begin(total, k + 1, ncta)) big = fmaxf(big, a.ml[slot_of(k) * R + r].x);
+        for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
+        float sum = 0.f;
+        for (int k = c0 + lane; k <= c1; k += 32) {
+            float w = 0.f;
+            if (share_begin(total, k, ncta) < share_begin(total, k + 1, ncta)) {
+                const float2 ml = a.ml[slot_of(k) * R + r];
+                w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - big);
+                sum += w * ml.y;
+            }
+            if (SV_IN(k - c0, kAttSMs * 8 + 8)) weight[q][k - c0] = w;
+        }
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (lane == 0) inv_s[q] = sum == 0.f ? 0.f : 1.f / sum;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kJoinRows * D / 4; i += kJoinThreads) {
+        const int q = i / (D / 4), d4 = i % (D / 4) * 4, r = r0 + q;
+        const int row = d.rt * R + r, node = row / a.G;
+        if (node >= a.T) continue;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (node < d.fresh) {
+#pragma unroll 4
+            for (int k = c0; k <= c1; ++k) {
+                const float w = weight[q][k - c0];
+                if (w == 0.f) continue;  // also: parts of empty shares, never written
+                const float4 v = *reinterpret_cast<const float4 *>(a.acc + (slot_of(k) * R + r) * D + d4);
+                o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+            }
+            const float inv = inv_s[q];
+            o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+        }
+        const int64_t head = d.h * a.G + row % a.G;
+        uint2 w;
+        w.x = uint32_t(kv_from_float(o.x, a.bf16)) | uint32_t(kv_from_float(o.y, a.bf16)) << 16;
+        w.y = uint32_t(kv_from_float(o.z, a.bf16)) | uint32_t(kv_from_float(o.w, a.bf16)) << 16;
+        *reinterpret_cast<uint2 *>(a.out + ((d.b * int64_t(a.T) + node) * a.H * a.G + head) * D + d4) = w;
+    }
+}
+
+template <int D, int NR>
+cudaError_t launch_attention(const AttArgs &a, int grid, cudaStream_t s) {
+    const size_t smem = sizeof(AttShared<D, NR>) + (a.parent ? size_t(a.T) * 4 + size_t(8 * NR) * ((a.T + 31) / 32) * 4 : 0);
+    cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    e = launch_after(kv_attention_kernel<D, NR>, unsigned(grid), unsigned(att_threads(D, NR)), smem, s, a);
+    if (e != cudaSuccess) return e;
+    return launch_after(kv_attention_join_kernel<D, NR>, unsigned((grid - 1) * (8 * NR / kJoinRows)), unsigned(kJoinThreads), 0, s, a, grid);
+}
+
+// The attention kernels of a head dimension, each instantiated in its own translation unit.
+template <int D>
+cudaError_t launch_attention_rows(const AttArgs &a, int nr, int grid, cudaStream_t s);
+
+#define SV_KV_ATTENTION_INSTANTIATE(D)                                                                    \
+    template <>                                                                                          \
+    cudaError_t launch_attention_rows<D>(const AttArgs &a, int nr, int grid, cudaStream_t s) {             \
+        switch (nr) {                                                                                    \
+        case 1: return launch_attention<D, 1>(a, grid, s);                                               \
+        case 2: return launch_attention<D, 2>(a, grid, s);                                               \
+        case 3: return launch_attention<D, 3>(a, grid, s);                                               \
+        case 4: return launch_attention<D, 4>(a, grid, s);                                               \
+        case 5: return launch_attention<D, 5>(a, grid, s);                                               \
+        case 6: return launch_attention<D, 6>(a, grid, s);                                               \
+        default: return launch_attention<D, 8>(a, grid, s);                                              \
+        }                                                                                                \
+    }
+
+}  // namespace sv
