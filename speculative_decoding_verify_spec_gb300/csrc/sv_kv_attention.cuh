@@ -228,6 +228,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same with sums that start from nothing.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 // The codes in half-bytes 0 and 4 of w, less 8, as fp16 (1024 + code has its code in the low bits), and
 // 16 times those in half-bytes 1 and 5: all exact.  (The factor is in the queries, or taken out of the
 // output.)  Centred, so that sums over thousands of tokens do not cancel against the zeros' part.
@@ -263,7 +269,7 @@ struct AttShared {
     alignas(16) float alpha[R];
     float red[2][NW][R];
     uint32_t redv[NW];
-    int row_node[R];  // the row's new token, -1: no live row
+    alignas(8) int row_node[R];  // the row's new token, -1: no live row
     alignas(8) uint64_t full[kStages], empty[kStages];
     Unit unit[kStages];
 };
@@ -409,36 +415,40 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
 
     // all units, then the sequence where this CTA's share begins (every warp for itself)
     int total = 0;
-    for (int b = lane; b < a.B; b += 32) total += seq_work<NT>(a, b, R).units;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+    SeqWork w0{};  // of sequence `lane`
+    for (int b = lane; b < a.B; b += 32) {
+        const SeqWork w = seq_work<NT>(a, b, R);
+        if (b == lane) w0 = w;
+        total += w.units;
+    }
+    total = __reduce_add_sync(0xFFFFFFFFu, total);
     const int ubegin = share_begin(total, cta, ncta), uend = share_begin(total, cta + 1, ncta);
     if (ubegin >= uend) return;
     Cursor<NT> cur;
-    {
-        int run = 0;
-        for (int b0 = 0;; b0 += 32) {  // (ubegin < total: some sequence holds it)
-            const int b = b0 + lane;
-            const int u = b < a.B ? seq_work<NT>(a, b, R).units : 0;
-            int inc = u;
+    for (int b0 = 0, run = 0;; b0 += 32) {  // (ubegin < total: some sequence holds it)
+        const int b = b0 + lane;
+        if (b0 > 0) w0 = b < a.B ? seq_work<NT>(a, b, R) : SeqWork{};
+        int inc = w0.units;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-                if (lane >= o) inc += v;
-            }
-            const int lo = run + inc - u;
-            const uint32_t hit = __ballot_sync(0xFFFFFFFFu, ubegin >= lo && ubegin < lo + u);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                cur.b = b0 + l;
-                cur.base = __shfl_sync(0xFFFFFFFFu, lo, l);
-                break;
-            }
-            run += __shfl_sync(0xFFFFFFFFu, inc, 31);
-            if (b0 + 32 >= a.B) return;  // never
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += v;
         }
+        const int lo = run + inc - w0.units;
+        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, ubegin >= lo && ubegin < run + inc);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            cur.b = b0 + l;
+            cur.base = __shfl_sync(0xFFFFFFFFu, lo, l);
+            int *to = reinterpret_cast<int *>(&cur.w);
+            const int *from = reinterpret_cast<const int *>(&w0);
+#pragma unroll
+            for (int i = 0; i < int(sizeof(SeqWork) / 4); ++i) to[i] = __shfl_sync(0xFFFFFFFFu, from[i], l);
+            break;
+        }
+        run += __shfl_sync(0xFFFFFFFFu, inc, 31);
+        if (b0 + 32 >= a.B) return;  // never
     }
-    cur.w = seq_work<NT>(a, cur.b, R);
     cur.place(a, ubegin);
     __syncthreads();
 
@@ -526,15 +536,9 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
                     }
                 }
             }
-#pragma unroll
-        for (int i = 0; i < NG; ++i)
-#pragma unroll
-            for (int n = 0; n < NR; ++n)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) s[i][n][k] = 0.f;
         // few independent sums: the odd k-steps have their own, so that products do not wait for one another
         constexpr bool kTwo = NG * NR <= 2;
-        float s2[kTwo ? NG : 1][kTwo ? NR : 1][4] = {};
+        float s2[kTwo ? NG : 1][kTwo ? NR : 1][4];
 #pragma unroll
         for (int w = 0; w < E; ++w) {  // a word of codes: two k-steps
             uint32_t af[2][NG][4];
@@ -556,9 +560,11 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
                 }
 #pragma unroll
                 for (int i = 0; i < NG; ++i) {
-                    mma16816(s[i][n], af[0][i], b[0], b[1]);
-                    if constexpr (kTwo) mma16816(s2[i][n], af[1][i], b[2], b[3]);
-                    else mma16816(s[i][n], af[1][i], b[2], b[3]);
+                    if (w == 0) mma16816_first(s[i][n], af[0][i], b[0], b[1]);
+                    else mma16816(s[i][n], af[0][i], b[0], b[1]);
+                    if constexpr (!kTwo) mma16816(s[i][n], af[1][i], b[2], b[3]);
+                    else if (w == 0) mma16816_first(s2[i][n], af[1][i], b[2], b[3]);
+                    else mma16816(s2[i][n], af[1][i], b[2], b[3]);
                 }
             }
         }
@@ -587,15 +593,27 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
             auto loaded = [&](int col) { return tok0 + col < un.len && (un.have >> (4 * (col / a.granule)) & 1u); };
             // bit (i NR + n) 4 + k: that score's token is seen by its row
             see = 0;
+            int idx[NG][2];  // of the tokens among the new ones; -1: before them, T: not there
+#pragma unroll
+            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int col = warp * TW + i * 16 + h * 8 + g;
+                    idx[i][h] = loaded(col) ? max(-1, tok0 + col - un.before) : a.T;
+                }
 #pragma unroll 1
-            for (int e = 0; e < NG * NR * 4; ++e) {
-                const int k = e & 3, n = (e >> 2) % NR, i = (e >> 2) / NR;
-                const int r = n * 8 + 2 * t4 + (k & 1), node = sh.row_node[r];
-                const int col = warp * TW + i * 16 + (k >> 1) * 8 + g;
-                const int idx = tok0 + col - un.before;  // below 0: before the new tokens
-                bool v = node >= 0 && loaded(col);
-                if (v && idx >= 0 && SV_IN(idx, a.T)) v = a.parent ? anc_s[r * anc_words + (idx >> 5)] >> (idx & 31) & 1u : idx <= node;
-                see |= uint32_t(v) << e;
+            for (int n = 0; n < NR; ++n) {
+                const int2 node = *reinterpret_cast<const int2 *>(&sh.row_node[n * 8 + 2 * t4]);
+                const uint32_t *anc = anc_s + (n * 8 + 2 * t4) * anc_words;
+#pragma unroll
+                for (int i = 0; i < NG; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int x = idx[i][k >> 1], own = k & 1 ? node.y : node.x;
+                        bool v = own >= 0 && x <= own;  // a row's ancestors come before it
+                        if (a.parent && v && x >= 0 && SV_IN(x, a.T)) v = anc[(k & 1) * anc_words + (x >> 5)] >> (x & 31) & 1u;
+                        see |= uint32_t(v) << ((i * NR + n) * 4 + k);
+                    }
             }
             // A masked token's weight is 0, and its scale and zero must not matter, whatever they are.  A
             // NaN value reaches the rows that see it by their score instead.
@@ -615,24 +633,31 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
         bool need = !(top < power2(vexp));
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            const float4 ry = *reinterpret_cast<const float4 *>(sh.row_y[n * 4 + t4]);
-            float y0 = -INFINITY, y1 = -INFINITY;
+            const float2 ry = *reinterpret_cast<const float2 *>(sh.row_y[n * 4 + t4]);
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
                 float *y = s[i][n];
                 y[0] = fmaf(y[0], ks[i][0], ry.x * kz[i][0]), y[1] = fmaf(y[1], ks[i][0], ry.y * kz[i][0]);
                 y[2] = fmaf(y[2], ks[i][1], ry.x * kz[i][1]), y[3] = fmaf(y[3], ks[i][1], ry.y * kz[i][1]);
             }
-            if (un.masked) {
+        }
+        if (un.masked) {
+            __syncwarp();  // (a branch, not a select on every unit's scores)
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
 #pragma unroll
                 for (int i = 0; i < NG; ++i)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if (!(see >> ((i * NR + n) * 4 + k) & 1u)) s[i][n][k] = -INFINITY;
-            }
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const float2 ry = *reinterpret_cast<const float2 *>(&sh.row_y[n * 4 + t4][2]);
+            float y0 = -INFINITY, y1 = -INFINITY;
 #pragma unroll
             for (int i = 0; i < NG; ++i) y0 = fmaxf(y0, fmaxf(s[i][n][0], s[i][n][2])), y1 = fmaxf(y1, fmaxf(s[i][n][1], s[i][n][3]));
-            need |= y0 > ry.z || y1 > ry.w;
+            need |= y0 > ry.x || y1 > ry.y;
         }
         return need;
     };
@@ -735,9 +760,9 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
         }
     };
 
-    for (int it = 0; it < units;) {  // segments
-        wait_unit(stage, phase);
-        const Unit seg = sh.unit[stage];
+    // the first segment is known already, and its queries load while its first unit is on its way
+    Unit seg{cur.b, cur.h, cur.rt, cur.tile, cur.tiles(), cur.w.before, cur.w.len, cur.live ? cur.w.fresh : 0, 0, 0};
+    for (int it = 0;;) {  // segments
         const int last = min(units, it + seg.tiles - seg.tile);  // past the segment's last unit here
         consumers_sync<C>();
         load_queries<D, NR>(a, sh, seg, tid);
@@ -775,6 +800,7 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
         const int seg_lo = ubegin + it - seg.tile;
         const bool whole = it >= seg.tile && it + seg.tiles - seg.tile <= units;
 
+        if (it == 0) wait_unit(stage, phase);
         bool need = score(stage);
         if (consumers_or<C>(need)) update();
         weigh(0);
@@ -844,6 +870,9 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
             }
         if (tid == 0 && seg_lo <= ubegin)  // the share's first segment
             a.desc[cta] = AttDesc{seg_lo, seg_lo + seg.tiles, total, seg.b, seg.h, seg.rt, seg.fresh};
+        if (it == units) break;
+        wait_unit(stage, phase);
+        seg = sh.unit[stage];
     }
 }
 
