@@ -81,7 +81,7 @@ __host__ __device__ constexpr int att_tokens(int D, int NR) {
 __host__ __device__ constexpr int att_stages(int D, int NR) { return D == 256 ? 4 : STG; }
 // CTAs per SM, by registers and shared memory.
 __host__ __device__ constexpr int att_occupancy(int D, int NR) {
-    return D == 256 ? 1 : D == 128 ? (NR <= 2 ? OC1 : NR <= 5 ? OC3 : OC8) : (NR <= 4 ? OCS : OCS - 1);
+    return D == 256 ? 1 : D == 128 ? (NR == 1 ? OC1 : NR <= 5 ? OC3 : OC8) : (NR <= 2 ? OCS : OCS - 1);
 }
 // Tiles of 8 NR rows: as few as there have to be and no larger than they need be.
 inline int att_nr(int64_t rows, int D) {
@@ -263,7 +263,7 @@ struct AttShared {
     alignas(16) __half q[R * kQStride];
     alignas(16) __half p[2][NT * kPStride];       // [token][row]
     // per pair of rows: their queries' sums and the scores that move the maximum (-inf until a score was
-    // seen); log2 scales of their scores and the maxima in log2 (0 until then)
+    // seen); log2 scales of their scores and the negated maxima in log2 (0 until then)
     alignas(16) float row_y[R / 2][4];
     alignas(16) float row_p[R / 2][4];
     alignas(16) float alpha[R];
@@ -274,6 +274,33 @@ struct AttShared {
     Unit unit[kStages];
 };
 
+// Two fp32 numbers in a register pair, worked on by one instruction.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float x, float y) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 split(Two a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+    return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ float power2(int e) { return __int_as_float((127 + e) << 23); }  // -126 <= e <= 127
 // Barriers of the D consumer threads.
 template <int N>
@@ -497,7 +524,7 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
 
     // MH 16-row tiles of dimensions x R rows: dimension 4 g + 2 h (+ 1, times 16) of the slice, rows 2 t4, 2 t4 + 1
     float acc[MH][NR][4];
-    float l[NR][2], z[NR][2];
+    Two l[NR], z[NR];     // of rows 2 t4, 2 t4 + 1
     float s[NG][NR][4];   // scores of tokens g, g + 8 of each group, rows 2 t4, 2 t4 + 1
     float vs[NG][2], vz[NG][2];
     uint32_t qf[kQRegs ? KS : 2][kQRegs ? NR : 1][2];
@@ -634,12 +661,15 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             const float2 ry = *reinterpret_cast<const float2 *>(sh.row_y[n * 4 + t4]);
+            const Two qs = two(ry.x, ry.y);
 #pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                float *y = s[i][n];
-                y[0] = fmaf(y[0], ks[i][0], ry.x * kz[i][0]), y[1] = fmaf(y[1], ks[i][0], ry.y * kz[i][0]);
-                y[2] = fmaf(y[2], ks[i][1], ry.x * kz[i][1]), y[3] = fmaf(y[3], ks[i][1], ry.y * kz[i][1]);
-            }
+            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float *y = s[i][n] + 2 * h;
+                    const float2 r = split(fma2(two(y[0], y[1]), two(ks[i][h], ks[i][h]), mul2(qs, two(kz[i][h], kz[i][h]))));
+                    y[0] = r.x, y[1] = r.y;
+                }
         }
         if (un.masked) {
             __syncwarp();  // (a branch, not a select on every unit's scores)
@@ -685,9 +715,9 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
 #pragma unroll
             for (int w = 1; w < NW; ++w) y = fmaxf(y, sh.red[0][w][r]);
             const float c = sh.row_p[r / 2][r & 1];
-            const float seen = sh.row_y[r / 2][2 + (r & 1)] == -INFINITY ? -INFINITY : sh.row_p[r / 2][2 + (r & 1)], mn = fmaxf(seen, y * c);
+            const float seen = sh.row_y[r / 2][2 + (r & 1)] == -INFINITY ? -INFINITY : -sh.row_p[r / 2][2 + (r & 1)], mn = fmaxf(seen, y * c);
             sh.alpha[r] = seen == -INFINITY ? 0.f : ex2(seen - mn);
-            if (mn != -INFINITY) sh.row_p[r / 2][2 + (r & 1)] = mn, sh.row_y[r / 2][2 + (r & 1)] = (mn + kLazy) / c;
+            if (mn != -INFINITY) sh.row_p[r / 2][2 + (r & 1)] = -mn, sh.row_y[r / 2][2 + (r & 1)] = (mn + kLazy) / c;
         }
         uint32_t all = 0;
 #pragma unroll
@@ -699,7 +729,7 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             const float2 al = *reinterpret_cast<const float2 *>(&sh.alpha[n * 8 + 2 * t4]);
-            l[n][0] *= al.x, z[n][0] *= al.x, l[n][1] *= al.y, z[n][1] *= al.y;
+            l[n] = mul2(l[n], two(al.x, al.y)), z[n] = mul2(z[n], two(al.x, al.y));
 #pragma unroll
             for (int h = 0; h < MH; ++h) {
                 acc[h][n][0] *= al.x * kfac, acc[h][n][1] *= al.y * kfac;
@@ -716,17 +746,19 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             const float4 rp = *reinterpret_cast<const float4 *>(sh.row_p[n * 4 + t4]);
+            const Two c = two(rp.x, rp.y), minus = two(rp.z, rp.w);
 #pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                const float p0 = ex2(fmaf(s[i][n][0], rp.x, -rp.z)), p1 = ex2(fmaf(s[i][n][1], rp.y, -rp.w));
-                const float p2 = ex2(fmaf(s[i][n][2], rp.x, -rp.z)), p3 = ex2(fmaf(s[i][n][3], rp.y, -rp.w));
-                l[n][0] += p0 + p2, l[n][1] += p1 + p3;
-                z[n][0] = fmaf(p0, vz[i][0], fmaf(p2, vz[i][1], z[n][0]));
-                z[n][1] = fmaf(p1, vz[i][0], fmaf(p3, vz[i][1], z[n][1]));
-                __half *dst = &sh.p[buf][(warp * TW + i * 16 + g) * Sh::kPStride + n * 8 + 2 * t4];
-                *reinterpret_cast<__half2 *>(dst) = __floats2half2_rn(p0 * vd[i][0], p1 * vd[i][0]);
-                *reinterpret_cast<__half2 *>(dst + 8 * Sh::kPStride) = __floats2half2_rn(p2 * vd[i][1], p3 * vd[i][1]);
-            }
+            for (int i = 0; i < NG; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float2 x = split(fma2(two(s[i][n][2 * h], s[i][n][2 * h + 1]), c, minus));
+                    const Two pw = two(ex2(x.x), ex2(x.y));
+                    l[n] = add2(l[n], pw);
+                    z[n] = fma2(pw, two(vz[i][h], vz[i][h]), z[n]);
+                    const float2 w = split(mul2(pw, two(vd[i][h], vd[i][h])));
+                    *reinterpret_cast<__half2 *>(&sh.p[buf][(warp * TW + i * 16 + h * 8 + g) * Sh::kPStride + n * 8 + 2 * t4]) =
+                        __floats2half2_rn(w.x, w.y);
+                }
         }
     };
     // This warp's dimensions of a unit's product.
@@ -790,7 +822,7 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
         }
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            l[n][0] = l[n][1] = z[n][0] = z[n][1] = 0.f;
+            l[n] = z[n] = 0;  // (two zeros)
 #pragma unroll
             for (int h = 0; h < MH; ++h)
 #pragma unroll
@@ -828,7 +860,7 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
         for (int n = 0; n < NR; ++n)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                float x = l[n][k], y = z[n][k];
+                float x = k ? split(l[n]).y : split(l[n]).x, y = k ? split(z[n]).y : split(z[n]).x;
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o), y += __shfl_xor_sync(0xFFFFFFFFu, y, o);
                 if (g == 0) sh.red[0][warp][n * 8 + 2 * t4 + k] = x, sh.red[1][warp][n * 8 + 2 * t4 + k] = y;
@@ -865,7 +897,7 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
 #pragma unroll
                     for (int h = 0; h < MH; ++h) dst[h] = make_float2(o[2 * h], o[2 * h + 1]);
                     if (warp == 0 && g == 0)
-                        a.ml[slot * R + r] = make_float2(sh.row_y[r / 2][2 + k] == -INFINITY ? -INFINITY : sh.row_p[r / 2][2 + k], sl);
+                        a.ml[slot * R + r] = make_float2(sh.row_y[r / 2][2 + k] == -INFINITY ? -INFINITY : -sh.row_p[r / 2][2 + k], sl);
                 }
             }
         if (tid == 0 && seg_lo <= ubegin)  // the share's first segment
@@ -952,6 +984,9 @@ template <int D, int NR>
 cudaError_t launch_attention(const AttArgs &a, int grid, cudaStream_t s) {
     const size_t smem = sizeof(AttShared<D, NR>) + (a.parent ? size_t(a.T) * 4 + size_t(8 * NR) * ((a.T + 31) / 32) * 4 : 0);
     cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    // as much shared memory as there is, so that att_occupancy CTAs are resident
+    e = cudaFuncSetAttribute(kv_attention_kernel<D, NR>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
     e = launch_after(kv_attention_kernel<D, NR>, unsigned(grid), unsigned(att_threads(D, NR)), smem, s, a);
     if (e != cudaSuccess) return e;
