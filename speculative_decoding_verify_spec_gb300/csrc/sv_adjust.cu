@@ -137,9 +137,11 @@ __global__ void __launch_bounds__(kAdjThreads, 2) adjust_kernel(const AdjustArgs
     using E = Elem<T>;
     constexpr int per = E::per;
     constexpr uint32_t kAll = (1u << per) - 1;
-    constexpr int kChunks = (TV / per + kChunkVecs - 1) / kChunkVecs;
+    // a warp keeps its place in the range, and steps through the rows
+    constexpr int kChunks = (TV / per + kChunkVecs - 1) / kChunkVecs, kRowStep = kAdjWarps / kChunks;
+    static_assert(kChunks * kRowStep == kAdjWarps, "");
+    const int part = warp % kChunks, v0 = part * kChunkVecs, first_row = warp / kChunks;
     const int64_t words = (int64_t(a.V) + 31) / 32;
-    const int items = a.rows * kChunks;
 
     griddep_launch_next();
     for (int i = tid; i < TV; i += kAdjThreads) sh.count[i] = 0;
@@ -147,48 +149,36 @@ __global__ void __launch_bounds__(kAdjThreads, 2) adjust_kernel(const AdjustArgs
     for (int i = tid; i < TV / 32; i += kAdjThreads) sh.touched[i] = 0, sh.drafted[i] = 0;
     griddep_wait();
 
-    // chunk `part` of row r: its vectors [v0, v1) after `head` elements off the 16-byte grid
-    struct Chunk {
-        const T *src;
-        T *dst;
-        const uint32_t *mask;
-        int r, part, head, nv, v0, v1;
-        bool vec;  // the two rows lie alike on the grid
-    };
-    auto chunk_of = [&](int item) {
-        Chunk c;
-        c.r = item / kChunks, c.part = item % kChunks;
-        c.src = static_cast<const T *>(a.in) + b * a.in_bs + c.r * a.in_rs + t0;
-        c.dst = static_cast<T *>(a.out) + b * a.out_bs + c.r * a.out_rs + t0;
-        c.mask = a.allowed ? a.allowed + (b * a.rows + c.r) * words : nullptr;
-        const uintptr_t ai = reinterpret_cast<uintptr_t>(c.src), ao = reinterpret_cast<uintptr_t>(c.dst);
-        c.vec = ((ai ^ ao) & 15) == 0;
-        c.head = min(n, int((16 - (ai & 15)) & 15) / int(sizeof(T)));
-        c.nv = (n - c.head) / per;
-        c.v0 = c.part * kChunkVecs, c.v1 = min(c.nv, c.v0 + kChunkVecs);
-        return c;
-    };
-    auto fetch = [&](int item, int slot) {
-        if (item < items) {
-            const Chunk c = chunk_of(item);
-            if (c.vec && c.v0 < c.v1) {
-                const uint4 *src4 = reinterpret_cast<const uint4 *>(c.src + c.head);
+    // Elements before the 16-byte grid, and this warp's vectors after them, of a row that begins at p.
+    auto head_of = [&](const T *p) { return min(n, int((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / int(sizeof(T))); };
+    auto vectors_of = [&](int head) { return max(0, min((n - head) / per - v0, kChunkVecs)); };
+    const T *src = static_cast<const T *>(a.in) + b * a.in_bs + first_row * a.in_rs + t0;
+    T *dst = static_cast<T *>(a.out) + b * a.out_bs + first_row * a.out_rs + t0;
+    const uint32_t *mask = a.allowed ? a.allowed + (b * a.rows + first_row) * words : nullptr;
+    // the copies run kRing - 1 rows ahead
+    const T *src_ahead = src;
+    const uint32_t *mask_ahead = mask;
+    int row_ahead = first_row;
+    auto fetch = [&](int slot) {
+        if (row_ahead < a.rows) {
+            const int head = head_of(src_ahead), count = vectors_of(head);
+            const uint4 *from = reinterpret_cast<const uint4 *>(src_ahead + head) + v0 + lane;
+            uint4 *to = &sh.chunk[warp][slot][lane];
 #pragma unroll
-                for (int u = 0; u < kVecs; ++u) {
-                    const int v = c.v0 + u * 32 + lane;
-                    if (v < c.v1) copy_async16(&sh.chunk[warp][slot][u * 32 + lane], src4 + v);
-                }
-                if (c.mask) {  // at most 33 words
-                    const int e0 = t0 + c.head + c.v0 * per, w0 = e0 >> 5, w1 = (t0 + c.head + c.v1 * per - 1) >> 5;
-                    if (w0 + lane <= w1) copy_async4(&sh.mask[warp][slot][lane], c.mask + w0 + lane);
-                    if (lane == 0 && w0 + 32 <= w1) copy_async4(&sh.mask[warp][slot][32], c.mask + w0 + 32);
-                }
+            for (int u = 0; u < kVecs; ++u)
+                if (u * 32 + lane < count) copy_async16(to + u * 32, from + u * 32);
+            if (mask_ahead && count > 0) {  // at most 33 words
+                const int e0 = t0 + head + v0 * per, w0 = e0 >> 5, w1 = (e0 + count * per - 1) >> 5;
+                if (w0 + lane <= w1) copy_async4(&sh.mask[warp][slot][lane], mask_ahead + w0 + lane);
+                if (lane == 0 && w0 + 32 <= w1) copy_async4(&sh.mask[warp][slot][32], mask_ahead + w0 + 32);
             }
+            row_ahead += kRowStep, src_ahead += kRowStep * a.in_rs;
+            if (mask_ahead) mask_ahead += kRowStep * words;
         }
         copy_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kRing - 1; ++i) fetch(warp + i * kAdjWarps, i);
+    for (int i = 0; i < kRing - 1; ++i) fetch(i);
 
     // the tokens of this range that the history, the drafts and the bias list hold
     for (int i = tid; i < a.ndraft; i += kAdjThreads) draft_s[i] = a.drafts[b * a.ndraft + i];
@@ -281,62 +271,68 @@ __global__ void __launch_bounds__(kAdjThreads, 2) adjust_kernel(const AdjustArgs
     auto is_touched = [&](int k) { return sh.touched[k >> 5] >> (k & 31) & 1u; };
     auto listed_before = [&](int k) { return sh.before[k >> 5] + __popc(sh.touched[k >> 5] & ((1u << (k & 31)) - 1)); };
 
-    for (int item = warp, slot = 0; item < items; item += kAdjWarps, slot = (slot + 1) % kRing) {
-        fetch(item + (kRing - 1) * kAdjWarps, (slot + kRing - 1) % kRing);
-        const Chunk c = chunk_of(item);
+    int slot = 0, listed_head = -1, e0 = 0, e1 = 0;
+    for (int r = first_row; r < a.rows; r += kRowStep) {
+        fetch(slot == 0 ? kRing - 1 : slot - 1);
+        const int head = head_of(src), count = vectors_of(head);
         auto scalar = [&](int k) {
-            const bool ok = c.mask == nullptr || (__ldg(c.mask + ((t0 + k) >> 5)) >> ((t0 + k) & 31) & 1u), mine = is_touched(k);
+            const bool ok = mask == nullptr || (__ldg(mask + ((t0 + k) >> 5)) >> ((t0 + k) & 31) & 1u), mine = is_touched(k);
             if (a.in_place && ok && !mine) return;
-            const T v = c.src[k];
-            c.dst[k] = !ok ? E::round(-__int_as_float(0x7f800000)) : mine ? E::round(adjust(E::get(v), c.r, k)) : v;
+            const T v = src[k];
+            dst[k] = !ok ? E::round(-__int_as_float(0x7f800000)) : mine ? E::round(adjust(E::get(v), r, k)) : v;
         };
         copy_wait<kRing - 1>();
         __syncwarp();
-        if (!c.vec) {
-            const int k1 = min(n, (c.part + 1) * kChunkVecs * per);
-            for (int k = c.part * kChunkVecs * per + lane; k < k1; k += 32) scalar(k);
-            continue;
-        }
-        if (c.part == 0) {  // the row's ends off the grid
-            const int tail = c.head + c.nv * per;
-            if (lane < c.head) scalar(lane);
-            if (lane < n - tail) scalar(tail + lane);
-        }
-        if (c.v0 < c.v1) {
-            uint4 *mine = sh.chunk[warp][slot];
-            const int k0 = c.head + c.v0 * per, k1 = c.head + c.v1 * per;  // the chunk's tokens
-            const int e0 = listed_before(k0), e1 = listed_before(k1 - 1) + int(is_touched(k1 - 1));
-            if (e0 < e1) {
+        if (((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15) != 0) {
+            // the two rows lie differently on the 16-byte grid
+            const int k1 = min(n, (part + 1) * kChunkVecs * per);
+            for (int k = v0 * per + lane; k < k1; k += 32) scalar(k);
+        } else {
+            if (part == 0 && (head > 0 || (n - head) % per != 0)) {  // the row's ends off the grid
+                const int tail = head + (n - head) / per * per;
+                if (lane < head) scalar(lane);
+                if (lane < n - tail) scalar(tail + lane);
+            }
+            uint4 *mine = &sh.chunk[warp][slot][0];
+            const int k0 = head + v0 * per;  // the chunk's first token
+            if (head != listed_head && count > 0) {
+                const int k1 = k0 + count * per;
+                e0 = listed_before(k0), e1 = listed_before(k1 - 1) + int(is_touched(k1 - 1));
+                listed_head = head;
+            }
+            if (count > 0 && e0 < e1) {
                 T *elems = reinterpret_cast<T *>(mine);
                 for (int e = e0 + lane; e < e1; e += 32) {
                     const int k = sh.list[e];
-                    if (SV_IN(k - k0, k1 - k0)) elems[k - k0] = E::round(adjust(E::get(elems[k - k0]), c.r, k));
+                    if (SV_IN(k - k0, count * per)) elems[k - k0] = E::round(adjust(E::get(elems[k - k0]), r, k));
                 }
                 __syncwarp();
             }
-            uint4 *dst4 = reinterpret_cast<uint4 *>(c.dst + c.head);
-            const uint32_t first = uint32_t(t0 + k0) & 31;
+            uint4 *to = reinterpret_cast<uint4 *>(dst + head) + v0 + lane;
+            const uint32_t first = (uint32_t(t0 + k0) & 31) + lane * per;
 #pragma unroll
             for (int u = 0; u < kVecs; ++u) {
-                const int v = c.v0 + u * 32 + lane;
-                if (v >= c.v1) continue;
+                if (u * 32 + lane >= count) continue;
                 uint32_t ok = kAll;
-                if (c.mask) {
-                    const uint32_t e = first + (u * 32 + lane) * per;
+                if (mask) {
+                    const uint32_t e = first + u * 32 * per;
                     const uint32_t *m = &sh.mask[warp][slot][e >> 5];
                     ok = __funnelshift_r(m[0], m[1], e & 31) & kAll;  // (m[1] unread bits: any)
                 }
                 if (a.in_place && ok == kAll) {  // only what changes is written
-                    const int k = c.head + v * per;
+                    const int k = k0 + (u * 32 + lane) * per;
                     const uint32_t s = uint32_t(k) & 31, hi = s + per > 32 ? sh.touched[(k >> 5) + 1] : 0u;
                     if ((__funnelshift_r(sh.touched[k >> 5], hi, s) & kAll) == 0) continue;
                 }
                 uint4 x = mine[u * 32 + lane];
                 if (ok != kAll) E::mask(x, ok);
-                dst4[v] = x;
+                to[u * 32] = x;
             }
         }
         __syncwarp();  // the buffer may be filled again
+        src += kRowStep * a.in_rs, dst += kRowStep * a.out_rs;
+        if (mask) mask += kRowStep * words;
+        slot = slot + 1 == kRing ? 0 : slot + 1;
     }
     copy_wait<0>();
 }

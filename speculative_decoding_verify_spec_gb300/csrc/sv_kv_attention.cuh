@@ -39,16 +39,16 @@ constexpr uint64_t kCopyLimitNs = 1000000000ull;
 constexpr int kAttSMs = 152;
 
 #ifndef CAP64
-#define CAP64 64
+#define CAP64 32
 #endif
 #ifndef CAP128
-#define CAP128 64
+#define CAP128 48
 #endif
 #ifndef NT1
-#define NT1 64
+#define NT1 128
 #endif
 #ifndef OC1
-#define OC1 4
+#define OC1 3
 #endif
 #ifndef MH3
 #define MH3 2
@@ -75,10 +75,10 @@ constexpr int kAttSMs = 152;
 __host__ __device__ constexpr int att_mh(int D, int NR) { return D == 64 ? 1 : D == 128 && NR >= 3 ? MH3 : 2; }
 // Tokens per unit.
 __host__ __device__ constexpr int att_tokens(int D, int NR) {
-    return D == 256 ? 128 : D == 128 ? (NR <= 2 ? NT1 : NT3) : NTS;
+    return D == 256 ? 128 : D == 128 ? (NR == 1 ? NT1 : NT3) : NTS;
 }
 // Units in the ring: one whose product runs, one whose scores run, and those on their way.
-__host__ __device__ constexpr int att_stages(int D, int NR) { return D == 256 ? 4 : STG; }
+__host__ __device__ constexpr int att_stages(int D, int NR) { return D == 256 ? 4 : D == 128 && NR == 1 ? 3 : STG; }
 // CTAs per SM, by registers and shared memory.
 __host__ __device__ constexpr int att_occupancy(int D, int NR) {
     return D == 256 ? 1 : D == 128 ? (NR == 1 ? OC1 : NR <= 5 ? OC3 : OC8) : (NR <= 2 ? OCS : OCS - 1);
@@ -87,7 +87,7 @@ __host__ __device__ constexpr int att_occupancy(int D, int NR) {
 inline int att_nr(int64_t rows, int D) {
     const int64_t cap = D == 64 ? CAP64 : CAP128, tiles = (rows + cap - 1) / cap;
     const int nr = int(((rows + tiles - 1) / tiles + 7) / 8);
-    return nr == 7 ? 8 : nr;
+    return nr;
 }
 
 struct AttArgs {
@@ -172,12 +172,14 @@ struct Cursor {
 };
 
 // What the consumers know of a unit; written by the copying warp.
-struct Unit {
+struct alignas(16) Unit {
     int b, h, rt, tile, tiles;
     int before, len, fresh;   // tokens before the step; all; new ones (0: no live row)
     uint32_t have;            // bit 4 g: granule g was loaded
     int masked;               // not every token is seen by every row
+    int unused[2];
 };
+static_assert(sizeof(Unit) == 48, "");
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
 __device__ __forceinline__ void mbar_init(uint32_t bar, int count) {
@@ -480,44 +482,55 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
     __syncthreads();
 
     if (warp == NW) {
-        // the copies, up to kStages units ahead of the consumers
-        const int64_t page_bytes = kv_page_bytes(a.page, D);
-        const int gi = lane >> 2, piece = lane & 3;
-        const uint32_t all_granules = NT / a.granule == 8 ? 0x11111111u : 0x11111111u & ((1u << (4 * (NT / a.granule))) - 1);
+        // the copies, up to kStages units ahead of the consumers.  Lanes take (granule, piece) pairs: keys,
+        // values and their scales; a page that is a unit is one piece.
+        const bool whole = a.page == NT;
+        const int gi = lane >> 2, piece = lane & 3, granules = NT / a.granule;
+        const bool busy = whole ? lane == 0 : gi < granules;
+        const uint32_t bytes = !busy ? 0 : whole ? NT * (D + 8) : piece < 2 ? a.granule * (D / 2) : a.granule * 4;
+        const int to = piece < 2 ? (piece * NT + gi * a.granule) * (D / 2) : NT * D + ((piece - 2) * NT + gi * a.granule) * 4;
+        const int from = piece < 2 ? piece * a.page * (D / 2) : a.page * D + (piece - 2) * a.page * 4, each = piece < 2 ? D / 2 : 4;
+        const uint32_t all_granules = granules == 8 ? 0x11111111u : 0x11111111u & ((1u << (4 * granules)) - 1);
+        const uint32_t all_bytes = __reduce_add_sync(0xFFFFFFFFu, bytes);
+        const int64_t page_bytes = kv_page_bytes(a.page, D), head_step = int64_t(a.H) * page_bytes;
+        int pi = 0, slot = 0, stage = 0, wrap = 0;  // this lane's granule: page of the sequence, slot in it
+        uint32_t phase = 1;
+        bool placed = false;
         for (int u = ubegin; u < uend; ++u) {
-            const int it = u - ubegin, stage = it % kStages;
-            const int tok = cur.tile * NT + gi * a.granule;
-            const uint8_t *src = nullptr;
-            int slot = 0;
-            if (gi * a.granule < NT && cur.live && tok < cur.w.len) {
-                const int pi = tok / a.page, pg = __ldg(a.table + int64_t(cur.b) * a.width + pi);
-                slot = tok - pi * a.page;
-                if (pg >= 0 && pg < a.num_pages && SV_IN(slot + a.granule - 1, a.page))
-                    src = a.cache + (int64_t(pg) * a.H + cur.h) * page_bytes;
+            if (!placed) {
+                const int tok = cur.tile * NT + gi * a.granule;
+                pi = tok / a.page, slot = tok - pi * a.page;
+                placed = true;
             }
-            const uint32_t bytes = src == nullptr ? 0 : piece < 2 ? a.granule * (D / 2) : a.granule * 4;
-            const uint32_t sum = __reduce_add_sync(0xFFFFFFFFu, bytes);
-            const uint32_t have = __ballot_sync(0xFFFFFFFFu, src != nullptr && piece == 0);
-            if (it >= kStages && !mbar_wait(smem_u32(&sh.empty[stage]), uint32_t(it / kStages - 1) & 1)) {
+            const bool inside = busy && cur.live && cur.tile * NT + gi * a.granule < cur.w.len;
+            const int pg = inside ? __ldg(a.table + int64_t(cur.b) * a.width + pi) : -1;
+            const bool here = pg >= 0 && pg < a.num_pages && SV_IN(slot + a.granule - 1, a.page);
+            const uint32_t got = __ballot_sync(0xFFFFFFFFu, here), have = got & 0x11111111u;
+            const uint32_t sum = have == all_granules ? all_bytes : __reduce_add_sync(0xFFFFFFFFu, here ? bytes : 0u);
+            if (wrap > 0 && !mbar_wait(smem_u32(&sh.empty[stage]), phase)) {
                 atomicExch(a.status, int(SV_ERR_TIMEOUT));
                 return;  // (the consumers' waits give up too)
             }
             const uint32_t bar = smem_u32(&sh.full[stage]);
             if (lane == 0) {
-                sh.unit[stage] = Unit{cur.b, cur.h, cur.rt, cur.tile, cur.tiles(), cur.w.before, cur.w.len, cur.live ? cur.w.fresh : 0, have,
-                                      int((cur.tile + 1) * NT > cur.w.before || have != all_granules)};
+                int4 *un = reinterpret_cast<int4 *>(&sh.unit[stage]);
+                un[0] = make_int4(cur.b, cur.h, cur.rt, cur.tile);
+                un[1] = make_int4(cur.tiles(), cur.w.before, cur.w.len, cur.live ? cur.w.fresh : 0);
+                un[2] = make_int4(int(have), int((cur.tile + 1) * NT > cur.w.before || have != all_granules), 0, 0);
                 mbar_expect(bar, sum);
             }
             __syncwarp();
-            if (src) {
-                const uint32_t dst = smem_u32(sh.stage[stage]);
-                if (piece < 2)
-                    bulk_load(dst + (piece * NT + gi * a.granule) * (D / 2), src + (piece * a.page + slot) * (D / 2), bytes, bar);
-                else
-                    bulk_load(dst + NT * D + ((piece - 2) * NT + gi * a.granule) * 4,
-                              src + a.page * D + ((piece - 2) * a.page + slot) * 4, bytes, bar);
+            if (here)
+                bulk_load(smem_u32(sh.stage[stage]) + to, a.cache + pg * head_step + cur.h * page_bytes + from + slot * each, bytes, bar);
+            if (++stage == kStages) stage = 0, phase ^= 1, wrap = 1;
+            if (cur.tile + 1 < cur.tiles()) {
+                ++cur.tile;
+                slot += NT;
+                while (slot >= a.page) slot -= a.page, ++pi;
+            } else if (u + 1 < uend) {
+                cur.next(a, R, u + 1);
+                placed = false;
             }
-            if (u + 1 < uend) cur.next(a, R, u + 1);
         }
         return;
     }
@@ -793,7 +806,7 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
     };
 
     // the first segment is known already, and its queries load while its first unit is on its way
-    Unit seg{cur.b, cur.h, cur.rt, cur.tile, cur.tiles(), cur.w.before, cur.w.len, cur.live ? cur.w.fresh : 0, 0, 0};
+    Unit seg{cur.b, cur.h, cur.rt, cur.tile, cur.tiles(), cur.w.before, cur.w.len, cur.live ? cur.w.fresh : 0, 0, 0, {0, 0}};
     for (int it = 0;;) {  // segments
         const int last = min(units, it + seg.tiles - seg.tile);  // past the segment's last unit here
         consumers_sync<C>();
