@@ -53,12 +53,13 @@ template <int TV>
 struct AdjustShared {
     uint4 chunk[kAdjWarps][kRing][kChunkVecs];
     uint32_t mask[kAdjWarps][kRing][36];           // the chunk's words of the allowed mask
-    uint32_t count[TV];
-    uint32_t winner[TV / 2];                       // 16 bits each: 1 + index of the token's last bias entry, 0: none
-    uint16_t list[TV];                             // the touched tokens in order
+    alignas(16) uint32_t count[TV];                // of a listed token that is no draft: what its logit gains, as a float
+    alignas(16) uint32_t winner[TV / 2];                       // 16 bits each: 1 + index of the token's last bias entry, 0: none
+    uint16_t list[TV];                             // the touched tokens in order, and two flags
     uint32_t touched[TV / 32], drafted[TV / 32];   // tokens of history, drafts or bias list; of the drafts
     int before[TV / 32];                           // listed tokens before each word of `touched`
 };
+constexpr uint32_t kSeen = 0x4000u, kDrafted = 0x8000u;  // flags of a listed token
 static_assert(SV_MAX_BIAS < 65535, "");
 
 // Four bits as byte masks' top bits: bit j to bit 8 j + 7.
@@ -124,44 +125,46 @@ __device__ __forceinline__ void for_path(const int *parent_s, int r, F f) {
 }
 
 template <typename T, int TV>
-__global__ void __launch_bounds__(kAdjThreads, 2) adjust_kernel(const AdjustArgs a, int tiles) {
+__global__ void __launch_bounds__(kAdjThreads, 2) adjust_kernel(const AdjustArgs a, int batch) {
     extern __shared__ __align__(16) unsigned char raw[];
     using Sh = AdjustShared<TV>;
     Sh &sh = *reinterpret_cast<Sh *>(raw);
     int *draft_s = reinterpret_cast<int *>(raw + sizeof(Sh));
     int *parent_s = a.parent ? draft_s + a.ndraft : nullptr;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t b = blockIdx.x / tiles;
-    const int t0 = int(blockIdx.x % tiles) * TV;
+    // low ranges first: they hold a vocabulary's frequent tokens, and with them most of the arithmetic
+    const int64_t b = blockIdx.x % batch;
+    const int t0 = int(blockIdx.x / batch) * TV;
     const int n = min(TV, a.V - t0);  // tokens of this range
     using E = Elem<T>;
     constexpr int per = E::per;
     constexpr uint32_t kAll = (1u << per) - 1;
-    // a warp keeps its place in the range, and steps through the rows
+    // warps step through the rows, each time at the next place in the range (the arithmetic is uneven over it)
     constexpr int kChunks = (TV / per + kChunkVecs - 1) / kChunkVecs, kRowStep = kAdjWarps / kChunks;
     static_assert(kChunks * kRowStep == kAdjWarps, "");
-    const int part = warp % kChunks, v0 = part * kChunkVecs, first_row = warp / kChunks;
+    const int first_row = warp / kChunks;
     const int64_t words = (int64_t(a.V) + 31) / 32;
 
     griddep_launch_next();
-    for (int i = tid; i < TV; i += kAdjThreads) sh.count[i] = 0;
-    for (int i = tid; i < TV / 2; i += kAdjThreads) sh.winner[i] = 0;
+    for (int i = tid; i < TV / 4; i += kAdjThreads) reinterpret_cast<uint4 *>(sh.count)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < TV / 8; i += kAdjThreads) reinterpret_cast<uint4 *>(sh.winner)[i] = make_uint4(0, 0, 0, 0);
     for (int i = tid; i < TV / 32; i += kAdjThreads) sh.touched[i] = 0, sh.drafted[i] = 0;
     griddep_wait();
 
     // Elements before the 16-byte grid, and this warp's vectors after them, of a row that begins at p.
     auto head_of = [&](const T *p) { return min(n, int((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / int(sizeof(T))); };
-    auto vectors_of = [&](int head) { return max(0, min((n - head) / per - v0, kChunkVecs)); };
+    auto vectors_of = [&](int head, int v0) { return max(0, min((n - head) / per - v0, kChunkVecs)); };
     const T *src = static_cast<const T *>(a.in) + b * a.in_bs + first_row * a.in_rs + t0;
     T *dst = static_cast<T *>(a.out) + b * a.out_bs + first_row * a.out_rs + t0;
     const uint32_t *mask = a.allowed ? a.allowed + (b * a.rows + first_row) * words : nullptr;
     // the copies run kRing - 1 rows ahead
     const T *src_ahead = src;
     const uint32_t *mask_ahead = mask;
-    int row_ahead = first_row;
+    int row_ahead = first_row, v0_ahead = warp % kChunks * kChunkVecs;
+    auto step = [](int v0) { return v0 + kChunkVecs == kChunks * kChunkVecs ? 0 : v0 + kChunkVecs; };
     auto fetch = [&](int slot) {
         if (row_ahead < a.rows) {
-            const int head = head_of(src_ahead), count = vectors_of(head);
+            const int v0 = v0_ahead, head = head_of(src_ahead), count = vectors_of(head, v0);
             const uint4 *from = reinterpret_cast<const uint4 *>(src_ahead + head) + v0 + lane;
             uint4 *to = &sh.chunk[warp][slot][lane];
 #pragma unroll
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(kAdjThreads, 2) adjust_kernel(const AdjustArgs
                 if (w0 + lane <= w1) copy_async4(&sh.mask[warp][slot][lane], mask_ahead + w0 + lane);
                 if (lane == 0 && w0 + 32 <= w1) copy_async4(&sh.mask[warp][slot][32], mask_ahead + w0 + 32);
             }
-            row_ahead += kRowStep, src_ahead += kRowStep * a.in_rs;
+            row_ahead += kRowStep, v0_ahead = step(v0), src_ahead += kRowStep * a.in_rs;
             if (mask_ahead) mask_ahead += kRowStep * words;
         }
         copy_commit();
@@ -186,11 +189,10 @@ __global__ void __launch_bounds__(kAdjThreads, 2) adjust_kernel(const AdjustArgs
         for (int i = tid; i < a.rows; i += kAdjThreads) parent_s[i] = a.parent[i];
     __syncthreads();
     if (a.history) {
-        const int64_t Lr = a.lengths[b];
-        const int64_t L = Lr < 0 ? 0 : (Lr > a.history_stride ? a.history_stride : Lr);
-        const int64_t P = a.prompt_lengths ? a.prompt_lengths[b] : 0;
+        const int stride = int(a.history_stride);
+        const int L = min(max(a.lengths[b], 0), stride), P = a.prompt_lengths ? a.prompt_lengths[b] : 0;
         const int32_t *h = a.history + b * a.history_stride;
-        auto note = [&](int32_t tok, int64_t i) {
+        auto note = [&](int32_t tok, int i) {
             const uint32_t k = uint32_t(tok) - uint32_t(t0);
             if (k < uint32_t(n)) {
                 if (i < P) atomicOr(&sh.count[k], kPrompt);
@@ -198,17 +200,20 @@ __global__ void __launch_bounds__(kAdjThreads, 2) adjust_kernel(const AdjustArgs
                 atomicOr(&sh.touched[k >> 5], 1u << (k & 31));
             }
         };
-        int64_t i = 0;
+        int i = 0;
         if ((reinterpret_cast<uintptr_t>(h) & 15) == 0) {
             const int4 *h4 = reinterpret_cast<const int4 *>(h);
-#pragma unroll 4
-            for (int64_t q = tid; q < L / 4; q += kAdjThreads) {
-                const int4 v = __ldg(h4 + q);
-                note(v.x, 4 * q), note(v.y, 4 * q + 1), note(v.z, 4 * q + 2), note(v.w, 4 * q + 3);
+            i = L & ~3;
+            for (int q = tid; q < L / 4; q += 2 * kAdjThreads) {  // two loads in flight
+                const int q2 = q + kAdjThreads;
+                const int4 none = make_int4(-1, -1, -1, -1), v = __ldg(h4 + q), w = q2 < L / 4 ? __ldg(h4 + q2) : none;
+                const uint32_t z = uint32_t(t0), m = uint32_t(n);
+                if ((uint32_t(v.x) - z < m) | (uint32_t(v.y) - z < m) | (uint32_t(v.z) - z < m) | (uint32_t(v.w) - z < m))
+                    note(v.x, 4 * q), note(v.y, 4 * q + 1), note(v.z, 4 * q + 2), note(v.w, 4 * q + 3);
+                if ((uint32_t(w.x) - z < m) | (uint32_t(w.y) - z < m) | (uint32_t(w.z) - z < m) | (uint32_t(w.w) - z < m))
+                    note(w.x, 4 * q2), note(w.y, 4 * q2 + 1), note(w.z, 4 * q2 + 2), note(w.w, 4 * q2 + 3);
             }
-            i = L / 4 * 4;
         }
-#pragma unroll 4
         for (i += tid; i < L; i += kAdjThreads) note(__ldg(h + i), i);
     }
     for (int i = tid; i < a.nbias; i += kAdjThreads) {
@@ -247,66 +252,82 @@ __global__ void __launch_bounds__(kAdjThreads, 2) adjust_kernel(const AdjustArgs
         }
     }
     __syncthreads();
-    for (int k = tid; k < n; k += kAdjThreads) {
-        const uint32_t w = sh.touched[k >> 5], bit = 1u << (k & 31);
-        if (w & bit) sh.list[sh.before[k >> 5] + __popc(w & (bit - 1))] = uint16_t(k);
+    // the list; a token that is no draft has the same penalties and bias in every row
+    const float rep = a.repetition ? a.repetition[b] : 1.f, inverse = 1.f / rep;
+    const float freq = a.frequency ? a.frequency[b] : 0.f;
+    const float pres = a.presence ? a.presence[b] : 0.f;
+    auto gain = [&](uint32_t word, int k) {  // of token k with a count word
+        const uint32_t c = word & ~kPrompt, won = sh.winner[k >> 1] >> (16 * (k & 1)) & 0xFFFFu;
+        const float penalty = fmaf(freq, float(c), c ? pres : 0.f);
+        return (won && SV_IN(won - 1, a.nbias) ? __ldg(a.bias_values + b * a.nbias + won - 1) : 0.f) - penalty;
+    };
+    for (int i = tid; i < TV / 32; i += kAdjThreads) {
+        const uint32_t drafts = sh.drafted[i];
+        int at = sh.before[i];
+        for (uint32_t w = sh.touched[i]; w; w &= w - 1) {
+            const int j = __ffs(w) - 1, k = i * 32 + j;
+            const uint32_t word = sh.count[k];
+            uint32_t flags = word ? kSeen : 0;
+            if (drafts >> j & 1) flags = kDrafted;
+            else sh.count[k] = __float_as_uint(gain(word, k));
+            sh.list[at++] = uint16_t(uint32_t(k) | flags);
+        }
     }
     __syncthreads();
 
-    const float rep = a.repetition ? a.repetition[b] : 1.f;
-    const float freq = a.frequency ? a.frequency[b] : 0.f;
-    const float pres = a.presence ? a.presence[b] : 0.f;
-    // a touched token k of row r
-    auto adjust = [&](float l, int r, int k) {
+    // Penalties and bias of a touched token in row r (a division by the repetition penalty is a product with
+    // its reciprocal: one more rounding of 2^-24).
+    auto adjust = [&](float l, int r, uint32_t entry) {
+        const int k = entry & 0x3FFFu;
         if (!SV_IN(k, n)) return l;
-        uint32_t w = sh.count[k];
-        if (r > 0 && (sh.drafted[k >> 5] >> (k & 31) & 1u)) for_path(parent_s, r, [&](int j) { w += draft_s[j] == t0 + k; });
-        const uint32_t c = w & ~kPrompt;
-        if (w) l = l > 0.f ? __fdiv_rn(l, rep) : __fmul_rn(l, rep);
-        l = __fsub_rn(__fsub_rn(l, __fmul_rn(freq, float(c))), c ? pres : 0.f);
-        const uint32_t won = sh.winner[k >> 1] >> (16 * (k & 1)) & 0xFFFFu;
-        if (won && SV_IN(won - 1, a.nbias)) l = __fadd_rn(l, __ldg(a.bias_values + b * a.nbias + won - 1));
-        return l;
+        uint32_t word = sh.count[k];
+        float g = __uint_as_float(word);
+        bool seen = entry & kSeen;
+        if (entry & kDrafted) {
+            if (r > 0) for_path(parent_s, r, [&](int j) { word += draft_s[j] == t0 + k; });
+            g = gain(word, k), seen = word != 0;
+        }
+        if (seen) l *= l > 0.f ? inverse : rep;
+        return l + g;
     };
     auto is_touched = [&](int k) { return sh.touched[k >> 5] >> (k & 31) & 1u; };
     auto listed_before = [&](int k) { return sh.before[k >> 5] + __popc(sh.touched[k >> 5] & ((1u << (k & 31)) - 1)); };
 
-    int slot = 0, listed_head = -1, e0 = 0, e1 = 0;
+    int slot = 0, v0 = warp % kChunks * kChunkVecs;
     for (int r = first_row; r < a.rows; r += kRowStep) {
         fetch(slot == 0 ? kRing - 1 : slot - 1);
-        const int head = head_of(src), count = vectors_of(head);
+        const int head = head_of(src), count = vectors_of(head, v0);
         auto scalar = [&](int k) {
             const bool ok = mask == nullptr || (__ldg(mask + ((t0 + k) >> 5)) >> ((t0 + k) & 31) & 1u), mine = is_touched(k);
             if (a.in_place && ok && !mine) return;
             const T v = src[k];
-            dst[k] = !ok ? E::round(-__int_as_float(0x7f800000)) : mine ? E::round(adjust(E::get(v), r, k)) : v;
+            dst[k] = !ok ? E::round(-__int_as_float(0x7f800000)) : mine ? E::round(adjust(E::get(v), r, sh.list[listed_before(k)])) : v;
         };
         copy_wait<kRing - 1>();
         __syncwarp();
         if (((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst)) & 15) != 0) {
             // the two rows lie differently on the 16-byte grid
-            const int k1 = min(n, (part + 1) * kChunkVecs * per);
+            const int k1 = min(n, (v0 + kChunkVecs) * per);
             for (int k = v0 * per + lane; k < k1; k += 32) scalar(k);
         } else {
-            if (part == 0 && (head > 0 || (n - head) % per != 0)) {  // the row's ends off the grid
+            if (v0 == 0 && (head > 0 || (n - head) % per != 0)) {  // the row's ends off the grid
                 const int tail = head + (n - head) / per * per;
                 if (lane < head) scalar(lane);
                 if (lane < n - tail) scalar(tail + lane);
             }
             uint4 *mine = &sh.chunk[warp][slot][0];
             const int k0 = head + v0 * per;  // the chunk's first token
-            if (head != listed_head && count > 0) {
-                const int k1 = k0 + count * per;
-                e0 = listed_before(k0), e1 = listed_before(k1 - 1) + int(is_touched(k1 - 1));
-                listed_head = head;
-            }
-            if (count > 0 && e0 < e1) {
-                T *elems = reinterpret_cast<T *>(mine);
-                for (int e = e0 + lane; e < e1; e += 32) {
-                    const int k = sh.list[e];
-                    if (SV_IN(k - k0, count * per)) elems[k - k0] = E::round(adjust(E::get(elems[k - k0]), r, k));
+            if (count > 0) {
+                const int last = k0 + count * per - 1, e0 = listed_before(k0), e1 = listed_before(last) + int(is_touched(last));
+                if (e0 < e1) {
+                    T *elems = reinterpret_cast<T *>(mine);
+                    for (int e = e0 + lane; e < e1; e += 32) {
+                        const uint32_t entry = sh.list[e];
+                        const int k = int(entry & 0x3FFFu) - k0;
+                        if (SV_IN(k, count * per)) elems[k] = E::round(adjust(E::get(elems[k]), r, entry));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
             uint4 *to = reinterpret_cast<uint4 *>(dst + head) + v0 + lane;
             const uint32_t first = (uint32_t(t0 + k0) & 31) + lane * per;
@@ -333,6 +354,7 @@ __global__ void __launch_bounds__(kAdjThreads, 2) adjust_kernel(const AdjustArgs
         src += kRowStep * a.in_rs, dst += kRowStep * a.out_rs;
         if (mask) mask += kRowStep * words;
         slot = slot + 1 == kRing ? 0 : slot + 1;
+        v0 = step(v0);
     }
     copy_wait<0>();
 }
@@ -345,7 +367,7 @@ cudaError_t launch_adjust(const AdjustArgs &a, int B, int tiles, cudaStream_t s)
             cudaFuncSetAttribute(adjust_kernel<T, TV>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return e;
     }
-    return launch_after(adjust_kernel<T, TV>, unsigned(int64_t(B) * tiles), kAdjThreads, smem, s, a, tiles);
+    return launch_after(adjust_kernel<T, TV>, unsigned(int64_t(B) * tiles), kAdjThreads, smem, s, a, B);
 }
 
 }  // namespace
