@@ -20,6 +20,7 @@
 #include "spec_serve.h"
 #include "sv_checks.cuh"
 #include "sv_device.cuh"
+#include "sv_launch.cuh"
 
 namespace sv {
 namespace {
@@ -362,11 +363,9 @@ __global__ void __launch_bounds__(kAdjThreads, 2) adjust_kernel(const AdjustArgs
 template <typename T, int TV>
 cudaError_t launch_adjust(const AdjustArgs &a, int B, int tiles, cudaStream_t s) {
     const size_t smem = sizeof(AdjustShared<TV>) + (size_t(a.ndraft) + (a.parent ? a.rows : 0)) * 4;
-    if (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(adjust_kernel<T, TV>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-        if (e != cudaSuccess) return e;
-    }
+    static std::atomic<int> allowed[64];
+    const cudaError_t e = allow_shared(adjust_kernel<T, TV>, int(smem), allowed);
+    if (e != cudaSuccess) return e;
     return launch_after(adjust_kernel<T, TV>, unsigned(int64_t(B) * tiles), kAdjThreads, smem, s, a, B);
 }
 

@@ -31,6 +31,7 @@
 #include "sv_device.cuh"
 #include "sv_grid.cuh"
 #include "sv_kv.cuh"
+#include "sv_launch.cuh"
 
 namespace sv {
 
@@ -996,10 +997,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const A
 template <int D, int NR>
 cudaError_t launch_attention(const AttArgs &a, int grid, cudaStream_t s) {
     const size_t smem = sizeof(AttShared<D, NR>) + (a.parent ? size_t(a.T) * 4 + size_t(8 * NR) * ((a.T + 31) / 32) * 4 : 0);
-    cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return e;
-    // as much shared memory as there is, so that att_occupancy CTAs are resident
-    e = cudaFuncSetAttribute(kv_attention_kernel<D, NR>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    static std::atomic<int> allowed[64];
+    cudaError_t e = allow_shared(kv_attention_kernel<D, NR>, int(smem), allowed);
     if (e != cudaSuccess) return e;
     e = launch_after(kv_attention_kernel<D, NR>, unsigned(grid), unsigned(att_threads(D, NR)), smem, s, a);
     if (e != cudaSuccess) return e;
@@ -1019,8 +1018,7 @@ cudaError_t launch_attention_rows(const AttArgs &a, int nr, int grid, cudaStream
         case 3: return launch_attention<D, 3>(a, grid, s);                                               \
         case 4: return launch_attention<D, 4>(a, grid, s);                                               \
         case 5: return launch_attention<D, 5>(a, grid, s);                                               \
-        case 6: return launch_attention<D, 6>(a, grid, s);                                               \
-        default: return launch_attention<D, 8>(a, grid, s);                                              \
+        default: return launch_attention<D, 6>(a, grid, s);                                              \
         }                                                                                                \
     }
 

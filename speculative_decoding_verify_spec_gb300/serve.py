@@ -8,6 +8,7 @@ the current stream from PyTorch and call the C entry of the same name.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -43,20 +44,36 @@ def _library() -> ctypes.CDLL:
     return _ready
 
 
+# The checks below take their common case first: a call's host time is what a small step waits for.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current(dev) -> int:
+    """The current stream's handle on dev."""
+    return _raw_stream(dev.index) if _raw_stream is not None and dev.index is not None else _stream(dev)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _like(t):
+    """A new contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _int32(t, name, shape, dev):
+    if t is None or (t.dtype is torch.int32 and t.device == dev and t.shape == shape and t.is_contiguous()):
+        return t
+    return _ints(t, name, shape, dev)
+
+
 def _floats(t, name, shape, dev):
-    if t is None:
-        return None
+    if t is None or (t.dtype is torch.float32 and t.device == dev and t.shape == shape and t.is_contiguous()):
+        return t
     if t.dtype != torch.float32 or t.device != dev or tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be float32 of shape {tuple(shape)} on {dev}")
     return t.contiguous()
-
-
-def _maybe_ints(t, name, shape, dev):
-    return None if t is None else _ints(t, name, shape, dev)
 
 
 def spec_logit_adjust(logits: torch.Tensor, *, history=None, lengths=None, prompt_lengths=None, draft_tokens=None,
@@ -77,39 +94,41 @@ def spec_logit_adjust(logits: torch.Tensor, *, history=None, lengths=None, promp
     B, R, V = logits.shape
     dt, dev = _dtype_code(logits), logits.device
     if out is None:
-        out = torch.empty((B, R, V), dtype=logits.dtype, device=dev)
+        out = _like(logits)
+        ob, orow, _ = out.stride()
     elif out.device != dev or out.dtype != logits.dtype or tuple(out.shape) != (B, R, V):
         raise ValueError(f"out must be {logits.dtype} of shape {(B, R, V)} on {dev}")
-    ob, orow = _logits3(out, "out")
+    else:
+        ob, orow = _logits3(out, "out")
     n = 0
     if history is not None:
         if history.dim() != 2 or lengths is None:
             raise ValueError("history must be [B, n], with lengths [B]")
         n = history.shape[1]
-        history = _ints(history, "history", (B, n), dev)
-        lengths = _ints(lengths, "lengths", (B,), dev)
-        prompt_lengths = _maybe_ints(prompt_lengths, "prompt_lengths", (B,), dev)
+        history = _int32(history, "history", (B, n), dev)
+        lengths = _int32(lengths, "lengths", (B,), dev)
+        prompt_lengths = _int32(prompt_lengths, "prompt_lengths", (B,), dev)
     if parent is not None:
         if draft_tokens is None:
             raise ValueError("a tree (parent) needs draft_tokens [B, rows]")
-        parent = _ints(parent, "parent", (R,), dev)
+        parent = _int32(parent, "parent", (R,), dev)
     if draft_tokens is not None:
-        draft_tokens = _ints(draft_tokens, "draft_tokens", (B, R if parent is not None else max(R - 1, 0)), dev)
+        draft_tokens = _int32(draft_tokens, "draft_tokens", (B, R if parent is not None else max(R - 1, 0)), dev)
     k = 0
     if (bias_tokens is None) != (bias_values is None):
         raise ValueError("bias_tokens and bias_values belong together")
     if bias_tokens is not None:
         k = bias_tokens.shape[1] if bias_tokens.dim() == 2 else -1
-        bias_tokens = _ints(bias_tokens, "bias_tokens", (B, k), dev)
+        bias_tokens = _int32(bias_tokens, "bias_tokens", (B, k), dev)
         bias_values = _floats(bias_values, "bias_values", (B, k), dev)
     repetition = _floats(repetition, "repetition", (B,), dev)
     frequency = _floats(frequency, "frequency", (B,), dev)
     presence = _floats(presence, "presence", (B,), dev)
-    allowed = _maybe_ints(allowed, "allowed", (B, R, (V + 31) // 32), dev)
+    allowed = _int32(allowed, "allowed", (B, R, (V + 31) // 32), dev)
     st = lib.spec_logit_adjust(logits.data_ptr(), sb, sr, out.data_ptr(), ob, orow, dt, B, R, V, _ptr(history), n,
                                _ptr(lengths), _ptr(prompt_lengths), _ptr(draft_tokens), _ptr(parent), _ptr(repetition),
                                _ptr(frequency), _ptr(presence), _ptr(bias_tokens), _ptr(bias_values), k, _ptr(allowed),
-                               _stream(dev))
+                               _current(dev))
     _check(st, "spec_logit_adjust")
     return out
 
@@ -130,9 +149,10 @@ def _kv_dtype(t: torch.Tensor, name: str) -> int:
 def _heads4(t: torch.Tensor, name: str):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
+    st = t.stride()
+    if len(st) != 4 or (st[3] != 1 and t.shape[3] > 1):
         raise ValueError(f"{name} must be [B, T, heads, head_dim] with a contiguous last axis")
-    return t.stride(0), t.stride(1), t.stride(2)
+    return st
 
 
 def _cache(cache, page_table, start, new_lens, B, heads, D, dev):
@@ -145,8 +165,8 @@ def _cache(cache, page_table, start, new_lens, B, heads, D, dev):
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, pages per sequence]")
     width = page_table.shape[1]
-    return (cache.shape[0], page, _ints(page_table, "page_table", (B, width), dev), width, _ints(start, "start", (B,), dev),
-            _maybe_ints(new_lens, "new_lens", (B,), dev))
+    return (cache.shape[0], page, _int32(page_table, "page_table", (B, width), dev), width, _int32(start, "start", (B,), dev),
+            _int32(new_lens, "new_lens", (B,), dev))
 
 
 def _rotation(cos, sin, positions, B, T, dev):
@@ -157,7 +177,7 @@ def _rotation(cos, sin, positions, B, T, dev):
     if cos.dim() != 2:
         raise ValueError("cos must be [positions, pairs]")
     cos, sin = _floats(cos, "cos", cos.shape, dev), _floats(sin, "sin", cos.shape, dev)
-    return cos, sin, cos.shape[0], cos.shape[1], _maybe_ints(positions, "positions", (B, T), dev)
+    return cos, sin, cos.shape[0], cos.shape[1], _int32(positions, "positions", (B, T), dev)
 
 
 def spec_kv_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor,
@@ -179,19 +199,21 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_t
     pages, page, page_table, width, start, new_lens = _cache(cache, page_table, start, new_lens, B, H, D, dev)
     cos, sin, length, pairs, positions = _rotation(cos, sin, positions, B, T, dev)
     if return_values:
-        k_values = torch.empty((B, T, H, D), dtype=k.dtype, device=dev) if k_values is None else k_values
-        v_values = torch.empty((B, T, H, D), dtype=k.dtype, device=dev) if v_values is None else v_values
+        k_values = _like(k) if k_values is None else k_values
+        v_values = _like(k) if v_values is None else v_values
     for name, t in (("k_values", k_values), ("v_values", v_values)):
         if t is not None and (t.shape != k.shape or t.dtype != k.dtype or t.device != dev or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous tensor like k")
-    st = lib.spec_kv_append(k.data_ptr(), *ks, v.data_ptr(), *vs, dt, B, T, H, D, cache.data_ptr(), pages, page,
+    st = lib.spec_kv_append(k.data_ptr(), ks[0], ks[1], ks[2], v.data_ptr(), vs[0], vs[1], vs[2], dt, B, T, H, D, cache.data_ptr(), pages, page,
                             page_table.data_ptr(), width, start.data_ptr(), _ptr(new_lens), _ptr(cos), _ptr(sin), length,
-                            pairs, int(interleaved), _ptr(positions), _ptr(k_values), _ptr(v_values), _stream(dev))
+                            pairs, int(interleaved), _ptr(positions), _ptr(k_values), _ptr(v_values), _current(dev))
     _check(st, "spec_kv_append")
     return None if k_values is None and v_values is None else (k_values, v_values)
 
 
+@functools.lru_cache(maxsize=1024)
 def spec_kv_attention_workspace_size(B: int, T: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace that spec_kv_attention needs for these sizes."""
     return int(_library().spec_kv_attention_workspace_size(B, T, heads, kv_heads, head_dim))
 
 
@@ -211,20 +233,21 @@ def spec_kv_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Te
     H = cache.shape[1]
     pages, page, page_table, width, start, new_lens = _cache(cache, page_table, start, new_lens, B, None, D, dev)
     cos, sin, length, pairs, positions = _rotation(cos, sin, positions, B, T, dev)
-    parent = _maybe_ints(parent, "parent", (T,), dev)
+    parent = _int32(parent, "parent", (T,), dev)
     if out is None:
-        out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=dev)
+        out = _like(q)
     elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor like q")
     n = spec_kv_attention_workspace_size(B, T, Hq, H, D)
     if workspace is None:
         workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
-    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    st = lib.spec_kv_attention(q.data_ptr(), *qs, dt, B, T, Hq, H, D, cache.data_ptr(), pages, page, page_table.data_ptr(),
+    else:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        n = workspace.numel() * workspace.element_size()
+    st = lib.spec_kv_attention(q.data_ptr(), qs[0], qs[1], qs[2], dt, B, T, Hq, H, D, cache.data_ptr(), pages, page, page_table.data_ptr(),
                                width, start.data_ptr(), _ptr(new_lens), _ptr(parent),
                                1.0 / math.sqrt(D) if scale is None else float(scale), _ptr(cos), _ptr(sin), length, pairs,
-                               int(interleaved), _ptr(positions), out.data_ptr(), workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), _stream(dev))
+                               int(interleaved), _ptr(positions), out.data_ptr(), workspace.data_ptr(), n, _current(dev))
     _check(st, "spec_kv_attention")
     return out
