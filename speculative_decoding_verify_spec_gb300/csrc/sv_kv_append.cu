@@ -5,7 +5,9 @@
 // row.  They rotate the key, reduce minimum and maximum over their lanes, and write the codes.  The result is
 // that of the exact rule: rotated keys are double-float (a 16-bit input times an fp32 cosine is exact in
 // two floats), and whatever lies so near a rounding border that 32 bits cannot tell -- about one scale
-// in a thousand, one code in 50,000 -- is decided in 64.  Everything is read once and written once.
+// in two thousand, one code in 100,000 -- is decided on exact differences.  Everything is read once and written
+// once.  The variants are by what the loads can be: rows and angles on the 16-byte grid with the rotation's
+// partners eight dimensions apart in one place (halves) or in the lane itself (neighbours), else any.
 #include <cstdint>
 
 #include "sv_checks.cuh"
@@ -20,8 +22,7 @@ constexpr int kAppThreads = 256;
 struct AppendArgs {
     const uint16_t *k, *v;
     int64_t k_bs, k_ts, k_hs, v_bs, v_ts, v_hs;
-    int bf16, vec, rot_vec;  // rows, and the angles' rows, lie on the 16-byte grid
-    int64_t items;  // B * T * H
+    uint32_t items;  // B * T * H
     int T, H;
     uint8_t *cache;
     int num_pages, page, width;
@@ -32,6 +33,17 @@ struct AppendArgs {
 
 __device__ __forceinline__ float saturate(float x) { return fminf(fmaxf(x, -65504.f), 65504.f); }
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // 1.5 * 2^23: added to a float of less than 2^22 it leaves the nearest integer (ties to even) in the low bits.
 constexpr float kRound = 12582912.f;
 
@@ -39,41 +51,43 @@ constexpr float kRound = 12582912.f;
 // each, and the scale and zero as fp16 bits in one word (scale low).
 template <int L, bool kLow>
 __device__ __forceinline__ uint32_t quantise(const float (&hi)[8], const float (&lo)[8], uint32_t &meta) {
-    float low = hi[0], high = hi[0], size = fabsf(hi[0]);
+    float low = hi[0], high = hi[0];  // (a NaN stays)
 #pragma unroll
-    for (int i = 1; i < 8; ++i) low = fminf(low, hi[i]), high = fmaxf(high, hi[i]);
-    bool bad = false;  // (fminf and fmaxf drop a NaN)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) bad |= !(fabsf(hi[i]) <= 3.4e38f);
-    if (bad) high = INFINITY;
+    for (int i = 1; i < 8; ++i) low = min_nan(low, hi[i]), high = max_nan(high, hi[i]);
 #pragma unroll
     for (int o = L / 2; o; o >>= 1) {
-        low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, o));
-        high = fmaxf(high, __shfl_xor_sync(0xFFFFFFFFu, high, o));
+        low = min_nan(low, __shfl_xor_sync(0xFFFFFFFFu, low, o));
+        high = max_nan(high, __shfl_xor_sync(0xFFFFFFFFu, high, o));
     }
-    bad = !(high <= 3.4e38f);
+    const bool bad = !(high <= 3.4e38f && low >= -3.4e38f);
     // zero = fp16(fp32(min)): the least hi is that fp32 number
     const float range = high - low, t = range * (1.f / 15.f);
-    // scale = fp16(fp32(range / 15)): t is off by a few units of its last place, and by what the low parts
-    // add; where that may matter, the quotient in 64 bits
-    float off = t * 4.8e-7f;
-    if (kLow) size = fmaxf(fabsf(low), fabsf(high)), off = fmaf(size, 2.4e-8f, off);
+    // scale = fp16(fp32(range / 15)): t is off by three roundings, and by what the low parts add (each at most 2^-24
+    // of its high part); where that may matter, the quotient of the exact range in 64 bits
+    float off = t * 2.4e-7f;
+    if constexpr (kLow) off = fmaf(fmaxf(fabsf(low), fabsf(high)), 1e-8f, off);
     const __half2 ends = __floats2half2_rn(saturate(t - off), saturate(t + off));
     uint32_t sb = __half_as_ushort(__low2half(ends));
     const bool doubt = !bad && sb != __half_as_ushort(__high2half(ends));
     if (__any_sync(0xFFFFFFFFu, doubt)) {  // (all lanes take part in the reductions)
-        double least = 1e300, most = -1e300;
+        float least = 0.f, most = 0.f;  // the low parts of the extremes
+        if constexpr (kLow) {
+            least = INFINITY, most = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const double x = double(hi[i]) + double(lo[i]);
-            least = fmin(least, x), most = fmax(most, x);
-        }
+            for (int i = 0; i < 8; ++i) {
+                if (hi[i] == low) least = fminf(least, lo[i]);
+                if (hi[i] == high) most = fmaxf(most, lo[i]);
+            }
 #pragma unroll
-        for (int o = L / 2; o; o >>= 1) {
-            least = fmin(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
-            most = fmax(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+            for (int o = L / 2; o; o >>= 1) {
+                least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
+                most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+            }
         }
-        if (doubt) sb = __half_as_ushort(__float2half_rn(saturate(__double2float_rn((most - least) / 15.0))));
+        if (doubt) {
+            const double exact = ((double(high) - double(low)) + (double(most) - double(least))) / 15.0;
+            sb = __half_as_ushort(__float2half_rn(saturate(__double2float_rn(exact))));
+        }
     }
     uint32_t zb = __half_as_ushort(__float2half_rn(saturate(low)));
     if (sb == 0) sb = 1;          // 2^-24
@@ -90,17 +104,26 @@ __device__ __forceinline__ uint32_t quantise(const float (&hi)[8], const float (
     float c[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        // clamped before rounding, which changes no code; |q| <= 16 and a few roundings of 2^-24 each: in doubt
-        // within 1e-5 of a border (a saturated zero or scale only meets the clamp)
+        // clamped before rounding, which changes no code; |q| <= 15 and four roundings of 2^-24: in doubt within
+        // 3.6e-6 of a border (a saturated zero or scale only meets the clamp)
         const float q = fminf(fmaxf(((hi[i] - z) + (kLow ? lo[i] : 0.f)) * inv, 0.f), 15.f);
         c[i] = q + kRound;
-        near |= fabsf(q - (c[i] - kRound)) > 0.49999f;
+        near |= fabsf(q - (c[i] - kRound)) > 0.499995f;
     }
     if (near) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const double q = ((double(hi[i]) - double(z)) + (kLow ? double(lo[i]) : 0.0)) / double(s);
-            c[i] = float(rint(fmin(fmax(q, 0.0), 15.0))) + kRound;
+            const float q = fminf(fmaxf(((hi[i] - z) + (kLow ? lo[i] : 0.f)) * inv, 0.f), 15.f), f = floorf(q);
+            if (fabsf(q - (f + 0.5f)) < 1e-4f) {
+                // the sign of x - z - s (f + 1/2), exact: s (f + 1/2) has 16 bits, and each difference keeps its error
+                const float sb2 = s * (f + 0.5f), u = __fsub_rn(hi[i], z), ub = __fsub_rn(u, hi[i]);
+                const float ue = __fsub_rn(__fsub_rn(hi[i], __fsub_rn(u, ub)), __fadd_rn(z, ub));
+                const float d = __fsub_rn(u, sb2), db = __fsub_rn(d, u);
+                const float de = __fsub_rn(__fsub_rn(u, __fsub_rn(d, db)), __fadd_rn(sb2, db));
+                const float t2 = __fadd_rn(d, __fadd_rn(__fadd_rn(de, ue), kLow ? lo[i] : 0.f));
+                const bool odd = (int(f) & 1) != 0;
+                c[i] = (t2 > 0.f || (t2 == 0.f && odd) ? f + 1.f : f) + kRound;
+            }
         }
     }
 #pragma unroll
@@ -108,19 +131,23 @@ __device__ __forceinline__ uint32_t quantise(const float (&hi)[8], const float (
     return codes;
 }
 
-// Eight 16-bit numbers (vec: 16-byte aligned).
-__device__ __forceinline__ uint4 load_row(const uint16_t *p, bool vec) {
-    if (vec) return __ldg(reinterpret_cast<const uint4 *>(p));
+enum Layout { kAny, kHalves, kNeighbours };  // how rows and rotation lie, see above
+
+// Eight 16-bit numbers.
+template <bool kVec>
+__device__ __forceinline__ uint4 load_row(const uint16_t *p) {
+    if (kVec) return __ldg(reinterpret_cast<const uint4 *>(p));
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = uint32_t(__ldg(p + 2 * i)) | uint32_t(__ldg(p + 2 * i + 1)) << 16;
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void widen(const uint4 &v, bool bf16, float (&x)[8]) {
+template <bool kBF16>
+__device__ __forceinline__ void widen(const uint4 &v, float (&x)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (bf16) {
+        if (kBF16) {
             x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         } else {
             const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
@@ -130,14 +157,15 @@ __device__ __forceinline__ void widen(const uint4 &v, bool bf16, float (&x)[8]) 
 }
 
 // What the codes stand for.
-__device__ __forceinline__ void store_values(uint16_t *p, uint32_t codes, uint32_t meta, bool live, bool bf16) {
+template <bool kBF16>
+__device__ __forceinline__ void store_values(uint16_t *p, uint32_t codes, uint32_t meta, bool live) {
     const float s = __half2float(__ushort_as_half(uint16_t(meta))), z = __half2float(__ushort_as_half(uint16_t(meta >> 16)));
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         // s code is exact: one rounding, then that to the type
         const float x = fmaf(s, float(codes >> (8 * i) & 15u), z), y = fmaf(s, float(codes >> (8 * i + 4) & 15u), z);
-        if (bf16) {
+        if (kBF16) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
         } else {
@@ -150,36 +178,38 @@ __device__ __forceinline__ void store_values(uint16_t *p, uint32_t codes, uint32
 
 // Rotates eight dimensions from d0 on of the key row kp, x, in two floats: both products exact, their sum exact, then
 // the rest.
+template <Layout kLayout, bool kBF16>
 __device__ __forceinline__ void rotate(const AppendArgs &a, const uint16_t *kp, int d0, int64_t row, float (&x)[8], float (&lo)[8]) {
     const int pairs = a.rot.pairs;
     const float *cp = a.rot.cos + row, *sp = a.rot.sin + row;
     float y[8], c[8], s[8];
-    if (!a.rot.interleaved && pairs % 8 == 0) {  // the eight lie within one half
+    if constexpr (kLayout == kHalves) {  // the eight lie within one half
         const bool low = d0 < pairs;
         const int e0 = low ? d0 : d0 - pairs;
-        widen(load_row(kp + (low ? d0 + pairs : e0), a.vec), a.bf16, y);
-        if (a.rot_vec) {
+        widen<kBF16>(load_row<true>(kp + (low ? d0 + pairs : e0)), y);
 #pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-                const float4 u = __ldg(reinterpret_cast<const float4 *>(cp + e0 + i)), v = __ldg(reinterpret_cast<const float4 *>(sp + e0 + i));
-                c[i] = u.x, c[i + 1] = u.y, c[i + 2] = u.z, c[i + 3] = u.w;
-                s[i] = v.x, s[i + 1] = v.y, s[i + 2] = v.z, s[i + 3] = v.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = __ldg(cp + e0 + i), s[i] = __ldg(sp + e0 + i);
+        for (int i = 0; i < 8; i += 4) {
+            const float4 u = __ldg(reinterpret_cast<const float4 *>(cp + e0 + i)), v = __ldg(reinterpret_cast<const float4 *>(sp + e0 + i));
+            c[i] = u.x, c[i + 1] = u.y, c[i + 2] = u.z, c[i + 3] = u.w;
+            s[i] = v.x, s[i + 1] = v.y, s[i + 2] = v.z, s[i + 3] = v.w;
         }
         if (low) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[i] = -s[i];
         }
+    } else if constexpr (kLayout == kNeighbours) {
+        const float4 u = __ldg(reinterpret_cast<const float4 *>(cp + d0 / 2)), v = __ldg(reinterpret_cast<const float4 *>(sp + d0 / 2));
+        c[0] = c[1] = u.x, c[2] = c[3] = u.y, c[4] = c[5] = u.z, c[6] = c[7] = u.w;
+        s[1] = v.x, s[3] = v.y, s[5] = v.z, s[7] = v.w;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) s[i] = -s[i + 1], y[i] = x[i + 1], y[i + 1] = x[i];
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             int partner, angle;
             float sign;
             if (kv_partner(a.rot, d0 + i, partner, angle, sign)) {
-                y[i] = a.rot.interleaved ? x[i ^ 1] : kv_to_float(__ldg(kp + partner), a.bf16);
+                y[i] = kv_to_float(__ldg(kp + partner), kBF16);
                 c[i] = __ldg(cp + angle), s[i] = sign * __ldg(sp + angle);
             } else {
                 y[i] = 0.f, c[i] = 1.f, s[i] = 0.f;
@@ -200,17 +230,16 @@ __device__ __forceinline__ void rotate(const AppendArgs &a, const uint16_t *kp, 
     for (int i = 0; i < 8; ++i) x[i] = y[i];
 }
 
-template <int D>
+template <int D, Layout kLayout, bool kBF16>
 __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const AppendArgs a) {
     constexpr int L = D / 8, kItems = kAppThreads / L;
-    const int64_t item = int64_t(blockIdx.x) * kItems + threadIdx.x / L;
+    const uint32_t item = blockIdx.x * kItems + threadIdx.x / L;
     griddep_launch_next();
     griddep_wait();
     const bool there = item < a.items;  // (the others only take part in the warp's reductions)
-    const int64_t it = there ? item : 0;
+    const uint32_t it = there ? item : 0;
     const int d0 = int(threadIdx.x % L) * 8;
-    const uint32_t bt = uint32_t(it / a.H), h = uint32_t(it - int64_t(bt) * a.H);  // (the host has checked that B T fits)
-    const uint32_t b = bt / uint32_t(a.T);
+    const uint32_t bt = it / uint32_t(a.H), h = it - bt * uint32_t(a.H), b = bt / uint32_t(a.T);
     const int t = int(bt - b * uint32_t(a.T));
     const int64_t capacity = int64_t(a.width) * a.page;
     int before, fresh;
@@ -220,7 +249,7 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const AppendArgs
     const uint16_t *kp = a.k + b * a.k_bs + t * a.k_ts + h * a.k_hs, *vp = a.v + b * a.v_bs + t * a.v_ts + h * a.v_hs;
     int pg = -1, sl = 0;
     if (live) {
-        kv = load_row(kp + d0, a.vec), vv = load_row(vp + d0, a.vec);
+        kv = load_row<kLayout != kAny>(kp + d0), vv = load_row<kLayout != kAny>(vp + d0);
         const int64_t slot = int64_t(before) + t;
         if (slot < capacity) {
             const uint32_t pi = uint32_t(slot) / uint32_t(a.page);
@@ -228,18 +257,24 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const AppendArgs
             pg = __ldg(a.table + int64_t(b) * a.width + pi);
         }
     }
+    if (!__any_sync(0xFFFFFFFFu, live)) {  // tokens past the new ones
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        if (there && a.k_values) *reinterpret_cast<uint4 *>(a.k_values + int64_t(item) * D + d0) = none;
+        if (there && a.v_values) *reinterpret_cast<uint4 *>(a.v_values + int64_t(item) * D + d0) = none;
+        return;
+    }
     float x[8], lo[8];
     uint32_t km, vm, kc, vc;
-    widen(kv, a.bf16, x);
+    widen<kBF16>(kv, x);
     if (a.rot.cos) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) lo[i] = 0.f;
-        if (live && d0 < 2 * a.rot.pairs) rotate(a, kp, d0, kv_rotation_row(a.rot, bt, before + t), x, lo);
+        if (live && d0 < 2 * a.rot.pairs) rotate<kLayout, kBF16>(a, kp, d0, kv_rotation_row(a.rot, bt, before + t), x, lo);
         kc = quantise<L, true>(x, lo, km);
     } else {
         kc = quantise<L, false>(x, x, km);
     }
-    widen(vv, a.bf16, x);
+    widen<kBF16>(vv, x);
     vc = quantise<L, false>(x, x, vm);
     if (!there) return;
     if (live && pg >= 0 && pg < a.num_pages && SV_IN(kv_value_byte(D, sl, d0 + 7), a.page * D / 2)) {
@@ -253,8 +288,18 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const AppendArgs
             *reinterpret_cast<uint32_t *>(base + kv_value_scale_byte(a.page, D, sl)) = vm;
         }
     }
-    if (a.k_values) store_values(a.k_values + item * D + d0, kc, km, live, a.bf16);
-    if (a.v_values) store_values(a.v_values + item * D + d0, vc, vm, live, a.bf16);
+    if (a.k_values) store_values<kBF16>(a.k_values + int64_t(item) * D + d0, kc, km, live);
+    if (a.v_values) store_values<kBF16>(a.v_values + int64_t(item) * D + d0, vc, vm, live);
+}
+
+template <int D>
+cudaError_t launch_append(const AppendArgs &a, Layout layout, bool bf16, unsigned blocks, cudaStream_t s) {
+    auto go = [&](auto kernel) { return launch_after(kernel, blocks, unsigned(kAppThreads), 0, s, a); };
+    switch (layout) {
+    case kHalves: return bf16 ? go(kv_append_kernel<D, kHalves, true>) : go(kv_append_kernel<D, kHalves, false>);
+    case kNeighbours: return bf16 ? go(kv_append_kernel<D, kNeighbours, true>) : go(kv_append_kernel<D, kNeighbours, false>);
+    default: return bf16 ? go(kv_append_kernel<D, kAny, true>) : go(kv_append_kernel<D, kAny, false>);
+    }
 }
 
 }  // namespace
@@ -293,10 +338,8 @@ sv_status spec_kv_append(const void *k, int64_t k_batch_stride, int64_t k_token_
     if (cos && (table_len < 1 || pairs < 1 || pairs > head_dim / 2)) return SV_ERR_INVALID_ARG;
     if (B == 0 || T == 0) return SV_OK;
     if (!k || !v || !start || (table_width > 0 && !page_table) || (num_pages > 0 && !cache)) return SV_ERR_INVALID_ARG;
-    if (int64_t(T) * kv_heads > 0x7FFFFFFF) return SV_ERR_INVALID_ARG;  // (so that the next product fits 64 bits)
-    if (int64_t(B) * T > 0x7FFFFFFF) return SV_ERR_INVALID_ARG;
+    if (int64_t(T) * kv_heads > 0x7FFFFFFF || int64_t(T) * kv_heads * B > 0x7FFFFFFF) return SV_ERR_INVALID_ARG;
     const int64_t items = int64_t(B) * T * kv_heads, per = sv::kAppThreads / (head_dim / 8);
-    if ((items + per - 1) / per > 0x7FFFFFFF) return SV_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(cache) % 16 || reinterpret_cast<uintptr_t>(k) % 2 || reinterpret_cast<uintptr_t>(v) % 2 ||
         reinterpret_cast<uintptr_t>(k_values) % 16 || reinterpret_cast<uintptr_t>(v_values) % 16)
         return SV_ERR_INVALID_ARG;
@@ -305,10 +348,11 @@ sv_status spec_kv_append(const void *k, int64_t k_batch_stride, int64_t k_token_
     a.k = static_cast<const uint16_t *>(k), a.v = static_cast<const uint16_t *>(v);
     a.k_bs = k_batch_stride, a.k_ts = k_token_stride, a.k_hs = k_head_stride;
     a.v_bs = v_batch_stride, a.v_ts = v_token_stride, a.v_hs = v_head_stride;
-    a.bf16 = dtype == SV_KV_BF16;
-    a.vec = all % 8 == 0 && (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 16 == 0;
-    a.rot_vec = pairs % 4 == 0 && (reinterpret_cast<uintptr_t>(cos) | reinterpret_cast<uintptr_t>(sin)) % 16 == 0;
-    a.items = items, a.T = T, a.H = kv_heads;
+    const bool bf16 = dtype == SV_KV_BF16;
+    const bool grid = all % 8 == 0 && (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 16 == 0 &&
+                      (!cos || (pairs % 4 == 0 && (reinterpret_cast<uintptr_t>(cos) | reinterpret_cast<uintptr_t>(sin)) % 16 == 0));
+    const sv::Layout layout = !grid ? sv::kAny : cos && interleaved ? sv::kNeighbours : cos && pairs % 8 ? sv::kAny : sv::kHalves;
+    a.items = uint32_t(items), a.T = T, a.H = kv_heads;
     a.cache = static_cast<uint8_t *>(cache), a.num_pages = num_pages, a.page = page_size, a.width = table_width;
     a.table = page_table, a.start = start, a.new_lens = new_lens;
     a.rot = sv::Rotation{cos, sin, table_len, cos ? pairs : 0, interleaved != 0, positions};
@@ -317,9 +361,9 @@ sv_status spec_kv_append(const void *k, int64_t k_batch_stride, int64_t k_token_
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     switch (head_dim) {
-    case 64: e = sv::launch_after(sv::kv_append_kernel<64>, blocks, sv::kAppThreads, 0, s, a); break;
-    case 128: e = sv::launch_after(sv::kv_append_kernel<128>, blocks, sv::kAppThreads, 0, s, a); break;
-    default: e = sv::launch_after(sv::kv_append_kernel<256>, blocks, sv::kAppThreads, 0, s, a); break;
+    case 64: e = sv::launch_append<64>(a, layout, bf16, blocks, s); break;
+    case 128: e = sv::launch_append<128>(a, layout, bf16, blocks, s); break;
+    default: e = sv::launch_append<256>(a, layout, bf16, blocks, s); break;
     }
     return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
