@@ -20,9 +20,15 @@
 // is unpacked once (or twice) per row tile and the accumulators need no joining.  Both products have
 // the cache as the 16-row operand (tokens x dimensions, dimensions x tokens) and the queries or
 // weights as the 8-column one, so that a single token's few heads are padded to 8 rows, not 16.  A
-// unit's scores are computed before the previous unit's output product, which leaves one barrier per
-// unit and independent work on both sides of it.  The running maximum moves only when a score passes
-// it by 2^8 (the weights fit fp16 either way).
+// unit's scores are computed two units ahead of its product, which leaves one barrier per unit and
+// straight-line code between two of them.  The running maximum moves only when a score passes it by 2^8
+// (the weights fit fp16 either way).
+//
+// What bounds it.  The cache is read once per row tile: for few rows a byte of it needs about one instruction
+// slot a lane (unpacking, one HMMA per 16 tokens and 16 dimensions, the scores), and the warps that fit
+// the registers issue 2.4 instructions a clock: 256 single tokens with 8 heads a kv head over 4600 cached ones
+// on average take 0.30 ms, 4.3 TB/s of the cache.  For many rows the HMMA rate (one m16n8k16 in 2 clocks a
+// SM) and the scores' exponentials join in: 64 x 9 drafts with 4 heads a kv head take 0.17 ms, 130 TFLOP/s.
 #pragma once
 
 #include <cstdint>
@@ -39,56 +45,21 @@ constexpr float kLazy = 8.f;            // log2 of how far a weight may pass 1
 constexpr uint64_t kCopyLimitNs = 1000000000ull;
 constexpr int kAttSMs = 152;
 
-#ifndef CAP64
-#define CAP64 32
-#endif
-#ifndef CAP128
-#define CAP128 48
-#endif
-#ifndef NT1
-#define NT1 128
-#endif
-#ifndef OC1
-#define OC1 3
-#endif
-#ifndef MH3
-#define MH3 2
-#endif
-#ifndef NT3
-#define NT3 64
-#endif
-#ifndef OC3
-#define OC3 3
-#endif
-#ifndef OC8
-#define OC8 2
-#endif
-#ifndef NTS
-#define NTS 64
-#endif
-#ifndef OCS
-#define OCS 4
-#endif
-#ifndef STG
-#define STG 4
-#endif
-// 16-row tiles of dimensions per consumer warp.
-__host__ __device__ constexpr int att_mh(int D, int NR) { return D == 64 ? 1 : D == 128 && NR >= 3 ? MH3 : 2; }
-// Tokens per unit.
-__host__ __device__ constexpr int att_tokens(int D, int NR) {
-    return D == 256 ? 128 : D == 128 ? (NR == 1 ? NT1 : NT3) : NTS;
-}
-// Units in the ring: one whose product runs, one whose scores run, and those on their way.
-__host__ __device__ constexpr int att_stages(int D, int NR) { return D == 256 ? 4 : D == 128 && NR == 1 ? 3 : STG; }
+// 16-row tiles of dimensions per consumer warp: 64 dimensions are shared by four warps too.
+__host__ __device__ constexpr int att_mh(int D, int NR) { return D == 64 ? 1 : 2; }
+// Tokens per unit, 16 or 32 a warp: as many as the registers for their scores allow.
+__host__ __device__ constexpr int att_tokens(int D, int NR) { return D == 256 || (D == 128 && NR == 1) ? 128 : 64; }
+// Units in the ring: one whose product runs, one that has its weights, one whose scores run, one on its way.
+__host__ __device__ constexpr int att_stages(int D, int NR) { return 4; }
 // CTAs per SM, by registers and shared memory.
-__host__ __device__ constexpr int att_occupancy(int D, int NR) {
-    return D == 256 ? 1 : D == 128 ? (NR == 1 ? OC1 : NR <= 5 ? OC3 : OC8) : (NR <= 2 ? OCS : OCS - 1);
-}
-// Tiles of 8 NR rows: as few as there have to be and no larger than they need be.
+__host__ __device__ constexpr int att_occupancy(int D, int NR) { return D == 256 ? 1 : D == 128 ? (NR <= 5 ? 3 : 2) : (NR <= 2 ? 4 : 3); }
+// Tiles of 8 NR rows: as few as there have to be and no larger than they need be.  At most 48 rows, for more spill
+// (64 rows of 128 dimensions do, by 250 bytes a thread); 32 of 64 dimensions, where 64 x 64 tree nodes with 4 query heads a
+// kv head take 253 us in tiles of 32 rows, 267 in tiles of 64 and 276 in tiles of 16.
+constexpr int att_cap(int D) { return D == 64 ? 32 : 48; }
 inline int att_nr(int64_t rows, int D) {
-    const int64_t cap = D == 64 ? CAP64 : CAP128, tiles = (rows + cap - 1) / cap;
-    const int nr = int(((rows + tiles - 1) / tiles + 7) / 8);
-    return nr;
+    const int64_t tiles = (rows + att_cap(D) - 1) / att_cap(D);
+    return int(((rows + tiles - 1) / tiles + 7) / 8);
 }
 
 struct AttArgs {
@@ -705,8 +676,9 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
         }
         return need;
     };
-    // Some row's maximum moves (the first unit's always does), or the values' exponent.
-    auto update = [&]() {
+    // Some row's maximum moves (the first unit's always does), or the values' exponent.  The weights of the unit before,
+    // in buffer buf (-1: none), move along.
+    auto update = [&](int buf) {
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < NG; ++i) top = fmaxf(top, fmaxf(vs[i][0], vs[i][1]));
@@ -749,6 +721,15 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
                 acc[h][n][0] *= al.x * kfac, acc[h][n][1] *= al.y * kfac;
                 acc[h][n][2] *= al.x * kfac, acc[h][n][3] *= al.y * kfac;
             }
+        }
+        if (buf >= 0) {
+            for (int i = tid; i < NT * NR * 4; i += C) {
+                const int tok = i / (NR * 4), r = i % (NR * 4) * 2;
+                __half2 *w = reinterpret_cast<__half2 *>(&sh.p[buf][tok * Sh::kPStride + r]);
+                const float2 v = __half22float2(*w);
+                *w = __floats2half2_rn(v.x * sh.alpha[r] * kfac, v.y * sh.alpha[r + 1] * kfac);
+            }
+            consumers_sync<C>();
         }
     };
     // Weights: p for the sums (this warp's tokens), p s' for the product, rounded to fp16.
@@ -846,27 +827,51 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
         const int seg_lo = ubegin + it - seg.tile;
         const bool whole = it >= seg.tile && it + seg.tiles - seg.tile <= units;
 
+        // Three units are under way: one's product, the next one's weights, and the scores of the one after.  One
+        // barrier per unit, and between two of them straight-line code without a dependence from part to part.
+        auto advance = [&]() {
+            if (++stage == kStages) stage = 0, phase ^= 1;
+        };
+        auto nothing = [&]() {  // scores of no token
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                vs[i][0] = vs[i][1] = vz[i][0] = vz[i][1] = 0.f;
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) s[i][n][k] = -INFINITY;
+            }
+        };
+        int here = stage;  // of the unit whose product is next; `stage` runs ahead
         if (it == 0) wait_unit(stage, phase);
         bool need = score(stage);
-        if (consumers_or<C>(need)) update();
+        advance();
+        if (consumers_or<C>(need)) update(-1);
         weigh(0);
+        need = false;
+        if (it + 1 < last) {
+            wait_unit(stage, phase);
+            need = score(stage);
+            advance();
+        } else {
+            nothing();
+        }
         for (int buf = 0; it < last; ++it, buf ^= 1) {
-            const int here = stage;
-            if (++stage == kStages) stage = 0, phase ^= 1;
-            const bool more = it + 1 < last;
+            if (consumers_or<C>(need)) update(buf);  // and this unit's weights are in place
+            const bool more = it + 2 < last;
+            if (more) wait_unit(stage, phase);
+            product(here, buf);
+            weigh(buf ^ 1);
             need = false;
             if (more) {
-                wait_unit(stage, phase);
                 need = score(stage);
+                advance();
+            } else {
+                nothing();
             }
-            need = consumers_or<C>(need);  // and this unit's weights are in place
-            product(here, buf);
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.empty[here]));
-            if (more) {
-                if (need) update();
-                weigh(buf ^ 1);
-            }
+            if (++here == kStages) here = 0;
         }
 
         // the rows' sums over lanes and warps
@@ -924,15 +929,16 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
 
 // Joins a segment that several CTAs share: out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c.
 // Block (c, y) acts if CTA c's share begins inside a segment whose previous owner held its start;
-// y takes four of the segment's rows.
-constexpr int kJoinThreads = 128, kJoinRows = 4;
+// y takes four of the segment's rows, a warp each for their weights.
+constexpr int kJoinThreads = 128, kJoinRows = 4, kJoinParts = 128;
 
 template <int D, int NR>
 __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const AttArgs a, int ncta) {
-    constexpr int R = 8 * NR;
-    __shared__ float weight[kJoinRows][kAttSMs * 8 + 8];
+    constexpr int R = 8 * NR, kAll = kJoinRows * D / 4, kItems = (kAll + kJoinThreads - 1) / kJoinThreads;
+    __shared__ float weight[kJoinRows][kJoinParts];
     __shared__ float inv_s[kJoinRows];
-    griddep_launch_next();
+    // (no griddep_launch_next: the next call's kernel, resident early beside this one's waiting blocks, would not find
+    // all its places; 256 single tokens took 389 us so, and 299 without)
     griddep_wait();
     const int c = int(blockIdx.x) / (R / kJoinRows) + 1;
     const int r0 = int(blockIdx.x % (R / kJoinRows)) * kJoinRows;
@@ -947,49 +953,62 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const A
     // the first non-empty share after the start's owner joins the segment
     if (share_owner(total, begin - 1, ncta) != c0) return;
     if (d.fresh <= 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = r0 + warp;
+    auto wrote = [&](int k) { return share_begin(total, k, ncta) < share_begin(total, k + 1, ncta); };  // an empty share did not
     // c0's part lies in its second slot unless its share begins with the segment
-    auto slot_of = [&](int k) { return int64_t(2) * k + (k == c0 && share_begin(total, c0, ncta) != d.lo ? 1 : 0); };
-    for (int q = warp; q < kJoinRows; q += kJoinThreads / 32) {
-        const int r = r0 + q;
-        float big = -INFINITY;
-        for (int k = c0 + lane; k <= c1; k += 32)
-            if (share_begin(total, k, ncta) < share_begin(total, k + 1, ncta)) big = fmaxf(big, a.ml[slot_of(k) * R + r].x);
-        for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
-        float sum = 0.f;
-        for (int k = c0 + lane; k <= c1; k += 32) {
+    const bool second = share_begin(total, c0, ncta) != d.lo;
+    auto slot_of = [&](int k) { return int64_t(2) * k + (k == c0 && second ? 1 : 0); };
+    float most = -INFINITY, sum = 0.f;
+    for (int k = c0 + lane; k <= c1; k += 32)
+        if (wrote(k)) most = fmaxf(most, a.ml[slot_of(k) * R + r].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+    float4 o[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = c0; k0 <= c1; k0 += kJoinParts) {
+        const int n = min(kJoinParts, c1 + 1 - k0);
+        for (int k = lane; k < n; k += 32) {
             float w = 0.f;
-            if (share_begin(total, k, ncta) < share_begin(total, k + 1, ncta)) {
-                const float2 ml = a.ml[slot_of(k) * R + r];
-                w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2(ml.x - big);
+            if (wrote(k0 + k)) {
+                const float2 ml = a.ml[slot_of(k0 + k) * R + r];
+                // a part that saw no score, or only NaN, weighs 1: its sums are 0, or NaN and to be kept
+                w = ml.x == -INFINITY ? 1.f : ex2(ml.x - most);
                 sum += w * ml.y;
             }
-            if (SV_IN(k - c0, kAttSMs * 8 + 8)) weight[q][k - c0] = w;
+            weight[warp][k] = w;
         }
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if (lane == 0) inv_s[q] = sum == 0.f ? 0.f : 1.f / sum;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < kJoinRows * D / 4; i += kJoinThreads) {
-        const int q = i / (D / 4), d4 = i % (D / 4) * 4, r = r0 + q;
-        const int row = d.rt * R + r, node = row / a.G;
-        if (node >= a.T) continue;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (node < d.fresh) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            const int item = threadIdx.x + i * kJoinThreads, q = item / (D / 4), d4 = item % (D / 4) * 4;
+            if (item >= kAll) continue;
 #pragma unroll 4
-            for (int k = c0; k <= c1; ++k) {
-                const float w = weight[q][k - c0];
-                if (w == 0.f) continue;  // also: parts of empty shares, never written
-                const float4 v = *reinterpret_cast<const float4 *>(a.acc + (slot_of(k) * R + r) * D + d4);
-                o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+            for (int k = 0; k < n; ++k) {
+                const float w = weight[q][k];
+                if (w == 0.f) continue;  // (and nothing was written there, if the share is empty)
+                const float4 v = *reinterpret_cast<const float4 *>(a.acc + (slot_of(k0 + k) * R + r0 + q) * D + d4);
+                o[i].x = fmaf(w, v.x, o[i].x), o[i].y = fmaf(w, v.y, o[i].y), o[i].z = fmaf(w, v.z, o[i].z), o[i].w = fmaf(w, v.w, o[i].w);
             }
-            const float inv = inv_s[q];
-            o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
         }
-        const int64_t head = d.h * a.G + row % a.G;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+    if (lane == 0) inv_s[warp] = sum == 0.f ? 0.f : 1.f / sum;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int item = threadIdx.x + i * kJoinThreads, q = item / (D / 4), d4 = item % (D / 4) * 4;
+        if (item >= kAll) continue;
+        const int row = d.rt * R + r0 + q, node = row / a.G;
+        if (node >= a.T) continue;
+        const float inv = node < d.fresh ? inv_s[q] : 0.f;
+        const bool none = inv == 0.f;
         uint2 w;
-        w.x = uint32_t(kv_from_float(o.x, a.bf16)) | uint32_t(kv_from_float(o.y, a.bf16)) << 16;
-        w.y = uint32_t(kv_from_float(o.z, a.bf16)) | uint32_t(kv_from_float(o.w, a.bf16)) << 16;
+        w.x = uint32_t(kv_from_float(none ? 0.f : o[i].x * inv, a.bf16)) | uint32_t(kv_from_float(none ? 0.f : o[i].y * inv, a.bf16)) << 16;
+        w.y = uint32_t(kv_from_float(none ? 0.f : o[i].z * inv, a.bf16)) | uint32_t(kv_from_float(none ? 0.f : o[i].w * inv, a.bf16)) << 16;
+        const int64_t head = d.h * a.G + row % a.G;
         *reinterpret_cast<uint2 *>(a.out + ((d.b * int64_t(a.T) + node) * a.H * a.G + head) * D + d4) = w;
     }
 }
@@ -1009,6 +1028,12 @@ cudaError_t launch_attention(const AttArgs &a, int grid, cudaStream_t s) {
 template <int D>
 cudaError_t launch_attention_rows(const AttArgs &a, int nr, int grid, cudaStream_t s);
 
+template <int D>
+cudaError_t launch_attention_more(const AttArgs &a, int nr, int grid, cudaStream_t s) {
+    if constexpr (att_cap(D) > 32) return nr == 5 ? launch_attention<D, 5>(a, grid, s) : launch_attention<D, 6>(a, grid, s);
+    return cudaErrorInvalidValue;
+}
+
 #define SV_KV_ATTENTION_INSTANTIATE(D)                                                                    \
     template <>                                                                                          \
     cudaError_t launch_attention_rows<D>(const AttArgs &a, int nr, int grid, cudaStream_t s) {             \
@@ -1017,8 +1042,7 @@ cudaError_t launch_attention_rows(const AttArgs &a, int nr, int grid, cudaStream
         case 2: return launch_attention<D, 2>(a, grid, s);                                               \
         case 3: return launch_attention<D, 3>(a, grid, s);                                               \
         case 4: return launch_attention<D, 4>(a, grid, s);                                               \
-        case 5: return launch_attention<D, 5>(a, grid, s);                                               \
-        default: return launch_attention<D, 6>(a, grid, s);                                              \
+        default: return launch_attention_more<D>(a, nr, grid, s);                                        \
         }                                                                                                \
     }
 
