@@ -23,8 +23,9 @@ OBJ_DIR = os.path.join(ROOT, "_build")
 CHECKS_FLAGS = ["-DSV_CHECKS", "-rdc=true"]
 SOURCES = ["sv_api.cu", "sv_sample.cu", "sv_greedy.cu", "sv_refine.cu", "sv_tree_sample.cu", "sv_tree_refine.cu",
            "sv_lazy.cu", "sv_ngram.cu", "sv_noalloc.cu", "sv_level.cu",
-           "sv_adjust.cu", "sv_kv_append.cu", "sv_kv_attention.cu", "sv_kv_attention_64.cu",
-           "sv_kv_attention_256.cu"]
+           "sv_adjust.cu", "sv_kv_append.cu", "sv_kv_attention.cu",
+           "sv_kv_attention_64.cu", "sv_kv_attention_128.cu", "sv_kv_attention_256.cu",
+           "sv_kv_attention_64_exact.cu", "sv_kv_attention_128_exact.cu", "sv_kv_attention_256_exact.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

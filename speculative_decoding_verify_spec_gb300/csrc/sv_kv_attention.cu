@@ -1,14 +1,21 @@
-// sv_kv_attention.cu -- the C entry of the attention over the 4-bit paged cache: argument checks,
-// workspace layout, and the kernels for 128 dimensions.
+// sv_kv_attention.cu -- the C entry of the attention over the 4-bit paged cache: argument checks and
+// workspace layout.
 #include "sv_kv_attention.cuh"
 
 namespace sv {
 
-SV_KV_ATTENTION_INSTANTIATE(128)
 template <>
-cudaError_t launch_attention_rows<64>(const AttArgs &a, int nr, int grid, cudaStream_t s);
+cudaError_t launch_attention_rows<64, false>(const AttArgs &a, int nr, int grid, cudaStream_t s);
 template <>
-cudaError_t launch_attention_rows<256>(const AttArgs &a, int nr, int grid, cudaStream_t s);
+cudaError_t launch_attention_rows<64, true>(const AttArgs &a, int nr, int grid, cudaStream_t s);
+template <>
+cudaError_t launch_attention_rows<128, false>(const AttArgs &a, int nr, int grid, cudaStream_t s);
+template <>
+cudaError_t launch_attention_rows<128, true>(const AttArgs &a, int nr, int grid, cudaStream_t s);
+template <>
+cudaError_t launch_attention_rows<256, false>(const AttArgs &a, int nr, int grid, cudaStream_t s);
+template <>
+cudaError_t launch_attention_rows<256, true>(const AttArgs &a, int nr, int grid, cudaStream_t s);
 
 namespace {
 
@@ -87,9 +94,15 @@ sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_tok
     a.ml = reinterpret_cast<float2 *>(ws + L.ml);
     a.acc = reinterpret_cast<float *>(ws + L.acc);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = head_dim == 64    ? sv::launch_attention_rows<64>(a, nr, L.grid, s)
-                          : head_dim == 128 ? sv::launch_attention_rows<128>(a, nr, L.grid, s)
-                                            : sv::launch_attention_rows<256>(a, nr, L.grid, s);
+    // rotated fp16 queries are multiplied in two parts
+    const bool exact = cos && dtype == SV_KV_FP16;
+    cudaError_t e;
+    if (head_dim == 64)
+        e = exact ? sv::launch_attention_rows<64, true>(a, nr, L.grid, s) : sv::launch_attention_rows<64, false>(a, nr, L.grid, s);
+    else if (head_dim == 128)
+        e = exact ? sv::launch_attention_rows<128, true>(a, nr, L.grid, s) : sv::launch_attention_rows<128, false>(a, nr, L.grid, s);
+    else
+        e = exact ? sv::launch_attention_rows<256, true>(a, nr, L.grid, s) : sv::launch_attention_rows<256, false>(a, nr, L.grid, s);
     return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 

@@ -55,8 +55,8 @@ __host__ __device__ constexpr int att_stages(int D, int NR) { return 4; }
 __host__ __device__ constexpr int att_occupancy(int D, int NR) { return D == 256 ? 1 : D == 128 ? (NR <= 5 ? 3 : 2) : (NR <= 2 ? 4 : 3); }
 // Tiles of 8 NR rows: as few as there have to be and no larger than they need be.  At most 48 rows, for more spill
 // (64 rows of 128 dimensions do, by 250 bytes a thread); 32 of 64 dimensions, where 64 x 64 tree nodes with 4 query heads a
-// kv head take 253 us in tiles of 32 rows, 267 in tiles of 64 and 276 in tiles of 16.
-constexpr int att_cap(int D) { return D == 64 ? 32 : 48; }
+// kv head take 253 us in tiles of 32 rows, 267 in tiles of 64 and 276 in tiles of 16; 40 of 256, by shared memory.
+constexpr int att_cap(int D) { return D == 64 ? 32 : D == 128 ? 48 : 40; }
 inline int att_nr(int64_t rows, int D) {
     const int64_t tiles = (rows + att_cap(D) - 1) / att_cap(D);
     return int(((rows + tiles - 1) / tiles + 7) / 8);
@@ -309,10 +309,12 @@ __device__ __forceinline__ void load8(const uint16_t *p, bool vec, bool bf16, fl
 }
 
 // The queries of a segment's rows into shared memory: rotated, scaled by a power of two into fp16's
-// range (exact for 16-bit inputs but for values 2^-25 of the row's largest; a rotated value is
-// rounded to 11 bits), columns in the order in which the codes unpack.  Eight dimensions a thread.
-template <int D, int NR>
-__device__ __forceinline__ void load_queries(const AttArgs &a, AttShared<D, NR> &sh, const Unit &un, int tid) {
+// range (exact for 16-bit inputs but for values 2^-25 of the row's largest), columns in the order in which the
+// codes unpack.  A rotated value is rounded to 11 bits: for bf16 outputs that is a tenth of their own
+// rounding; for fp16 ones it would be as large, so that what the rounding took (rest) is multiplied too, in a second
+// product.  Eight dimensions a thread.
+template <int D, int NR, bool kExact>
+__device__ __forceinline__ void load_queries(const AttArgs &a, AttShared<D, NR> &sh, const Unit &un, int tid, bool rest, __half *out) {
     using Sh = AttShared<D, NR>;
     constexpr int R = Sh::R, L = D / 8, P = Sh::kConsumers / L;  // lanes of a row, rows at a time
     const int c = tid % L, d0 = c * 8;
@@ -367,20 +369,21 @@ __device__ __forceinline__ void load_queries(const AttArgs &a, AttShared<D, NR> 
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float v = a.scale < 0.f ? -x[i] : (a.scale == 0.f ? 0.f : x[i]);
-            x[i] = __half2float(__float2half_rn(ldexpf(v, -e2)));
-            sum += x[i];
+            const float y = ldexpf(v, -e2), r = __half2float(__float2half_rn(y));
+            x[i] = rest ? y - r : r;
+            sum += kExact ? y : r;
         }
 #pragma unroll
         for (int o = L / 2; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         if (R % P != 0 && r >= R) continue;
         // dimension 8 w + n of quad's quarter: k-step 2 w + (n % 4) / 2, the odd n scaled by 1 / 16
-        __half *dst = &sh.q[r * Sh::kQStride + 2 * (d0 / (D / 4)) + 2 * (d0 % (D / 4) / 8) * 16];
+        __half *dst = &out[r * Sh::kQStride + 2 * (d0 / (D / 4)) + 2 * (d0 % (D / 4) / 8) * 16];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const float f = n & 1 ? 0.0625f : 1.f;
             *reinterpret_cast<__half2 *>(dst + (n >> 1) * 16 + (n & 1) * 8) = __floats2half2_rn(x[n] * f, x[n + 4] * f);
         }
-        if (c == 0) {
+        if (c == 0 && !rest) {
             const float c2 = a.scale == 0.f ? 1.f : fmaxf(ldexpf(fabsf(a.scale) * 1.4426950408889634f, e2), 1.2e-38f);
             sh.row_y[r / 2][r & 1] = sum, sh.row_y[r / 2][2 + (r & 1)] = -INFINITY;
             sh.row_p[r / 2][r & 1] = c2, sh.row_p[r / 2][2 + (r & 1)] = 0.f;
@@ -389,16 +392,19 @@ __device__ __forceinline__ void load_queries(const AttArgs &a, AttShared<D, NR> 
     }
 }
 
-template <int D, int NR>
+// kExact: queries have a second fp16 part (see load_queries).
+template <int D, int NR, bool kExact>
 __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_attention_kernel(const AttArgs a) {
     using Sh = AttShared<D, NR>;
     constexpr int R = Sh::R, NW = Sh::NW, NT = Sh::NT, TW = NT / NW, NG = TW / 16, kStages = Sh::kStages, KS = D / 16, E = D / 32;
     constexpr int MH = att_mh(D, NR), kThreads = att_threads(D, NR), C = Sh::kConsumers;
-    constexpr bool kQRegs = NR * KS <= 16;  // the queries' fragments stay in registers
+    constexpr bool kQRegs = NR * KS <= 16;  // the queries' fragments stay in registers (as launch_attention knows)
     static_assert(NG >= 1 && TW % 16 == 0 && NT <= 128 && NT % 32 == 0 && NG * NR <= 8, "");
     extern __shared__ __align__(128) unsigned char raw[];
     Sh &sh = *reinterpret_cast<Sh *>(raw);
-    int *parent_s = reinterpret_cast<int *>(raw + sizeof(Sh));
+    // the queries' second part takes the first one's place where that is in registers
+    __half *q_rest = kQRegs ? sh.q : reinterpret_cast<__half *>(raw + sizeof(Sh));
+    int *parent_s = reinterpret_cast<int *>(raw + sizeof(Sh) + (kQRegs || !kExact ? 0 : sizeof(sh.q)));
     const int anc_words = (a.T + 31) / 32;
     uint32_t *anc_s = reinterpret_cast<uint32_t *>(parent_s + (a.parent ? a.T : 0));  // [R][anc_words]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
@@ -587,6 +593,23 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
                 for (int n = 0; n < NR; ++n)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) s[i][n][k] += s2[i][n][k];
+        }
+        if constexpr (kExact) {
+#pragma unroll
+            for (int w = 0; w < E; ++w)
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    uint32_t b[4];
+                    ldmatrix4(b, smem_u32(&q_rest[(n * 8 + (lane & 7)) * Sh::kQStride + w * 32 + (lane >> 3) * 8]));
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) {
+                        const uint32_t x = kw[i][0][w], y = kw[i][1][w];
+                        const uint32_t even[4] = {codes_even(x), codes_even(y), codes_odd(x), codes_odd(y)};
+                        const uint32_t odd[4] = {codes_even(x >> 8), codes_even(y >> 8), codes_odd(x >> 8), codes_odd(y >> 8)};
+                        mma16816(s[i][n], even, b[0], b[1]);
+                        mma16816(s[i][n], odd, b[2], b[3]);
+                    }
+                }
         }
         // y = s_j (q . (code_j - 8)) + (z_j + 8 s_j) sum(q)
         float ks[NG][2], kz[NG][2], top = 0.f;
@@ -792,7 +815,7 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
     for (int it = 0;;) {  // segments
         const int last = min(units, it + seg.tiles - seg.tile);  // past the segment's last unit here
         consumers_sync<C>();
-        load_queries<D, NR>(a, sh, seg, tid);
+        load_queries<D, NR, kExact>(a, sh, seg, tid, false, sh.q);
         if (a.parent)
             for (int r = tid; r < R; r += C) {
                 uint32_t *anc = anc_s + r * anc_words;
@@ -814,6 +837,11 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
                     ldmatrix4(b, smem_u32(&sh.q[(n * 8 + (lane & 7)) * Sh::kQStride + w * 32 + (lane >> 3) * 8]));
                     qf[2 * w][n][0] = b[0], qf[2 * w][n][1] = b[1], qf[2 * w + 1][n][0] = b[2], qf[2 * w + 1][n][1] = b[3];
                 }
+        }
+        if constexpr (kExact) {
+            consumers_sync<C>();
+            load_queries<D, NR, kExact>(a, sh, seg, tid, true, q_rest);
+            consumers_sync<C>();
         }
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
@@ -1013,37 +1041,43 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const A
     }
 }
 
-template <int D, int NR>
+template <int D, int NR, bool kExact>
 cudaError_t launch_attention(const AttArgs &a, int grid, cudaStream_t s) {
-    const size_t smem = sizeof(AttShared<D, NR>) + (a.parent ? size_t(a.T) * 4 + size_t(8 * NR) * ((a.T + 31) / 32) * 4 : 0);
+    constexpr size_t fixed = sizeof(AttShared<D, NR>) + (kExact && NR * (D / 16) > 16 ? sizeof(AttShared<D, NR>::q) : 0);
+    static_assert(fixed + (1 + NR / 4.0) * 4 * SV_MAX_TREE_NODES <= 227 * 1024, "");
+    const size_t smem = fixed + (a.parent ? size_t(a.T) * 4 + size_t(8 * NR) * ((a.T + 31) / 32) * 4 : 0);
     static std::atomic<int> allowed[64];
-    cudaError_t e = allow_shared(kv_attention_kernel<D, NR>, int(smem), allowed);
+    cudaError_t e = allow_shared(kv_attention_kernel<D, NR, kExact>, int(smem), allowed);
     if (e != cudaSuccess) return e;
-    e = launch_after(kv_attention_kernel<D, NR>, unsigned(grid), unsigned(att_threads(D, NR)), smem, s, a);
+    e = launch_after(kv_attention_kernel<D, NR, kExact>, unsigned(grid), unsigned(att_threads(D, NR)), smem, s, a);
     if (e != cudaSuccess) return e;
     return launch_after(kv_attention_join_kernel<D, NR>, unsigned((grid - 1) * (8 * NR / kJoinRows)), unsigned(kJoinThreads), 0, s, a, grid);
 }
 
 // The attention kernels of a head dimension, each instantiated in its own translation unit.
-template <int D>
+template <int D, bool kExact>
 cudaError_t launch_attention_rows(const AttArgs &a, int nr, int grid, cudaStream_t s);
 
-template <int D>
-cudaError_t launch_attention_more(const AttArgs &a, int nr, int grid, cudaStream_t s) {
-    if constexpr (att_cap(D) > 32) return nr == 5 ? launch_attention<D, 5>(a, grid, s) : launch_attention<D, 6>(a, grid, s);
-    return cudaErrorInvalidValue;
+template <int D, bool kExact>
+cudaError_t launch_attention_of(const AttArgs &a, int nr, int grid, cudaStream_t s) {
+    if constexpr (att_cap(D) >= 40) {
+        if (nr == 5) return launch_attention<D, 5, kExact>(a, grid, s);
+    }
+    if constexpr (att_cap(D) >= 48) {
+        if (nr == 6) return launch_attention<D, 6, kExact>(a, grid, s);
+    }
+    switch (nr) {
+    case 1: return launch_attention<D, 1, kExact>(a, grid, s);
+    case 2: return launch_attention<D, 2, kExact>(a, grid, s);
+    case 3: return launch_attention<D, 3, kExact>(a, grid, s);
+    default: return launch_attention<D, 4, kExact>(a, grid, s);
+    }
 }
 
-#define SV_KV_ATTENTION_INSTANTIATE(D)                                                                    \
-    template <>                                                                                          \
-    cudaError_t launch_attention_rows<D>(const AttArgs &a, int nr, int grid, cudaStream_t s) {             \
-        switch (nr) {                                                                                    \
-        case 1: return launch_attention<D, 1>(a, grid, s);                                               \
-        case 2: return launch_attention<D, 2>(a, grid, s);                                               \
-        case 3: return launch_attention<D, 3>(a, grid, s);                                               \
-        case 4: return launch_attention<D, 4>(a, grid, s);                                               \
-        default: return launch_attention_more<D>(a, nr, grid, s);                                        \
-        }                                                                                                \
+#define SV_KV_ATTENTION_INSTANTIATE(D, EXACT)                                                          \
+    template <>                                                                                       \
+    cudaError_t launch_attention_rows<D, EXACT>(const AttArgs &a, int nr, int grid, cudaStream_t s) {   \
+        return launch_attention_of<D, EXACT>(a, nr, grid, s);                                         \
     }
 
 }  // namespace sv

@@ -2,5 +2,5 @@
 #include "sv_kv_attention.cuh"
 
 namespace sv {
-SV_KV_ATTENTION_INSTANTIATE(64)
+SV_KV_ATTENTION_INSTANTIATE(64, false)
 }  // namespace sv

@@ -1,8 +1,8 @@
 """spec_kv_append and spec_kv_attention against their formulas in 64 bits.
 
 The append is exact: every byte of the cache is compared.  The attention's tolerance, from its
-roundings: a rotated query to 11 bits moves a score by at most 2^-11 scale sum|q_d k_d| (a 16-bit query that
-is not rotated is exact), each weight to fp16 by 2^-11 of itself, the output by half a step of its type; fp32 sums
+roundings: a rotated query to 11 bits moves a score by at most 2^-11 scale sum|q_d k_d| (an fp16 one is held
+exactly, and a 16-bit query that is not rotated is exact), each weight to fp16 by 2^-11 of itself, the output by half a step of its type; fp32 sums
 and exponentials stay below 2^-16 of the largest value."""
 import numpy as np
 import pytest
@@ -227,7 +227,7 @@ def check_attention(q, cache, table, start, new, page, parent=None, cos=None, si
             ok = np.isfinite(k) & np.isfinite(v)
             vmax = np.abs(np.where(ok, v, 0)).max()
             kk = np.repeat(np.where(ok, np.abs(k), 0).max(0)[None], T, 0) if n else 0
-            move = 0.0 if cos is None else 2.0**-11 * abs(sc) * (np.abs(qr[b]) * np.repeat(kk, Hq // H, 1)).sum(-1).max()
+            move = 0.0 if cos is None or q.dtype == torch.float16 else 2.0**-11 * abs(sc) * (np.abs(qr[b]) * np.repeat(kk, Hq // H, 1)).sum(-1).max()
             tol = vmax * (2.0**-11 + 2 * move + 2.0**-16) + np.abs(want) * U.half_step(q.dtype)
             assert (np.abs(x - want)[fine] <= tol[fine]).all(), float((np.abs(x - want) - tol)[fine].max())
         else:
@@ -269,6 +269,19 @@ def test_attention_tree(D, H, G, T, page):
     check_attention(q, cache, table, start, new, page, parent, cos, sin, (start[:, None] + depth).to(torch.int32))
     parent[T // 3], parent[T // 2] = T + 5, -9  # malformed: their paths end there
     check_attention(q, cache, table, start, None, page, parent)
+
+
+@pytest.mark.parametrize("D,G,dtype,rope", [(256, 8, "fp16", True), (128, 8, "bf16", True), (64, 1, "fp16", False)])
+def test_attention_largest_tree(D, G, dtype, rope):
+    """1024 nodes: the tree's own tables beside the largest rings in shared memory."""
+    g = torch.Generator().manual_seed(D)
+    T, page, L = 1024, 128, 5
+    start = torch.tensor([L], dtype=torch.int32)
+    parent = torch.tensor([-1] + [int(torch.randint(0, i, (1,), generator=g)) for i in range(1, T)], dtype=torch.int32)
+    cache, table = filled(1, start + T, 1, page, D, 9, g)
+    q = torch.randn((1, T, G, D), generator=g).to(DT[dtype])
+    cos, sin = U.tables(T + L, D // 2) if rope else (None, None)
+    check_attention(q, cache, table, start, None, page, parent, cos, sin)
 
 
 def test_attention_tree_of_a_chain_is_the_chain():
