@@ -1,6 +1,6 @@
 // sv_kv_attention.cu -- the C entry of the attention over the 4-bit paged cache: argument checks and
 // workspace layout.
-#include "sv_kv_attention.cuh"
+#include "sv_kv_wide.cuh"
 
 namespace sv {
 
@@ -17,16 +17,33 @@ cudaError_t launch_attention_rows<256, false>(const AttArgs &a, int nr, int grid
 template <>
 cudaError_t launch_attention_rows<256, true>(const AttArgs &a, int nr, int grid, cudaStream_t s);
 
+template <int D, bool kExact>
+cudaError_t launch_wide_of(const AttArgs &a, int grid, cudaStream_t s);
+template <>
+cudaError_t launch_wide_of<64, false>(const AttArgs &a, int grid, cudaStream_t s);
+template <>
+cudaError_t launch_wide_of<64, true>(const AttArgs &a, int grid, cudaStream_t s);
+template <>
+cudaError_t launch_wide_of<128, false>(const AttArgs &a, int grid, cudaStream_t s);
+
 namespace {
+
+#ifndef WIDE64
+#define WIDE64 65
+#endif
+#ifndef WIDE128
+#define WIDE128 65
+#endif
+bool att_wide(int64_t rows, int D) { return D == 64 ? rows >= WIDE64 : D == 128 && rows >= WIDE128; }
 
 struct AttLayout {
     size_t desc, ml, acc, total;
     int grid;
 };
-AttLayout att_layout(int64_t rows, int D) {
-    const int nr = att_nr(rows, D), R = 8 * nr;
+AttLayout att_layout(int64_t rows, int D, bool wide) {
+    const int nr = att_nr(rows, D), R = wide ? kWideRows : 8 * nr;
     AttLayout L;
-    L.grid = kAttSMs * att_occupancy(D, nr);
+    L.grid = kAttSMs * (wide ? kWideOccupancy : att_occupancy(D, nr));
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     L.desc = 256;
     L.ml = up(L.desc + size_t(L.grid) * sizeof(AttDesc));
@@ -42,7 +59,11 @@ extern "C" {
 
 size_t spec_kv_attention_workspace_size(int B, int T, int heads, int kv_heads, int head_dim) {
     if (B <= 0 || T <= 0 || kv_heads < 1 || heads < kv_heads || heads % kv_heads || !sv::kv_head_dim_ok(head_dim)) return 0;
-    return sv::att_layout(int64_t(T) * (heads / kv_heads), head_dim).total;
+    const int64_t rows = int64_t(T) * (heads / kv_heads);
+    const size_t narrow = sv::att_layout(rows, head_dim, false).total;
+    if (!sv::att_wide(rows, head_dim)) return narrow;
+    const size_t wide = sv::att_layout(rows, head_dim, true).total;  // which one runs depends on more than the sizes
+    return narrow > wide ? narrow : wide;
 }
 
 sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,
@@ -68,12 +89,15 @@ sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_tok
         return SV_ERR_INVALID_ARG;
     const int G = heads / kv_heads;
     const int64_t rows = int64_t(T) * G;
-    const sv::AttLayout L = sv::att_layout(rows, head_dim);
+    // rotated fp16 queries are multiplied in two parts (128 dimensions of them do not fit the wide kernel twice an SM)
+    const bool exact = cos && dtype == SV_KV_FP16, wide = sv::att_wide(rows, head_dim) && !(exact && head_dim == 128);
+    const sv::AttLayout L = sv::att_layout(rows, head_dim, wide);
     if (!workspace || workspace_bytes < L.total || reinterpret_cast<uintptr_t>(workspace) % 16) return SV_ERR_WORKSPACE;
     char *ws = static_cast<char *>(workspace);
-    const int nr = sv::att_nr(rows, head_dim);
-    const int64_t row_tiles = (rows + 8 * nr - 1) / (8 * nr), tokens = int64_t(table_width) * page_size;
-    const int64_t most = row_tiles * (tokens / sv::att_tokens(head_dim, nr) + 1);  // units of a sequence and head
+    const int nr = sv::att_nr(rows, head_dim), R = wide ? sv::kWideRows : 8 * nr;
+    const int unit = wide ? sv::kWideTokens : sv::att_tokens(head_dim, nr);
+    const int64_t row_tiles = (rows + R - 1) / R, tokens = int64_t(table_width) * page_size;
+    const int64_t most = row_tiles * (tokens / unit + 1);  // units of a sequence and head
     if (most > 0x7FFFFFFF / kv_heads || most * kv_heads > 0x7FFFFFFF / B) return SV_ERR_INVALID_ARG;
     sv::AttArgs a{};
     a.q = static_cast<const uint16_t *>(q);
@@ -82,7 +106,7 @@ sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_tok
     a.B = B, a.T = T, a.H = kv_heads, a.G = G;
     a.cache = static_cast<const uint8_t *>(cache), a.num_pages = num_pages, a.page = page_size, a.width = table_width;
     a.granule = 16;
-    while (a.granule < sv::att_tokens(head_dim, nr) && page_size % (2 * a.granule) == 0) a.granule *= 2;
+    while (a.granule < unit && page_size % (2 * a.granule) == 0) a.granule *= 2;
     a.vec = (q_batch_stride | q_token_stride | q_head_stride) % 8 == 0 && reinterpret_cast<uintptr_t>(q) % 16 == 0;
     a.table = page_table, a.start = start, a.new_lens = new_lens, a.parent = parent;
     a.scale = scale;
@@ -94,10 +118,12 @@ sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_tok
     a.ml = reinterpret_cast<float2 *>(ws + L.ml);
     a.acc = reinterpret_cast<float *>(ws + L.acc);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // rotated fp16 queries are multiplied in two parts
-    const bool exact = cos && dtype == SV_KV_FP16;
     cudaError_t e;
-    if (head_dim == 64)
+    if (wide)
+        e = head_dim == 128 ? sv::launch_wide_of<128, false>(a, L.grid, s)
+            : exact         ? sv::launch_wide_of<64, true>(a, L.grid, s)
+                            : sv::launch_wide_of<64, false>(a, L.grid, s);
+    else if (head_dim == 64)
         e = exact ? sv::launch_attention_rows<64, true>(a, nr, L.grid, s) : sv::launch_attention_rows<64, false>(a, nr, L.grid, s);
     else if (head_dim == 128)
         e = exact ? sv::launch_attention_rows<128, true>(a, nr, L.grid, s) : sv::launch_attention_rows<128, false>(a, nr, L.grid, s);

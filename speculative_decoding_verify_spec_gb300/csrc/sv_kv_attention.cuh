@@ -248,6 +248,104 @@ struct AttShared {
     Unit unit[kStages];
 };
 
+// All units, and this CTA's share of them: where it begins and ends, and the cursor at its beginning (every warp for
+// itself).  False: the share is empty.
+template <int NT>
+__device__ __forceinline__ bool find_share(const AttArgs &a, int R, int lane, int cta, int ncta, Cursor<NT> &cur, int &total,
+                                           int &ubegin, int &uend) {
+    total = 0;
+    SeqWork w0{};  // of sequence `lane`
+    for (int b = lane; b < a.B; b += 32) {
+        const SeqWork w = seq_work<NT>(a, b, R);
+        if (b == lane) w0 = w;
+        total += w.units;
+    }
+    total = __reduce_add_sync(0xFFFFFFFFu, total);
+    ubegin = share_begin(total, cta, ncta), uend = share_begin(total, cta + 1, ncta);
+    if (ubegin >= uend) return false;
+    for (int b0 = 0, run = 0;; b0 += 32) {  // (ubegin < total: some sequence holds it)
+        const int b = b0 + lane;
+        if (b0 > 0) w0 = b < a.B ? seq_work<NT>(a, b, R) : SeqWork{};
+        int inc = w0.units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        const int lo = run + inc - w0.units;
+        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, ubegin >= lo && ubegin < run + inc);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            cur.b = b0 + l;
+            cur.base = __shfl_sync(0xFFFFFFFFu, lo, l);
+            int *to = reinterpret_cast<int *>(&cur.w);
+            const int *from = reinterpret_cast<const int *>(&w0);
+#pragma unroll
+            for (int i = 0; i < int(sizeof(SeqWork) / 4); ++i) to[i] = __shfl_sync(0xFFFFFFFFu, from[i], l);
+            break;
+        }
+        run += __shfl_sync(0xFFFFFFFFu, inc, 31);
+        if (b0 + 32 >= a.B) return false;  // never
+    }
+    cur.place(a, ubegin);
+    return true;
+}
+
+// The copying warp: the units of the share into the ring, up to kStages ahead of the consumers.
+template <int D, int NT, int kStages, typename Shared>
+__device__ __forceinline__ void copy_units(const AttArgs &a, Shared &sh, Cursor<NT> &cur, int ubegin, int uend, int R, int lane) {
+    // Lanes take (granule, piece) pairs: keys,
+    // values and their scales; a page that is a unit is one piece.
+    const bool whole = a.page == NT;
+    const int gi = lane >> 2, piece = lane & 3, granules = NT / a.granule;
+    const bool busy = whole ? lane == 0 : gi < granules;
+    const uint32_t bytes = !busy ? 0 : whole ? NT * (D + 8) : piece < 2 ? a.granule * (D / 2) : a.granule * 4;
+    const int to = piece < 2 ? (piece * NT + gi * a.granule) * (D / 2) : NT * D + ((piece - 2) * NT + gi * a.granule) * 4;
+    const int from = piece < 2 ? piece * a.page * (D / 2) : a.page * D + (piece - 2) * a.page * 4, each = piece < 2 ? D / 2 : 4;
+    const uint32_t all_granules = granules == 8 ? 0x11111111u : 0x11111111u & ((1u << (4 * granules)) - 1);
+    const uint32_t all_bytes = __reduce_add_sync(0xFFFFFFFFu, bytes);
+    const int64_t page_bytes = kv_page_bytes(a.page, D), head_step = int64_t(a.H) * page_bytes;
+    int pi = 0, slot = 0, stage = 0, wrap = 0;  // this lane's granule: page of the sequence, slot in it
+    uint32_t phase = 1;
+    bool placed = false;
+    for (int u = ubegin; u < uend; ++u) {
+        if (!placed) {
+            const int tok = cur.tile * NT + gi * a.granule;
+            pi = tok / a.page, slot = tok - pi * a.page;
+            placed = true;
+        }
+        const bool inside = busy && cur.live && cur.tile * NT + gi * a.granule < cur.w.len;
+        const int pg = inside ? __ldg(a.table + int64_t(cur.b) * a.width + pi) : -1;
+        const bool here = pg >= 0 && pg < a.num_pages && SV_IN(slot + a.granule - 1, a.page);
+        const uint32_t got = __ballot_sync(0xFFFFFFFFu, here), have = got & 0x11111111u;
+        const uint32_t sum = have == all_granules ? all_bytes : __reduce_add_sync(0xFFFFFFFFu, here ? bytes : 0u);
+        if (wrap > 0 && !mbar_wait(smem_u32(&sh.empty[stage]), phase)) {
+            atomicExch(a.status, int(SV_ERR_TIMEOUT));
+            return;  // (the consumers' waits give up too)
+        }
+        const uint32_t bar = smem_u32(&sh.full[stage]);
+        if (lane == 0) {
+            int4 *un = reinterpret_cast<int4 *>(&sh.unit[stage]);
+            un[0] = make_int4(cur.b, cur.h, cur.rt, cur.tile);
+            un[1] = make_int4(cur.tiles(), cur.w.before, cur.w.len, cur.live ? cur.w.fresh : 0);
+            un[2] = make_int4(int(have), int((cur.tile + 1) * NT > cur.w.before || have != all_granules), 0, 0);
+            mbar_expect(bar, sum);
+        }
+        __syncwarp();
+        if (here)
+            bulk_load(smem_u32(sh.stage[stage]) + to, a.cache + pg * head_step + cur.h * page_bytes + from + slot * each, bytes, bar);
+        if (++stage == kStages) stage = 0, phase ^= 1, wrap = 1;
+        if (cur.tile + 1 < cur.tiles()) {
+            ++cur.tile;
+            slot += NT;
+            while (slot >= a.page) slot -= a.page, ++pi;
+        } else if (u + 1 < uend) {
+            cur.next(a, R, u + 1);
+            placed = false;
+        }
+    }
+}
+
 // Two fp32 numbers in a register pair, worked on by one instruction.
 using Two = unsigned long long;
 __device__ __forceinline__ Two two(float x, float y) {
@@ -308,6 +406,40 @@ __device__ __forceinline__ void load8(const uint16_t *p, bool vec, bool bf16, fl
     }
 }
 
+// Eight dimensions from d0 on of a query row, rotated.
+__device__ __forceinline__ void query_chunk(const AttArgs &a, const Unit &un, int node, int head, int d0, float (&x)[8]) {
+    const uint16_t *qp = a.q + un.b * a.q_bs + node * a.q_ts + head * a.q_hs;
+    load8(qp + d0, a.vec, a.bf16, x);
+    if (a.rot.cos && d0 < 2 * a.rot.pairs) {
+        const int64_t arow = kv_rotation_row(a.rot, int64_t(un.b) * a.T + node, un.before + node);
+        const float *cp = a.rot.cos + arow, *sp = a.rot.sin + arow;
+        float y[8], cs[8], sn[8];
+        if (!a.rot.interleaved && a.rot.pairs % 8 == 0) {  // the chunk lies within one half
+            const int e0 = d0 < a.rot.pairs ? d0 : d0 - a.rot.pairs;
+            load8(qp + (d0 < a.rot.pairs ? d0 + a.rot.pairs : e0), a.vec, a.bf16, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                cs[i] = __ldg(cp + e0 + i);
+                sn[i] = d0 < a.rot.pairs ? -__ldg(sp + e0 + i) : __ldg(sp + e0 + i);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                int partner, angle;
+                float sign;
+                if (kv_partner(a.rot, d0 + i, partner, angle, sign)) {
+                    y[i] = kv_to_float(__ldg(qp + partner), a.bf16);
+                    cs[i] = __ldg(cp + angle), sn[i] = sign * __ldg(sp + angle);
+                } else {
+                    y[i] = 0.f, cs[i] = 1.f, sn[i] = 0.f;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], cs[i], y[i] * sn[i]);
+    }
+}
+
 // The queries of a segment's rows into shared memory: rotated, scaled by a power of two into fp16's
 // range (exact for 16-bit inputs but for values 2^-25 of the row's largest), columns in the order in which the
 // codes unpack.  A rotated value is rounded to 11 bits: for bf16 outputs that is a tenth of their own
@@ -327,38 +459,7 @@ __device__ __forceinline__ void load_queries(const AttArgs &a, AttShared<D, NR> 
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = 0.f;
-        if (on) {
-            const uint16_t *qp = a.q + un.b * a.q_bs + node * a.q_ts + head * a.q_hs;
-            load8(qp + d0, a.vec, a.bf16, x);
-            if (a.rot.cos && d0 < 2 * a.rot.pairs) {
-                const int64_t arow = kv_rotation_row(a.rot, int64_t(un.b) * a.T + node, un.before + node);
-                const float *cp = a.rot.cos + arow, *sp = a.rot.sin + arow;
-                float y[8], cs[8], sn[8];
-                if (!a.rot.interleaved && a.rot.pairs % 8 == 0) {  // the chunk lies within one half
-                    const int e0 = d0 < a.rot.pairs ? d0 : d0 - a.rot.pairs;
-                    load8(qp + (d0 < a.rot.pairs ? d0 + a.rot.pairs : e0), a.vec, a.bf16, y);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        cs[i] = __ldg(cp + e0 + i);
-                        sn[i] = d0 < a.rot.pairs ? -__ldg(sp + e0 + i) : __ldg(sp + e0 + i);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        int partner, angle;
-                        float sign;
-                        if (kv_partner(a.rot, d0 + i, partner, angle, sign)) {
-                            y[i] = kv_to_float(__ldg(qp + partner), a.bf16);
-                            cs[i] = __ldg(cp + angle), sn[i] = sign * __ldg(sp + angle);
-                        } else {
-                            y[i] = 0.f, cs[i] = 1.f, sn[i] = 0.f;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], cs[i], y[i] * sn[i]);
-            }
-        }
+        if (on) query_chunk(a, un, node, head, d0, x);
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(fabsf(x[i])));
@@ -420,96 +521,13 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
     if (a.parent)
         for (int i = tid; i < a.T; i += kThreads) parent_s[i] = a.parent[i];
 
-    // all units, then the sequence where this CTA's share begins (every warp for itself)
-    int total = 0;
-    SeqWork w0{};  // of sequence `lane`
-    for (int b = lane; b < a.B; b += 32) {
-        const SeqWork w = seq_work<NT>(a, b, R);
-        if (b == lane) w0 = w;
-        total += w.units;
-    }
-    total = __reduce_add_sync(0xFFFFFFFFu, total);
-    const int ubegin = share_begin(total, cta, ncta), uend = share_begin(total, cta + 1, ncta);
-    if (ubegin >= uend) return;
     Cursor<NT> cur;
-    for (int b0 = 0, run = 0;; b0 += 32) {  // (ubegin < total: some sequence holds it)
-        const int b = b0 + lane;
-        if (b0 > 0) w0 = b < a.B ? seq_work<NT>(a, b, R) : SeqWork{};
-        int inc = w0.units;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        const int lo = run + inc - w0.units;
-        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, ubegin >= lo && ubegin < run + inc);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            cur.b = b0 + l;
-            cur.base = __shfl_sync(0xFFFFFFFFu, lo, l);
-            int *to = reinterpret_cast<int *>(&cur.w);
-            const int *from = reinterpret_cast<const int *>(&w0);
-#pragma unroll
-            for (int i = 0; i < int(sizeof(SeqWork) / 4); ++i) to[i] = __shfl_sync(0xFFFFFFFFu, from[i], l);
-            break;
-        }
-        run += __shfl_sync(0xFFFFFFFFu, inc, 31);
-        if (b0 + 32 >= a.B) return;  // never
-    }
-    cur.place(a, ubegin);
+    int total, ubegin, uend;
+    if (!find_share<NT>(a, R, lane, cta, ncta, cur, total, ubegin, uend)) return;
     __syncthreads();
 
     if (warp == NW) {
-        // the copies, up to kStages units ahead of the consumers.  Lanes take (granule, piece) pairs: keys,
-        // values and their scales; a page that is a unit is one piece.
-        const bool whole = a.page == NT;
-        const int gi = lane >> 2, piece = lane & 3, granules = NT / a.granule;
-        const bool busy = whole ? lane == 0 : gi < granules;
-        const uint32_t bytes = !busy ? 0 : whole ? NT * (D + 8) : piece < 2 ? a.granule * (D / 2) : a.granule * 4;
-        const int to = piece < 2 ? (piece * NT + gi * a.granule) * (D / 2) : NT * D + ((piece - 2) * NT + gi * a.granule) * 4;
-        const int from = piece < 2 ? piece * a.page * (D / 2) : a.page * D + (piece - 2) * a.page * 4, each = piece < 2 ? D / 2 : 4;
-        const uint32_t all_granules = granules == 8 ? 0x11111111u : 0x11111111u & ((1u << (4 * granules)) - 1);
-        const uint32_t all_bytes = __reduce_add_sync(0xFFFFFFFFu, bytes);
-        const int64_t page_bytes = kv_page_bytes(a.page, D), head_step = int64_t(a.H) * page_bytes;
-        int pi = 0, slot = 0, stage = 0, wrap = 0;  // this lane's granule: page of the sequence, slot in it
-        uint32_t phase = 1;
-        bool placed = false;
-        for (int u = ubegin; u < uend; ++u) {
-            if (!placed) {
-                const int tok = cur.tile * NT + gi * a.granule;
-                pi = tok / a.page, slot = tok - pi * a.page;
-                placed = true;
-            }
-            const bool inside = busy && cur.live && cur.tile * NT + gi * a.granule < cur.w.len;
-            const int pg = inside ? __ldg(a.table + int64_t(cur.b) * a.width + pi) : -1;
-            const bool here = pg >= 0 && pg < a.num_pages && SV_IN(slot + a.granule - 1, a.page);
-            const uint32_t got = __ballot_sync(0xFFFFFFFFu, here), have = got & 0x11111111u;
-            const uint32_t sum = have == all_granules ? all_bytes : __reduce_add_sync(0xFFFFFFFFu, here ? bytes : 0u);
-            if (wrap > 0 && !mbar_wait(smem_u32(&sh.empty[stage]), phase)) {
-                atomicExch(a.status, int(SV_ERR_TIMEOUT));
-                return;  // (the consumers' waits give up too)
-            }
-            const uint32_t bar = smem_u32(&sh.full[stage]);
-            if (lane == 0) {
-                int4 *un = reinterpret_cast<int4 *>(&sh.unit[stage]);
-                un[0] = make_int4(cur.b, cur.h, cur.rt, cur.tile);
-                un[1] = make_int4(cur.tiles(), cur.w.before, cur.w.len, cur.live ? cur.w.fresh : 0);
-                un[2] = make_int4(int(have), int((cur.tile + 1) * NT > cur.w.before || have != all_granules), 0, 0);
-                mbar_expect(bar, sum);
-            }
-            __syncwarp();
-            if (here)
-                bulk_load(smem_u32(sh.stage[stage]) + to, a.cache + pg * head_step + cur.h * page_bytes + from + slot * each, bytes, bar);
-            if (++stage == kStages) stage = 0, phase ^= 1, wrap = 1;
-            if (cur.tile + 1 < cur.tiles()) {
-                ++cur.tile;
-                slot += NT;
-                while (slot >= a.page) slot -= a.page, ++pi;
-            } else if (u + 1 < uend) {
-                cur.next(a, R, u + 1);
-                placed = false;
-            }
-        }
+        copy_units<D, NT, kStages>(a, sh, cur, ubegin, uend, R, lane);
         return;
     }
 
