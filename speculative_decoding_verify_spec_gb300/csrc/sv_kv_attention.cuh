@@ -406,6 +406,10 @@ __device__ __forceinline__ void load8(const uint16_t *p, bool vec, bool bf16, fl
     }
 }
 
+// The power of two that is taken out of a row whose largest number has the bits `top`: that number becomes 2^10 .. 2^11
+// (less for rows below 2^-100).
+__device__ __forceinline__ int query_exponent(uint32_t top) { return top == 0 ? 0 : max(int(top >> 23) - 127 - 10, -110); }
+
 // Eight dimensions from d0 on of a query row, rotated.
 __device__ __forceinline__ void query_chunk(const AttArgs &a, const Unit &un, int node, int head, int d0, float (&x)[8]) {
     const uint16_t *qp = a.q + un.b * a.q_bs + node * a.q_ts + head * a.q_hs;
@@ -454,7 +458,7 @@ __device__ __forceinline__ void load_queries(const AttArgs &a, AttShared<D, NR> 
     for (int r0 = 0; r0 < R; r0 += P) {
         const int r = r0 + tid / L;
         const int row = un.rt * R + r;
-        const int node = row / a.G, head = un.h * a.G + row % a.G;
+        const int node = row / a.G, head = un.h * a.G + row - node * a.G;
         const bool on = r < R && node < un.fresh;
         float x[8];
 #pragma unroll
@@ -465,12 +469,13 @@ __device__ __forceinline__ void load_queries(const AttArgs &a, AttShared<D, NR> 
         for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(fabsf(x[i])));
 #pragma unroll
         for (int o = L / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        const int e2 = top == 0 ? 0 : int(top >> 23) - 127 - 10;  // the largest becomes 2^10 .. 2^11
+        const int e2 = query_exponent(top);
+        const float shrink = power2(-e2);
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float v = a.scale < 0.f ? -x[i] : (a.scale == 0.f ? 0.f : x[i]);
-            const float y = ldexpf(v, -e2), r = __half2float(__float2half_rn(y));
+            const float y = v * shrink, r = __half2float(__float2half_rn(y));
             x[i] = rest ? y - r : r;
             sum += kExact ? y : r;
         }
@@ -485,7 +490,7 @@ __device__ __forceinline__ void load_queries(const AttArgs &a, AttShared<D, NR> 
             *reinterpret_cast<__half2 *>(dst + (n >> 1) * 16 + (n & 1) * 8) = __floats2half2_rn(x[n] * f, x[n + 4] * f);
         }
         if (c == 0 && !rest) {
-            const float c2 = a.scale == 0.f ? 1.f : fmaxf(ldexpf(fabsf(a.scale) * 1.4426950408889634f, e2), 1.2e-38f);
+            const float c2 = a.scale == 0.f ? 1.f : fmaxf(fabsf(a.scale) * 1.4426950408889634f * power2(e2), 1.2e-38f);
             sh.row_y[r / 2][r & 1] = sum, sh.row_y[r / 2][2 + (r & 1)] = -INFINITY;
             sh.row_p[r / 2][r & 1] = c2, sh.row_p[r / 2][2 + (r & 1)] = 0.f;
             sh.row_node[r] = on ? node : -1;

@@ -93,7 +93,7 @@ __device__ __forceinline__ void wide_queries(const AttArgs &a, WideShared<D, kEx
 #pragma unroll 2
     for (int r0 = 0; r0 < kWideRows; r0 += P) {
         const int r = r0 + tid / L, row = un.rt * kWideRows + r;
-        const int node = row / a.G, head = un.h * a.G + row % a.G;
+        const int node = row / a.G, head = un.h * a.G + row - node * a.G;
         const bool on = node < un.fresh;
         float x[8];
 #pragma unroll
@@ -104,12 +104,13 @@ __device__ __forceinline__ void wide_queries(const AttArgs &a, WideShared<D, kEx
         for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(fabsf(x[i])));
 #pragma unroll
         for (int o = L / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        const int e2 = top == 0 ? 0 : int(top >> 23) - 127 - 10;  // the largest becomes 2^10 .. 2^11
+        const int e2 = query_exponent(top);
+        const float shrink = power2(-e2);
         float sum = 0.f, rest[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float v = a.scale < 0.f ? -x[i] : (a.scale == 0.f ? 0.f : x[i]);
-            const float y = ldexpf(v, -e2), f = __half2float(__float2half_rn(y));
+            const float y = v * shrink, f = __half2float(__float2half_rn(y));
             x[i] = f, rest[i] = y - f;
             sum += kExact ? y : f;
         }
@@ -130,7 +131,7 @@ __device__ __forceinline__ void wide_queries(const AttArgs &a, WideShared<D, kEx
         *reinterpret_cast<uint4 *>(sh.q[c / 8] + at) = chunk(x);
         if constexpr (kExact) *reinterpret_cast<uint4 *>(sh.q[D / 64 + c / 8] + at) = chunk(rest);
         if (c == 0) {
-            sh.row_c[r] = a.scale == 0.f ? 1.f : fmaxf(ldexpf(fabsf(a.scale) * 1.4426950408889634f, e2), 1.2e-38f);
+            sh.row_c[r] = a.scale == 0.f ? 1.f : fmaxf(fabsf(a.scale) * 1.4426950408889634f * power2(e2), 1.2e-38f);
             sh.row_q[r] = sum;
             sh.row_node[r] = on ? node : -1;
         }
@@ -337,8 +338,10 @@ __global__ void __launch_bounds__(kWideThreads, kWideOccupancy) kv_wide_kernel(c
                 }
                 need |= !(top < power2(vexp));
                 Two dl, dz;
+                bool weighed = it > first;  // a segment's first unit moves the maximum: no use in weights before
+                need |= !weighed;
                 while (true) {
-                    if (warp_on) {
+                    if (warp_on && weighed) {
                         const float down = power2(-vexp);
                         const Two minus = two(-m, -m), dd = two(down, down);
                         dl = 0, dz = 0;
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(kWideThreads, kWideOccupancy) kv_wide_kernel(c
                         }
                     }
                     vexp = vnew;
-                    need = false;
+                    need = false, weighed = true;
                 }
                 if (warp_on) l = add2(l, dl), z = add2(z, dz);
                 if (tid == 0) {
