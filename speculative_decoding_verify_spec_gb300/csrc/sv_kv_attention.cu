@@ -28,13 +28,11 @@ cudaError_t launch_wide_of<128, false>(const AttArgs &a, int grid, cudaStream_t 
 
 namespace {
 
-#ifndef WIDE64
-#define WIDE64 65
-#endif
-#ifndef WIDE128
-#define WIDE128 65
-#endif
-bool att_wide(int64_t rows, int D) { return D == 64 ? rows >= WIDE64 : D == 128 && rows >= WIDE128; }
+// More rows than this a kv head go to the kernel for many rows.  48 sequences of 3000 cached tokens at most, us: 128 dimensions
+// and 56 rows 154 in tiles of 32 and 170 in one of 128; 72 rows 192 and 173; 128 rows 407 and 184; 64 dimensions and
+// 72 rows 75 and 81; 96 rows 92 and 79; 128 rows 119 and 81.
+constexpr int kNarrowRows = 64;
+bool att_wide(int64_t rows, int D) { return D <= 128 && rows > kNarrowRows; }
 
 struct AttLayout {
     size_t desc, ml, acc, total;

@@ -62,6 +62,16 @@ __device__ __forceinline__ void wide_commit(uint64_t *bar) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_operands() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// 16 columns of this warp's 32 rows (a lane a row).
+__device__ __forceinline__ void tmem_load16(float (&x)[16], uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]),
+          "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
+        : "r"(addr)
+        : "memory");
+}
 // 32 columns of this warp's 32 rows (a lane a row).
 __device__ __forceinline__ void tmem_load32(float (&x)[32], uint32_t addr) {
     asm volatile(
@@ -313,55 +323,55 @@ __global__ void __launch_bounds__(kWideThreads, kWideOccupancy) kv_wide_kernel(c
                 if (lane == 0) mbar_arrive(smem_u32(&sh.empty[stage]));  // (nothing more of the stage, or `un`, is read)
                 wait(&sh.scores, turn);
                 fence_after();
-                float s[32];
-                bool need = false;
                 const float top = __uint_as_float(max(sh.redv[0], sh.redv[1]));
-                if (warp_on) {
-                    tmem_load32(s, tmem_s + half * 32);
-                    float y = -INFINITY;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float4 k = *reinterpret_cast<const float4 *>(sh.key_of[half * 16 + j]);
-                        const float2 v = split(fma2(two(s[2 * j], s[2 * j + 1]), two(k.x, k.y), mul2(qs, two(k.z, k.w))));
-                        s[2 * j] = v.x, s[2 * j + 1] = v.y;
-                    }
-                    if (masked) {
-                        __syncwarp();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (!(see >> j & 1u)) s[j] = -INFINITY;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) y = fmaxf(y, s[j]);
-                    need = y > thr;
-                    sh.red[0][half][r] = y;
-                }
-                need |= !(top < power2(vexp));
-                Two dl, dz;
                 bool weighed = it > first;  // a segment's first unit moves the maximum: no use in weights before
-                need |= !weighed;
+                bool need = !weighed || !(top < power2(vexp)), again = false;
+                Two dl = 0, dz = 0;
                 while (true) {
-                    if (warp_on && weighed) {
-                        const float down = power2(-vexp);
-                        const Two minus = two(-m, -m), dd = two(down, down);
+                    if (warp_on) {
+                        const Two minus = two(-m, -m), dd = two(power2(-vexp), power2(-vexp));
+                        float most = -INFINITY;
                         dl = 0, dz = 0;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t w[4];
+                        for (int c = 0; c < 2; ++c) {  // 16 tokens at a time
+                            float s[16];
+                            tmem_load16(s, tmem_s + half * 32 + 16 * c);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int j = 4 * c + i;
-                                const float4 v = *reinterpret_cast<const float4 *>(sh.value_of[half * 16 + j]);
-                                const float2 x = split(fma2(two(s[2 * j], s[2 * j + 1]), cc, minus));
-                                const Two p = two(ex2(x.x), ex2(x.y));
-                                dl = add2(dl, p);
-                                dz = fma2(p, two(v.z, v.w), dz);
-                                const float2 f = split(mul2(p, mul2(two(v.x, v.y), dd)));
-                                const __half2 h = __floats2half2_rn(f.x, f.y);
-                                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                            for (int j = 0; j < 8; ++j) {
+                                const float4 k = *reinterpret_cast<const float4 *>(sh.key_of[half * 16 + 8 * c + j]);
+                                const float2 v = split(fma2(two(s[2 * j], s[2 * j + 1]), two(k.x, k.y), mul2(qs, two(k.z, k.w))));
+                                s[2 * j] = v.x, s[2 * j + 1] = v.y;
                             }
-                            *reinterpret_cast<uint4 *>(sh.w + wide_chunk(r, half * 4 + c)) = make_uint4(w[0], w[1], w[2], w[3]);
+                            if (masked) {
+                                __syncwarp();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    if (!(see >> (16 * c + j) & 1u)) s[j] = -INFINITY;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) most = fmaxf(most, s[j]);
+                            if (weighed) {
+#pragma unroll
+                                for (int d = 0; d < 2; ++d) {
+                                    uint32_t w[4];
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const int j = 4 * d + i;
+                                        const float4 v = *reinterpret_cast<const float4 *>(sh.value_of[half * 16 + 8 * c + j]);
+                                        const float2 x = split(fma2(two(s[2 * j], s[2 * j + 1]), cc, minus));
+                                        const Two p = two(ex2(x.x), ex2(x.y));
+                                        dl = add2(dl, p);
+                                        dz = fma2(p, two(v.z, v.w), dz);
+                                        const float2 f = split(mul2(p, mul2(two(v.x, v.y), dd)));
+                                        const __half2 h = __floats2half2_rn(f.x, f.y);
+                                        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                                    }
+                                    *reinterpret_cast<uint4 *>(sh.w + wide_chunk(r, half * 4 + 2 * c + d)) = make_uint4(w[0], w[1], w[2], w[3]);
+                                }
+                            }
                         }
+                        sh.red[0][half][r] = most;
+                        need |= !again && most > thr;  // (a second pass is the last one, whatever the scores are)
                     }
                     fence_operands();
                     fence_before();
@@ -387,7 +397,8 @@ __global__ void __launch_bounds__(kWideThreads, kWideOccupancy) kv_wide_kernel(c
                         }
                     }
                     vexp = vnew;
-                    need = false, weighed = true;
+                    need = false, weighed = again = true;
+                    consumers_sync<C>();  // (the maxima are read)
                 }
                 if (warp_on) l = add2(l, dl), z = add2(z, dz);
                 if (tid == 0) {

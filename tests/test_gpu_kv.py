@@ -328,6 +328,41 @@ def test_attention_masked_nan_does_not_spread():
     assert not bad[0].any() and not bad[4].any()
 
 
+@pytest.mark.parametrize("D,rope", [(64, False), (64, True), (128, False)])
+def test_attention_many_rows_masks_nan_and_growing_scores(D, rope):
+    """The kernel for many rows: a NaN token stays with its descendants, NaN and infinite queries with their rows, scores that
+    grow along the context move the maximum in the middle, and rows past the new tokens are 0."""
+    g = torch.Generator().manual_seed(D)
+    B, T, H, G, page, L = 2, 40, 1, 4, 16, 200
+    start = torch.tensor([L, 70], dtype=torch.int32)
+    width = (L + T) // page + 1
+    cache, table = pool(B, width, H, page, D, g)
+    c = cache.numpy()
+    c[:, :, page * D:] = 255
+    for b in range(B):
+        m = int(start[b]) + T
+        k = torch.randn((1, m, H, D), generator=g).numpy().astype(np.float64) * np.linspace(0.1, 12, m)[None, :, None, None]
+        v = torch.randn((1, m, H, D), generator=g).numpy().astype(np.float64) * np.exp(np.linspace(-6, 6, m))[None, :, None, None]
+        c[:] = expected_append(cache, table[b:b + 1].numpy(), k, v, np.array([0]), np.array([m]), page)[0]
+    parent = torch.tensor([-1] + [int(torch.randint(max(0, i - 4), i, (1,), generator=g)) for i in range(1, T)], dtype=torch.int32)
+    q = torch.randn((B, T, H * G, D), generator=g).to(torch.float16)
+    cos, sin = U.tables(L + T, D // 2) if rope else (None, None)
+    check_attention(q, cache, table, start, torch.tensor([T, 23], dtype=torch.int32), page, parent, cos, sin)
+    check_attention(q, cache, table, start, None, page, None, cos, sin)
+    j = L + 7
+    for o in (page * D + (j % page) * 4, page * D + (page + j % page) * 4):
+        c[int(table[0, j // page]), 0, o:o + 4] = 0xFF
+    out = check_attention(q, cache, table, start, None, page, parent, cos, sin)
+    sees = torch.from_numpy(U.lines(parent.numpy(), T)[:, 7])
+    assert torch.equal(torch.isnan(out[0]).any(-1).any(-1).cpu(), sees) and not torch.isnan(out[1]).any()
+    q[1, 3, 2, 5], q[1, 4, 0, 0] = float("nan"), float("inf")
+    q[1, 5] = 60000.0
+    out = sv.spec_kv_attention(q.to(DEV), cache.to(DEV), table.to(DEV), start.to(DEV), parent=parent.to(DEV))
+    bad = torch.isnan(out[1]).any(-1).cpu()
+    assert bad[3].tolist() == [False, False, True, False] and bad[4].tolist() == [True, False, False, False]
+    assert not bad[0].any() and not bad[6:].any()
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 5.0, 1e-20])
 def test_attention_scales(scale):
     g = torch.Generator().manual_seed(10)
