@@ -97,6 +97,9 @@ sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_tok
     const int64_t row_tiles = (rows + R - 1) / R, tokens = int64_t(table_width) * page_size;
     const int64_t most = row_tiles * (tokens / unit + 1);  // units of a sequence and head
     if (most > 0x7FFFFFFF / kv_heads || most * kv_heads > 0x7FFFFFFF / B) return SV_ERR_INVALID_ARG;
+    // no more CTAs than the page tables have room for units: empty shares would only lengthen the joins
+    const int64_t units = most * kv_heads * B;
+    const int grid = units < L.grid ? int(units) : L.grid;
     sv::AttArgs a{};
     a.q = static_cast<const uint16_t *>(q);
     a.q_bs = q_batch_stride, a.q_ts = q_token_stride, a.q_hs = q_head_stride;
@@ -118,15 +121,15 @@ sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_tok
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (wide)
-        e = head_dim == 128 ? sv::launch_wide_of<128, false>(a, L.grid, s)
-            : exact         ? sv::launch_wide_of<64, true>(a, L.grid, s)
-                            : sv::launch_wide_of<64, false>(a, L.grid, s);
+        e = head_dim == 128 ? sv::launch_wide_of<128, false>(a, grid, s)
+            : exact         ? sv::launch_wide_of<64, true>(a, grid, s)
+                            : sv::launch_wide_of<64, false>(a, grid, s);
     else if (head_dim == 64)
-        e = exact ? sv::launch_attention_rows<64, true>(a, nr, L.grid, s) : sv::launch_attention_rows<64, false>(a, nr, L.grid, s);
+        e = exact ? sv::launch_attention_rows<64, true>(a, nr, grid, s) : sv::launch_attention_rows<64, false>(a, nr, grid, s);
     else if (head_dim == 128)
-        e = exact ? sv::launch_attention_rows<128, true>(a, nr, L.grid, s) : sv::launch_attention_rows<128, false>(a, nr, L.grid, s);
+        e = exact ? sv::launch_attention_rows<128, true>(a, nr, grid, s) : sv::launch_attention_rows<128, false>(a, nr, grid, s);
     else
-        e = exact ? sv::launch_attention_rows<256, true>(a, nr, L.grid, s) : sv::launch_attention_rows<256, false>(a, nr, L.grid, s);
+        e = exact ? sv::launch_attention_rows<256, true>(a, nr, grid, s) : sv::launch_attention_rows<256, false>(a, nr, grid, s);
     return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 

@@ -80,15 +80,25 @@ struct AttArgs {
     float *acc;            // [2 grid][R][D]
 };
 
-// The first segment of a CTA's share, for the joining kernel.
-struct AttDesc {
-    int lo, hi, total;  // the segment's units, and all units
+// What the joining kernel has to do for the segment inside which a CTA's share begins.
+struct alignas(16) AttDesc {
+    int join;           // 1: this share is the one after that of the segment's start; 0: nothing to do
+    int first, last;    // the shares that hold parts of the segment, 2 first + 1: the first one's part lies in its second slot
+    int total;          // all units: if they are fewer than the shares, some shares are empty
     int b, h, rt, fresh;
 };
 
 // Where a CTA's share begins.
 __device__ __forceinline__ int share_begin(int total, int c, int n) { return int(int64_t(c) * total / n); }
 __device__ __forceinline__ int share_owner(int total, int u, int n) { return int((int64_t(u + 1) * n - 1) / total); }
+
+// Written once by every CTA: seg_lo and seg_hi bound the units of the share's first segment.
+__device__ __forceinline__ AttDesc describe(int total, int cta, int ncta, int ubegin, int seg_lo, int seg_hi, int b, int h, int rt, int fresh) {
+    if (seg_lo >= ubegin || fresh <= 0) return AttDesc{0, 0, 0, 0, 0, 0, 0, 0};
+    const int first = share_owner(total, seg_lo, ncta);
+    return AttDesc{share_owner(total, ubegin - 1, ncta) == first, 2 * first + (share_begin(total, first, ncta) != seg_lo),
+                   share_owner(total, seg_hi - 1, ncta), total, b, h, rt, fresh};
+}
 
 struct SeqWork {
     int before, fresh, len;
@@ -528,7 +538,10 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
 
     Cursor<NT> cur;
     int total, ubegin, uend;
-    if (!find_share<NT>(a, R, lane, cta, ncta, cur, total, ubegin, uend)) return;
+    if (!find_share<NT>(a, R, lane, cta, ncta, cur, total, ubegin, uend)) {
+        if (tid == 0) a.desc[cta] = AttDesc{0, 0, 0, 0, 0, 0, 0, 0};
+        return;
+    }
     __syncthreads();
 
     if (warp == NW) {
@@ -971,97 +984,77 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
                 }
             }
         if (tid == 0 && seg_lo <= ubegin)  // the share's first segment
-            a.desc[cta] = AttDesc{seg_lo, seg_lo + seg.tiles, total, seg.b, seg.h, seg.rt, seg.fresh};
+            a.desc[cta] = describe(total, cta, ncta, ubegin, seg_lo, seg_lo + seg.tiles, seg.b, seg.h, seg.rt, seg.fresh);
         if (it == units) break;
         wait_unit(stage, phase);
         seg = sh.unit[stage];
     }
 }
 
-// Joins a segment that several CTAs share: out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c.
-// Block (c, y) acts if CTA c's share begins inside a segment whose previous owner held its start;
-// y takes four of the segment's rows, a warp each for their weights.
-constexpr int kJoinThreads = 128, kJoinRows = 4, kJoinParts = 128;
+// Joins a segment that several CTAs share: out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c, in one pass with a
+// running M.  Block (c, y) acts if CTA c's share is the second one with a part of a segment; y takes the rows that 256
+// threads hold at four dimensions a thread.  What bounds it is the latency of three dependent reads.
+constexpr int kJoinThreads = 256;
+__host__ __device__ constexpr int join_rows(int D) { return kJoinThreads * 4 / D; }
 
-template <int D, int NR>
-__global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const AttArgs a, int ncta) {
-    constexpr int R = 8 * NR, kAll = kJoinRows * D / 4, kItems = (kAll + kJoinThreads - 1) / kJoinThreads;
-    __shared__ float weight[kJoinRows][kJoinParts];
-    __shared__ float inv_s[kJoinRows];
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const AttArgs a, int ncta, int R, int groups) {
     // (no griddep_launch_next: the next call's kernel, resident early beside this one's waiting blocks, would not find
     // all its places; 256 single tokens took 389 us so, and 299 without)
     griddep_wait();
-    const int c = int(blockIdx.x) / (R / kJoinRows) + 1;
-    const int r0 = int(blockIdx.x % (R / kJoinRows)) * kJoinRows;
-    if (c >= ncta) return;
-    // (CTA 0's share is empty only if all are; a CTA with an empty share wrote no descriptor)
-    const int total = a.desc[ncta - 1].total;  // the last share is never empty
-    const int begin = share_begin(total, c, ncta);
-    if (begin >= share_begin(total, c + 1, ncta)) return;
+    const int c = int(blockIdx.x) / groups + 1, r = int(blockIdx.x) % groups * join_rows(D) + threadIdx.x / (D / 4);
     const AttDesc d = a.desc[c];
-    if (begin <= d.lo) return;
-    const int c0 = share_owner(total, d.lo, ncta), c1 = share_owner(total, d.hi - 1, ncta);
-    // the first non-empty share after the start's owner joins the segment
-    if (share_owner(total, begin - 1, ncta) != c0) return;
-    if (d.fresh <= 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = r0 + warp;
-    auto wrote = [&](int k) { return share_begin(total, k, ncta) < share_begin(total, k + 1, ncta); };  // an empty share did not
-    // c0's part lies in its second slot unless its share begins with the segment
-    const bool second = share_begin(total, c0, ncta) != d.lo;
-    auto slot_of = [&](int k) { return int64_t(2) * k + (k == c0 && second ? 1 : 0); };
-    float most = -INFINITY, sum = 0.f;
-    for (int k = c0 + lane; k <= c1; k += 32)
-        if (wrote(k)) most = fmaxf(most, a.ml[slot_of(k) * R + r].x);
+    if (!d.join || r >= R) return;
+    const int d4 = threadIdx.x % (D / 4) * 4, row = d.rt * R + r, node = row / a.G;
+    if (node >= a.T) return;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (node < d.fresh) {
+        float m = -INFINITY, l = 0.f;
+        constexpr int kAhead = 4;
+        for (int k0 = d.first / 2; k0 <= d.last; k0 += kAhead) {
+            float2 ml[kAhead];
+            float4 v[kAhead];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-    float4 o[kItems];
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = c0; k0 <= c1; k0 += kJoinParts) {
-        const int n = min(kJoinParts, c1 + 1 - k0);
-        for (int k = lane; k < n; k += 32) {
-            float w = 0.f;
-            if (wrote(k0 + k)) {
-                const float2 ml = a.ml[slot_of(k0 + k) * R + r];
-                // a part that saw no score, or only NaN, weighs 1: its sums are 0, or NaN and to be kept
-                w = ml.x == -INFINITY ? 1.f : ex2(ml.x - most);
-                sum += w * ml.y;
+            for (int i = 0; i < kAhead; ++i) {
+                const int k = k0 + i;
+                const int64_t slot = k == d.first / 2 ? d.first : int64_t(2) * k;
+                ml[i] = make_float2(-INFINITY, 0.f), v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                const bool wrote = k <= d.last && (d.total >= ncta || share_begin(d.total, k, ncta) < share_begin(d.total, k + 1, ncta));
+                if (wrote && SV_IN(slot, 2 * ncta)) {
+                    ml[i] = a.ml[slot * R + r];
+                    v[i] = *reinterpret_cast<const float4 *>(a.acc + (slot * R + r) * D + d4);
+                }
             }
-            weight[warp][k] = w;
-        }
-        __syncthreads();
+            float most = m;
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-            const int item = threadIdx.x + i * kJoinThreads, q = item / (D / 4), d4 = item % (D / 4) * 4;
-            if (item >= kAll) continue;
-#pragma unroll 4
-            for (int k = 0; k < n; ++k) {
-                const float w = weight[q][k];
-                if (w == 0.f) continue;  // (and nothing was written there, if the share is empty)
-                const float4 v = *reinterpret_cast<const float4 *>(a.acc + (slot_of(k0 + k) * R + r0 + q) * D + d4);
-                o[i].x = fmaf(w, v.x, o[i].x), o[i].y = fmaf(w, v.y, o[i].y), o[i].z = fmaf(w, v.z, o[i].z), o[i].w = fmaf(w, v.w, o[i].w);
+            for (int i = 0; i < kAhead; ++i) most = fmaxf(most, ml[i].x);
+            const float keep = most == -INFINITY ? 1.f : ex2(m - most);
+            l *= keep, o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                // a part that saw no score, or only NaN, has no maximum: its sums are 0, or NaN and to be kept
+                const float w = ml[i].x == -INFINITY ? 1.f : ex2(ml[i].x - most);
+                l = fmaf(w, ml[i].y, l);
+                o.x = fmaf(w, v[i].x, o.x), o.y = fmaf(w, v[i].y, o.y), o.z = fmaf(w, v[i].z, o.z), o.w = fmaf(w, v[i].w, o.w);
             }
+            m = most;
         }
-        __syncthreads();
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        o.x = l == 0.f ? 0.f : o.x * inv, o.y = l == 0.f ? 0.f : o.y * inv;
+        o.z = l == 0.f ? 0.f : o.z * inv, o.w = l == 0.f ? 0.f : o.w * inv;
     }
-#pragma unroll
-    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
-    if (lane == 0) inv_s[warp] = sum == 0.f ? 0.f : 1.f / sum;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const int item = threadIdx.x + i * kJoinThreads, q = item / (D / 4), d4 = item % (D / 4) * 4;
-        if (item >= kAll) continue;
-        const int row = d.rt * R + r0 + q, node = row / a.G;
-        if (node >= a.T) continue;
-        const float inv = node < d.fresh ? inv_s[q] : 0.f;
-        const bool none = inv == 0.f;
-        uint2 w;
-        w.x = uint32_t(kv_from_float(none ? 0.f : o[i].x * inv, a.bf16)) | uint32_t(kv_from_float(none ? 0.f : o[i].y * inv, a.bf16)) << 16;
-        w.y = uint32_t(kv_from_float(none ? 0.f : o[i].z * inv, a.bf16)) | uint32_t(kv_from_float(none ? 0.f : o[i].w * inv, a.bf16)) << 16;
-        const int64_t head = d.h * a.G + row % a.G;
-        *reinterpret_cast<uint2 *>(a.out + ((d.b * int64_t(a.T) + node) * a.H * a.G + head) * D + d4) = w;
-    }
+    uint2 w;
+    w.x = uint32_t(kv_from_float(o.x, a.bf16)) | uint32_t(kv_from_float(o.y, a.bf16)) << 16;
+    w.y = uint32_t(kv_from_float(o.z, a.bf16)) | uint32_t(kv_from_float(o.w, a.bf16)) << 16;
+    const int64_t head = d.h * a.G + row - node * a.G;
+    *reinterpret_cast<uint2 *>(a.out + ((d.b * int64_t(a.T) + node) * a.H * a.G + head) * D + d4) = w;
+}
+
+template <int D>
+cudaError_t launch_join(const AttArgs &a, int grid, int R, cudaStream_t s) {
+    const int groups = (R + join_rows(D) - 1) / join_rows(D);
+    if (grid < 2) return cudaSuccess;  // nothing is shared
+    return launch_after(kv_attention_join_kernel<D>, unsigned((grid - 1) * groups), unsigned(kJoinThreads), 0, s, a, grid, R, groups);
 }
 
 template <int D, int NR, bool kExact>
@@ -1074,7 +1067,7 @@ cudaError_t launch_attention(const AttArgs &a, int grid, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     e = launch_after(kv_attention_kernel<D, NR, kExact>, unsigned(grid), unsigned(att_threads(D, NR)), smem, s, a);
     if (e != cudaSuccess) return e;
-    return launch_after(kv_attention_join_kernel<D, NR>, unsigned((grid - 1) * (8 * NR / kJoinRows)), unsigned(kJoinThreads), 0, s, a, grid);
+    return launch_join<D>(a, grid, 8 * NR, s);
 }
 
 // The attention kernels of a head dimension, each instantiated in its own translation unit.

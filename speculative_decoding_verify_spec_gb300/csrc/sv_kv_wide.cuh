@@ -173,7 +173,10 @@ __global__ void __launch_bounds__(kWideThreads, kWideOccupancy) kv_wide_kernel(c
         for (int i = tid; i < a.T; i += kWideThreads) parent_s[i] = a.parent[i];
     Cursor<NT> cur;
     int total, ubegin, uend;
-    if (!find_share<NT>(a, R, lane, cta, ncta, cur, total, ubegin, uend)) return;
+    if (!find_share<NT>(a, R, lane, cta, ncta, cur, total, ubegin, uend)) {
+        if (tid == 0) a.desc[cta] = AttDesc{0, 0, 0, 0, 0, 0, 0, 0};
+        return;
+    }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "r"(wide_columns(D))
                      : "memory");
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(kWideThreads, kWideOccupancy) kv_wide_kernel(c
             }
             fence_before();
             if (tid == 0 && seg_lo <= ubegin)  // the share's first segment
-                a.desc[cta] = AttDesc{seg_lo, seg_lo + seg.tiles, total, seg.b, seg.h, seg.rt, seg.fresh};
+                a.desc[cta] = describe(total, cta, ncta, ubegin, seg_lo, seg_lo + seg.tiles, seg.b, seg.h, seg.rt, seg.fresh);
             if (it == units) break;
             wait(&sh.full[stage], phase);
             seg = sh.unit[stage];
@@ -475,7 +478,7 @@ cudaError_t launch_wide(const AttArgs &a, int grid, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     e = launch_after(kv_wide_kernel<D, kExact>, unsigned(grid), unsigned(kWideThreads), smem, s, a);
     if (e != cudaSuccess) return e;
-    return launch_after(kv_attention_join_kernel<D, kWideRows / 8>, unsigned((grid - 1) * (kWideRows / kJoinRows)), unsigned(kJoinThreads), 0, s, a, grid);
+    return launch_join<D>(a, grid, kWideRows, s);
 }
 
 }  // namespace sv
