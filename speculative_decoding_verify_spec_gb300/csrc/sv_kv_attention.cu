@@ -109,6 +109,7 @@ sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_tok
     a.granule = 16;
     while (a.granule < unit && page_size % (2 * a.granule) == 0) a.granule *= 2;
     a.vec = (q_batch_stride | q_token_stride | q_head_stride) % 8 == 0 && reinterpret_cast<uintptr_t>(q) % 16 == 0;
+    a.rot_vec = cos && pairs % 4 == 0 && (reinterpret_cast<uintptr_t>(cos) | reinterpret_cast<uintptr_t>(sin)) % 16 == 0;
     a.table = page_table, a.start = start, a.new_lens = new_lens, a.parent = parent;
     a.scale = scale;
     a.rot = sv::Rotation{cos, sin, table_len, cos ? pairs : 0, interleaved != 0, positions};

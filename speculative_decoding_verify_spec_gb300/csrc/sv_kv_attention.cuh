@@ -65,7 +65,7 @@ inline int att_nr(int64_t rows, int D) {
 struct AttArgs {
     const uint16_t *q;
     int64_t q_bs, q_ts, q_hs;
-    int bf16, vec;  // vec: query rows lie on the 16-byte grid
+    int bf16, vec, rot_vec;  // query rows, and the angles' rows, lie on the 16-byte grid
     int B, T, H, G;  // H kv heads, G query heads each
     const uint8_t *cache;
     int num_pages, page, width, granule;  // granule: tokens per copy, a power of two dividing page and a unit
@@ -431,11 +431,20 @@ __device__ __forceinline__ void query_chunk(const AttArgs &a, const Unit &un, in
         if (!a.rot.interleaved && a.rot.pairs % 8 == 0) {  // the chunk lies within one half
             const int e0 = d0 < a.rot.pairs ? d0 : d0 - a.rot.pairs;
             load8(qp + (d0 < a.rot.pairs ? d0 + a.rot.pairs : e0), a.vec, a.bf16, y);
+            if (a.rot_vec) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                cs[i] = __ldg(cp + e0 + i);
-                sn[i] = d0 < a.rot.pairs ? -__ldg(sp + e0 + i) : __ldg(sp + e0 + i);
+                for (int i = 0; i < 8; i += 4) {
+                    const float4 u = __ldg(reinterpret_cast<const float4 *>(cp + e0 + i)), v = __ldg(reinterpret_cast<const float4 *>(sp + e0 + i));
+                    cs[i] = u.x, cs[i + 1] = u.y, cs[i + 2] = u.z, cs[i + 3] = u.w;
+                    sn[i] = v.x, sn[i + 1] = v.y, sn[i + 2] = v.z, sn[i + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) cs[i] = __ldg(cp + e0 + i), sn[i] = __ldg(sp + e0 + i);
             }
+            const float sign = d0 < a.rot.pairs ? -1.f : 1.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sn[i] *= sign;
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -471,9 +480,9 @@ __device__ __forceinline__ void load_queries(const AttArgs &a, AttShared<D, NR> 
         const int node = row / a.G, head = un.h * a.G + row - node * a.G;
         const bool on = r < R && node < un.fresh;
         float x[8];
+        query_chunk(a, un, on ? node : 0, on ? head : 0, d0, x);  // (no branch: the rows' loads go out together)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.f;
-        if (on) query_chunk(a, un, node, head, d0, x);
+        for (int i = 0; i < 8; ++i) x[i] = on ? x[i] : 0.f;
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(fabsf(x[i])));

@@ -106,9 +106,9 @@ __device__ __forceinline__ void wide_queries(const AttArgs &a, WideShared<D, kEx
         const int node = row / a.G, head = un.h * a.G + row - node * a.G;
         const bool on = node < un.fresh;
         float x[8];
+        query_chunk(a, un, on ? node : 0, on ? head : 0, d0, x);  // (no branch: the rows' loads go out together)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.f;
-        if (on) query_chunk(a, un, node, head, d0, x);
+        for (int i = 0; i < 8; ++i) x[i] = on ? x[i] : 0.f;
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(fabsf(x[i])));
