@@ -15,6 +15,10 @@
 // arithmetic branch in the stream itself would leave most lanes idle most of the time), and then
 // masked on its way from shared memory to the output.  The history is read once per token range from L2,
 // the price of needing no second kernel and no table in DRAM.
+//
+// Measured: 256 x 9 rows of 128256 bf16 logits with masks, histories of up to 1500 tokens and 16 biases 251 us, 4.9 TB/s
+// read and written (a copy 175 us; masks alone 182; histories alone 226: counting them is instruction-bound and overlaps the
+// stream only in part); 64 x 64 tree rows of 50257 fp32 logits 303 us, 5.5 TB/s (a copy 240 us).
 #include <cstdint>
 
 #include "spec_serve.h"
@@ -48,7 +52,7 @@ struct AdjustArgs {
 constexpr uint32_t kPrompt = 0x80000000u;  // table word: the prompt holds the token; low bits: output count
 
 constexpr int kVecs = 4, kChunkVecs = 32 * kVecs;  // 16-byte vectors per lane and per chunk
-constexpr int kRing = 4;                           // chunks of a warp in shared memory
+constexpr int kRing = 3;                           // chunks of a warp in shared memory (4: 255 us for 251 below)
 
 template <int TV>
 struct AdjustShared {

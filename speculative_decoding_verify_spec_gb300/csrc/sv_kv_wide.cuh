@@ -11,6 +11,10 @@
 // row's maximum and sums need no shuffles.  A ninth warp copies units into the ring.  Within a unit the value codes
 // are unpacked while S is computed, and the next unit's key codes while O is.
 //
+// Measured: 64 x 64 tree nodes with 4 query heads a kv head over up to 2047 tokens 124 us (250 in tiles of 32 rows); a unit
+// takes a block 1.9 us at 64 dimensions and 3.5 at 128, whatever its rows: the chain of unpacking, product, scores, weights,
+// product and its two barriers, with two blocks an SM to fill it.
+//
 // Why: with eight rows a tile column, 256 rows unpack every code eight times and spend most of their instructions
 // around the products; here what is left a row and token is the exponential and seven more instructions.
 #pragma once
