@@ -59,17 +59,18 @@ def _ptr(t):
 
 def _like(t):
     """A new contiguous tensor of t's shape and type."""
-    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _int32(t, name, shape, dev):
-    if t is None or (t.dtype is torch.int32 and t.device == dev and t.shape == shape and t.is_contiguous()):
+    """t, an int32 tensor of that shape on dev (or None), contiguous."""
+    if t is None or (t.dtype is torch.int32 and t.shape == shape and t.get_device() == dev.index and t.is_contiguous()):
         return t
     return _ints(t, name, shape, dev)
 
 
 def _floats(t, name, shape, dev):
-    if t is None or (t.dtype is torch.float32 and t.device == dev and t.shape == shape and t.is_contiguous()):
+    if t is None or (t.dtype is torch.float32 and t.shape == shape and t.get_device() == dev.index and t.is_contiguous()):
         return t
     if t.dtype != torch.float32 or t.device != dev or tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be float32 of shape {tuple(shape)} on {dev}")
@@ -92,7 +93,7 @@ def spec_logit_adjust(logits: torch.Tensor, *, history=None, lengths=None, promp
     lib = _library()
     sb, sr = _logits3(logits, "logits")
     B, R, V = logits.shape
-    dt, dev = _dtype_code(logits), logits.device
+    dt, dev, row = _dtype_code(logits), logits.device, (B,)
     if out is None:
         out = _like(logits)
         ob, orow, _ = out.stride()
@@ -106,8 +107,8 @@ def spec_logit_adjust(logits: torch.Tensor, *, history=None, lengths=None, promp
             raise ValueError("history must be [B, n], with lengths [B]")
         n = history.shape[1]
         history = _int32(history, "history", (B, n), dev)
-        lengths = _int32(lengths, "lengths", (B,), dev)
-        prompt_lengths = _int32(prompt_lengths, "prompt_lengths", (B,), dev)
+        lengths = _int32(lengths, "lengths", row, dev)
+        prompt_lengths = _int32(prompt_lengths, "prompt_lengths", row, dev)
     if parent is not None:
         if draft_tokens is None:
             raise ValueError("a tree (parent) needs draft_tokens [B, rows]")
@@ -121,9 +122,9 @@ def spec_logit_adjust(logits: torch.Tensor, *, history=None, lengths=None, promp
         k = bias_tokens.shape[1] if bias_tokens.dim() == 2 else -1
         bias_tokens = _int32(bias_tokens, "bias_tokens", (B, k), dev)
         bias_values = _floats(bias_values, "bias_values", (B, k), dev)
-    repetition = _floats(repetition, "repetition", (B,), dev)
-    frequency = _floats(frequency, "frequency", (B,), dev)
-    presence = _floats(presence, "presence", (B,), dev)
+    repetition = _floats(repetition, "repetition", row, dev)
+    frequency = _floats(frequency, "frequency", row, dev)
+    presence = _floats(presence, "presence", row, dev)
     allowed = _int32(allowed, "allowed", (B, R, (V + 31) // 32), dev)
     st = lib.spec_logit_adjust(logits.data_ptr(), sb, sr, out.data_ptr(), ob, orow, dt, B, R, V, _ptr(history), n,
                                _ptr(lengths), _ptr(prompt_lengths), _ptr(draft_tokens), _ptr(parent), _ptr(repetition),
@@ -156,28 +157,31 @@ def _heads4(t: torch.Tensor, name: str):
 
 
 def _cache(cache, page_table, start, new_lens, B, heads, D, dev):
-    """(num_pages, page_size, table width) of a checked cache."""
-    if cache.dtype != torch.uint8 or cache.device != dev or cache.dim() != 3 or not cache.is_contiguous():
+    """(num_pages, page_size, checked page_table, its width, start, new_lens) of a checked cache."""
+    cs = cache.shape
+    if cache.dtype is not torch.uint8 or len(cs) != 3 or cache.get_device() != dev.index or not cache.is_contiguous():
         raise ValueError(f"cache must be a contiguous uint8 tensor [pages, kv_heads, page bytes] on {dev}")
-    page, rest = divmod(cache.shape[2], D + 8)
-    if (heads is not None and cache.shape[1] != heads) or rest:
-        raise ValueError(f"cache of shape {tuple(cache.shape)} does not hold {heads} heads of {D} dimensions")
-    if page_table.dim() != 2:
+    page, rest = divmod(cs[2], D + 8)
+    if (heads is not None and cs[1] != heads) or rest:
+        raise ValueError(f"cache of shape {tuple(cs)} does not hold {heads} heads of {D} dimensions")
+    ps = page_table.shape
+    if len(ps) != 2:
         raise ValueError("page_table must be [B, pages per sequence]")
-    width = page_table.shape[1]
-    return (cache.shape[0], page, _int32(page_table, "page_table", (B, width), dev), width, _int32(start, "start", (B,), dev),
-            _int32(new_lens, "new_lens", (B,), dev))
+    width, row = ps[1], (B,)
+    return (cs[0], page, _int32(page_table, "page_table", (B, width), dev), width, _int32(start, "start", row, dev),
+            _int32(new_lens, "new_lens", row, dev))
 
 
 def _rotation(cos, sin, positions, B, T, dev):
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin belong together")
-    if cos is None:
+    if cos is None and sin is None:
         return None, None, 0, 0, None
-    if cos.dim() != 2:
+    if cos is None or sin is None:
+        raise ValueError("cos and sin belong together")
+    shape = cos.shape
+    if len(shape) != 2:
         raise ValueError("cos must be [positions, pairs]")
-    cos, sin = _floats(cos, "cos", cos.shape, dev), _floats(sin, "sin", cos.shape, dev)
-    return cos, sin, cos.shape[0], cos.shape[1], _int32(positions, "positions", (B, T), dev)
+    return (_floats(cos, "cos", shape, dev), _floats(sin, "sin", shape, dev), shape[0], shape[1],
+            _int32(positions, "positions", (B, T), dev))
 
 
 def spec_kv_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor,
@@ -191,19 +195,19 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_t
     (`positions` [B, T], else start[b] + t).  With `return_values`, or `k_values` and `v_values` given, returns what the
     cache now holds for the new tokens, in the inputs' type; else None."""
     lib = _library()
-    ks, dt, dev = _heads4(k, "k"), _kv_dtype(k, "k"), k.device
+    ks, dt, dev, shape = _heads4(k, "k"), _kv_dtype(k, "k"), k.device, k.shape
     vs = _heads4(v, "v")
-    if v.shape != k.shape or v.dtype != k.dtype or v.device != dev:
+    if v.shape != shape or v.dtype != k.dtype or v.device != dev:
         raise ValueError("v must have k's shape, type and device")
-    B, T, H, D = k.shape
+    B, T, H, D = shape
     pages, page, page_table, width, start, new_lens = _cache(cache, page_table, start, new_lens, B, H, D, dev)
     cos, sin, length, pairs, positions = _rotation(cos, sin, positions, B, T, dev)
+    for name, t in (("k_values", k_values), ("v_values", v_values)):
+        if t is not None and (t.shape != shape or t.dtype != k.dtype or t.device != dev or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous tensor like k")
     if return_values:
         k_values = _like(k) if k_values is None else k_values
         v_values = _like(k) if v_values is None else v_values
-    for name, t in (("k_values", k_values), ("v_values", v_values)):
-        if t is not None and (t.shape != k.shape or t.dtype != k.dtype or t.device != dev or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous tensor like k")
     st = lib.spec_kv_append(k.data_ptr(), ks[0], ks[1], ks[2], v.data_ptr(), vs[0], vs[1], vs[2], dt, B, T, H, D, cache.data_ptr(), pages, page,
                             page_table.data_ptr(), width, start.data_ptr(), _ptr(new_lens), _ptr(cos), _ptr(sin), length,
                             pairs, int(interleaved), _ptr(positions), _ptr(k_values), _ptr(v_values), _current(dev))
@@ -228,12 +232,13 @@ def spec_kv_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Te
     lib = _library()
     qs, dt, dev = _heads4(q, "q"), _kv_dtype(q, "q"), q.device
     B, T, Hq, D = q.shape
-    if cache.dim() != 3 or cache.shape[1] < 1 or Hq % cache.shape[1]:
+    H = cache.shape[1] if cache.dim() == 3 else 0
+    if H < 1 or Hq % H:
         raise ValueError(f"{Hq} query heads do not share the cache's heads (shape {tuple(cache.shape)}) evenly")
-    H = cache.shape[1]
     pages, page, page_table, width, start, new_lens = _cache(cache, page_table, start, new_lens, B, None, D, dev)
     cos, sin, length, pairs, positions = _rotation(cos, sin, positions, B, T, dev)
-    parent = _int32(parent, "parent", (T,), dev)
+    if parent is not None:
+        parent = _int32(parent, "parent", (T,), dev)
     if out is None:
         out = _like(q)
     elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
