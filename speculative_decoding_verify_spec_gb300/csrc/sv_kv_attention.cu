@@ -25,12 +25,14 @@ template <>
 cudaError_t launch_wide_of<64, true>(const AttArgs &a, int grid, cudaStream_t s);
 template <>
 cudaError_t launch_wide_of<128, false>(const AttArgs &a, int grid, cudaStream_t s);
+template <>
+cudaError_t launch_wide_of<128, true>(const AttArgs &a, int grid, cudaStream_t s);
 
 namespace {
 
-// More rows than this a kv head go to the kernel for many rows.  48 sequences of 3000 cached tokens at most, us: 128 dimensions
-// and 56 rows 154 in tiles of 32 and 170 in one of 128; 72 rows 192 and 173; 128 rows 407 and 184; 64 dimensions and
-// 72 rows 75 and 81; 96 rows 92 and 79; 128 rows 119 and 81.
+// More rows than this a kv head go to the kernel for many rows.  64 sequences of 2047 cached tokens at most, 128 dimensions,
+// rotated fp16 queries, us: 56 rows 130 in tiles of 32, 72 rows 173 and 146 in one of 128, 128 rows 316 and 156, 256 rows 619
+// and 286.  48 of 3000, 64 dimensions: 72 rows 75 and 81, 96 rows 92 and 79, 128 rows 119 and 81.
 constexpr int kNarrowRows = 64;
 bool att_wide(int64_t rows, int D) { return D <= 128 && rows > kNarrowRows; }
 
@@ -41,7 +43,7 @@ struct AttLayout {
 AttLayout att_layout(int64_t rows, int D, bool wide) {
     const int nr = att_nr(rows, D), R = wide ? kWideRows : 8 * nr;
     AttLayout L;
-    L.grid = kAttSMs * (wide ? kWideOccupancy : att_occupancy(D, nr));
+    L.grid = kAttSMs * (wide ? wide_occupancy(D) : att_occupancy(D, nr));
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     L.desc = 256;
     L.ml = up(L.desc + size_t(L.grid) * sizeof(AttDesc));
@@ -58,10 +60,7 @@ extern "C" {
 size_t spec_kv_attention_workspace_size(int B, int T, int heads, int kv_heads, int head_dim) {
     if (B <= 0 || T <= 0 || kv_heads < 1 || heads < kv_heads || heads % kv_heads || !sv::kv_head_dim_ok(head_dim)) return 0;
     const int64_t rows = int64_t(T) * (heads / kv_heads);
-    const size_t narrow = sv::att_layout(rows, head_dim, false).total;
-    if (!sv::att_wide(rows, head_dim)) return narrow;
-    const size_t wide = sv::att_layout(rows, head_dim, true).total;  // which one runs depends on more than the sizes
-    return narrow > wide ? narrow : wide;
+    return sv::att_layout(rows, head_dim, sv::att_wide(rows, head_dim)).total;
 }
 
 sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,
@@ -87,8 +86,8 @@ sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_tok
         return SV_ERR_INVALID_ARG;
     const int G = heads / kv_heads;
     const int64_t rows = int64_t(T) * G;
-    // rotated fp16 queries are multiplied in two parts (128 dimensions of them do not fit the wide kernel twice an SM)
-    const bool exact = cos && dtype == SV_KV_FP16, wide = sv::att_wide(rows, head_dim) && !(exact && head_dim == 128);
+    // rotated fp16 queries are multiplied in two parts
+    const bool exact = cos && dtype == SV_KV_FP16, wide = sv::att_wide(rows, head_dim);
     const sv::AttLayout L = sv::att_layout(rows, head_dim, wide);
     if (!workspace || workspace_bytes < L.total || reinterpret_cast<uintptr_t>(workspace) % 16) return SV_ERR_WORKSPACE;
     char *ws = static_cast<char *>(workspace);
@@ -122,7 +121,7 @@ sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_tok
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (wide)
-        e = head_dim == 128 ? sv::launch_wide_of<128, false>(a, grid, s)
+        e = head_dim == 128 ? exact ? sv::launch_wide_of<128, true>(a, grid, s) : sv::launch_wide_of<128, false>(a, grid, s)
             : exact         ? sv::launch_wide_of<64, true>(a, grid, s)
                             : sv::launch_wide_of<64, false>(a, grid, s);
     else if (head_dim == 64)

@@ -12,8 +12,8 @@
 // are unpacked while S is computed, and the next unit's key codes while O is.
 //
 // Measured: 64 x 64 tree nodes with 4 query heads a kv head over up to 2047 tokens 124 us (250 in tiles of 32 rows); a unit
-// takes a block 1.9 us at 64 dimensions and 3.5 at 128, whatever its rows: the chain of unpacking, product, scores, weights,
-// product and its two barriers, with two blocks an SM to fill it.
+// takes a block 1.9 us at 64 dimensions, two blocks an SM, and 1.6 at 128, one block an SM, whatever its rows: the chain of
+// unpacking, product, scores, weights, product and its two barriers.
 //
 // Why: with eight rows a tile column, 256 rows unpack every code eight times and spend most of their instructions
 // around the products; here what is left a row and token is the exponential and seven more instructions.
@@ -24,7 +24,10 @@
 namespace sv {
 
 constexpr int kWideRows = 128, kWideTokens = 64, kWideThreads = 288, kWideStages = 3;
-constexpr int kWideOccupancy = 2;  // CTAs per SM
+// CTAs per SM.  64 x 64 tree nodes as above, us: 128 dimensions 241 with one and 260 with two (one sequence: 25 and 41), 64
+// dimensions 159 and 124 (20 and 29).  One leaves a thread 164 registers instead of 112 and halves the split segments; the
+// unpacking of 128 dimensions is long enough to fill the waits by itself.
+__host__ __device__ constexpr int wide_occupancy(int D) { return D == 64 ? 2 : 1; }
 __host__ __device__ constexpr int wide_columns(int D) { return D == 64 ? 128 : 256; }  // of tensor memory: S, then O
 
 template <int D, bool kExact>
@@ -153,7 +156,7 @@ __device__ __forceinline__ void wide_queries(const AttArgs &a, WideShared<D, kEx
 }
 
 template <int D, bool kExact>
-__global__ void __launch_bounds__(kWideThreads, kWideOccupancy) kv_wide_kernel(const AttArgs a) {
+__global__ void __launch_bounds__(kWideThreads, wide_occupancy(D)) kv_wide_kernel(const AttArgs a) {
     using Sh = WideShared<D, kExact>;
     constexpr int R = kWideRows, NT = kWideTokens, NW = 8, C = 32 * NW, kStages = kWideStages;
     extern __shared__ unsigned char raw0[];

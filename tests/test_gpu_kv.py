@@ -328,7 +328,7 @@ def test_attention_masked_nan_does_not_spread():
     assert not bad[0].any() and not bad[4].any()
 
 
-@pytest.mark.parametrize("D,rope", [(64, False), (64, True), (128, False)])
+@pytest.mark.parametrize("D,rope", [(64, False), (64, True), (128, False), (128, True)])
 def test_attention_many_rows_masks_nan_and_growing_scores(D, rope):
     """The kernel for many rows: a NaN token stays with its descendants, NaN and infinite queries with their rows, scores that
     grow along the context move the maximum in the middle, and rows past the new tokens are 0."""
