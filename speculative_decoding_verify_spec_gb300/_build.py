@@ -27,7 +27,7 @@ SOURCES = ["sv_api.cu", "sv_sample.cu", "sv_greedy.cu", "sv_refine.cu", "sv_tree
            "sv_kv_attention_64.cu", "sv_kv_attention_128.cu", "sv_kv_attention_256.cu",
            "sv_kv_attention_64_exact.cu", "sv_kv_attention_128_exact.cu", "sv_kv_attention_256_exact.cu",
            "sv_kv_wide_64.cu", "sv_kv_wide_64_exact.cu", "sv_kv_wide_128.cu",
-           "sv_kv_wide_128_exact.cu"]
+           "sv_kv_wide_128_exact.cu", "sv_kv_wide_256.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -27,14 +27,18 @@ template <>
 cudaError_t launch_wide_of<128, false>(const AttArgs &a, int grid, cudaStream_t s);
 template <>
 cudaError_t launch_wide_of<128, true>(const AttArgs &a, int grid, cudaStream_t s);
+template <>
+cudaError_t launch_wide_of<256, false>(const AttArgs &a, int grid, cudaStream_t s);
 
 namespace {
 
 // More rows than this a kv head go to the kernel for many rows.  64 sequences of 2047 cached tokens at most, 128 dimensions,
 // rotated fp16 queries, us: 56 rows 130 in tiles of 32, 72 rows 173 and 146 in one of 128, 128 rows 316 and 156, 256 rows 619
-// and 286.  48 of 3000, 64 dimensions: 72 rows 75 and 81, 96 rows 92 and 79, 128 rows 119 and 81.
+// and 286; 256 dimensions, bf16: 72 rows 225 in tiles of 40 and 204, 128 rows 350 and 222, 256 rows 755 and 395, but 27 and
+// 35 for one sequence alone, whose blocks have a unit or two each.  48 of 3000, 64 dimensions: 72 rows 75 and 81, 96 rows 92 and 79, 128 rows 119 and 81.
 constexpr int kNarrowRows = 64;
-bool att_wide(int64_t rows, int D) { return D <= 128 && rows > kNarrowRows; }
+// Both parts of rotated fp16 queries of 256 dimensions do not fit its shared memory.
+bool att_wide(int64_t rows, int D, bool exact) { return rows > kNarrowRows && !(D == 256 && exact); }
 
 struct AttLayout {
     size_t desc, ml, acc, total;
@@ -60,7 +64,9 @@ extern "C" {
 size_t spec_kv_attention_workspace_size(int B, int T, int heads, int kv_heads, int head_dim) {
     if (B <= 0 || T <= 0 || kv_heads < 1 || heads < kv_heads || heads % kv_heads || !sv::kv_head_dim_ok(head_dim)) return 0;
     const int64_t rows = int64_t(T) * (heads / kv_heads);
-    return sv::att_layout(rows, head_dim, sv::att_wide(rows, head_dim)).total;
+    const size_t plain = sv::att_layout(rows, head_dim, sv::att_wide(rows, head_dim, false)).total;
+    const size_t exact = sv::att_layout(rows, head_dim, sv::att_wide(rows, head_dim, true)).total;
+    return plain > exact ? plain : exact;
 }
 
 sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,
@@ -87,7 +93,7 @@ sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_tok
     const int G = heads / kv_heads;
     const int64_t rows = int64_t(T) * G;
     // rotated fp16 queries are multiplied in two parts
-    const bool exact = cos && dtype == SV_KV_FP16, wide = sv::att_wide(rows, head_dim);
+    const bool exact = cos && dtype == SV_KV_FP16, wide = sv::att_wide(rows, head_dim, exact);
     const sv::AttLayout L = sv::att_layout(rows, head_dim, wide);
     if (!workspace || workspace_bytes < L.total || reinterpret_cast<uintptr_t>(workspace) % 16) return SV_ERR_WORKSPACE;
     char *ws = static_cast<char *>(workspace);
@@ -121,7 +127,8 @@ sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_tok
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (wide)
-        e = head_dim == 128 ? exact ? sv::launch_wide_of<128, true>(a, grid, s) : sv::launch_wide_of<128, false>(a, grid, s)
+        e = head_dim == 256 ? sv::launch_wide_of<256, false>(a, grid, s)
+            : head_dim == 128 ? exact ? sv::launch_wide_of<128, true>(a, grid, s) : sv::launch_wide_of<128, false>(a, grid, s)
             : exact         ? sv::launch_wide_of<64, true>(a, grid, s)
                             : sv::launch_wide_of<64, false>(a, grid, s);
     else if (head_dim == 64)

@@ -12,8 +12,8 @@
 // are unpacked while S is computed, and the next unit's key codes while O is.
 //
 // Measured: 64 x 64 tree nodes with 4 query heads a kv head over up to 2047 tokens 124 us (250 in tiles of 32 rows); a unit
-// takes a block 1.9 us at 64 dimensions, two blocks an SM, and 1.6 at 128, one block an SM, whatever its rows: the chain of
-// unpacking, product, scores, weights, product and its two barriers.
+// takes a block 2.0 us at 64 dimensions, two blocks an SM, and 1.6 at 128 and 2.4 at 256, one block an SM, whatever its rows:
+// the chain of unpacking, product, scores, weights, product and its two barriers.
 //
 // Why: with eight rows a tile column, 256 rows unpack every code eight times and spend most of their instructions
 // around the products; here what is left a row and token is the exponential and seven more instructions.
@@ -25,10 +25,10 @@ namespace sv {
 
 constexpr int kWideRows = 128, kWideTokens = 64, kWideThreads = 288, kWideStages = 3;
 // CTAs per SM.  64 x 64 tree nodes as above, us: 128 dimensions 241 with one and 260 with two (one sequence: 25 and 41), 64
-// dimensions 159 and 124 (20 and 29).  One leaves a thread 164 registers instead of 112 and halves the split segments; the
+// dimensions 159 and 124 (20 and 29).  One leaves a thread 166 registers instead of 96 and halves the split segments; the
 // unpacking of 128 dimensions is long enough to fill the waits by itself.
 __host__ __device__ constexpr int wide_occupancy(int D) { return D == 64 ? 2 : 1; }
-__host__ __device__ constexpr int wide_columns(int D) { return D == 64 ? 128 : 256; }  // of tensor memory: S, then O
+__host__ __device__ constexpr int wide_columns(int D) { return D == 64 ? 128 : D == 128 ? 256 : 512; }  // of tensor memory: S, then O
 
 template <int D, bool kExact>
 struct WideShared {
@@ -250,8 +250,11 @@ __global__ void __launch_bounds__(kWideThreads, wide_occupancy(D)) kv_wide_kerne
                         const uint2 x = *reinterpret_cast<const uint2 *>(kc + t * (D / 2) + w0 * 4);
                         kw[0] = x.x, kw[1] = x.y;
                     } else {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(kc + t * (D / 2) + w0 * 4);
-                        kw[0] = x.x, kw[1] = x.y, kw[2] = x.z, kw[3] = x.w;
+#pragma unroll
+                        for (int i = 0; i < D / 32; i += 4) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(kc + t * (D / 2) + (w0 + i) * 4);
+                            kw[i] = x.x, kw[i + 1] = x.y, kw[i + 2] = x.z, kw[i + 3] = x.w;
+                        }
                     }
 #pragma unroll
                     for (int i = 0; i < D / 32; ++i) {
@@ -285,8 +288,9 @@ __global__ void __launch_bounds__(kWideThreads, wide_occupancy(D)) kv_wide_kerne
                 }
                 // value codes, once the last unit's product has been read: (chunk of 8 tokens, group of 4 dimensions)
                 if (it > first) wait(&sh.products, turn ^ 1);
-                if (tid < 2 * D) {
-                    const int c = tid & 7, group = tid >> 3;  // tokens 8 c .. ; dimensions 4 group ..
+#pragma unroll
+                for (int at = tid; at < 2 * D; at += C) {
+                    const int c = at & 7, group = at >> 3;  // tokens 8 c .. ; dimensions 4 group ..
                     const uint4 *src = reinterpret_cast<const uint4 *>(vc + c / 2 * 8 * D + group / 8 * 256 + group % 8 * 32);
                     const uint4 x = src[0], y = src[1];
                     const bool j = c & 1;
@@ -479,6 +483,7 @@ __global__ void __launch_bounds__(kWideThreads, wide_occupancy(D)) kv_wide_kerne
 template <int D, bool kExact>
 cudaError_t launch_wide(const AttArgs &a, int grid, cudaStream_t s) {
     constexpr size_t fixed = sizeof(WideShared<D, kExact>) + 1024;
+    static_assert(fixed + SV_MAX_TREE_NODES * 4 + kWideRows * (SV_MAX_TREE_NODES / 32 + 1) * 4 <= 227 * 1024, "the largest tree");
     const size_t smem = fixed + (a.parent ? size_t(a.T) * 4 + size_t(kWideRows) * ((a.T + 31) / 32 + 1) * 4 : 0);
     static std::atomic<int> allowed[64];
     cudaError_t e = allow_shared(kv_wide_kernel<D, kExact>, int(smem), allowed);

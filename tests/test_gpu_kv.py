@@ -271,7 +271,7 @@ def test_attention_tree(D, H, G, T, page):
     check_attention(q, cache, table, start, None, page, parent)
 
 
-@pytest.mark.parametrize("D,G,dtype,rope", [(256, 8, "fp16", True), (128, 8, "bf16", True), (64, 1, "fp16", False)])
+@pytest.mark.parametrize("D,G,dtype,rope", [(256, 8, "fp16", True), (256, 8, "bf16", True), (128, 8, "bf16", True), (64, 1, "fp16", False)])
 def test_attention_largest_tree(D, G, dtype, rope):
     """1024 nodes: the tree's own tables beside the largest rings in shared memory."""
     g = torch.Generator().manual_seed(D)
@@ -328,7 +328,7 @@ def test_attention_masked_nan_does_not_spread():
     assert not bad[0].any() and not bad[4].any()
 
 
-@pytest.mark.parametrize("D,rope", [(64, False), (64, True), (128, False), (128, True)])
+@pytest.mark.parametrize("D,rope", [(64, False), (64, True), (128, False), (128, True), (256, False)])
 def test_attention_many_rows_masks_nan_and_growing_scores(D, rope):
     """The kernel for many rows: a NaN token stays with its descendants, NaN and infinite queries with their rows, scores that
     grow along the context move the maximum in the middle, and rows past the new tokens are 0."""
