@@ -19,8 +19,9 @@
  * Conventions shared by every entry point
  *   - Every array argument is a DEVICE pointer; the caller owns all memory.  The library
  *     allocates nothing and keeps no state between calls, apart from the optional,
- *     thread-local timing events of spec_verify_set_stage_events and the fixed scratch
- *     array of spec_verify_greedy_noalloc.
+ *     thread-local timing events of spec_verify_set_stage_events, the fixed scratch
+ *     array of spec_verify_greedy_noalloc and, per kernel and device, the largest shared
+ *     memory that a call of spec_serve.h has asked the runtime to allow (under a lock).
  *   - Logits are [B][rows][V] with a contiguous last axis.  Strides are in ELEMENTS and may
  *     be 0 (broadcast).  Rows are read with 16-byte vector loads when the base pointer and
  *     both strides (times the element size) are multiples of 16 bytes, else element-wise.
@@ -393,8 +394,7 @@ sv_status spec_verify_exp_df(const float *y_hi, const float *y_lo, int n, float 
                              void *stream);
 
 /*
- * Optional timing instrumentation for the CALLING THREAD (the only state the library
- * keeps, and it is thread-local).  With events != NULL, each later call of
+ * Optional timing instrumentation for the CALLING THREAD.  With events != NULL, each later call of
  * spec_verify_sample / _greedy / _greedy_noalloc / _tree_greedy / _tree_sample / _sample_lazy /
  * _typical / _sample_onehot on this thread
  * records events[0] on its stream before its first kernel and events[s] after its s-th
