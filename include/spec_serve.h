@@ -77,7 +77,8 @@ sv_status spec_logit_adjust(const void *logits, int64_t batch_stride, int64_t ro
  *   page_table  [B][table_width]  token j of sequence b is in page page_table[b][j / page_size],
  *               slot j % page_size.  Entries past a sequence's length are not used.  A page
  *               outside [0, num_pages) is never touched: appended tokens are dropped, and its
- *               tokens are masked in the attention.
+ *               tokens are masked in the attention.  A table spans at most 2^31 - 128 tokens
+ *               (2^31 - 1 for the append).
  *   start       [B]  tokens of each sequence in the cache before this step; its new tokens are
  *               start .. start + new_lens[b] - 1 (NULL new_lens: all T).  start is clamped to
  *               [0, table_width * page_size], new_lens to [0, T]; tokens past the table's end

@@ -80,7 +80,7 @@ sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_tok
     if (B < 0 || T < 0 || kv_heads < 1 || heads < kv_heads || heads % kv_heads || num_pages < 0 || table_width < 0)
         return SV_ERR_INVALID_ARG;
     if (q_batch_stride < 0 || q_token_stride < 0 || q_head_stride < 0) return SV_ERR_INVALID_ARG;
-    if (int64_t(table_width) * page_size > 0x7FFFFFC0) return SV_ERR_INVALID_ARG;
+    if (int64_t(table_width) * page_size > 0x7FFFFF80) return SV_ERR_INVALID_ARG;  // (rounded up to a unit of 128: 31 bits)
     if (parent && T > SV_MAX_TREE_NODES) return SV_ERR_INVALID_ARG;
     if (int64_t(T) * heads > 0x3FFFFFFF) return SV_ERR_INVALID_ARG;
     if (!(scale - scale == 0.f)) return SV_ERR_INVALID_ARG;

@@ -135,3 +135,15 @@ def test_reference_quantiser_error_is_half_a_step():
     tol = s / 2 + np.abs(z) * 2.0**-11 + 15 * s * 2.0**-10 + 2.0**-20
     assert (np.abs(z + s * code - x) <= tol).all()
     assert ctypes.sizeof(ctypes.c_void_p) == 8
+
+
+@pytest.mark.parametrize("D,Hq,T", [(64, 4, 1), (64, 16, 40), (128, 4, 2), (128, 16, 9), (256, 8, 1), (256, 16, 40)])
+def test_attention_capacity_limit(lib, D, Hq, T):
+    """Token counts are rounded up to units of at most 128 tokens in 31 bits, so a table may span 2^31 - 128 tokens.  (No
+    workspace: what passes the size check is refused after it, whatever the machine.)"""
+    most = (1 << 31) - 128
+    for page in (16, 128):
+        call = dict(D=D, Hq=Hq, T=T, pairs=D // 2, page=page, ws=None)
+        assert attend(lib, width=most // page, **call) == WORKSPACE
+        assert attend(lib, width=most // page + 1, **call) == INVALID
+    assert attend(lib, D=D, Hq=Hq, T=T, pairs=D // 2, page=48, width=most // 48 + 1, ws=None) == INVALID
