@@ -49,9 +49,10 @@ __device__ __forceinline__ void kv_lengths(const int32_t *start, const int32_t *
     fresh = n < 0 ? 0 : (n > T ? T : n);
 }
 
-__device__ __forceinline__ int64_t kv_rotation_row(const Rotation &r, int64_t bt, int position) {
-    const int p = r.positions ? r.positions[bt] : position;
-    return int64_t(p < 0 ? 0 : (p >= r.len ? r.len - 1 : p)) * r.pairs;
+// Where the angles of a sequence's new token t begin.
+__device__ __forceinline__ int64_t kv_rotation_row(const Rotation &r, int64_t bt, int before, int t) {
+    const int64_t p = r.positions ? r.positions[bt] : int64_t(before) + t;  // (the sum may pass 31 bits)
+    return (p < 0 ? 0 : (p >= r.len ? r.len - 1 : p)) * r.pairs;
 }
 
 // Dimension d's partner, angle index and the sign of the sine: rotated = x c + sign partner s.

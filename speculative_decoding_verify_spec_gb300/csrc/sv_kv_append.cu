@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const AppendArgs
     if (a.rot.cos) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) lo[i] = 0.f;
-        if (live && d0 < 2 * a.rot.pairs) rotate<kLayout, kBF16>(a, kp, d0, kv_rotation_row(a.rot, bt, before + t), x, lo);
+        if (live && d0 < 2 * a.rot.pairs) rotate<kLayout, kBF16>(a, kp, d0, kv_rotation_row(a.rot, bt, before, t), x, lo);
         kc = quantise<L, true>(x, lo, km);
     } else {
         kc = quantise<L, false>(x, x, km);

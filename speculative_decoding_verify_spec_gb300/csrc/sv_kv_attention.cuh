@@ -425,7 +425,7 @@ __device__ __forceinline__ void query_chunk(const AttArgs &a, const Unit &un, in
     const uint16_t *qp = a.q + un.b * a.q_bs + node * a.q_ts + head * a.q_hs;
     load8(qp + d0, a.vec, a.bf16, x);
     if (a.rot.cos && d0 < 2 * a.rot.pairs) {
-        const int64_t arow = kv_rotation_row(a.rot, int64_t(un.b) * a.T + node, un.before + node);
+        const int64_t arow = kv_rotation_row(a.rot, int64_t(un.b) * a.T + node, un.before, node);
         const float *cp = a.rot.cos + arow, *sp = a.rot.sin + arow;
         float y[8], cs[8], sn[8];
         if (!a.rot.interleaved && a.rot.pairs % 8 == 0) {  // the chunk lies within one half
