@@ -8,6 +8,12 @@
 // so the matrix products run on the bare codes (exact in fp16) and each token's scale and zero
 // cost a multiply-add per score instead of one per dimension.
 //
+// The second product's weights w_j = p_j s'_j are fp16, so their own maximum is what counts: with
+// X_j = x_j log2(e) + log2(s'_j) and m near the row's largest X_j of the tokens that it sees, w_j = 2^(X_j - m), p_j =
+// w_j / s'_j, and m cancels in the quotient.  Neither a token that the row does not see nor one of little weight then takes
+// bits from the others, however large its values are.  m lies so that the largest weight is 2^7 to 2^15: a weight keeps fp16's 11
+// bits down to 2^-21 of the largest at least, and is off by 2^-32 of that below.
+//
 // Work: a unit is 32 to 128 tokens for one (sequence, kv head, tile of 8 NR rows).  All units of the
 // batch form one list; each CTA takes an equal, contiguous share of it, so ragged lengths balance
 // by themselves and a long context spreads over the card.  A segment (one sequence, head, row
@@ -21,8 +27,8 @@
 // the cache as the 16-row operand (tokens x dimensions, dimensions x tokens) and the queries or
 // weights as the 8-column one, so that a single token's few heads are padded to 8 rows, not 16.  A
 // unit's scores are computed two units ahead of its product, which leaves one barrier per unit and
-// straight-line code between two of them.  The running maximum moves only when a score passes it by 2^8
-// (the weights fit fp16 either way).
+// straight-line code between two of them.  m moves only when a weight passes 2^15, to where it is 2^7 (the weights fit
+// fp16 either way).
 //
 // What bounds it.  The cache is read once per row tile: for few rows a byte of it needs about one instruction
 // slot a lane (unpacking, one HMMA per 16 tokens and 16 dimensions, the scores), and the warps that fit
@@ -41,7 +47,7 @@
 
 namespace sv {
 
-constexpr float kLazy = 8.f;            // log2 of how far a weight may pass 1
+constexpr float kTop = 7.f, kMost = 15.f;  // log2 of the largest weight where m moves, and of the largest there may be
 constexpr uint64_t kCopyLimitNs = 1000000000ull;
 constexpr int kAttSMs = 152;
 
@@ -76,7 +82,7 @@ struct AttArgs {
     int row_tiles;
     int *status;
     struct AttDesc *desc;  // [grid]
-    float2 *ml;            // [2 grid][R] running maximum (log2) and sum
+    float2 *ml;            // [2 grid][R] m (-inf: no score was seen) and the sum of w / s'
     float *acc;            // [2 grid][R][D]
 };
 
@@ -246,13 +252,12 @@ struct AttShared {
     alignas(128) uint8_t stage[kStages][kStageBytes];
     alignas(16) __half q[R * kQStride];
     alignas(16) __half p[2][NT * kPStride];       // [token][row]
-    // per pair of rows: their queries' sums and the scores that move the maximum (-inf until a score was
-    // seen); log2 scales of their scores and the negated maxima in log2 (0 until then)
+    // per pair of rows: their queries' sums and the log2 scales of their scores; what moves m (-inf until a score was
+    // seen), and -m (0 until then)
     alignas(16) float row_y[R / 2][4];
     alignas(16) float row_p[R / 2][4];
     alignas(16) float alpha[R];
     float red[2][NW][R];
-    uint32_t redv[NW];
     alignas(8) int row_node[R];  // the row's new token, -1: no live row
     alignas(8) uint64_t full[kStages], empty[kStages];
     Unit unit[kStages];
@@ -416,6 +421,23 @@ __device__ __forceinline__ void load8(const uint16_t *p, bool vec, bool bf16, fl
     }
 }
 
+// A value's scale s' and zero z', from their fp16 words, as the weights need them.
+struct ValueScale {
+    float log2, inverse, shift;  // log2(s'), 1 / s', (z' + 8 s') / s'
+    bool finite;
+};
+__device__ __forceinline__ ValueScale value_scale(uint32_t word) {
+    // at least 2^-24, as all are that were appended (so that slots of zeros have a logarithm too); NaN stays
+    asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(word) : "r"(0xFC000001u));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&word));
+    ValueScale v;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(v.log2) : "f"(f.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(v.inverse) : "f"(f.x));
+    v.shift = fmaf(f.y, v.inverse, 8.f);
+    v.finite = fabsf(f.x) < INFINITY && fabsf(f.y) < INFINITY;
+    return v;
+}
+
 // The power of two that is taken out of a row whose largest number has the bits `top`: that number becomes 2^10 .. 2^11
 // (less for rows below 2^-100).
 __device__ __forceinline__ int query_exponent(uint32_t top) { return top == 0 ? 0 : max(int(top >> 23) - 127 - 10, -110); }
@@ -510,8 +532,8 @@ __device__ __forceinline__ void load_queries(const AttArgs &a, AttShared<D, NR> 
         }
         if (c == 0 && !rest) {
             const float c2 = a.scale == 0.f ? 1.f : fmaxf(fabsf(a.scale) * 1.4426950408889634f * power2(e2), 1.2e-38f);
-            sh.row_y[r / 2][r & 1] = sum, sh.row_y[r / 2][2 + (r & 1)] = -INFINITY;
-            sh.row_p[r / 2][r & 1] = c2, sh.row_p[r / 2][2 + (r & 1)] = 0.f;
+            sh.row_y[r / 2][r & 1] = sum, sh.row_y[r / 2][2 + (r & 1)] = c2;
+            sh.row_p[r / 2][r & 1] = -INFINITY, sh.row_p[r / 2][2 + (r & 1)] = 0.f;
             sh.row_node[r] = on ? node : -1;
         }
     }
@@ -561,10 +583,9 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
     // MH 16-row tiles of dimensions x R rows: dimension 4 g + 2 h (+ 1, times 16) of the slice, rows 2 t4, 2 t4 + 1
     float acc[MH][NR][4];
     Two l[NR], z[NR];     // of rows 2 t4, 2 t4 + 1
-    float s[NG][NR][4];   // scores of tokens g, g + 8 of each group, rows 2 t4, 2 t4 + 1
-    float vs[NG][2], vz[NG][2];
+    float s[NG][NR][4];   // X of tokens g, g + 8 of each group, rows 2 t4, 2 t4 + 1
+    float vi[NG][2], vz[NG][2];  // of those tokens' values: 1 / s', (z' + 8 s') / s'
     uint32_t qf[kQRegs ? KS : 2][kQRegs ? NR : 1][2];
-    int vexp = 0;         // values' scales are divided by 2^vexp: all are below 1 then
     bool waits = true;
     int stage = 0;
     uint32_t phase = 0;
@@ -577,7 +598,7 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
             atomicExch(a.status, int(SV_ERR_TIMEOUT));
         }
     };
-    // The scores of this warp's tokens of a unit; whether they move a maximum.
+    // X of this warp's tokens of a unit; whether they move some row's m.
     auto score = [&](int st) -> bool {
         const Unit &un = sh.unit[st];
         const uint8_t *kc = sh.stage[st];
@@ -657,15 +678,16 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
                 }
         }
         // y = s_j (q . (code_j - 8)) + (z_j + 8 s_j) sum(q)
-        float ks[NG][2], kz[NG][2], top = 0.f;
+        float ks[NG][2], kz[NG][2], vl[NG][2];
 #pragma unroll
         for (int i = 0; i < NG; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t kk = km[i * 16 + h * 8], vv = vm[i * 16 + h * 8];
-                const float2 kf = __half22float2(*reinterpret_cast<const __half2 *>(&kk)), vf = __half22float2(*reinterpret_cast<const __half2 *>(&vv));
+                const float2 kf = __half22float2(*reinterpret_cast<const __half2 *>(&kk));
                 ks[i][h] = kf.x, kz[i][h] = fmaf(8.f, kf.x, kf.y);
-                vs[i][h] = vf.x, vz[i][h] = fmaf(8.f, vf.x, vf.y);
+                const ValueScale v = value_scale(vv);
+                vl[i][h] = v.log2, vi[i][h] = v.inverse, vz[i][h] = v.shift;
             }
         uint32_t see = 0xFFFFFFFFu;
         if (un.masked) {
@@ -702,25 +724,24 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const bool here = loaded(warp * TW + i * 16 + h * 8 + g);
-                    if (!here || !(fabsf(vs[i][h]) < INFINITY && fabsf(vz[i][h]) < INFINITY)) {
-                        vs[i][h] = vz[i][h] = 0.f;
+                    if (!here || !value_scale(vm[i * 16 + h * 8]).finite) {
+                        vl[i][h] = vi[i][h] = vz[i][h] = 0.f;
                         ks[i][h] = NAN;
                     }
                 }
         }
-#pragma unroll
-        for (int i = 0; i < NG; ++i) top = fmaxf(top, fmaxf(vs[i][0], vs[i][1]));
-        bool need = !(top < power2(vexp));
+        bool need = false;
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            const float2 ry = *reinterpret_cast<const float2 *>(sh.row_y[n * 4 + t4]);
-            const Two qs = two(ry.x, ry.y);
+            const float4 ry = *reinterpret_cast<const float4 *>(sh.row_y[n * 4 + t4]);
+            const Two qs = two(ry.x, ry.y), c = two(ry.z, ry.w);
 #pragma unroll
             for (int i = 0; i < NG; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float *y = s[i][n] + 2 * h;
-                    const float2 r = split(fma2(two(y[0], y[1]), two(ks[i][h], ks[i][h]), mul2(qs, two(kz[i][h], kz[i][h]))));
+                    const Two x = fma2(two(y[0], y[1]), two(ks[i][h], ks[i][h]), mul2(qs, two(kz[i][h], kz[i][h])));
+                    const float2 r = split(fma2(x, c, two(vl[i][h], vl[i][h])));
                     y[0] = r.x, y[1] = r.y;
                 }
         }
@@ -736,22 +757,17 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
         }
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            const float2 ry = *reinterpret_cast<const float2 *>(&sh.row_y[n * 4 + t4][2]);
+            const float2 most = *reinterpret_cast<const float2 *>(sh.row_p[n * 4 + t4]);
             float y0 = -INFINITY, y1 = -INFINITY;
 #pragma unroll
             for (int i = 0; i < NG; ++i) y0 = fmaxf(y0, fmaxf(s[i][n][0], s[i][n][2])), y1 = fmaxf(y1, fmaxf(s[i][n][1], s[i][n][3]));
-            need |= y0 > ry.x || y1 > ry.y;
+            need |= y0 > most.x || y1 > most.y;
         }
         return need;
     };
-    // Some row's maximum moves (the first unit's always does), or the values' exponent.  The weights of the unit before,
-    // in buffer buf (-1: none), move along.
+    // Some row's m moves (the first unit's always does).  The weights of the unit before, in buffer buf (-1: none), move
+    // along.
     auto update = [&](int buf) {
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < NG; ++i) top = fmaxf(top, fmaxf(vs[i][0], vs[i][1]));
-        const uint32_t wtop = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
-        if (lane == 0) sh.redv[warp] = wtop;
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -768,17 +784,10 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
             float y = sh.red[0][0][r];
 #pragma unroll
             for (int w = 1; w < NW; ++w) y = fmaxf(y, sh.red[0][w][r]);
-            const float c = sh.row_p[r / 2][r & 1];
-            const float seen = sh.row_y[r / 2][2 + (r & 1)] == -INFINITY ? -INFINITY : -sh.row_p[r / 2][2 + (r & 1)], mn = fmaxf(seen, y * c);
+            const float seen = sh.row_p[r / 2][r & 1] == -INFINITY ? -INFINITY : -sh.row_p[r / 2][2 + (r & 1)], mn = fmaxf(seen, y - kTop);
             sh.alpha[r] = seen == -INFINITY ? 0.f : ex2(seen - mn);
-            if (mn != -INFINITY) sh.row_p[r / 2][2 + (r & 1)] = -mn, sh.row_y[r / 2][2 + (r & 1)] = (mn + kLazy) / c;
+            if (mn != -INFINITY) sh.row_p[r / 2][r & 1] = mn + kMost, sh.row_p[r / 2][2 + (r & 1)] = -mn;
         }
-        uint32_t all = 0;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) all = max(all, sh.redv[w]);
-        const int vnew = max(vexp, int(all >> 23) - 126);
-        const float kfac = power2(vexp - vnew);
-        vexp = vnew;
         consumers_sync<C>();
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
@@ -786,8 +795,8 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
             l[n] = mul2(l[n], two(al.x, al.y)), z[n] = mul2(z[n], two(al.x, al.y));
 #pragma unroll
             for (int h = 0; h < MH; ++h) {
-                acc[h][n][0] *= al.x * kfac, acc[h][n][1] *= al.y * kfac;
-                acc[h][n][2] *= al.x * kfac, acc[h][n][3] *= al.y * kfac;
+                acc[h][n][0] *= al.x, acc[h][n][1] *= al.y;
+                acc[h][n][2] *= al.x, acc[h][n][3] *= al.y;
             }
         }
         if (buf >= 0) {
@@ -795,32 +804,28 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
                 const int tok = i / (NR * 4), r = i % (NR * 4) * 2;
                 __half2 *w = reinterpret_cast<__half2 *>(&sh.p[buf][tok * Sh::kPStride + r]);
                 const float2 v = __half22float2(*w);
-                *w = __floats2half2_rn(v.x * sh.alpha[r] * kfac, v.y * sh.alpha[r + 1] * kfac);
+                *w = __floats2half2_rn(v.x * sh.alpha[r], v.y * sh.alpha[r + 1]);
             }
             consumers_sync<C>();
         }
     };
-    // Weights: p for the sums (this warp's tokens), p s' for the product, rounded to fp16.
+    // Weights: w / s' and w (z' + 8 s') / s' for the sums (this warp's tokens), w for the product, rounded to fp16.
     auto weigh = [&](int buf) {
-        const float down = power2(-vexp);
-        float vd[NG][2];
-#pragma unroll
-        for (int i = 0; i < NG; ++i) vd[i][0] = vs[i][0] * down, vd[i][1] = vs[i][1] * down;
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            const float4 rp = *reinterpret_cast<const float4 *>(sh.row_p[n * 4 + t4]);
-            const Two c = two(rp.x, rp.y), minus = two(rp.z, rp.w);
+            const float2 rp = *reinterpret_cast<const float2 *>(&sh.row_p[n * 4 + t4][2]);
+            const Two minus = two(rp.x, rp.y);
 #pragma unroll
             for (int i = 0; i < NG; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float2 x = split(fma2(two(s[i][n][2 * h], s[i][n][2 * h + 1]), c, minus));
-                    const Two pw = two(ex2(x.x), ex2(x.y));
-                    l[n] = add2(l[n], pw);
-                    z[n] = fma2(pw, two(vz[i][h], vz[i][h]), z[n]);
-                    const float2 w = split(mul2(pw, two(vd[i][h], vd[i][h])));
+                    const float2 x = split(add2(two(s[i][n][2 * h], s[i][n][2 * h + 1]), minus));
+                    const float w0 = ex2(x.x), w1 = ex2(x.y);
+                    const Two w = two(w0, w1);
+                    l[n] = fma2(w, two(vi[i][h], vi[i][h]), l[n]);
+                    z[n] = fma2(w, two(vz[i][h], vz[i][h]), z[n]);
                     *reinterpret_cast<__half2 *>(&sh.p[buf][(warp * TW + i * 16 + h * 8 + g) * Sh::kPStride + n * 8 + 2 * t4]) =
-                        __floats2half2_rn(w.x, w.y);
+                        __floats2half2_rn(w0, w1);
                 }
         }
     };
@@ -896,7 +901,6 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[h][n][k] = 0.f;
         }
-        vexp = -24;
         const int seg_lo = ubegin + it - seg.tile;
         const bool whole = it >= seg.tile && it + seg.tiles - seg.tile <= units;
 
@@ -908,7 +912,7 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
         auto nothing = [&]() {  // scores of no token
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
-                vs[i][0] = vs[i][1] = vz[i][0] = vz[i][1] = 0.f;
+                vi[i][0] = vi[i][1] = vz[i][0] = vz[i][1] = 0.f;
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -959,7 +963,6 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
             }
         consumers_sync<C>();
         const int64_t slot = 2 * cta + (seg_lo > ubegin ? 1 : 0);
-        const float up = power2(vexp), up16 = up * 0.0625f;
         const int d0 = slice * 32 + 4 * g + 2 * part;
 #pragma unroll
         for (int n = 0; n < NR; ++n)
@@ -971,7 +974,7 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
                 for (int w = 0; w < NW; ++w) sl += sh.red[0][w][r], sz += sh.red[1][w][r];
                 float o[2 * MH];
 #pragma unroll
-                for (int h = 0; h < MH; ++h) o[2 * h] = fmaf(acc[h][n][k], up, sz), o[2 * h + 1] = fmaf(acc[h][n][2 + k], up16, sz);
+                for (int h = 0; h < MH; ++h) o[2 * h] = acc[h][n][k] + sz, o[2 * h + 1] = fmaf(acc[h][n][2 + k], 0.0625f, sz);
                 if (whole) {
                     const int row = seg.rt * R + r, node = row / a.G;
                     if (node < a.T) {
@@ -989,7 +992,7 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
 #pragma unroll
                     for (int h = 0; h < MH; ++h) dst[h] = make_float2(o[2 * h], o[2 * h + 1]);
                     if (warp == 0 && g == 0)
-                        a.ml[slot * R + r] = make_float2(sh.row_y[r / 2][2 + k] == -INFINITY ? -INFINITY : -sh.row_p[r / 2][2 + k], sl);
+                        a.ml[slot * R + r] = make_float2(sh.row_p[r / 2][k] == -INFINITY ? -INFINITY : -sh.row_p[r / 2][2 + k], sl);
                 }
             }
         if (tid == 0 && seg_lo <= ubegin)  // the share's first segment

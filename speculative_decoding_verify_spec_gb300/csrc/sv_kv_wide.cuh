@@ -39,11 +39,11 @@ struct WideShared {
     alignas(1024) uint8_t w[kWideRows * 128];   // [row][64 tokens]
     alignas(128) uint8_t stage[kWideStages][kStageBytes];
     alignas(16) float key_of[kWideTokens / 2][4];    // of a token pair: scales, zeros + 8 scales
-    alignas(16) float value_of[kWideTokens / 2][4];
+    alignas(16) float value_of[kWideTokens / 2][4];  // 1 / s', (z' + 8 s') / s'
+    alignas(8) float log2_of[kWideTokens / 2][2];    // log2(s')
     float row_c[kWideRows], row_q[kWideRows];
     int row_node[kWideRows];
     float red[2][2][kWideRows];
-    uint32_t redv[8];
     alignas(8) uint64_t full[kWideStages], empty[kWideStages], scores, products;
     alignas(16) Unit unit[kWideStages];
     uint32_t tmem;
@@ -229,8 +229,7 @@ __global__ void __launch_bounds__(kWideThreads, wide_occupancy(D)) kv_wide_kerne
             const bool warp_on = __any_sync(0xFFFFFFFFu, node >= 0);  // rows past the last one: nothing to score
             const Two qs = two(qsum, qsum), cc = two(c2, c2);
             Two l = 0, z = 0;
-            float m = 0.f, thr = -INFINITY;  // the maximum in log2, 0 until a score was seen
-            int vexp = -24;
+            float m = 0.f, thr = -INFINITY;  // m, 0 until a score was seen, and what moves it
             const int seg_lo = ubegin + it - seg.tile;
             const bool whole = it >= seg.tile && it + seg.tiles - seg.tile <= units;
 
@@ -264,14 +263,14 @@ __global__ void __launch_bounds__(kWideThreads, wide_occupancy(D)) kv_wide_kerne
                     }
                 }
                 if (tid < NT) {  // scales and zeros; of tokens that are not there, nothing
-                    const float2 kf = __half22float2(*reinterpret_cast<const __half2 *>(km + tid)), vf = __half22float2(*reinterpret_cast<const __half2 *>(vm + tid));
-                    float ks = kf.x, kz = fmaf(8.f, kf.x, kf.y), vs = vf.x, vz = fmaf(8.f, vf.x, vf.y);
+                    const float2 kf = __half22float2(*reinterpret_cast<const __half2 *>(km + tid));
+                    float ks = kf.x, kz = fmaf(8.f, kf.x, kf.y);
+                    ValueScale v = value_scale(vm[tid]);
                     // a NaN value reaches the rows that see it by their score
-                    if ((masked && !loaded(tid)) || !(fabsf(vs) < INFINITY && fabsf(vz) < INFINITY)) vs = vz = 0.f, ks = NAN;
+                    if ((masked && !loaded(tid)) || !v.finite) v.log2 = v.inverse = v.shift = 0.f, ks = NAN;
                     sh.key_of[tid / 2][tid & 1] = ks, sh.key_of[tid / 2][2 + (tid & 1)] = kz;
-                    sh.value_of[tid / 2][tid & 1] = vs, sh.value_of[tid / 2][2 + (tid & 1)] = vz;
-                    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(vs, 0.f)));
-                    if (lane == 0) sh.redv[warp] = top;
+                    sh.value_of[tid / 2][tid & 1] = v.inverse, sh.value_of[tid / 2][2 + (tid & 1)] = v.shift;
+                    sh.log2_of[tid / 2][tid & 1] = v.log2;
                 }
                 fence_operands();
                 fence_before();
@@ -337,13 +336,12 @@ __global__ void __launch_bounds__(kWideThreads, wide_occupancy(D)) kv_wide_kerne
                 if (lane == 0) mbar_arrive(smem_u32(&sh.empty[stage]));  // (nothing more of the stage, or `un`, is read)
                 wait(&sh.scores, turn);
                 fence_after();
-                const float top = __uint_as_float(max(sh.redv[0], sh.redv[1]));
-                bool weighed = it > first;  // a segment's first unit moves the maximum: no use in weights before
-                bool need = !weighed || !(top < power2(vexp)), again = false;
+                bool weighed = it > first;  // a segment's first unit moves m: no use in weights before
+                bool need = !weighed, again = false;
                 Two dl = 0, dz = 0;
                 while (true) {
                     if (warp_on) {
-                        const Two minus = two(-m, -m), dd = two(power2(-vexp), power2(-vexp));
+                        const Two minus = two(-m, -m);
                         float most = -INFINITY;
                         dl = 0, dz = 0;
 #pragma unroll
@@ -353,8 +351,10 @@ __global__ void __launch_bounds__(kWideThreads, wide_occupancy(D)) kv_wide_kerne
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 const float4 k = *reinterpret_cast<const float4 *>(sh.key_of[half * 16 + 8 * c + j]);
-                                const float2 v = split(fma2(two(s[2 * j], s[2 * j + 1]), two(k.x, k.y), mul2(qs, two(k.z, k.w))));
-                                s[2 * j] = v.x, s[2 * j + 1] = v.y;
+                                const float2 v = *reinterpret_cast<const float2 *>(sh.log2_of[half * 16 + 8 * c + j]);
+                                const Two y = fma2(two(s[2 * j], s[2 * j + 1]), two(k.x, k.y), mul2(qs, two(k.z, k.w)));
+                                const float2 x = split(fma2(y, cc, two(v.x, v.y)));
+                                s[2 * j] = x.x, s[2 * j + 1] = x.y;
                             }
                             if (masked) {
                                 __syncwarp();
@@ -372,12 +372,11 @@ __global__ void __launch_bounds__(kWideThreads, wide_occupancy(D)) kv_wide_kerne
                                     for (int i = 0; i < 4; ++i) {
                                         const int j = 4 * d + i;
                                         const float4 v = *reinterpret_cast<const float4 *>(sh.value_of[half * 16 + 8 * c + j]);
-                                        const float2 x = split(fma2(two(s[2 * j], s[2 * j + 1]), cc, minus));
-                                        const Two p = two(ex2(x.x), ex2(x.y));
-                                        dl = add2(dl, p);
-                                        dz = fma2(p, two(v.z, v.w), dz);
-                                        const float2 f = split(mul2(p, mul2(two(v.x, v.y), dd)));
-                                        const __half2 h = __floats2half2_rn(f.x, f.y);
+                                        const float2 x = split(add2(two(s[2 * j], s[2 * j + 1]), minus));
+                                        const float p0 = ex2(x.x), p1 = ex2(x.y);
+                                        dl = fma2(two(p0, p1), two(v.x, v.y), dl);
+                                        dz = fma2(two(p0, p1), two(v.z, v.w), dz);
+                                        const __half2 h = __floats2half2_rn(p0, p1);
                                         w[i] = *reinterpret_cast<const uint32_t *>(&h);
                                     }
                                     *reinterpret_cast<uint4 *>(sh.w + wide_chunk(r, half * 4 + 2 * c + d)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -390,13 +389,12 @@ __global__ void __launch_bounds__(kWideThreads, wide_occupancy(D)) kv_wide_kerne
                     fence_operands();
                     fence_before();
                     if (!consumers_or<C>(need)) break;
-                    // some row's maximum moves (the first unit's always does), or the values' exponent: again
-                    const int vnew = max(vexp, int(__float_as_uint(top) >> 23) - 126);
+                    // some row's m moves (the first unit's always does): again
                     if (warp_on) {
                         const float y = fmaxf(sh.red[0][0][r], sh.red[0][1][r]);
-                        const float seen = thr == -INFINITY ? -INFINITY : m, mn = fmaxf(seen, y * c2);
-                        const float al = seen == -INFINITY ? 0.f : ex2(seen - mn), f = al * power2(vexp - vnew);
-                        if (mn != -INFINITY) m = mn, thr = (mn + kLazy) / c2;
+                        const float seen = thr == -INFINITY ? -INFINITY : m, mn = fmaxf(seen, y - kTop);
+                        const float al = seen == -INFINITY ? 0.f : ex2(seen - mn);
+                        if (mn != -INFINITY) m = mn, thr = mn + kMost;
                         l = mul2(l, two(al, al)), z = mul2(z, two(al, al));
                         if (it > first) {  // (the last unit's product is done: its codes' place has been taken)
                             fence_after();
@@ -405,12 +403,11 @@ __global__ void __launch_bounds__(kWideThreads, wide_occupancy(D)) kv_wide_kerne
                                 float o[32];
                                 tmem_load32(o, tmem_o + col);
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) o[j] *= f;
+                                for (int j = 0; j < 32; ++j) o[j] *= al;
                                 tmem_store32(o, tmem_o + col);
                             }
                         }
                     }
-                    vexp = vnew;
                     need = false, weighed = again = true;
                     consumers_sync<C>();  // (the maxima are read)
                 }
@@ -435,7 +432,6 @@ __global__ void __launch_bounds__(kWideThreads, wide_occupancy(D)) kv_wide_kerne
             wait(&sh.products, turn ^ 1);
             fence_after();
             const float sl = sh.red[0][0][r] + sh.red[0][1][r], sz = sh.red[1][0][r] + sh.red[1][1][r];
-            const float up = power2(vexp), up16 = up * 0.0625f;
             const int row = seg.rt * R + r, at = row / a.G;
             const int64_t slot = 2 * cta + (seg_lo > ubegin ? 1 : 0);
             const float inv = node < 0 || sl == 0.f ? 0.f : 1.f / sl;
@@ -445,7 +441,7 @@ __global__ void __launch_bounds__(kWideThreads, wide_occupancy(D)) kv_wide_kerne
                 float o[32];
                 tmem_load32(o, tmem_o + col);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = warp_on ? fmaf(o[j], j & 1 ? up16 : up, sz) : 0.f;
+                for (int j = 0; j < 32; ++j) o[j] = warp_on ? fmaf(o[j], j & 1 ? 0.0625f : 1.f, sz) : 0.f;
                 if (whole) {
                     if (at < a.T) {
 #pragma unroll
