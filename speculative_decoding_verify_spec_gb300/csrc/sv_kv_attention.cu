@@ -4,6 +4,10 @@
 
 namespace sv {
 
+#ifdef SV_CHECKS
+__device__ int g_kv_lose = -1;
+#endif
+
 template <>
 cudaError_t launch_attention_rows<64, false>(const AttArgs &a, int nr, int grid, cudaStream_t s);
 template <>
@@ -138,6 +142,15 @@ sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_tok
     else
         e = exact ? sv::launch_attention_rows<256, true>(a, nr, grid, s) : sv::launch_attention_rows<256, false>(a, nr, grid, s);
     return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+sv_status spec_kv_lose_unit(int unit) {
+#ifdef SV_CHECKS
+    return cudaMemcpyToSymbol(sv::g_kv_lose, &unit, sizeof(unit)) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+#else
+    (void)unit;
+    return SV_ERR_UNSUPPORTED;
+#endif
 }
 
 }  // extern "C"

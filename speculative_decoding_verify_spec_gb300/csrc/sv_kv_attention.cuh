@@ -306,7 +306,12 @@ __device__ __forceinline__ bool find_share(const AttArgs &a, int R, int lane, in
     return true;
 }
 
-// The copying warp: the units of the share into the ring, up to kStages ahead of the consumers.
+#ifdef SV_CHECKS
+extern __device__ int g_kv_lose;  // see spec_kv_lose_unit
+#endif
+
+// The copying warp: the units of the share into the ring, up to kStages ahead of the consumers.  Returns when all copies
+// that it has begun are there (waiting as long as it may): a block must not end with copies under way into its shared memory.
 template <int D, int NT, int kStages, typename Shared>
 __device__ __forceinline__ void copy_units(const AttArgs &a, Shared &sh, Cursor<NT> &cur, int ubegin, int uend, int R, int lane) {
     // Lanes take (granule, piece) pairs: keys,
@@ -322,6 +327,7 @@ __device__ __forceinline__ void copy_units(const AttArgs &a, Shared &sh, Cursor<
     const int64_t page_bytes = kv_page_bytes(a.page, D), head_step = int64_t(a.H) * page_bytes;
     int pi = 0, slot = 0, stage = 0, wrap = 0;  // this lane's granule: page of the sequence, slot in it
     uint32_t phase = 1;
+    int begun = 0;
     bool placed = false;
     for (int u = ubegin; u < uend; ++u) {
         if (!placed) {
@@ -336,8 +342,11 @@ __device__ __forceinline__ void copy_units(const AttArgs &a, Shared &sh, Cursor<
         const uint32_t sum = have == all_granules ? all_bytes : __reduce_add_sync(0xFFFFFFFFu, here ? bytes : 0u);
         if (wrap > 0 && !mbar_wait(smem_u32(&sh.empty[stage]), phase)) {
             atomicExch(a.status, int(SV_ERR_TIMEOUT));
-            return;  // (the consumers' waits give up too)
+            break;  // (the consumers' waits give up too)
         }
+#ifdef SV_CHECKS
+        if (u - ubegin == g_kv_lose) break;
+#endif
         const uint32_t bar = smem_u32(&sh.full[stage]);
         if (lane == 0) {
             int4 *un = reinterpret_cast<int4 *>(&sh.unit[stage]);
@@ -349,6 +358,7 @@ __device__ __forceinline__ void copy_units(const AttArgs &a, Shared &sh, Cursor<
         __syncwarp();
         if (here)
             bulk_load(smem_u32(sh.stage[stage]) + to, a.cache + pg * head_step + cur.h * page_bytes + from + slot * each, bytes, bar);
+        ++begun;
         if (++stage == kStages) stage = 0, phase ^= 1, wrap = 1;
         if (cur.tile + 1 < cur.tiles()) {
             ++cur.tile;
@@ -359,6 +369,8 @@ __device__ __forceinline__ void copy_units(const AttArgs &a, Shared &sh, Cursor<
             placed = false;
         }
     }
+    for (int i = max(0, begun - kStages); i < begun; ++i)
+        if (!mbar_wait(smem_u32(&sh.full[i % kStages]), uint32_t(i / kStages) & 1u)) atomicExch(a.status, int(SV_ERR_TIMEOUT));
 }
 
 // Two fp32 numbers in a register pair, worked on by one instruction.
@@ -864,7 +876,7 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
     Unit seg{cur.b, cur.h, cur.rt, cur.tile, cur.tiles(), cur.w.before, cur.w.len, cur.live ? cur.w.fresh : 0, 0, 0, {0, 0}};
     for (int it = 0;;) {  // segments
         const int last = min(units, it + seg.tiles - seg.tile);  // past the segment's last unit here
-        consumers_sync<C>();
+        if (consumers_or<C>(!waits)) break;  // a wait gave up, some thread's at least: `seg` may not be there
         load_queries<D, NR, kExact>(a, sh, seg, tid, false, sh.q);
         if (a.parent)
             for (int r = tid; r < R; r += C) {

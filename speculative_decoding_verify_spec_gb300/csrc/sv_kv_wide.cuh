@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kWideThreads, wide_occupancy(D)) kv_wide_kerne
         Unit seg{cur.b, cur.h, cur.rt, cur.tile, cur.tiles(), cur.w.before, cur.w.len, cur.live ? cur.w.fresh : 0, 0, 0, {0, 0}};
         for (int it = 0;;) {  // segments
             const int last = min(units, it + seg.tiles - seg.tile), first = it;
-            consumers_sync<C>();
+            if (consumers_or<C>(!waits)) break;  // a wait gave up, some thread's at least: `seg` may not be there
             wide_queries<D, kExact>(a, sh, seg, tid);
             if (a.parent && tid < R) {
                 uint32_t *anc = anc_s + tid * anc_words;
@@ -469,6 +469,8 @@ __global__ void __launch_bounds__(kWideThreads, wide_occupancy(D)) kv_wide_kerne
             wait(&sh.full[stage], phase);
             seg = sh.unit[stage];
         }
+        // where a wait gave up, products may still be under way: the last chance that they get before their operands' place goes
+        if (tid == 0 && !waits) mbar_wait(smem_u32(&sh.scores), turn ^ 1), mbar_wait(smem_u32(&sh.products), turn ^ 1);
     }
     __syncthreads();
     fence_after();

@@ -40,6 +40,8 @@ def _library() -> ctypes.CDLL:
         lib.spec_kv_attention.argtypes = [P, i64, i64, i64, i32, i32, i32, i32, i32, i32, P, i32, i32, P, i32, P, P, P,
                                           f32, P, P, i32, i32, i32, P, P, P, sz, P]
         lib.spec_kv_attention.restype = i32
+        lib.spec_kv_lose_unit.argtypes = [i32]
+        lib.spec_kv_lose_unit.restype = i32
         _ready = lib
     return _ready
 
@@ -256,3 +258,8 @@ def spec_kv_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Te
                                int(interleaved), _ptr(positions), out.data_ptr(), workspace.data_ptr(), n, _current(dev))
     _check(st, "spec_kv_attention")
     return out
+
+
+def lose_unit(unit: int) -> int:
+    """Test hook of the bounds-checked build (see spec_kv_lose_unit); returns the status."""
+    return int(_library().spec_kv_lose_unit(unit))
