@@ -401,10 +401,11 @@ __device__ __forceinline__ Two add2(Two a, Two b) {
     return r;
 }
 __device__ __forceinline__ float power2(int e) { return __int_as_float((127 + e) << 23); }  // -126 <= e <= 127
-// Barriers of the D consumer threads.
+// Barriers of the N consumer threads, whole warps: each warp is together afterwards, as the matrix instructions need it.
 template <int N>
 __device__ __forceinline__ void consumers_sync() {
     asm volatile("barrier.cta.sync 1, %0;" ::"n"(N) : "memory");
+    __syncwarp();
 }
 template <int N>
 __device__ __forceinline__ bool consumers_or(bool x) {
@@ -414,6 +415,7 @@ __device__ __forceinline__ bool consumers_or(bool x) {
         : "=r"(r)
         : "r"(uint32_t(x)), "n"(N)
         : "memory");
+    __syncwarp();
     return r != 0;
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
@@ -609,6 +611,7 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
             waits = false;  // reported; no further waits
             atomicExch(a.status, int(SV_ERR_TIMEOUT));
         }
+        __syncwarp();  // (lanes may leave the wait at different times, and matrix instructions follow)
     };
     // X of this warp's tokens of a unit; whether they move some row's m.
     auto score = [&](int st) -> bool {

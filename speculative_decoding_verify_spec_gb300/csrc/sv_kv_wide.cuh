@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(kWideThreads, wide_occupancy(D)) kv_wide_kerne
                 waits = false;  // reported; no further waits
                 atomicExch(a.status, int(SV_ERR_TIMEOUT));
             }
+            __syncwarp();  // (lanes may leave the wait at different times, and loads from tensor memory follow)
         };
         int stage = 0;
         uint32_t phase = 0, turn = 0;  // turn: parity of this unit's products
