@@ -102,7 +102,8 @@ size_t spec_kv_page_bytes(int page_size, int head_dim);
  *              the first three axes, contiguous last axis.
  *   k_values, v_values   [B][T][kv_heads][head_dim] contiguous, of the inputs' type, NULL: not
  *              wanted: what the cache holds for the new tokens, as an attention over them in
- *              16 bits would read it; 0 for tokens from new_lens[b] on.
+ *              16 bits would read it; 0 for tokens from new_lens[b] on.  A token that is dropped
+ *              (past the table, or its page out of range) gets what it would have been held as.
  * Two sequences must not append to the same slot.  No workspace.
  */
 sv_status spec_kv_append(const void *k, int64_t k_batch_stride, int64_t k_token_stride, int64_t k_head_stride,

@@ -195,7 +195,8 @@ def spec_kv_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_t
 
     cos, sin [positions, pairs] fp32 turn the first 2 * pairs dimensions by the angles of the tokens' positions
     (`positions` [B, T], else start[b] + t).  With `return_values`, or `k_values` and `v_values` given, returns what the
-    cache now holds for the new tokens, in the inputs' type; else None."""
+    cache now holds for the new tokens, in the inputs' type (0 from new_lens[b] on; for a token dropped at the table's end or at a
+    page out of range, what it would have been held as); else None."""
     lib = _library()
     ks, dt, dev, shape = _heads4(k, "k"), _kv_dtype(k, "k"), k.device, k.shape
     vs = _heads4(v, "v")
@@ -230,7 +231,10 @@ def spec_kv_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Te
     the new tokens already (see spec_kv_append: same cache, page_table, start, new_lens and rotation).
 
     Token t sees the tokens before start[b], and of the new ones 0 .. t (a chain), or its ancestors and itself
-    if `parent` [T] gives a tree.  scale defaults to head_dim ** -0.5.  Returns [B, T, heads, head_dim]."""
+    if `parent` [T] gives a tree.  scale defaults to head_dim ** -0.5.  Returns [B, T, heads, head_dim].
+
+    The first int32 of `workspace` (spec_kv_attention_workspace_size bytes; one of the call's own unless given) is the call's status
+    once the stream has completed: 0, or 4 if a bounded wait on the device gave up and the result is of no use."""
     lib = _library()
     qs, dt, dev = _heads4(q, "q"), _kv_dtype(q, "q"), q.device
     B, T, Hq, D = q.shape
