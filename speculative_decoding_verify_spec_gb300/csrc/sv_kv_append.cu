@@ -10,8 +10,8 @@
 // partners eight dimensions apart in one place (halves) or in the lane itself (neighbours), else any.
 //
 // Measured: 256 x 9 tokens of 8 heads of 128 dimensions 11.7 us (1.9 TB/s), 8 prompts of up to 2001 tokens, 16 heads
-// of 64, 52 us (2.5 TB/s).  The two-float rotation, the extremes and the codes are 70 % of the ALU's issue rate: that
-// bounds it, at about 25 instructions a dimension.
+// of 64, 52 us (2.5 TB/s).  The two-float rotation, the extremes and the codes keep the ALU pipe at 60 %: the
+// largest part of what bounds it, at about 25 instructions a dimension.
 #include <cstdint>
 
 #include "sv_checks.cuh"

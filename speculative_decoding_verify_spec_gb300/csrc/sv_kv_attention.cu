@@ -36,10 +36,11 @@ cudaError_t launch_wide_of<256, false>(const AttArgs &a, int grid, cudaStream_t 
 
 namespace {
 
-// More rows than this a kv head go to the kernel for many rows.  64 sequences of 2047 cached tokens at most, 128 dimensions,
-// rotated fp16 queries, us: 56 rows 130 in tiles of 32, 72 rows 173 and 146 in one of 128, 128 rows 316 and 156, 256 rows 619
-// and 286; 256 dimensions, bf16: 72 rows 225 in tiles of 40 and 204, 128 rows 350 and 222, 256 rows 755 and 395, but 27 and
-// 35 for one sequence alone, whose blocks have a unit or two each.  48 of 3000, 64 dimensions: 72 rows 75 and 81, 96 rows 92 and 79, 128 rows 119 and 81.
+// More rows than this a kv head go to the kernel for many rows.  64 sequences of up to 2047 cached tokens, 4 query heads a kv head, us in
+// tiles of up to 48 rows and in one of 128: 64 dimensions, bf16, 56 rows 67 and 64, 72 rows 75 and 67; 128 dimensions, bf16, 64 rows 90 and
+// 120, 72 rows 107 and 122, 96 rows 161 and 122; the same, rotated fp16, 56 rows 137 and 145, 72 rows 185 and 150, 256 rows 608 and 291;
+// 256 dimensions, bf16, 48 rows 147 and 194, 64 rows 184 and 200, 72 rows 216 and 206, 256 rows 717 and 402, but 26 and 36 for one
+// sequence alone, whose blocks have a unit or two each.
 constexpr int kNarrowRows = 64;
 // Both parts of rotated fp16 queries of 256 dimensions do not fit its shared memory.
 bool att_wide(int64_t rows, int D, bool exact) { return rows > kNarrowRows && !(D == 256 && exact); }

@@ -33,8 +33,8 @@
 // What bounds it.  The cache is read once per row tile: for few rows a byte of it needs about one instruction
 // slot a lane (unpacking, one HMMA per 16 tokens and 16 dimensions, the scores), and the warps that fit
 // the registers issue 2.4 instructions a clock: 256 single tokens with 8 heads a kv head over 4600 cached ones
-// on average take 0.30 ms, 4.3 TB/s of the cache.  For many rows the HMMA rate (one m16n8k16 in 2 clocks a
-// SM) and the scores' exponentials join in: 64 x 9 drafts with 4 heads a kv head take 0.17 ms, 130 TFLOP/s.
+// on average take 0.31 ms, 4.2 TB/s of the cache.  For many rows the HMMA rate (one m16n8k16 in 2 clocks a
+// SM) and the scores' exponentials join in: 64 x 9 drafts with 4 heads a kv head take 0.16 ms, 140 TFLOP/s.
 #pragma once
 
 #include <cstdint>
@@ -61,7 +61,7 @@ __host__ __device__ constexpr int att_stages(int D, int NR) { return 4; }
 __host__ __device__ constexpr int att_occupancy(int D, int NR) { return D == 256 ? 1 : D == 128 ? (NR <= 5 ? 3 : 2) : (NR <= 2 ? 4 : 3); }
 // Tiles of 8 NR rows: as few as there have to be and no larger than they need be.  At most 48 rows, for more spill
 // (64 rows of 128 dimensions do, by 250 bytes a thread); 32 of 64 dimensions, where 64 x 64 tree nodes with 4 query heads a
-// kv head take 253 us in tiles of 32 rows, 267 in tiles of 64 and 276 in tiles of 16; 40 of 256, by shared memory.
+// kv head took 253 us in tiles of 32 rows (255 now), 267 in tiles of 64 and 276 in tiles of 16; 40 of 256, by shared memory.
 constexpr int att_cap(int D) { return D == 64 ? 32 : D == 128 ? 48 : 40; }
 inline int att_nr(int64_t rows, int D) {
     const int64_t tiles = (rows + att_cap(D) - 1) / att_cap(D);

@@ -11,12 +11,12 @@
 // row's maximum and sums need no shuffles.  A ninth warp copies units into the ring.  Within a unit the value codes
 // are unpacked while S is computed, and the next unit's key codes while O is.
 //
-// Measured: 64 x 64 tree nodes with 4 query heads a kv head over up to 2047 tokens 124 us (250 in tiles of 32 rows); a unit
-// takes a block 2.0 us at 64 dimensions, two blocks an SM, and 1.6 at 128 and 2.4 at 256, one block an SM, whatever its rows:
+// Measured: 64 x 64 tree nodes with 4 query heads a kv head over up to 2047 tokens 123 us (255 in tiles of 32 rows); a unit
+// takes a block 2.0 us at 64 dimensions, two blocks an SM, and 1.7 at 128 and 2.5 at 256, one block an SM, whatever its rows:
 // the chain of unpacking, product, scores, weights, product and its two barriers.
 //
 // Why: with eight rows a tile column, 256 rows unpack every code eight times and spend most of their instructions
-// around the products; here what is left a row and token is the exponential and seven more instructions.
+// around the products; here what is left a row and token is the exponential and a few more instructions.
 #pragma once
 
 #include "sv_kv_attention.cuh"
@@ -25,7 +25,7 @@ namespace sv {
 
 constexpr int kWideRows = 128, kWideTokens = 64, kWideThreads = 288, kWideStages = 3;
 // CTAs per SM.  64 x 64 tree nodes as above, us: 128 dimensions 241 with one and 260 with two (one sequence: 25 and 41), 64
-// dimensions 159 and 124 (20 and 29).  One leaves a thread 166 registers instead of 96 and halves the split segments; the
+// dimensions 159 and 124 (20 and 29).  One leaves a thread 164 registers instead of 96 and halves the split segments; the
 // unpacking of 128 dimensions is long enough to fill the waits by itself.
 __host__ __device__ constexpr int wide_occupancy(int D) { return D == 64 ? 2 : 1; }
 __host__ __device__ constexpr int wide_columns(int D) { return D == 64 ? 128 : D == 128 ? 256 : 512; }  // of tensor memory: S, then O
