@@ -7,6 +7,8 @@
  *   spec_logit_adjust   penalties, biases and grammar masks on the verified rows' logits
  *   spec_kv_append      the new tokens' keys and values into a paged cache held in 4 bits
  *   spec_kv_attention   the new tokens' attention (chain or tree) over that cache
+ *   spec_kv8_append, spec_kv8_read, spec_kv8_attention
+ *                       the same over a paged cache held in 8 bits, and its tokens back in 16 bits
  *
  * Arrays may be read and written by the kernels in any order: outputs must not overlap
  * inputs except where an entry says so.
@@ -137,6 +139,65 @@ sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_tok
                             float scale, const float *cos, const float *sin, int table_len, int pairs,
                             int interleaved, const int32_t *positions, void *out, void *workspace,
                             size_t workspace_bytes, void *stream);
+
+/*
+ * The paged cache held in 8 bits: floats of 8 bits with a scale for each block of 16 slots and head.  Pages, page tables,
+ * start, new_lens, head dimensions, page sizes, the rotation and what is out of range are as for the cache held in 4 bits.
+ *
+ *   cache       [num_pages][kv_heads][spec_kv8_page_bytes(page_size, head_dim)] bytes, 16-byte aligned.  A page and head
+ *               holds, for its page_size slots: the keys' codes (page_size * head_dim bytes), the values' codes (as many), then
+ *               16 bytes for each block of 16 slots.  Code d of slot t is in byte t / 8 * 8 head_dim + d / 16 * 128 + t % 8 * 16 +
+ *               d % 16.  A block's bytes are a 32-bit word for its keys, one for its values, and 8 unused bytes; a word has
+ *               the block's scale as a bfloat16 in its upper half, and in bit t % 16 of its lower half whether slot t's
+ *               vector is held as NaN.  Nothing needs initialising: only what was appended is ever used.
+ * A code is a float with a sign, 4 bits of exponent and 3 of mantissa (1 to 448, steps of 2^-9 below 2^-6).  A number x is
+ * held as the code nearest to x / scale (ties to the even one, at most 448 in magnitude, zero as +0), of the exact rotated
+ * key: what 32 bits leave in doubt is settled in 64.  A vector with a NaN or an infinity is held as NaN throughout.
+ * A block's scale is a power of two, 2^-40 .. 2^40.  An append that writes slots of a block takes 2^(e - 8), with 2^e the least
+ * power of two that is not below the largest magnitude that it writes there (NaN vectors left out).  If the block's first slots
+ * hold tokens from before `start`, the scale is no less than it was, and where it grows their codes are
+ * rounded to it (exact but for codes below 2^-6).  A block that begins with a new token takes no account of what it held.
+ */
+size_t spec_kv8_page_bytes(int page_size, int head_dim);
+
+/*
+ * Appends T new tokens per sequence.  Arguments as for spec_kv_append.  Tokens of k_values, v_values that are dropped
+ * get what they would have been held as in a block without older tokens.
+ */
+sv_status spec_kv8_append(const void *k, int64_t k_batch_stride, int64_t k_token_stride, int64_t k_head_stride,
+                          const void *v, int64_t v_batch_stride, int64_t v_token_stride, int64_t v_head_stride,
+                          sv_kv_dtype dtype, int B, int T, int kv_heads, int head_dim, void *cache, int num_pages,
+                          int page_size, const int32_t *page_table, int table_width, const int32_t *start,
+                          const int32_t *new_lens, const float *cos, const float *sin, int table_len, int pairs,
+                          int interleaved, const int32_t *positions, void *k_values, void *v_values, void *stream);
+
+/*
+ * Tokens of the cache in 16 bits.
+ *   start, lens  [B]  row t of sequence b is its token start[b] + t (start clamped to [0, table_width * page_size]) for t <
+ *                lens[b] (clamped to [0, T]; NULL: T).
+ *   slots        NULL, or [B][T]: row t is token slots[b][t] instead.
+ *   k, v         [B][T][kv_heads][head_dim] contiguous, 16-byte aligned, bf16 or fp16 (sv_kv_dtype): the keys as they are held,
+ *                rotated; rounded to the type.  0 for rows from lens[b] on, tokens outside the table and pages out of range.
+ */
+sv_status spec_kv8_read(const void *cache, int num_pages, int page_size, int B, int T, int kv_heads, int head_dim,
+                        const int32_t *page_table, int table_width, const int32_t *start, const int32_t *lens,
+                        const int32_t *slots, sv_kv_dtype dtype, void *k, void *v, void *stream);
+
+/*
+ * Attention of the T new tokens over the cache, which holds them already.  Arguments, workspace and status as for
+ * spec_kv_attention.  A row that sees a token whose key or value is held as NaN is NaN.
+ */
+size_t spec_kv8_attention_workspace_size(int B, int T, int heads, int kv_heads, int head_dim);
+sv_status spec_kv8_attention(const void *q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,
+                             sv_kv_dtype dtype, int B, int T, int heads, int kv_heads, int head_dim,
+                             const void *cache, int num_pages, int page_size, const int32_t *page_table,
+                             int table_width, const int32_t *start, const int32_t *new_lens, const int32_t *parent,
+                             float scale, const float *cos, const float *sin, int table_len, int pairs,
+                             int interleaved, const int32_t *positions, void *out, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* Test hook (host only): the byte of code `dim` of slot `token` within a page and head.  -1 if an argument is out of range. */
+int64_t spec_kv8_code_offset(int page_size, int head_dim, int values, int token, int dim);
 
 /*
  * Test hook (host only): where code `dim` of slot `token` is within a page and head, in

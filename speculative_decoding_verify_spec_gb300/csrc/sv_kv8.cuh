@@ -1,0 +1,64 @@
+// sv_kv8.cuh -- the 8-bit paged cache: its byte layout, and what its append, read and attention share.
+//
+// Layout of one page and head, for P slots of D dimensions (see spec_serve.h):
+//   keys    P D codes, values P D codes: code d of slot t in byte t / 8 * 8 D + d / 16 * 128 + t % 8 * 16 + d % 16.
+//           Eight slots by 16 bytes are 128 contiguous bytes, the unit from which the fifth-generation tensor cores
+//           read 8-bit operands without a swizzle: the keys as a K-major operand (slots are rows), the values
+//           as an M-major one (dimensions are rows), both as they lie in memory.  Copies into shared memory are plain.
+//   blocks  16 bytes for each 16 slots: a word for the keys, one for the values, 8 unused bytes.  A word's upper half is the scale
+//           as a bfloat16 (a power of two), bit t % 16 of its lower half says that slot t's vector is held as NaN.
+#pragma once
+
+#include "sv_kv.cuh"
+
+namespace sv {
+
+constexpr int kKv8Block = 16;                      // slots that share a scale
+constexpr int kKv8Least = -40, kKv8Most = 40;      // exponents of scales
+constexpr int kKv8Top = 8;                         // the largest code of a block is in 2^7 .. 2^8
+
+__host__ __device__ inline int kv8_page_bytes(int page, int D) { return page * (2 * D + 1); }
+// within the keys' or the values' codes (these begin at page * D)
+__host__ __device__ inline int kv8_code_byte(int D, int slot, int d) {
+    return slot / 8 * (8 * D) + d / 16 * 128 + slot % 8 * 16 + d % 16;
+}
+__host__ __device__ inline int kv8_word_byte(int page, int D, int slot, int values) {
+    return 2 * page * D + slot / kKv8Block * 16 + values * 4;
+}
+
+// The exponent of a word's scale, within the range that scales have (whatever the word holds).
+__device__ __forceinline__ int kv8_exponent(uint32_t word) {
+    const int e = int(word >> 23 & 255u) - 127;
+    return e < kKv8Least ? kKv8Least : (e > kKv8Most ? kKv8Most : e);
+}
+__device__ __forceinline__ float kv8_power(int e) { return __int_as_float((127 + e) << 23); }  // -126 <= e <= 127
+
+// Codes nearest to two numbers (ties to even, at most 448 in magnitude): x in the low byte.
+__device__ __forceinline__ uint32_t kv8_codes(float x, float y) {
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(y), "f"(x));
+    return c;
+}
+// What the two codes in the low half of w stand for.
+__device__ __forceinline__ float2 kv8_numbers(uint32_t w) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(w)));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+// Four codes with those of -0 replaced by +0.
+__device__ __forceinline__ uint32_t kv8_no_minus_zero(uint32_t w) {
+    return w & (((w & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | 0x7F7F7F7Fu);
+}
+
+// Two numbers rounded to the type, the first in the low half.
+template <bool kBF16>
+__device__ __forceinline__ uint32_t kv8_pack(float x, float y) {
+    if (kBF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+}  // namespace sv

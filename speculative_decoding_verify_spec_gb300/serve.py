@@ -1,7 +1,8 @@
 """Python entry points of the operators around the verification step (``include/spec_serve.h``).
 
 ``spec_logit_adjust`` applies penalties, biases and grammar masks to the verified rows' logits;
-``spec_kv_append`` and ``spec_kv_attention`` keep and read a paged key/value cache held in 4 bits.
+``spec_kv_append`` and ``spec_kv_attention`` keep and read a paged key/value cache held in 4 bits,
+``spec_kv8_append``, ``spec_kv8_read`` and ``spec_kv8_attention`` one held in 8 bits.
 As in ``binding``, these only marshal: they check placement, type and shape, take strides and
 the current stream from PyTorch and call the C entry of the same name.
 """
@@ -40,6 +41,18 @@ def _library() -> ctypes.CDLL:
         lib.spec_kv_attention.argtypes = [P, i64, i64, i64, i32, i32, i32, i32, i32, i32, P, i32, i32, P, i32, P, P, P,
                                           f32, P, P, i32, i32, i32, P, P, P, sz, P]
         lib.spec_kv_attention.restype = i32
+        lib.spec_kv8_page_bytes.argtypes = [i32, i32]
+        lib.spec_kv8_page_bytes.restype = sz
+        lib.spec_kv8_code_offset.argtypes = [i32] * 5
+        lib.spec_kv8_code_offset.restype = i64
+        lib.spec_kv8_append.argtypes = lib.spec_kv_append.argtypes
+        lib.spec_kv8_append.restype = i32
+        lib.spec_kv8_read.argtypes = [P, i32, i32, i32, i32, i32, i32, P, i32, P, P, P, i32, P, P, P]
+        lib.spec_kv8_read.restype = i32
+        lib.spec_kv8_attention_workspace_size.argtypes = [i32] * 5
+        lib.spec_kv8_attention_workspace_size.restype = sz
+        lib.spec_kv8_attention.argtypes = lib.spec_kv_attention.argtypes
+        lib.spec_kv8_attention.restype = i32
         lib.spec_kv_lose_unit.argtypes = [i32]
         lib.spec_kv_lose_unit.restype = i32
         _ready = lib
@@ -158,12 +171,13 @@ def _heads4(t: torch.Tensor, name: str):
     return st
 
 
-def _cache(cache, page_table, start, new_lens, B, heads, D, dev):
-    """(num_pages, page_size, checked page_table, its width, start, new_lens) of a checked cache."""
+def _cache(cache, page_table, start, new_lens, B, heads, D, dev, slot_bytes=0):
+    """(num_pages, page_size, checked page_table, its width, start, new_lens) of a checked cache; slot_bytes: of a token and
+    head, unless it is the 4-bit cache."""
     cs = cache.shape
     if cache.dtype is not torch.uint8 or len(cs) != 3 or cache.get_device() != dev.index or not cache.is_contiguous():
         raise ValueError(f"cache must be a contiguous uint8 tensor [pages, kv_heads, page bytes] on {dev}")
-    page, rest = divmod(cs[2], D + 8)
+    page, rest = divmod(cs[2], slot_bytes or D + 8)
     if (heads is not None and cs[1] != heads) or rest:
         raise ValueError(f"cache of shape {tuple(cs)} does not hold {heads} heads of {D} dimensions")
     ps = page_table.shape
@@ -261,6 +275,118 @@ def spec_kv_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Te
                                1.0 / math.sqrt(D) if scale is None else float(scale), _ptr(cos), _ptr(sin), length, pairs,
                                int(interleaved), _ptr(positions), out.data_ptr(), workspace.data_ptr(), n, _current(dev))
     _check(st, "spec_kv_attention")
+    return out
+
+
+def spec_kv8_page_bytes(page_size: int, head_dim: int) -> int:
+    """Bytes of one page and head of the 8-bit cache (0 if the sizes are not supported)."""
+    return int(_library().spec_kv8_page_bytes(page_size, head_dim))
+
+
+def spec_kv8_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor,
+                    *, new_lens=None, cos=None, sin=None, positions=None, interleaved: bool = False,
+                    return_values: bool = False, k_values=None, v_values=None):
+    """Writes the new tokens' keys (rotated) and values [B, T, kv_heads, head_dim] into the 8-bit `cache`
+    [pages, kv_heads, spec_kv8_page_bytes(page_size, head_dim)] uint8; arguments and result as for spec_kv_append.
+
+    A number is held as a float of 8 bits (3 of mantissa) times a scale, a power of two, which 16 neighbouring slots of a head share.
+    Where a new token is louder than the tokens that its block of 16 holds already, these are rounded to the larger scale (exact but for
+    numbers 2^14 times smaller than the largest)."""
+    lib = _library()
+    ks, dt, dev, shape = _heads4(k, "k"), _kv_dtype(k, "k"), k.device, k.shape
+    vs = _heads4(v, "v")
+    if v.shape != shape or v.dtype != k.dtype or v.device != dev:
+        raise ValueError("v must have k's shape, type and device")
+    B, T, H, D = shape
+    pages, page, page_table, width, start, new_lens = _cache(cache, page_table, start, new_lens, B, H, D, dev, 2 * D + 1)
+    cos, sin, length, pairs, positions = _rotation(cos, sin, positions, B, T, dev)
+    for name, t in (("k_values", k_values), ("v_values", v_values)):
+        if t is not None and (t.shape != shape or t.dtype != k.dtype or t.device != dev or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous tensor like k")
+    if return_values:
+        k_values = _like(k) if k_values is None else k_values
+        v_values = _like(k) if v_values is None else v_values
+    st = lib.spec_kv8_append(k.data_ptr(), ks[0], ks[1], ks[2], v.data_ptr(), vs[0], vs[1], vs[2], dt, B, T, H, D, cache.data_ptr(), pages, page,
+                             page_table.data_ptr(), width, start.data_ptr(), _ptr(new_lens), _ptr(cos), _ptr(sin), length,
+                             pairs, int(interleaved), _ptr(positions), _ptr(k_values), _ptr(v_values), _current(dev))
+    _check(st, "spec_kv8_append")
+    return None if k_values is None and v_values is None else (k_values, v_values)
+
+
+def _head_dim8(page_bytes: int) -> int:
+    """The head dimension of an 8-bit cache with such pages (no two have a page size with the same bytes)."""
+    for D in (64, 128, 256):
+        page, rest = divmod(page_bytes, 2 * D + 1)
+        if rest == 0 and page % 16 == 0 and 16 <= page <= 1024:
+            return D
+    raise ValueError(f"pages of {page_bytes} bytes are not those of an 8-bit cache (see spec_kv8_page_bytes)")
+
+
+def spec_kv8_read(cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor, T: int, *, lens=None, slots=None,
+                  dtype: torch.dtype = torch.bfloat16, k=None, v=None):
+    """Tokens of the 8-bit cache back in 16 bits: (keys, values) [B, T, kv_heads, head_dim], new unless `k` and `v` are given.
+
+    Row t of sequence b is its token start[b] + t, or slots[b, t] if `slots` [B, T] int32 is given (a tree's accepted path, to be
+    appended again behind the context); `lens` [B] of the rows are read, all T if None.  Rows from lens[b] on, tokens outside the
+    page table and pages out of range are 0.  Keys come as they are held, rotated."""
+    lib = _library()
+    if not cache.is_cuda or cache.dim() != 3:
+        raise ValueError("cache must be a CUDA tensor [pages, kv_heads, page bytes]")
+    dev, H, D, B, T = cache.device, cache.shape[1], _head_dim8(cache.shape[2]), page_table.shape[0], int(T)
+    if T < 0:
+        raise ValueError(f"T must not be negative, got {T}")
+    pages, page, page_table, width, start, lens = _cache(cache, page_table, start, lens, B, H, D, dev, 2 * D + 1)
+    slots = _int32(slots, "slots", (B, T), dev)
+    if k is None:
+        k = torch.empty((B, T, H, D), dtype=dtype, device=dev)
+    if v is None:
+        v = torch.empty((B, T, H, D), dtype=k.dtype, device=dev)
+    for name, t in (("k", k), ("v", v)):
+        if t.shape != (B, T, H, D) or t.dtype != k.dtype or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor of {k.dtype} and shape {(B, T, H, D)} on {dev}")
+    st = lib.spec_kv8_read(cache.data_ptr(), pages, page, B, T, H, D, page_table.data_ptr(), width, start.data_ptr(), _ptr(lens), _ptr(slots),
+                           _kv_dtype(k, "k"), k.data_ptr(), v.data_ptr(), _current(dev))
+    _check(st, "spec_kv8_read")
+    return k, v
+
+
+@functools.lru_cache(maxsize=1024)
+def spec_kv8_attention_workspace_size(B: int, T: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace that spec_kv8_attention needs for these sizes."""
+    return int(_library().spec_kv8_attention_workspace_size(B, T, heads, kv_heads, head_dim))
+
+
+def spec_kv8_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor, *,
+                       new_lens=None, parent=None, scale=None, cos=None, sin=None, positions=None,
+                       interleaved: bool = False, workspace=None, out=None) -> torch.Tensor:
+    """Attention of the step's new tokens' queries [B, T, heads, head_dim] over the 8-bit cache, which holds the new tokens
+    already (see spec_kv8_append); arguments, result and the workspace's status word as for spec_kv_attention."""
+    lib = _library()
+    qs, dt, dev = _heads4(q, "q"), _kv_dtype(q, "q"), q.device
+    B, T, Hq, D = q.shape
+    H = cache.shape[1] if cache.dim() == 3 else 0
+    if H < 1 or Hq % H:
+        raise ValueError(f"{Hq} query heads do not share the cache's heads (shape {tuple(cache.shape)}) evenly")
+    pages, page, page_table, width, start, new_lens = _cache(cache, page_table, start, new_lens, B, None, D, dev, 2 * D + 1)
+    cos, sin, length, pairs, positions = _rotation(cos, sin, positions, B, T, dev)
+    if parent is not None:
+        parent = _int32(parent, "parent", (T,), dev)
+    if out is None:
+        out = _like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor like q")
+    n = spec_kv8_attention_workspace_size(B, T, Hq, H, D)
+    if workspace is None:
+        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+    else:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        n = workspace.numel() * workspace.element_size()
+    st = lib.spec_kv8_attention(q.data_ptr(), qs[0], qs[1], qs[2], dt, B, T, Hq, H, D, cache.data_ptr(), pages, page, page_table.data_ptr(),
+                                width, start.data_ptr(), _ptr(new_lens), _ptr(parent),
+                                1.0 / math.sqrt(D) if scale is None else float(scale), _ptr(cos), _ptr(sin), length, pairs,
+                                int(interleaved), _ptr(positions), out.data_ptr(), workspace.data_ptr(), n, _current(dev))
+    _check(st, "spec_kv8_attention")
     return out
 
 
