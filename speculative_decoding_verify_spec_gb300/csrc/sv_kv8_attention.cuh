@@ -1,0 +1,743 @@
+// sv_kv8_attention.cuh -- the new tokens' attention over the 8-bit paged cache: the kernel, instantiated per head
+// dimension by the translation units sv_kv8_attention_*.cu.
+//
+// For a query row q (one of the T x G rows that share a kv head) and cached tokens j with keys s_j c_j and values s'_j c'_j,
+//   t_j = log2(e) scale s_j (q . c_j) + log2(s'_j),  w_j = 2^(t_j - m) = p_j s'_j,  out = sum_j w_j c'_j / sum_j (w_j / s'_j).
+// Both products run on the fifth-generation tensor cores with the cache's bytes as they lie in memory as the 128-row operand,
+// so that no code is ever unpacked:
+//   S [128 tokens x rows]     = K codes [128 x D]  times  q^T          D / 32 steps a part of q
+//   O [D (128) x rows]        = V codes^T [D x 128]  times  w          4 steps a part of w
+// The other operands are 8-bit floats too, so a query and a weight are held as sums of parts, each the rounding of what the parts
+// before it left: two have the 8 bits of a bfloat16, three 12.  A part's products are summed in fp32 with the others', which
+// costs no more than one product in 16 bits would.
+//
+// Weights of 8 bits reach down to 2^-18 of the largest at most.  So every tile of 128 tokens has its own m, a whole number (the rounded
+// largest t of the row's tokens that it sees, less 8), and its own O, which is added to the row's sums in registers times 2^(m -
+// M), with M the row's first m; M moves only when a later m is 60 above it.  Hidden or far heavier tokens of other
+// tiles take no bits from a tile's weights.
+//
+// A block has a warp that copies tiles into rings in shared memory (keys and values apart: a key's place is free
+// once its scores are there), a thread that issues the products, two warps that bring the next segment's queries into parts,
+// and one or two groups of four warps for the softmax.  A thread of those has one token's scores for the 16 or 32 rows of its
+// group, and one dimension of their output: maxima are one reduction over the warp and one barrier, the weights' sums stay in the
+// thread until the segment ends, and a tile's weights are stored in 16 bytes a row block and part (rows are the operand's
+// contiguous axis).  Scores and outputs have two places each in tensor memory, so that the next tile's scores are computed
+// during this one's softmax, and its output is taken up after the next one's weights.
+//
+// Work: all tiles of the batch form one list that is cut into equal shares, as in sv_kv_attention.cuh, whose list, descriptors
+// and join of split segments these are.
+#pragma once
+
+#include "sv_kv8.cuh"
+#include "sv_kv_wide.cuh"
+
+namespace sv {
+
+constexpr int kTile8 = 128;
+__host__ __device__ constexpr int att8_groups(int NR) { return NR == 64 ? 2 : 1; }
+__host__ __device__ constexpr int att8_threads(int NR) { return 128 + 128 * att8_groups(NR); }
+// Tiles in the rings, places for queries and weights, and blocks an SM: by shared memory and registers.
+__host__ __device__ constexpr int att8_stages(int D, int NR) { return D == 64 ? (NR == 16 ? 5 : NR == 32 ? 4 : 6) : D == 128 ? (NR == 64 ? 4 : 2) : (NR == 16 ? 3 : 2); }
+__host__ __device__ constexpr int att8_q_places(int D, int NR) { return D == 256 && NR == 64 ? 1 : 2; }
+__host__ __device__ constexpr int att8_w_places(int D, int NR) { return NR == 64 || (D == 256 && NR == 16) || (D == 128 && NR == 32) ? 1 : 2; }
+__host__ __device__ constexpr int att8_occupancy(int D, int NR) { return D == 256 || NR == 64 ? 1 : 2; }
+// Rows a tile, by the rows that share a kv head.
+inline int att8_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+enum : int { kMasked8 = 1, kRagged8 = 2, kFirst8 = 4, kLast8 = 8 };  // in Unit::masked: not every row sees every token; not every token is there; of a segment
+
+struct alignas(16) Info8 {
+    Unit unit;
+    uint32_t word[kTile8 / kKv8Block][4];
+};
+
+template <int D, int NR, int NP>
+struct Att8Shared {
+    static constexpr int W = att8_groups(NR), RW = NR / W, kStages = att8_stages(D, NR), kInfos = kStages + 2;
+    static constexpr int kQ = att8_q_places(D, NR), kP = att8_w_places(D, NR), MB = D == 256 ? 2 : 1;
+    // Few rows: a product reads the cache's operand at its full width whatever the columns, so the parts are columns of
+    // one product and are added up afterwards.
+    static constexpr bool kStackQ = NR == 16, kStackP = NR == 16;
+    static constexpr int kScoreCols = kStackQ ? 64 : NR, kOutEach = kStackP && NP == 3 ? 64 : NR < 32 ? 32 : NR, kOutCols = MB * kOutEach;
+    static constexpr int kUsed = 2 * (kScoreCols + kOutCols), kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+    alignas(1024) uint8_t k[kStages][kTile8 * D];
+    uint8_t v[kStages][kTile8 * D];       // (64 dimensions: a product's upper 64 rows read past the end, into w)
+    uint8_t w[kP][NP * NR * kTile8];      // [part][16 rows][token][16 bytes]
+    uint8_t q[kQ][3 * NR * D];            // [part][row], laid out as the keys
+    Info8 info[kInfos];
+    alignas(16) float row_f[kQ][NR];      // log2(e) scale times the power of two taken out of the row
+    alignas(16) float red[W][4][RW];
+    alignas(16) float4 move[W][2][RW / 2];  // of a row pair: -m, then 2^(m - M)
+    alignas(16) float shrink[W][RW];
+    alignas(16) float2 fin[W][RW];
+    // Each is waited for before what it tells of can come about once more, so that a phase's parity is enough: a unit's place in `info`
+    // is taken again after the scores of two units later, which wait for the softmax to have read this one's.
+    alignas(8) uint64_t full_k[kStages], full_v[kStages], empty_k[kStages], empty_v[kStages], full_i[kInfos];
+    uint64_t full_s[2], free_s[2], full_o[2], free_o[2], full_w[2], full_q[kQ], free_q[kQ], done;
+    uint32_t tmem;
+};
+
+__device__ __forceinline__ uint64_t operand8(uint32_t addr, uint32_t along_k, uint32_t across) {
+    return uint64_t((addr & 0x3FFFF) >> 4) | uint64_t(along_k >> 4) << 16 | uint64_t(across >> 4) << 32 | uint64_t(1) << 46;
+}
+// 8-bit floats (4 bits of exponent) into fp32, 128 rows, N columns; `turned`: both operands have their rows contiguous.
+__device__ __forceinline__ constexpr uint32_t kind8(int N, bool turned) { return 1u << 4 | (turned ? 3u << 15 : 0u) | uint32_t(N / 8) << 17 | 8u << 24; }
+__device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(kind), "r"(uint32_t(add))
+        : "memory");
+}
+// Eight columns of this warp's 32 rows, there after tmem_loaded().
+__device__ __forceinline__ void tmem_get8(float (&x)[8], uint32_t addr) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// (what follows uses x after the wait)
+__device__ __forceinline__ void tmem_here(float (&x)[8]) {
+    asm volatile("" : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]));
+}
+__device__ __forceinline__ float warp_largest(float x) {  // NaN left out
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Barrier kId of N threads; true if x is for any of them.
+template <int kId, int N>
+__device__ __forceinline__ bool group_or(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(uint32_t(x)), "n"(kId), "n"(N)
+        : "memory");
+    __syncwarp();
+    return r != 0;
+}
+
+// The parts of a pair of numbers, two codes each (the first number's in the low byte).
+__device__ __forceinline__ uint32_t codes8_of_halves(uint32_t h) {
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
+    return c;
+}
+__device__ __forceinline__ uint32_t halves_of_codes8(uint32_t c) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(c)));
+    return h;
+}
+// Two parts, through fp16: 11 bits are more than both hold.
+__device__ __forceinline__ void parts8(float x, float y, uint32_t (&c)[2]) {
+    const __half2 h = __floats2half2_rn(x, y);
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(&h);
+    c[0] = codes8_of_halves(w);
+    const uint32_t b = halves_of_codes8(c[0]);
+    const __half2 rest = __hsub2(h, *reinterpret_cast<const __half2 *>(&b));  // exact
+    c[1] = codes8_of_halves(*reinterpret_cast<const uint32_t *>(&rest));
+}
+__device__ __forceinline__ void parts8(float x, float y, uint32_t (&c)[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        c[i] = kv8_codes(x, y);
+        const float2 b = kv8_numbers(c[i]);
+        x -= b.x, y -= b.y;  // exact
+    }
+}
+
+// The copying warp: a unit's keys and words ahead of the values of the one before.  Returns when all that it has begun is there.
+template <int D, int NR, int NP>
+__device__ __forceinline__ void copy_tiles8(const AttArgs &a, Att8Shared<D, NR, NP> &sh, Cursor<kTile8> &cur, int ubegin, int uend, int lane) {
+    using Sh = Att8Shared<D, NR, NP>;
+    constexpr int NT = kTile8, kStages = Sh::kStages;
+    // lanes take (granule, piece) pairs: keys, values, words
+    const int gi = lane >> 2, piece = lane & 3, granules = NT / a.granule;
+    const bool busy = gi < granules && piece < 3;
+    const uint32_t all = granules == 8 ? 0x11111111u : 0x11111111u & ((1u << (4 * granules)) - 1);
+    const int64_t page_bytes = kv8_page_bytes(a.page, D), head_step = int64_t(a.H) * page_bytes;
+    const int each = piece < 2 ? D : 1;  // bytes a slot
+    const int from = piece == 0 ? 0 : piece == 1 ? a.page * D : 2 * a.page * D;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (ok && !mbar_wait(smem_u32(bar), parity)) {
+            ok = false;
+            atomicExch(a.status, int(SV_ERR_TIMEOUT));
+        }
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        return ok;
+    };
+    const uint8_t *vsrc = nullptr;  // of the unit whose values are next
+    uint32_t vbytes = 0, vsum = 0;
+    int values = 0, keys = 0;  // begun
+    auto copy_values = [&] {
+        const int s = values % kStages;
+        if (values >= kStages && !wait(&sh.empty_v[s], uint32_t(values / kStages - 1) & 1u)) return false;
+        if (lane == 0) mbar_expect(smem_u32(&sh.full_v[s]), vsum);
+        __syncwarp();
+        if (vbytes) bulk_load(smem_u32(sh.v[s]) + gi * a.granule * D, vsrc, vbytes, smem_u32(&sh.full_v[s]));
+        ++values;
+        return true;
+    };
+    bool placed = false;
+    int pi = 0, slot = 0;
+    for (int u = ubegin; u < uend; ++u) {
+        const int tok = cur.tile * NT + gi * a.granule;
+        if (!placed) pi = tok / a.page, slot = tok - pi * a.page, placed = true;
+        const bool inside = busy && cur.live && tok < cur.w.len;
+        const int pg = inside ? __ldg(a.table + int64_t(cur.b) * a.width + pi) : -1;
+        const bool here = pg >= 0 && pg < a.num_pages && SV_IN(slot + a.granule - 1, a.page);
+        const int there = here ? min(a.granule, (cur.w.len - tok + kKv8Block - 1) / kKv8Block * kKv8Block) : 0;  // tokens of whole blocks
+        const uint32_t have = __ballot_sync(0xFFFFFFFFu, here) & 0x11111111u, bytes = uint32_t(there * each);
+        const uint32_t sum = __reduce_add_sync(0xFFFFFFFFu, piece == 0 ? bytes : 0u);  // of the keys, and of the values
+        const uint8_t *src = here ? a.cache + pg * head_step + cur.h * page_bytes + from + int64_t(slot) * each : nullptr;
+#ifdef SV_CHECKS
+        if (u - ubegin == g_kv_lose) break;
+#endif
+        const int s = keys % kStages;
+        if (keys >= kStages && !wait(&sh.empty_k[s], uint32_t(keys / kStages - 1) & 1u)) break;
+        Info8 &in = sh.info[keys % Sh::kInfos];
+        if (lane == 0) {
+            int4 *un = reinterpret_cast<int4 *>(&in.unit);
+            const bool ragged = (cur.tile + 1) * NT > cur.w.len || have != all;
+            const int flags = (ragged || (cur.tile + 1) * NT > cur.w.before ? kMasked8 : 0) | (ragged ? kRagged8 : 0) |
+                              (u == ubegin || cur.tile == 0 ? kFirst8 : 0) | (u + 1 == uend || cur.tile + 1 == cur.tiles() ? kLast8 : 0);
+            un[0] = make_int4(cur.b, cur.h, cur.rt, cur.tile);
+            un[1] = make_int4(cur.tiles(), cur.w.before, cur.w.len, cur.live ? cur.w.fresh : 0);
+            un[2] = make_int4(int(have), flags, 0, 0);
+            mbar_expect(smem_u32(&sh.full_i[keys % Sh::kInfos]), sum / D);  // a byte of words for D of codes
+            mbar_expect(smem_u32(&sh.full_k[s]), sum);
+        }
+        __syncwarp();
+        if (bytes && piece == 0) bulk_load(smem_u32(sh.k[s]) + gi * a.granule * D, src, bytes, smem_u32(&sh.full_k[s]));
+        if (bytes && piece == 2) bulk_load(smem_u32(in.word) + gi * a.granule, src, bytes, smem_u32(&sh.full_i[keys % Sh::kInfos]));
+        if (++keys > 1 && !copy_values()) break;
+        vsrc = src, vbytes = piece == 1 ? bytes : 0u, vsum = sum;
+        if (cur.tile + 1 < cur.tiles()) {
+            ++cur.tile;
+            slot += NT;
+            while (slot >= a.page) slot -= a.page, ++pi;
+        } else if (u + 1 < uend) {
+            cur.next(a, NR, u + 1);
+            placed = false;
+        }
+    }
+    if (keys > values && ok) copy_values();
+    for (int i = max(0, keys - kStages); i < keys; ++i)
+        if (!mbar_wait(smem_u32(&sh.full_k[i % kStages]), uint32_t(i / kStages) & 1u) ||
+            !mbar_wait(smem_u32(&sh.full_i[i % Sh::kInfos]), uint32_t(i / Sh::kInfos) & 1u))
+            atomicExch(a.status, int(SV_ERR_TIMEOUT));
+    for (int i = max(0, values - kStages); i < values; ++i)
+        if (!mbar_wait(smem_u32(&sh.full_v[i % kStages]), uint32_t(i / kStages) & 1u)) atomicExch(a.status, int(SV_ERR_TIMEOUT));
+}
+
+// The issuing thread.
+template <int D, int NR, int NP>
+__device__ __forceinline__ void issue_products8(const AttArgs &a, Att8Shared<D, NR, NP> &sh, int units, int nq) {
+    using Sh = Att8Shared<D, NR, NP>;
+    constexpr int kStages = Sh::kStages, MB = Sh::MB;
+    const uint32_t tmem = sh.tmem;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (ok && !mbar_wait(smem_u32(bar), parity)) {
+            ok = false;  // nothing more is issued; the other warps' waits give up too
+            atomicExch(a.status, int(SV_ERR_TIMEOUT));
+        }
+    };
+    int segment = -1;
+    auto scores = [&](int n) {
+        const int s = n % kStages;
+        wait(&sh.full_k[s], uint32_t(n / kStages) & 1u);
+        if (!ok) return;
+        const int flags = sh.info[n % Sh::kInfos].unit.masked;
+        if (flags & kFirst8) ++segment, wait(&sh.full_q[segment % Sh::kQ], uint32_t(segment / Sh::kQ) & 1u);
+        if (n >= 2) wait(&sh.free_s[n & 1], uint32_t((n >> 1) - 1) & 1u);
+        if (!ok) return;
+        fence_after();
+        const uint32_t d = tmem + (n & 1) * Sh::kScoreCols, k = smem_u32(sh.k[s]), q = smem_u32(sh.q[segment % Sh::kQ]);
+        if constexpr (Sh::kStackQ) {
+            const uint32_t kind = kind8(NR, false) + uint32_t((nq - 1) * NR / 8) * (1u << 17);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) mma8(d, operand8(k + i * 256, 128, 8 * D), operand8(q + i * 256, 128, 8 * D), kind, i > 0);
+        } else {
+            for (int p = 0; p < nq; ++p)
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i)
+                    mma8(d, operand8(k + i * 256, 128, 8 * D), operand8(q + p * NR * D + i * 256, 128, 8 * D), kind8(NR, false), p > 0 || i > 0);
+        }
+        wide_commit(&sh.empty_k[s]);
+        wide_commit(&sh.full_s[n & 1]);
+        if (flags & kLast8) wide_commit(&sh.free_q[segment % Sh::kQ]);
+    };
+    auto products = [&](int n) {
+        const int s = n % kStages;
+        wait(&sh.full_w[n & 1], uint32_t(n >> 1) & 1u);
+        wait(&sh.full_v[s], uint32_t(n / kStages) & 1u);
+        if (n >= 2) wait(&sh.free_o[n & 1], uint32_t((n >> 1) - 1) & 1u);
+        if (!ok) return;
+        fence_after();
+        const uint32_t d = tmem + 2 * Sh::kScoreCols + (n & 1) * Sh::kOutCols, v = smem_u32(sh.v[s]), w = smem_u32(sh.w[n % Sh::kP]);
+        constexpr int parts = Sh::kStackP ? 1 : NP, cols = Sh::kStackP ? NP * NR : NR;
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int p = 0; p < parts; ++p)
+#pragma unroll
+                for (int i = 0; i < kTile8 / 32; ++i)
+                    mma8(d + mb * Sh::kOutEach, operand8(v + mb * 1024 + i * 32 * D, 8 * D, 128), operand8(w + p * NR * kTile8 + i * 512, 128, 2048),
+                         kind8(cols, true), p > 0 || i > 0);
+        wide_commit(&sh.empty_v[s]);
+        wide_commit(&sh.full_o[n & 1]);
+    };
+    scores(0);
+    for (int n = 1; n < units; ++n) scores(n), products(n - 1);
+    products(units - 1);
+    // nothing may be under way when the block ends
+    wide_commit(&sh.done);
+    if (!mbar_wait(smem_u32(&sh.done), 0)) atomicExch(a.status, int(SV_ERR_TIMEOUT));
+}
+
+// The query warps, 64 threads: each segment's rows, rotated, times a power of two that brings the row's largest number to 2^7 ..
+// 2^8, in parts.  A row with a NaN or an infinity is NaN throughout.
+template <int D, int NR, int NP>
+__device__ __forceinline__ void bring_queries8(const AttArgs &a, Att8Shared<D, NR, NP> &sh, const int *parent_s, uint32_t *see_s, Cursor<kTile8> &cur,
+                                               int ubegin, int uend, int tid) {
+    using Sh = Att8Shared<D, NR, NP>;
+    constexpr int L = D / 8, P = 64 / L, W = Sh::W;
+    const int c = tid % L, d0 = c * 8;
+    int u = ubegin;
+    for (int segment = 0; u < uend; ++segment) {
+        const int at = segment % Sh::kQ;
+        bool ok = true;
+        if (segment >= Sh::kQ) ok = mbar_wait(smem_u32(&sh.free_q[at]), uint32_t(segment / Sh::kQ - 1) & 1u);
+        if (!ok) atomicExch(a.status, int(SV_ERR_TIMEOUT));
+        if (group_or<3, 64>(!ok)) return;
+        const Unit un{cur.b, cur.h, cur.rt, cur.tile, cur.tiles(), cur.w.before, cur.w.len, cur.live ? cur.w.fresh : 0, 0, 0, {0, 0}};
+        uint8_t *q = sh.q[at];
+#pragma unroll 2
+        for (int r0 = 0; r0 < NR; r0 += P) {
+            const int r = r0 + tid / L, row = un.rt * NR + r;
+            const int node = row / a.G, head = un.h * a.G + row - node * a.G;
+            const bool on = node < un.fresh;
+            float x[8];
+            query_chunk(a, un, on ? node : 0, on ? head : 0, d0, x);  // (no branch: the rows' loads go out together)
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] = on ? x[i] : 0.f;
+                top = max(top, __float_as_uint(fabsf(x[i])));
+            }
+#pragma unroll
+            for (int o = L / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            const int e2 = top == 0 ? 0 : max(int(top >> 23) - 127 - 7, -110);
+            const bool odd = top >= 0x7F800000u;
+            const float shrink = power2(odd ? 0 : -e2);
+            uint32_t code[3][2] = {};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t p[3];
+                parts8(odd ? NAN : x[2 * i] * shrink, odd ? NAN : x[2 * i + 1] * shrink, p);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) code[k][i / 2] |= p[k] << (16 * (i & 1));
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                *reinterpret_cast<uint2 *>(q + kv8_code_byte(D, k * NR + r, d0)) = make_uint2(code[k][0], code[k][1]);
+            if (c == 0) sh.row_f[at][r] = a.scale * 1.4426950408889634f * power2(odd ? 0 : e2);
+        }
+        if (a.parent) {  // which rows see a new token
+            uint32_t *see = see_s + at * a.T * W;
+            for (int i = tid; i < a.T * W; i += 64) see[i] = 0;
+            group_or<3, 64>(false);
+            if (tid < NR) {
+                const int node = (un.rt * NR + tid) / a.G;
+                for (int v = node < un.fresh ? node : -1; v >= 0;) {
+                    atomicOr(see + v * W + tid / 32, 1u << (tid & 31));
+                    const int up = parent_s[v];
+                    v = up < v ? up : -1;
+                }
+            }
+        }
+        fence_operands();
+        mbar_arrive(smem_u32(&sh.full_q[at]));
+        u += cur.tiles() - cur.tile;
+        if (u < uend) {
+            cur.tile = cur.tiles() - 1;
+            cur.next(a, NR, u);
+        }
+    }
+}
+
+template <int D, int NR, int NP>
+__global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_attention_kernel(const AttArgs a, int nq) {
+    using Sh = Att8Shared<D, NR, NP>;
+    constexpr int W = Sh::W, RW = Sh::RW, MB = Sh::MB, kStages = Sh::kStages;
+    extern __shared__ unsigned char raw0[];
+    unsigned char *raw = raw0 + ((1024 - (smem_u32(raw0) & 1023)) & 1023);
+    Sh &sh = *reinterpret_cast<Sh *>(raw);
+    int *parent_s = reinterpret_cast<int *>(raw + sizeof(Sh));
+    uint32_t *see_s = reinterpret_cast<uint32_t *>(parent_s + (a.parent ? a.T : 0));  // [kQ][T][W]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ncta = int(gridDim.x), cta = int(blockIdx.x);
+
+    griddep_launch_next();
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i)
+            mbar_init(smem_u32(&sh.full_k[i]), 1), mbar_init(smem_u32(&sh.full_v[i]), 1), mbar_init(smem_u32(&sh.empty_k[i]), 1),
+                mbar_init(smem_u32(&sh.empty_v[i]), 1);
+        for (int i = 0; i < 2; ++i)
+            mbar_init(smem_u32(&sh.full_s[i]), 1), mbar_init(smem_u32(&sh.free_s[i]), 4 * W), mbar_init(smem_u32(&sh.full_o[i]), 1),
+                mbar_init(smem_u32(&sh.free_o[i]), 4 * W), mbar_init(smem_u32(&sh.full_w[i]), 4 * W);
+        for (int i = 0; i < Sh::kQ; ++i) mbar_init(smem_u32(&sh.full_q[i]), 64), mbar_init(smem_u32(&sh.free_q[i]), 4 * W + 1);
+        for (int i = 0; i < Sh::kInfos; ++i) mbar_init(smem_u32(&sh.full_i[i]), 1);
+        mbar_init(smem_u32(&sh.done), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    griddep_wait();
+    if (cta == 0 && tid == 0) *a.status = SV_OK;
+    if (a.parent)
+        for (int i = tid; i < a.T; i += att8_threads(NR)) parent_s[i] = a.parent[i];
+    Cursor<kTile8> cur;
+    int total, ubegin, uend;
+    if (!find_share<kTile8>(a, NR, lane, cta, ncta, cur, total, ubegin, uend)) {
+        if (tid == 0) a.desc[cta] = AttDesc{0, 0, 0, 0, 0, 0, 0, 0};
+        return;
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "r"(Sh::kCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        fence_before();
+    }
+    __syncthreads();
+    fence_after();
+    const int units = uend - ubegin;
+
+    if (warp == 0) {
+        copy_tiles8<D, NR, NP>(a, sh, cur, ubegin, uend, lane);
+    } else if (warp == 1) {
+        if (lane == 0) issue_products8<D, NR, NP>(a, sh, units, nq);
+        __syncwarp();
+    } else if (warp < 4) {
+        bring_queries8<D, NR, NP>(a, sh, parent_s, see_s, cur, ubegin, uend, tid - 64);
+    } else {
+        const int wg = (warp - 4) / 4, quarter = warp & 3, token = quarter * 32 + lane;
+        const int r0 = wg * RW;  // the group's first row
+        const uint32_t lanes = uint32_t(quarter * 32) << 16;
+        const uint32_t tmem_s = sh.tmem + lanes + r0, tmem_o = sh.tmem + lanes + 2 * Sh::kScoreCols + r0;
+        const bool writes = D >= 128 || quarter < 2;  // has a dimension
+        auto any = [&](bool x) { return W == 1 || wg == 0 ? group_or<1, 128>(x) : group_or<2, 128>(x); };
+        bool failed = false;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (!failed && !mbar_wait(smem_u32(bar), parity)) {
+                failed = true;
+                atomicExch(a.status, int(SV_ERR_TIMEOUT));
+            }
+            failed = __any_sync(0xFFFFFFFFu, failed);
+        };
+        Unit seg{};
+        int seg_lo = 0, segment = -1, live = 0;  // live: rows of this group
+        Two l[RW / 2], acc[MB][RW / 2];
+        float M = -INFINITY;  // of row `token` of the group
+        // the output of unit n, which is of the segment at hand
+        auto take_up = [&](int n) {
+            wait(&sh.full_o[n & 1], uint32_t(n >> 1) & 1u);
+            if (failed) return;
+            fence_after();
+            if (writes) {
+                constexpr int parts = Sh::kStackP ? NP : 1;
+                const uint32_t o_at = tmem_o + (n & 1) * Sh::kOutCols;
+#pragma unroll
+                for (int c = 0; c < RW / 8; ++c) {
+                    if (8 * c >= live) continue;
+                    float o[MB][parts][8];
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                        for (int p = 0; p < parts; ++p) tmem_get8(o[mb][p], o_at + mb * Sh::kOutEach + p * NR + 8 * c);
+                    tmem_loaded();
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                        for (int p = 0; p < parts; ++p) tmem_here(o[mb][p]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 mv = sh.move[wg][n & 1][4 * c + j];
+#pragma unroll
+                        for (int mb = 0; mb < MB; ++mb) {
+                            Two x = two(o[mb][0][2 * j], o[mb][0][2 * j + 1]);
+#pragma unroll
+                            for (int p = 1; p < parts; ++p) x = add2(x, two(o[mb][p][2 * j], o[mb][p][2 * j + 1]));
+                            acc[mb][4 * c + j] = fma2(x, two(mv.z, mv.w), acc[mb][4 * c + j]);
+                        }
+                    }
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.free_o[n & 1]));
+        };
+
+        for (int n = 0; n < units; ++n) {
+            const int s = n % kStages;
+            const Info8 &in = sh.info[n % Sh::kInfos];
+            wait(&sh.full_i[n % Sh::kInfos], uint32_t(n / Sh::kInfos) & 1u);
+            int flags = 0;
+            float t[RW];
+            float inv = 0.f;  // 1 / s'
+            if (!failed) {
+                flags = in.unit.masked;
+                if (flags & kFirst8) {
+                    seg = in.unit;
+                    ++segment;
+                    seg_lo = ubegin + n - seg.tile;
+                    live = min(max(seg.fresh * a.G - seg.rt * NR - r0, 0), RW);
+                    M = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < RW / 2; ++i) l[i] = acc[0][i] = acc[MB - 1][i] = 0;
+                    wait(&sh.full_q[segment % Sh::kQ], uint32_t(segment / Sh::kQ) & 1u);
+                }
+                wait(&sh.full_s[n & 1], uint32_t(n >> 1) & 1u);
+            }
+            if (!failed) {
+                fence_after();
+                const int tok0 = in.unit.tile * kTile8, at = segment % Sh::kQ;
+                float ks = 0.f, log2vs = 0.f;
+                uint32_t see = 0xFFFFFFFFu;
+                bool there = true;
+                if (flags & kMasked8) {
+                    const int x = tok0 + token - seg.before;  // among the new tokens
+                    there = tok0 + token < seg.len && (in.unit.have >> (4 * (token / a.granule)) & 1u);
+                    see = live >= 32 ? 0xFFFFFFFFu : (1u << live) - 1;
+                    if (!there) {
+                        see = 0;
+                    } else if (x >= 0) {
+                        if (a.parent) {
+                            see &= see_s[(at * a.T + x) * W + wg];
+                        } else {
+                            const int hidden = min(max(x * a.G - seg.rt * NR - r0, 0), 32);  // rows of earlier tokens
+                            see &= hidden >= 32 ? 0u : 0xFFFFFFFFu << hidden;
+                        }
+                    }
+                }
+                if (there) {
+                    const uint2 word = *reinterpret_cast<const uint2 *>(in.word[token / kKv8Block]);
+                    const int e = kv8_exponent(word.y);
+                    ks = (word.x | word.y) >> (token & 15) & 1u ? NAN : __uint_as_float(word.x & 0xFFFF0000u);
+                    log2vs = float(e), inv = kv8_power(-e);
+                }
+                const Two ks2 = two(ks, ks), vs2 = two(log2vs, log2vs);
+                const uint32_t s_at = tmem_s + (n & 1) * Sh::kScoreCols;
+#pragma unroll
+                for (int c = 0; c < RW / 8; ++c)
+                    if (8 * c < live) tmem_get8(*reinterpret_cast<float(*)[8]>(t + 8 * c), s_at + 8 * c);
+                if constexpr (Sh::kStackQ) {
+                    float more[2][RW];
+#pragma unroll
+                    for (int c = 0; c < RW / 8; ++c)
+                        if (8 * c < live) {
+                            tmem_get8(*reinterpret_cast<float(*)[8]>(more[0] + 8 * c), s_at + NR + 8 * c);
+                            if (nq > 2) tmem_get8(*reinterpret_cast<float(*)[8]>(more[1] + 8 * c), s_at + 2 * NR + 8 * c);
+                        }
+                    tmem_loaded();
+#pragma unroll
+                    for (int c = 0; c < RW / 8; ++c)
+                        if (8 * c < live) {
+                            tmem_here(*reinterpret_cast<float(*)[8]>(t + 8 * c));
+                            tmem_here(*reinterpret_cast<float(*)[8]>(more[0] + 8 * c));
+                            if (nq > 2) tmem_here(*reinterpret_cast<float(*)[8]>(more[1] + 8 * c));
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) t[8 * c + j] += nq > 2 ? more[0][8 * c + j] + more[1][8 * c + j] : more[0][8 * c + j];
+                        }
+                } else {
+                    tmem_loaded();
+#pragma unroll
+                    for (int c = 0; c < RW / 8; ++c)
+                        if (8 * c < live) tmem_here(*reinterpret_cast<float(*)[8]>(t + 8 * c));
+                }
+#pragma unroll
+                for (int c = 0; c < RW / 8; ++c) {
+                    if (8 * c >= live) continue;
+                    float most[8];
+#pragma unroll
+                    for (int j = 0; j < 4; j += 2) {
+                        const float4 f = *reinterpret_cast<const float4 *>(&sh.row_f[at][r0 + 8 * c + 2 * j]);
+                        const float2 x = split(fma2(mul2(two(t[8 * c + 2 * j], t[8 * c + 2 * j + 1]), two(f.x, f.y)), ks2, vs2));
+                        const float2 y = split(fma2(mul2(two(t[8 * c + 2 * j + 2], t[8 * c + 2 * j + 3]), two(f.z, f.w)), ks2, vs2));
+                        t[8 * c + 2 * j] = x.x, t[8 * c + 2 * j + 1] = x.y, t[8 * c + 2 * j + 2] = y.x, t[8 * c + 2 * j + 3] = y.y;
+                    }
+                    if (flags & kMasked8) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (!(see >> (8 * c + j) & 1u)) t[8 * c + j] = -INFINITY;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) most[j] = warp_largest(t[8 * c + j]);
+                    if (lane == 0) {
+                        float4 *to = reinterpret_cast<float4 *>(&sh.red[wg][quarter][8 * c]);
+                        to[0] = make_float4(most[0], most[1], most[2], most[3]), to[1] = make_float4(most[4], most[5], most[6], most[7]);
+                    }
+                }
+                if ((flags & kRagged8) && wg == 0) wait(&sh.full_v[s], uint32_t(n / kStages) & 1u);
+                fence_before();
+                __syncwarp();
+                if (lane == 0) {  // the scores and what is known of the unit are read
+                    mbar_arrive(smem_u32(&sh.free_s[n & 1]));
+                    if (flags & kLast8) mbar_arrive(smem_u32(&sh.free_q[at]));
+                }
+            }
+            if (any(failed)) break;
+            bool moves = false;
+            if (token < RW) {
+                const float m = fmaxf(fmaxf(sh.red[wg][0][token], sh.red[wg][1][token]), fmaxf(sh.red[wg][2][token], sh.red[wg][3][token]));
+                const float whole = rintf(m);
+                float f = 1.f, g = 1.f, minus = 0.f;
+                if (token < live && fabsf(whole) < INFINITY) {
+                    if (M == -INFINITY) M = whole;
+                    if (whole > M + 60.f) g = ex2(fmaxf(M - whole, -126.f)), M = whole, moves = true;
+                    f = ex2(fmaxf(whole - M, -127.f));
+                    minus = float(kKv8Top) - whole;
+                } else if (m == INFINITY) {
+                    minus = -INFINITY;
+                }
+                float *mv = reinterpret_cast<float *>(&sh.move[wg][n & 1][token / 2]);
+                mv[token & 1] = minus, mv[2 + (token & 1)] = f;
+                sh.shrink[wg][token] = g;
+            }
+            moves = any(moves);
+            bool taken = (flags & kFirst8) != 0;
+            if (moves) {  // (rare)
+                if (!taken) take_up(n - 1);
+                taken = true;
+#pragma unroll
+                for (int i = 0; i < RW / 2; ++i) {
+                    const float2 g = *reinterpret_cast<const float2 *>(&sh.shrink[wg][2 * i]);
+                    l[i] = mul2(l[i], two(g.x, g.y));
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb) acc[mb][i] = mul2(acc[mb][i], two(g.x, g.y));
+                }
+            }
+            // the weights
+            uint4 parts[NP][RW / 16];
+            const Two inv2 = two(inv, inv);
+#pragma unroll
+            for (int c = 0; c < RW / 8; ++c) {
+                uint32_t code[NP][2] = {};
+                if (8 * c < live) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 mv = sh.move[wg][n & 1][4 * c + j];
+                        const float2 x = split(add2(two(t[8 * c + 2 * j], t[8 * c + 2 * j + 1]), two(mv.x, mv.y)));
+                        const float w0 = ex2(x.x), w1 = ex2(x.y);
+                        l[4 * c + j] = fma2(mul2(two(w0, w1), inv2), two(mv.z, mv.w), l[4 * c + j]);
+                        uint32_t p[NP];
+                        parts8(w0, w1, p);
+#pragma unroll
+                        for (int k = 0; k < NP; ++k) code[k][j / 2] |= p[k] << (16 * (j & 1));
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < NP; ++k) {
+                    if (c & 1)
+                        parts[k][c / 2].z = code[k][0], parts[k][c / 2].w = code[k][1];
+                    else
+                        parts[k][c / 2].x = code[k][0], parts[k][c / 2].y = code[k][1];
+                }
+            }
+            if (Sh::kP == 1 && !taken) wait(&sh.full_o[(n - 1) & 1], uint32_t((n - 1) >> 1) & 1u);  // its weights are in this place
+            if (!failed) {
+                uint8_t *to = sh.w[n % Sh::kP] + r0 / 16 * 2048 + token * 16;
+#pragma unroll
+                for (int k = 0; k < NP; ++k)
+#pragma unroll
+                    for (int c = 0; c < RW / 16; ++c)
+                        if (16 * c < live) *reinterpret_cast<uint4 *>(to + (k * (NR / 16) + c) * 2048) = parts[k][c];
+                if ((flags & kRagged8) && wg == 0 && inv == 0.f) {  // a code that is not there may be a NaN, which no weight of 0 takes away
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) *reinterpret_cast<uint4 *>(sh.v[s] + kv8_code_byte(D, token, 16 * i)) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            fence_operands();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.full_w[n & 1]));
+            if (!taken) take_up(n - 1);
+            if (!(flags & kLast8)) continue;
+
+            // the segment's end
+            take_up(n);
+#pragma unroll
+            for (int i = 0; i < RW / 2; ++i) {
+                float2 x = split(l[i]);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) x.x += __shfl_xor_sync(0xFFFFFFFFu, x.x, o), x.y += __shfl_xor_sync(0xFFFFFFFFu, x.y, o);
+                if (lane == 0) *reinterpret_cast<float2 *>(&sh.red[wg][quarter][2 * i]) = x;
+            }
+            if (any(failed)) break;
+            const bool whole = seg_lo >= ubegin && seg_lo + seg.tiles <= uend;
+            const int64_t slot = 2 * cta + (seg_lo > ubegin ? 1 : 0);
+            if (token < RW) {
+                const float sum = (sh.red[wg][0][token] + sh.red[wg][1][token]) + (sh.red[wg][2][token] + sh.red[wg][3][token]);
+                sh.fin[wg][token] = make_float2(token >= live || sum == 0.f ? 0.f : 1.f / sum, 0.f);
+                if (!whole && SV_IN(slot, 2 * ncta)) a.ml[slot * NR + r0 + token] = make_float2(M, sum);
+            }
+            any(false);
+            if (writes) {
+                const int d = token;
+#pragma unroll
+                for (int i = 0; i < RW; ++i) {
+                    const int r = r0 + i, row = seg.rt * NR + r, node = row / a.G;
+                    if (node >= a.T) break;
+                    const float scale = sh.fin[wg][i].x;
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb) {
+                        const float2 x2 = split(acc[mb][i / 2]);
+                        const float x = i & 1 ? x2.y : x2.x;
+                        if (whole) {
+                            a.out[((seg.b * int64_t(a.T) + node) * a.H * a.G + seg.h * a.G + row - node * a.G) * D + mb * 128 + d] =
+                                kv_from_float(scale == 0.f ? 0.f : x * scale, a.bf16);
+                        } else if (SV_IN(slot, 2 * ncta)) {
+                            a.acc[(slot * NR + r) * D + mb * 128 + d] = x;
+                        }
+                    }
+                }
+            }
+            if (tid == 128 && seg_lo <= ubegin)  // the share's first segment
+                a.desc[cta] = describe(total, cta, ncta, ubegin, seg_lo, seg_lo + seg.tiles, seg.b, seg.h, seg.rt, seg.fresh);
+        }
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(Sh::kCols));
+}
+
+template <int D, int NR, int NP>
+cudaError_t launch_attention8(const AttArgs &a, int nq, int grid, cudaStream_t s) {
+    using Sh = Att8Shared<D, NR, NP>;
+    constexpr size_t fixed = sizeof(Sh) + 1024;
+    static_assert(fixed + (NR == 64 ? SV_MAX_TREE_NODES : NR) * 4 * (1 + Sh::kQ * Sh::W) <= 227 * 1024, "the largest tree");
+    static_assert((fixed + 1024) * att8_occupancy(D, NR) <= 228 * 1024 && Sh::kUsed <= Sh::kCols && Sh::kCols * att8_occupancy(D, NR) <= 512, "");
+    const size_t smem = fixed + (a.parent ? size_t(a.T) * 4 * (1 + Sh::kQ * Sh::W) : 0);
+    static std::atomic<int> allowed[64];
+    cudaError_t e = allow_shared(kv8_attention_kernel<D, NR, NP>, int(smem), allowed);
+    if (e != cudaSuccess) return e;
+    e = launch_after(kv8_attention_kernel<D, NR, NP>, unsigned(grid), unsigned(att8_threads(NR)), smem, s, a, nq);
+    if (e != cudaSuccess) return e;
+    return launch_join<D>(a, grid, NR, s);
+}
+
+// The kernels of a head dimension and number of weights' parts, each in its own translation unit.
+template <int D, int NP>
+cudaError_t launch_attention8_rows(const AttArgs &a, int nr, int nq, int grid, cudaStream_t s);
+
+#define SV_KV8_ATTENTION_INSTANTIATE(D, NP)                                                                   \
+    template <>                                                                                              \
+    cudaError_t launch_attention8_rows<D, NP>(const AttArgs &a, int nr, int nq, int grid, cudaStream_t s) {    \
+        return nr == 16 ? launch_attention8<D, 16, NP>(a, nq, grid, s)                                         \
+               : nr == 32 ? launch_attention8<D, 32, NP>(a, nq, grid, s)                                       \
+                          : launch_attention8<D, 64, NP>(a, nq, grid, s);                                      \
+    }
+
+}  // namespace sv
