@@ -34,15 +34,19 @@
 namespace sv {
 
 constexpr int kTile8 = 128;
-__host__ __device__ constexpr int att8_groups(int NR) { return NR == 64 ? 2 : 1; }
+constexpr int kGroupRows8 = 16;  // query rows of a softmax group
+__host__ __device__ constexpr int att8_groups(int NR) { return NR / kGroupRows8; }
 __host__ __device__ constexpr int att8_threads(int NR) { return 128 + 128 * att8_groups(NR); }
 // Tiles in the rings, places for queries and weights, and blocks an SM: by shared memory and registers.
-__host__ __device__ constexpr int att8_stages(int D, int NR) { return D == 64 ? (NR == 16 ? 5 : NR == 32 ? 4 : 6) : D == 128 ? (NR == 64 ? 4 : 2) : (NR == 16 ? 3 : 2); }
-__host__ __device__ constexpr int att8_q_places(int D, int NR) { return D == 256 && NR == 64 ? 1 : 2; }
-__host__ __device__ constexpr int att8_w_places(int D, int NR) { return NR == 64 || (D == 256 && NR == 16) || (D == 128 && NR == 32) ? 1 : 2; }
-__host__ __device__ constexpr int att8_occupancy(int D, int NR) { return D == 256 || NR == 64 ? 1 : 2; }
-// Rows a tile, by the rows that share a kv head.
-inline int att8_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+__host__ __device__ constexpr int att8_stages(int D, int NR) { return D == 64 ? (NR == 16 ? 5 : NR == 32 ? 4 : 6) : D == 128 ? (NR <= 32 ? 2 : 3) : (NR == 16 ? 3 : 2); }
+__host__ __device__ constexpr int att8_q_places(int D, int NR) { return D == 256 && NR >= 48 ? 1 : 2; }
+__host__ __device__ constexpr int att8_w_places(int D, int NR) { return NR >= 48 || (D == 256 && NR == 16) || (D == 128 && NR == 32) ? 1 : 2; }
+__host__ __device__ constexpr int att8_occupancy(int D, int NR) { return D == 256 || NR >= 48 ? 1 : 2; }
+// Rows a tile, by the rows that share a kv head: as few tiles of up to 64 as there have to be, and no larger than they need be.
+inline int att8_rows(int64_t rows) {
+    const int64_t tiles = (rows + 63) / 64;
+    return int((rows + tiles * kGroupRows8 - 1) / (tiles * kGroupRows8)) * kGroupRows8;
+}
 
 enum : int { kMasked8 = 1, kRagged8 = 2, kFirst8 = 4, kLast8 = 8 };  // in Unit::masked: not every row sees every token; not every token is there; of a segment
 
@@ -53,12 +57,12 @@ struct alignas(16) Info8 {
 
 template <int D, int NR, int NP>
 struct Att8Shared {
-    static constexpr int W = att8_groups(NR), RW = NR / W, kStages = att8_stages(D, NR), kInfos = kStages + 2;
+    static constexpr int W = att8_groups(NR), RW = kGroupRows8, SW = (NR + 31) / 32, kStages = att8_stages(D, NR), kInfos = kStages + 2;
     static constexpr int kQ = att8_q_places(D, NR), kP = att8_w_places(D, NR), MB = D == 256 ? 2 : 1;
     // Few rows: a product reads the cache's operand at its full width whatever the columns, so the parts are columns of
     // one product and are added up afterwards.
     static constexpr bool kStackQ = NR == 16, kStackP = NR == 16;
-    static constexpr int kScoreCols = kStackQ ? 64 : NR, kOutEach = kStackP && NP == 3 ? 64 : NR < 32 ? 32 : NR, kOutCols = MB * kOutEach;
+    static constexpr int kScoreCols = NR == 32 ? 32 : 64, kOutEach = NR >= 48 || (kStackP && NP == 3) ? 64 : 32, kOutCols = MB * kOutEach;
     static constexpr int kUsed = 2 * (kScoreCols + kOutCols), kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     alignas(1024) uint8_t k[kStages][kTile8 * D];
     uint8_t v[kStages][kTile8 * D];       // (64 dimensions: a product's upper 64 rows read past the end, into w)
@@ -66,10 +70,9 @@ struct Att8Shared {
     uint8_t q[kQ][3 * NR * D];            // [part][row], laid out as the keys
     Info8 info[kInfos];
     alignas(16) float row_f[kQ][NR];      // log2(e) scale times the power of two taken out of the row
-    alignas(16) float red[W][4][RW];
-    alignas(16) float4 move[W][2][RW / 2];  // of a row pair: -m, then 2^(m - M)
-    alignas(16) float shrink[W][RW];
-    alignas(16) float2 fin[W][RW];
+    alignas(16) float red[W][2][4][RW];        // maxima of a warp's 32 tokens
+    alignas(16) float sums[W][4][RW];
+    alignas(16) float4 move[W][4][2][RW / 2];  // of a row pair: -m, then 2^(m - M); every warp has its own
     // Each is waited for before what it tells of can come about once more, so that a phase's parity is enough: a unit's place in `info`
     // is taken again after the scores of two units later, which wait for the softmax to have read this one's.
     alignas(8) uint64_t full_k[kStages], full_v[kStages], empty_k[kStages], empty_v[kStages], full_i[kInfos];
@@ -77,15 +80,17 @@ struct Att8Shared {
     uint32_t tmem;
 };
 
-__device__ __forceinline__ uint64_t operand8(uint32_t addr, uint32_t along_k, uint32_t across) {
-    return uint64_t((addr & 0x3FFFF) >> 4) | uint64_t(along_k >> 4) << 16 | uint64_t(across >> 4) << 32 | uint64_t(1) << 46;
-}
+// A shared-memory operand without a swizzle: blocks of 8 x 16 bytes, `along_k` and `across` bytes apart.  Its words: the address and the
+// first distance, and the second.  Later steps are sums with the first word (computed anew, a descriptor cost the issuing thread 150 clocks a product).
+__device__ __forceinline__ uint32_t operand8(uint32_t addr, uint32_t along_k) { return (addr & 0x3FFFF) >> 4 | along_k >> 4 << 16; }
+__host__ __device__ constexpr uint32_t operand8_high(uint32_t across) { return across >> 4 | 1u << 14; }
 // 8-bit floats (4 bits of exponent) into fp32, 128 rows, N columns; `turned`: both operands have their rows contiguous.
 __device__ __forceinline__ constexpr uint32_t kind8(int N, bool turned) { return 1u << 4 | (turned ? 3u << 15 : 0u) | uint32_t(N / 8) << 17 | 8u << 24; }
-__device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
+__device__ __forceinline__ void mma8(uint32_t d, uint32_t a, uint32_t a_high, uint32_t b, uint32_t b_high, uint32_t kind, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(kind), "r"(uint32_t(add))
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(a_high), "r"(b), "r"(b_high), "r"(kind), "r"(uint32_t(add))
         : "memory");
 }
 // Eight columns of this warp's 32 rows, there after tmem_loaded().
@@ -105,6 +110,14 @@ __device__ __forceinline__ float warp_largest(float x) {  // NaN left out
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
 }
+// mbar_wait by a whole warp: true for all its lanes or none.
+static __device__ __noinline__ bool warp_wait_long(uint32_t bar, uint32_t parity) {
+    const bool there = mbar_wait(bar, parity);
+    return __all_sync(0xFFFFFFFFu, there);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, mbar_try(smem_u32(bar), parity)) || warp_wait_long(smem_u32(bar), parity);
+}
 // Barrier kId of N threads; true if x is for any of them.
 template <int kId, int N>
 __device__ __forceinline__ bool group_or(bool x) {
@@ -118,32 +131,21 @@ __device__ __forceinline__ bool group_or(bool x) {
     return r != 0;
 }
 
-// The parts of a pair of numbers, two codes each (the first number's in the low byte).
-__device__ __forceinline__ uint32_t codes8_of_halves(uint32_t h) {
-    uint16_t c;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
-    return c;
-}
-__device__ __forceinline__ uint32_t halves_of_codes8(uint32_t c) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(c)));
-    return h;
-}
-// Two parts, through fp16: 11 bits are more than both hold.
-__device__ __forceinline__ void parts8(float x, float y, uint32_t (&c)[2]) {
-    const __half2 h = __floats2half2_rn(x, y);
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(&h);
-    c[0] = codes8_of_halves(w);
-    const uint32_t b = halves_of_codes8(c[0]);
-    const __half2 rest = __hsub2(h, *reinterpret_cast<const __half2 *>(&b));  // exact
-    c[1] = codes8_of_halves(*reinterpret_cast<const uint32_t *>(&rest));
-}
-__device__ __forceinline__ void parts8(float x, float y, uint32_t (&c)[3]) {
+// The parts of a pair of numbers, NP times two codes (the first number's in the low byte).  A part is the number rounded to 4 bits, by the
+// difference with a multiple of it (Dekker's splitting): the conversion to a code then rounds only what is below 2^-6, and a conversion back
+// would cost four times a conversion there.
+template <int NP>
+__device__ __forceinline__ void parts8(float x, float y, uint32_t (&c)[NP]) {
+    const Two minus = two(-1.f, -1.f), split4 = two(1048577.f, 1048577.f);  // 2^20 + 1
+    Two v = two(x, y);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        c[i] = kv8_codes(x, y);
-        const float2 b = kv8_numbers(c[i]);
-        x -= b.x, y -= b.y;  // exact
+    for (int i = 0; i < NP; ++i) {
+        const float2 f = split(v);
+        c[i] = kv8_codes(f.x, f.y);
+        if (i + 1 < NP) {
+            const Two m = mul2(v, split4), top = fma2(fma2(v, minus, m), minus, m);  // m - (m - v)
+            v = fma2(top, minus, v);
+        }
     }
 }
 
@@ -255,16 +257,20 @@ __device__ __forceinline__ void issue_products8(const AttArgs &a, Att8Shared<D, 
         if (n >= 2) wait(&sh.free_s[n & 1], uint32_t((n >> 1) - 1) & 1u);
         if (!ok) return;
         fence_after();
-        const uint32_t d = tmem + (n & 1) * Sh::kScoreCols, k = smem_u32(sh.k[s]), q = smem_u32(sh.q[segment % Sh::kQ]);
+        constexpr uint32_t high = operand8_high(8 * D);
+        const uint32_t d = tmem + (n & 1) * Sh::kScoreCols, k = operand8(smem_u32(sh.k[s]), 128);
+        uint32_t q = operand8(smem_u32(sh.q[segment % Sh::kQ]), 128);
         if constexpr (Sh::kStackQ) {
             const uint32_t kind = kind8(NR, false) + uint32_t((nq - 1) * NR / 8) * (1u << 17);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) mma8(d, operand8(k + i * 256, 128, 8 * D), operand8(q + i * 256, 128, 8 * D), kind, i > 0);
+            for (int i = 0; i < D / 32; ++i) mma8(d, k + i * 16, high, q + i * 16, high, kind, i > 0);
         } else {
-            for (int p = 0; p < nq; ++p)
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i)
-                    mma8(d, operand8(k + i * 256, 128, 8 * D), operand8(q + p * NR * D + i * 256, 128, 8 * D), kind8(NR, false), p > 0 || i > 0);
+            for (int p = 0; p < 3; ++p, q += NR * D / 16)
+                if (p < 2 || nq > 2) {
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) mma8(d, k + i * 16, high, q + i * 16, high, kind8(NR, false), p > 0 || i > 0);
+                }
         }
         wide_commit(&sh.empty_k[s]);
         wide_commit(&sh.full_s[n & 1]);
@@ -277,15 +283,16 @@ __device__ __forceinline__ void issue_products8(const AttArgs &a, Att8Shared<D, 
         if (n >= 2) wait(&sh.free_o[n & 1], uint32_t((n >> 1) - 1) & 1u);
         if (!ok) return;
         fence_after();
-        const uint32_t d = tmem + 2 * Sh::kScoreCols + (n & 1) * Sh::kOutCols, v = smem_u32(sh.v[s]), w = smem_u32(sh.w[n % Sh::kP]);
         constexpr int parts = Sh::kStackP ? 1 : NP, cols = Sh::kStackP ? NP * NR : NR;
+        const uint32_t d = tmem + 2 * Sh::kScoreCols + (n & 1) * Sh::kOutCols;
+        const uint32_t v = operand8(smem_u32(sh.v[s]), 8 * D), w = operand8(smem_u32(sh.w[n % Sh::kP]), 128);
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
             for (int p = 0; p < parts; ++p)
 #pragma unroll
                 for (int i = 0; i < kTile8 / 32; ++i)
-                    mma8(d + mb * Sh::kOutEach, operand8(v + mb * 1024 + i * 32 * D, 8 * D, 128), operand8(w + p * NR * kTile8 + i * 512, 128, 2048),
+                    mma8(d + mb * Sh::kOutEach, v + mb * 64 + i * 2 * D, operand8_high(128), w + p * NR * kTile8 / 16 + i * 32, operand8_high(2048),
                          kind8(cols, true), p > 0 || i > 0);
         wide_commit(&sh.empty_v[s]);
         wide_commit(&sh.full_o[n & 1]);
@@ -304,7 +311,7 @@ template <int D, int NR, int NP>
 __device__ __forceinline__ void bring_queries8(const AttArgs &a, Att8Shared<D, NR, NP> &sh, const int *parent_s, uint32_t *see_s, Cursor<kTile8> &cur,
                                                int ubegin, int uend, int tid) {
     using Sh = Att8Shared<D, NR, NP>;
-    constexpr int L = D / 8, P = 64 / L, W = Sh::W;
+    constexpr int L = D / 8, P = 64 / L, SW = Sh::SW;
     const int c = tid % L, d0 = c * 8;
     int u = ubegin;
     for (int segment = 0; u < uend; ++segment) {
@@ -347,13 +354,13 @@ __device__ __forceinline__ void bring_queries8(const AttArgs &a, Att8Shared<D, N
             if (c == 0) sh.row_f[at][r] = a.scale * 1.4426950408889634f * power2(odd ? 0 : e2);
         }
         if (a.parent) {  // which rows see a new token
-            uint32_t *see = see_s + at * a.T * W;
-            for (int i = tid; i < a.T * W; i += 64) see[i] = 0;
+            uint32_t *see = see_s + at * a.T * SW;
+            for (int i = tid; i < a.T * SW; i += 64) see[i] = 0;
             group_or<3, 64>(false);
             if (tid < NR) {
                 const int node = (un.rt * NR + tid) / a.G;
                 for (int v = node < un.fresh ? node : -1; v >= 0;) {
-                    atomicOr(see + v * W + tid / 32, 1u << (tid & 31));
+                    atomicOr(see + v * SW + tid / 32, 1u << (tid & 31));
                     const int up = parent_s[v];
                     v = up < v ? up : -1;
                 }
@@ -377,7 +384,7 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
     unsigned char *raw = raw0 + ((1024 - (smem_u32(raw0) & 1023)) & 1023);
     Sh &sh = *reinterpret_cast<Sh *>(raw);
     int *parent_s = reinterpret_cast<int *>(raw + sizeof(Sh));
-    uint32_t *see_s = reinterpret_cast<uint32_t *>(parent_s + (a.parent ? a.T : 0));  // [kQ][T][W]
+    uint32_t *see_s = reinterpret_cast<uint32_t *>(parent_s + (a.parent ? a.T : 0));  // [kQ][T][SW]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ncta = int(gridDim.x), cta = int(blockIdx.x);
 
@@ -426,19 +433,25 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         const uint32_t tmem_s = sh.tmem + lanes + r0, tmem_o = sh.tmem + lanes + 2 * Sh::kScoreCols + r0;
         const bool writes = D >= 128 || quarter < 2;  // has a dimension
-        auto any = [&](bool x) { return W == 1 || wg == 0 ? group_or<1, 128>(x) : group_or<2, 128>(x); };
+        int granule_log2 = 4;
+        while (1 << granule_log2 < a.granule) ++granule_log2;
+        auto any = [&](bool x) {
+            if (W > 3 && wg == 3) return group_or<4, 128>(x);
+            if (W > 2 && wg == 2) return group_or<5, 128>(x);
+            if (W > 1 && wg == 1) return group_or<2, 128>(x);
+            return group_or<1, 128>(x);
+        };
         bool failed = false;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            if (!failed && !mbar_wait(smem_u32(bar), parity)) {
+            if (!warp_wait(bar, parity) && !failed) {
                 failed = true;
                 atomicExch(a.status, int(SV_ERR_TIMEOUT));
             }
-            failed = __any_sync(0xFFFFFFFFu, failed);
         };
         Unit seg{};
         int seg_lo = 0, segment = -1, live = 0;  // live: rows of this group
         Two l[RW / 2], acc[MB][RW / 2];
-        float M = -INFINITY;  // of row `token` of the group
+        float M = -INFINITY;  // of row lane % 16 of the group
         // the output of unit n, which is of the segment at hand
         auto take_up = [&](int n) {
             wait(&sh.full_o[n & 1], uint32_t(n >> 1) & 1u);
@@ -462,7 +475,7 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                         for (int p = 0; p < parts; ++p) tmem_here(o[mb][p]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float4 mv = sh.move[wg][n & 1][4 * c + j];
+                        const float4 mv = sh.move[wg][quarter][n & 1][4 * c + j];
 #pragma unroll
                         for (int mb = 0; mb < MB; ++mb) {
                             Two x = two(o[mb][0][2 * j], o[mb][0][2 * j + 1]);
@@ -478,10 +491,9 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
             if (lane == 0) mbar_arrive(smem_u32(&sh.free_o[n & 1]));
         };
 
-        for (int n = 0; n < units; ++n) {
-            const int s = n % kStages;
-            const Info8 &in = sh.info[n % Sh::kInfos];
-            wait(&sh.full_i[n % Sh::kInfos], uint32_t(n / Sh::kInfos) & 1u);
+        for (int n = 0, s = 0, at_info = 0; n < units; ++n) {
+            const Info8 &in = sh.info[at_info];
+            wait(&sh.full_i[at_info], uint32_t(n / Sh::kInfos) & 1u);
             int flags = 0;
             float t[RW];
             float inv = 0.f;  // 1 / s'
@@ -497,89 +509,71 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                     for (int i = 0; i < RW / 2; ++i) l[i] = acc[0][i] = acc[MB - 1][i] = 0;
                     wait(&sh.full_q[segment % Sh::kQ], uint32_t(segment / Sh::kQ) & 1u);
                 }
-                wait(&sh.full_s[n & 1], uint32_t(n >> 1) & 1u);
-            }
-            if (!failed) {
-                fence_after();
-                const int tok0 = in.unit.tile * kTile8, at = segment % Sh::kQ;
+                // the scale of this thread's token, and the rows that see it
+                const int at = segment % Sh::kQ;
                 float ks = 0.f, log2vs = 0.f;
-                uint32_t see = 0xFFFFFFFFu;
+                uint32_t see = 0xFFFFu;
                 bool there = true;
                 if (flags & kMasked8) {
-                    const int x = tok0 + token - seg.before;  // among the new tokens
-                    there = tok0 + token < seg.len && (in.unit.have >> (4 * (token / a.granule)) & 1u);
-                    see = live >= 32 ? 0xFFFFFFFFu : (1u << live) - 1;
-                    if (!there) {
-                        see = 0;
-                    } else if (x >= 0) {
+                    const int j = in.unit.tile * kTile8 + token, x = j - seg.before;  // among the new tokens
+                    there = j < seg.len && (in.unit.have >> (4 * (token >> granule_log2)) & 1u);
+                    see = there ? (1u << live) - 1 : 0u;
+                    if (there && x >= 0) {
                         if (a.parent) {
-                            see &= see_s[(at * a.T + x) * W + wg];
+                            see &= see_s[(at * a.T + x) * Sh::SW + wg / 2] >> (16 * (wg & 1));
                         } else {
-                            const int hidden = min(max(x * a.G - seg.rt * NR - r0, 0), 32);  // rows of earlier tokens
-                            see &= hidden >= 32 ? 0u : 0xFFFFFFFFu << hidden;
+                            see &= 0xFFFFu << min(max(x * a.G - seg.rt * NR - r0, 0), 16);  // not the rows of earlier tokens
                         }
                     }
                 }
+                const uint2 word = *reinterpret_cast<const uint2 *>(in.word[token / kKv8Block]);
                 if (there) {
-                    const uint2 word = *reinterpret_cast<const uint2 *>(in.word[token / kKv8Block]);
                     const int e = kv8_exponent(word.y);
                     ks = (word.x | word.y) >> (token & 15) & 1u ? NAN : __uint_as_float(word.x & 0xFFFF0000u);
                     log2vs = float(e), inv = kv8_power(-e);
                 }
+                if (flags & kRagged8) wait(&sh.full_v[s], uint32_t(n / kStages) & 1u);
+                wait(&sh.full_s[n & 1], uint32_t(n >> 1) & 1u);
+                fence_after();
                 const Two ks2 = two(ks, ks), vs2 = two(log2vs, log2vs);
                 const uint32_t s_at = tmem_s + (n & 1) * Sh::kScoreCols;
-#pragma unroll
-                for (int c = 0; c < RW / 8; ++c)
-                    if (8 * c < live) tmem_get8(*reinterpret_cast<float(*)[8]>(t + 8 * c), s_at + 8 * c);
-                if constexpr (Sh::kStackQ) {
-                    float more[2][RW];
-#pragma unroll
-                    for (int c = 0; c < RW / 8; ++c)
-                        if (8 * c < live) {
-                            tmem_get8(*reinterpret_cast<float(*)[8]>(more[0] + 8 * c), s_at + NR + 8 * c);
-                            if (nq > 2) tmem_get8(*reinterpret_cast<float(*)[8]>(more[1] + 8 * c), s_at + 2 * NR + 8 * c);
-                        }
-                    tmem_loaded();
-#pragma unroll
-                    for (int c = 0; c < RW / 8; ++c)
-                        if (8 * c < live) {
-                            tmem_here(*reinterpret_cast<float(*)[8]>(t + 8 * c));
-                            tmem_here(*reinterpret_cast<float(*)[8]>(more[0] + 8 * c));
-                            if (nq > 2) tmem_here(*reinterpret_cast<float(*)[8]>(more[1] + 8 * c));
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) t[8 * c + j] += nq > 2 ? more[0][8 * c + j] + more[1][8 * c + j] : more[0][8 * c + j];
-                        }
-                } else {
-                    tmem_loaded();
-#pragma unroll
-                    for (int c = 0; c < RW / 8; ++c)
-                        if (8 * c < live) tmem_here(*reinterpret_cast<float(*)[8]>(t + 8 * c));
-                }
+                constexpr int parts = Sh::kStackQ ? 3 : 1;
 #pragma unroll
                 for (int c = 0; c < RW / 8; ++c) {
                     if (8 * c >= live) continue;
-                    float most[8];
+                    float x[parts][8], most[8];
+                    tmem_get8(x[0], s_at + 8 * c);
+                    if constexpr (parts > 1) {
+                        tmem_get8(x[1], s_at + NR + 8 * c);
+                        tmem_get8(x[2], s_at + (nq > 2 ? 2 * NR : NR) + 8 * c);
+                    }
+                    tmem_loaded();
 #pragma unroll
-                    for (int j = 0; j < 4; j += 2) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&sh.row_f[at][r0 + 8 * c + 2 * j]);
-                        const float2 x = split(fma2(mul2(two(t[8 * c + 2 * j], t[8 * c + 2 * j + 1]), two(f.x, f.y)), ks2, vs2));
-                        const float2 y = split(fma2(mul2(two(t[8 * c + 2 * j + 2], t[8 * c + 2 * j + 3]), two(f.z, f.w)), ks2, vs2));
-                        t[8 * c + 2 * j] = x.x, t[8 * c + 2 * j + 1] = x.y, t[8 * c + 2 * j + 2] = y.x, t[8 * c + 2 * j + 3] = y.y;
+                    for (int p = 0; p < parts; ++p) tmem_here(x[p]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = *reinterpret_cast<const float2 *>(&sh.row_f[at][r0 + 8 * c + 2 * j]);
+                        Two y = two(x[0][2 * j], x[0][2 * j + 1]);
+                        if constexpr (parts > 1) {
+                            const Two z = two(x[1][2 * j], x[1][2 * j + 1]);
+                            y = add2(y, nq > 2 ? add2(z, two(x[2][2 * j], x[2][2 * j + 1])) : z);
+                        }
+                        const float2 u = split(fma2(mul2(y, two(f.x, f.y)), ks2, vs2));
+                        t[8 * c + 2 * j] = u.x, t[8 * c + 2 * j + 1] = u.y;
                     }
                     if (flags & kMasked8) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             if (!(see >> (8 * c + j) & 1u)) t[8 * c + j] = -INFINITY;
+                        __syncwarp();
                     }
-                    __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 8; ++j) most[j] = warp_largest(t[8 * c + j]);
                     if (lane == 0) {
-                        float4 *to = reinterpret_cast<float4 *>(&sh.red[wg][quarter][8 * c]);
+                        float4 *to = reinterpret_cast<float4 *>(&sh.red[wg][n & 1][quarter][8 * c]);
                         to[0] = make_float4(most[0], most[1], most[2], most[3]), to[1] = make_float4(most[4], most[5], most[6], most[7]);
                     }
                 }
-                if ((flags & kRagged8) && wg == 0) wait(&sh.full_v[s], uint32_t(n / kStages) & 1u);
                 fence_before();
                 __syncwarp();
                 if (lane == 0) {  // the scores and what is known of the unit are read
@@ -588,71 +582,63 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                 }
             }
             if (any(failed)) break;
-            bool moves = false;
-            if (token < RW) {
-                const float m = fmaxf(fmaxf(sh.red[wg][0][token], sh.red[wg][1][token]), fmaxf(sh.red[wg][2][token], sh.red[wg][3][token]));
+            bool taken = (flags & kFirst8) != 0;
+            {  // each warp for itself: m, and what it makes of M (lane: row)
+                const int row = lane & 15;
+                const float(*red)[RW] = sh.red[wg][n & 1];
+                const float m = fmaxf(fmaxf(red[0][row], red[1][row]), fmaxf(red[2][row], red[3][row]));
                 const float whole = rintf(m);
-                float f = 1.f, g = 1.f, minus = 0.f;
-                if (token < live && fabsf(whole) < INFINITY) {
+                float f = 1.f, g = 1.f, minus = m == INFINITY ? -INFINITY : 0.f;
+                if (row < live && fabsf(whole) < INFINITY) {
                     if (M == -INFINITY) M = whole;
-                    if (whole > M + 60.f) g = ex2(fmaxf(M - whole, -126.f)), M = whole, moves = true;
+                    if (whole > M + 60.f) g = ex2(fmaxf(M - whole, -126.f)), M = whole;
                     f = ex2(fmaxf(whole - M, -127.f));
                     minus = float(kKv8Top) - whole;
-                } else if (m == INFINITY) {
-                    minus = -INFINITY;
                 }
-                float *mv = reinterpret_cast<float *>(&sh.move[wg][n & 1][token / 2]);
-                mv[token & 1] = minus, mv[2 + (token & 1)] = f;
-                sh.shrink[wg][token] = g;
-            }
-            moves = any(moves);
-            bool taken = (flags & kFirst8) != 0;
-            if (moves) {  // (rare)
-                if (!taken) take_up(n - 1);
-                taken = true;
-#pragma unroll
-                for (int i = 0; i < RW / 2; ++i) {
-                    const float2 g = *reinterpret_cast<const float2 *>(&sh.shrink[wg][2 * i]);
-                    l[i] = mul2(l[i], two(g.x, g.y));
-#pragma unroll
-                    for (int mb = 0; mb < MB; ++mb) acc[mb][i] = mul2(acc[mb][i], two(g.x, g.y));
+                if (lane < 16) {
+                    float *mv = reinterpret_cast<float *>(&sh.move[wg][quarter][n & 1][row / 2]);
+                    mv[row & 1] = minus, mv[2 + (row & 1)] = f;
                 }
+                if (__any_sync(0xFFFFFFFFu, g != 1.f)) {  // (rare)
+                    if (!taken) take_up(n - 1);
+                    taken = true;
+#pragma unroll
+                    for (int i = 0; i < RW / 2; ++i) {
+                        const Two g2 = two(__shfl_sync(0xFFFFFFFFu, g, 2 * i), __shfl_sync(0xFFFFFFFFu, g, 2 * i + 1));
+                        l[i] = mul2(l[i], g2);
+#pragma unroll
+                        for (int mb = 0; mb < MB; ++mb) acc[mb][i] = mul2(acc[mb][i], g2);
+                    }
+                }
+                __syncwarp();
             }
             // the weights
-            uint4 parts[NP][RW / 16];
+            uint32_t code[NP][4];
             const Two inv2 = two(inv, inv);
 #pragma unroll
             for (int c = 0; c < RW / 8; ++c) {
-                uint32_t code[NP][2] = {};
-                if (8 * c < live) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 mv = sh.move[wg][n & 1][4 * c + j];
-                        const float2 x = split(add2(two(t[8 * c + 2 * j], t[8 * c + 2 * j + 1]), two(mv.x, mv.y)));
-                        const float w0 = ex2(x.x), w1 = ex2(x.y);
-                        l[4 * c + j] = fma2(mul2(two(w0, w1), inv2), two(mv.z, mv.w), l[4 * c + j]);
-                        uint32_t p[NP];
-                        parts8(w0, w1, p);
+                for (int k = 0; k < NP; ++k) code[k][2 * c] = code[k][2 * c + 1] = 0;
+                if (8 * c >= live) continue;
 #pragma unroll
-                        for (int k = 0; k < NP; ++k) code[k][j / 2] |= p[k] << (16 * (j & 1));
-                    }
-                }
+                for (int j = 0; j < 4; ++j) {
+                    const float4 mv = sh.move[wg][quarter][n & 1][4 * c + j];
+                    const float2 x = split(add2(two(t[8 * c + 2 * j], t[8 * c + 2 * j + 1]), two(mv.x, mv.y)));
+                    const float w0 = ex2(x.x), w1 = ex2(x.y);
+                    l[4 * c + j] = fma2(mul2(two(w0, w1), inv2), two(mv.z, mv.w), l[4 * c + j]);
+                    uint32_t p[NP];
+                    parts8(w0, w1, p);
 #pragma unroll
-                for (int k = 0; k < NP; ++k) {
-                    if (c & 1)
-                        parts[k][c / 2].z = code[k][0], parts[k][c / 2].w = code[k][1];
-                    else
-                        parts[k][c / 2].x = code[k][0], parts[k][c / 2].y = code[k][1];
+                    for (int k = 0; k < NP; ++k) code[k][2 * c + j / 2] |= p[k] << (16 * (j & 1));
                 }
             }
             if (Sh::kP == 1 && !taken) wait(&sh.full_o[(n - 1) & 1], uint32_t((n - 1) >> 1) & 1u);  // its weights are in this place
             if (!failed) {
-                uint8_t *to = sh.w[n % Sh::kP] + r0 / 16 * 2048 + token * 16;
+                uint8_t *to = sh.w[n % Sh::kP] + wg * 2048 + token * 16;
+                if (live > 0) {
 #pragma unroll
-                for (int k = 0; k < NP; ++k)
-#pragma unroll
-                    for (int c = 0; c < RW / 16; ++c)
-                        if (16 * c < live) *reinterpret_cast<uint4 *>(to + (k * (NR / 16) + c) * 2048) = parts[k][c];
+                    for (int k = 0; k < NP; ++k) *reinterpret_cast<uint4 *>(to + k * NR * kTile8) = make_uint4(code[k][0], code[k][1], code[k][2], code[k][3]);
+                }
                 if ((flags & kRagged8) && wg == 0 && inv == 0.f) {  // a code that is not there may be a NaN, which no weight of 0 takes away
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) *reinterpret_cast<uint4 *>(sh.v[s] + kv8_code_byte(D, token, 16 * i)) = make_uint4(0, 0, 0, 0);
@@ -662,6 +648,8 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.full_w[n & 1]));
             if (!taken) take_up(n - 1);
+            if (++s == kStages) s = 0;
+            if (++at_info == Sh::kInfos) at_info = 0;
             if (!(flags & kLast8)) continue;
 
             // the segment's end
@@ -671,36 +659,34 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                 float2 x = split(l[i]);
 #pragma unroll
                 for (int o = 16; o; o >>= 1) x.x += __shfl_xor_sync(0xFFFFFFFFu, x.x, o), x.y += __shfl_xor_sync(0xFFFFFFFFu, x.y, o);
-                if (lane == 0) *reinterpret_cast<float2 *>(&sh.red[wg][quarter][2 * i]) = x;
+                if (lane == 0) *reinterpret_cast<float2 *>(&sh.sums[wg][quarter][2 * i]) = x;
             }
             if (any(failed)) break;
             const bool whole = seg_lo >= ubegin && seg_lo + seg.tiles <= uend;
             const int64_t slot = 2 * cta + (seg_lo > ubegin ? 1 : 0);
-            if (token < RW) {
-                const float sum = (sh.red[wg][0][token] + sh.red[wg][1][token]) + (sh.red[wg][2][token] + sh.red[wg][3][token]);
-                sh.fin[wg][token] = make_float2(token >= live || sum == 0.f ? 0.f : 1.f / sum, 0.f);
-                if (!whole && SV_IN(slot, 2 * ncta)) a.ml[slot * NR + r0 + token] = make_float2(M, sum);
-            }
-            any(false);
-            if (writes) {
-                const int d = token;
+            const int row = lane & 15;
+            const float sum = (sh.sums[wg][0][row] + sh.sums[wg][1][row]) + (sh.sums[wg][2][row] + sh.sums[wg][3][row]);
+            const float part = row >= live || sum == 0.f ? 0.f : 1.f / sum;
+            if (!whole && token < RW && SV_IN(slot, 2 * ncta)) a.ml[slot * NR + r0 + row] = make_float2(M, sum);
+            const int first = seg.rt * NR + r0;
+            int node = first / a.G, head = first - node * a.G;
+            uint16_t *out = a.out + (seg.b * int64_t(a.T) * a.H + seg.h) * a.G * D + token;  // of token 0's first head
+            float *part_out = a.acc + (slot * NR + r0) * D + token;
 #pragma unroll
-                for (int i = 0; i < RW; ++i) {
-                    const int r = r0 + i, row = seg.rt * NR + r, node = row / a.G;
-                    if (node >= a.T) break;
-                    const float scale = sh.fin[wg][i].x;
+            for (int i = 0; i < RW; ++i) {
+                const float scale = __shfl_sync(0xFFFFFFFFu, part, i);
+                if (node < a.T && writes) {
 #pragma unroll
                     for (int mb = 0; mb < MB; ++mb) {
                         const float2 x2 = split(acc[mb][i / 2]);
                         const float x = i & 1 ? x2.y : x2.x;
-                        if (whole) {
-                            a.out[((seg.b * int64_t(a.T) + node) * a.H * a.G + seg.h * a.G + row - node * a.G) * D + mb * 128 + d] =
-                                kv_from_float(scale == 0.f ? 0.f : x * scale, a.bf16);
-                        } else if (SV_IN(slot, 2 * ncta)) {
-                            a.acc[(slot * NR + r) * D + mb * 128 + d] = x;
-                        }
+                        if (whole)
+                            out[(int64_t(node) * a.H * a.G + head) * D + mb * 128] = kv_from_float(scale == 0.f ? 0.f : x * scale, a.bf16);
+                        else if (SV_IN(slot, 2 * ncta))
+                            part_out[i * D + mb * 128] = x;
                     }
                 }
+                if (++head == a.G) head = 0, ++node;
             }
             if (tid == 128 && seg_lo <= ubegin)  // the share's first segment
                 a.desc[cta] = describe(total, cta, ncta, ubegin, seg_lo, seg_lo + seg.tiles, seg.b, seg.h, seg.rt, seg.fresh);
@@ -717,9 +703,9 @@ template <int D, int NR, int NP>
 cudaError_t launch_attention8(const AttArgs &a, int nq, int grid, cudaStream_t s) {
     using Sh = Att8Shared<D, NR, NP>;
     constexpr size_t fixed = sizeof(Sh) + 1024;
-    static_assert(fixed + (NR == 64 ? SV_MAX_TREE_NODES : NR) * 4 * (1 + Sh::kQ * Sh::W) <= 227 * 1024, "the largest tree");
+    static_assert(fixed + (NR == 64 ? SV_MAX_TREE_NODES : NR) * 4 * (1 + Sh::kQ * Sh::SW) <= 227 * 1024, "the largest tree");
     static_assert((fixed + 1024) * att8_occupancy(D, NR) <= 228 * 1024 && Sh::kUsed <= Sh::kCols && Sh::kCols * att8_occupancy(D, NR) <= 512, "");
-    const size_t smem = fixed + (a.parent ? size_t(a.T) * 4 * (1 + Sh::kQ * Sh::W) : 0);
+    const size_t smem = fixed + (a.parent ? size_t(a.T) * 4 * (1 + Sh::kQ * Sh::SW) : 0);
     static std::atomic<int> allowed[64];
     cudaError_t e = allow_shared(kv8_attention_kernel<D, NR, NP>, int(smem), allowed);
     if (e != cudaSuccess) return e;
@@ -737,6 +723,7 @@ cudaError_t launch_attention8_rows(const AttArgs &a, int nr, int nq, int grid, c
     cudaError_t launch_attention8_rows<D, NP>(const AttArgs &a, int nr, int nq, int grid, cudaStream_t s) {    \
         return nr == 16 ? launch_attention8<D, 16, NP>(a, nq, grid, s)                                         \
                : nr == 32 ? launch_attention8<D, 32, NP>(a, nq, grid, s)                                       \
+               : nr == 48 ? launch_attention8<D, 48, NP>(a, nq, grid, s)                                       \
                           : launch_attention8<D, 64, NP>(a, nq, grid, s);                                      \
     }
 
