@@ -149,83 +149,129 @@ __device__ __forceinline__ void parts8(float x, float y, uint32_t (&c)[NP]) {
     }
 }
 
-// The copying warp: a unit's keys and words ahead of the values of the one before.  Returns when all that it has begun is there.
-template <int D, int NR, int NP>
-__device__ __forceinline__ void copy_tiles8(const AttArgs &a, Att8Shared<D, NR, NP> &sh, Cursor<kTile8> &cur, int ubegin, int uend, int lane) {
-    using Sh = Att8Shared<D, NR, NP>;
-    constexpr int NT = kTile8, kStages = Sh::kStages;
-    // lanes take (granule, piece) pairs: keys, values, words
-    const int gi = lane >> 2, piece = lane & 3, granules = NT / a.granule;
-    const bool busy = gi < granules && piece < 3;
-    const uint32_t all = granules == 8 ? 0x11111111u : 0x11111111u & ((1u << (4 * granules)) - 1);
-    const int64_t page_bytes = kv8_page_bytes(a.page, D), head_step = int64_t(a.H) * page_bytes;
-    const int each = piece < 2 ? D : 1;  // bytes a slot
-    const int from = piece == 0 ? 0 : piece == 1 ? a.page * D : 2 * a.page * D;
-    bool ok = true;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (ok && !mbar_wait(smem_u32(bar), parity)) {
-            ok = false;
-            atomicExch(a.status, int(SV_ERR_TIMEOUT));
-        }
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        return ok;
-    };
-    const uint8_t *vsrc = nullptr;  // of the unit whose values are next
-    uint32_t vbytes = 0, vsum = 0;
-    int values = 0, keys = 0;  // begun
-    auto copy_values = [&] {
-        const int s = values % kStages;
-        if (values >= kStages && !wait(&sh.empty_v[s], uint32_t(values / kStages - 1) & 1u)) return false;
-        if (lane == 0) mbar_expect(smem_u32(&sh.full_v[s]), vsum);
-        __syncwarp();
-        if (vbytes) bulk_load(smem_u32(sh.v[s]) + gi * a.granule * D, vsrc, vbytes, smem_u32(&sh.full_v[s]));
-        ++values;
+// Whether a phase is over, without a wait.
+__device__ __forceinline__ bool mbar_test(const uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Between two looks at several barriers: false when nothing has come for as long as a wait may take.
+struct Patience {
+    uint64_t since = 0;
+    uint32_t looks = 0;
+    __device__ __forceinline__ void reset() { looks = 0; }
+    __device__ __forceinline__ bool go_on() {
+        if (looks++ == 0) since = global_ns();
+        if ((looks & 63) == 0 && global_ns() - since > kCopyLimitNs) return false;
+        if (looks > 8) __nanosleep(20);
         return true;
-    };
+    }
+};
+
+// Where a unit's pieces lie for a lane of the copying warp: a granule's keys or values and words.
+struct Source8 {
+    const uint8_t *at;
+    uint32_t bytes, sum, have;  // this lane's bytes, those of all granules (of codes), bit 4 g: granule g is there
+};
+// The units of the share in turn, each with a lane's piece (0: keys, 1: values, 2: words).
+template <int D, int NR>
+struct Walk8 {
+    Cursor<kTile8> cur;
+    int u, pi = 0, slot = 0;
     bool placed = false;
-    int pi = 0, slot = 0;
-    for (int u = ubegin; u < uend; ++u) {
-        const int tok = cur.tile * NT + gi * a.granule;
+    __device__ __forceinline__ Source8 source(const AttArgs &a, int gi, int piece, bool busy) {
+        const int tok = cur.tile * kTile8 + gi * a.granule;
         if (!placed) pi = tok / a.page, slot = tok - pi * a.page, placed = true;
         const bool inside = busy && cur.live && tok < cur.w.len;
         const int pg = inside ? __ldg(a.table + int64_t(cur.b) * a.width + pi) : -1;
         const bool here = pg >= 0 && pg < a.num_pages && SV_IN(slot + a.granule - 1, a.page);
         const int there = here ? min(a.granule, (cur.w.len - tok + kKv8Block - 1) / kKv8Block * kKv8Block) : 0;  // tokens of whole blocks
-        const uint32_t have = __ballot_sync(0xFFFFFFFFu, here) & 0x11111111u, bytes = uint32_t(there * each);
-        const uint32_t sum = __reduce_add_sync(0xFFFFFFFFu, piece == 0 ? bytes : 0u);  // of the keys, and of the values
-        const uint8_t *src = here ? a.cache + pg * head_step + cur.h * page_bytes + from + int64_t(slot) * each : nullptr;
-#ifdef SV_CHECKS
-        if (u - ubegin == g_kv_lose) break;
-#endif
-        const int s = keys % kStages;
-        if (keys >= kStages && !wait(&sh.empty_k[s], uint32_t(keys / kStages - 1) & 1u)) break;
-        Info8 &in = sh.info[keys % Sh::kInfos];
-        if (lane == 0) {
-            int4 *un = reinterpret_cast<int4 *>(&in.unit);
-            const bool ragged = (cur.tile + 1) * NT > cur.w.len || have != all;
-            const int flags = (ragged || (cur.tile + 1) * NT > cur.w.before ? kMasked8 : 0) | (ragged ? kRagged8 : 0) |
-                              (u == ubegin || cur.tile == 0 ? kFirst8 : 0) | (u + 1 == uend || cur.tile + 1 == cur.tiles() ? kLast8 : 0);
-            un[0] = make_int4(cur.b, cur.h, cur.rt, cur.tile);
-            un[1] = make_int4(cur.tiles(), cur.w.before, cur.w.len, cur.live ? cur.w.fresh : 0);
-            un[2] = make_int4(int(have), flags, 0, 0);
-            mbar_expect(smem_u32(&sh.full_i[keys % Sh::kInfos]), sum / D);  // a byte of words for D of codes
-            mbar_expect(smem_u32(&sh.full_k[s]), sum);
-        }
-        __syncwarp();
-        if (bytes && piece == 0) bulk_load(smem_u32(sh.k[s]) + gi * a.granule * D, src, bytes, smem_u32(&sh.full_k[s]));
-        if (bytes && piece == 2) bulk_load(smem_u32(in.word) + gi * a.granule, src, bytes, smem_u32(&sh.full_i[keys % Sh::kInfos]));
-        if (++keys > 1 && !copy_values()) break;
-        vsrc = src, vbytes = piece == 1 ? bytes : 0u, vsum = sum;
+        const int each = piece < 2 ? D : 1;  // bytes a slot
+        const int64_t page_bytes = kv8_page_bytes(a.page, D);
+        Source8 r;
+        r.at = a.cache + (here ? (int64_t(pg) * a.H + cur.h) * page_bytes + min(piece, 2) * a.page * D + int64_t(slot) * each : 0);
+        r.bytes = uint32_t(there * each);
+        r.sum = __reduce_add_sync(0xFFFFFFFFu, piece < 2 ? r.bytes : 0u);
+        r.have = __ballot_sync(0xFFFFFFFFu, here);
+        return r;
+    }
+    __device__ __forceinline__ void advance(const AttArgs &a, int uend) {
+        ++u;
         if (cur.tile + 1 < cur.tiles()) {
             ++cur.tile;
-            slot += NT;
+            slot += kTile8;
             while (slot >= a.page) slot -= a.page, ++pi;
-        } else if (u + 1 < uend) {
-            cur.next(a, NR, u + 1);
+        } else if (u < uend) {
+            cur.next(a, NR, u);
             placed = false;
         }
     }
-    if (keys > values && ok) copy_values();
+};
+
+// The copying warp.  Keys and words, and values, each go as far ahead as their rings have room.  Returns when all that it has begun is there.
+template <int D, int NR, int NP>
+__device__ __forceinline__ void copy_tiles8(const AttArgs &a, Att8Shared<D, NR, NP> &sh, Cursor<kTile8> &cur, int ubegin, int uend, int lane) {
+    using Sh = Att8Shared<D, NR, NP>;
+    constexpr int NT = kTile8, kStages = Sh::kStages;
+    const int gi = lane & 7, piece = lane >> 3, granules = NT / a.granule;  // lanes 0 .. 7 keys, 8 .. 15 words, 16 .. 23 values
+    const uint32_t all = (1u << granules) - 1;
+    const int units = uend - ubegin;
+    int keys = 0, values = 0;  // begun
+    Walk8<D, NR> kw{cur, ubegin}, vw{cur, ubegin};
+    Patience patience;
+#ifdef SV_CHECKS
+    const int most = g_kv_lose < 0 ? units : min(units, g_kv_lose);
+#else
+    const int most = units;
+#endif
+    while (keys < most || values < most) {
+        bool did = false;
+        // (a warp looks as one: the lanes' looks may differ)
+        if (keys < most && __all_sync(0xFFFFFFFFu, keys < kStages || mbar_test(&sh.empty_k[keys % kStages], uint32_t(keys / kStages - 1) & 1u))) {
+            const int s = keys % kStages, at = keys % Sh::kInfos;
+            const Source8 src = kw.source(a, gi, piece == 1 ? 2 : 0, piece < 2 && gi < granules);
+            const uint32_t have = src.have & all;
+            Info8 &in = sh.info[at];
+            if (lane == 0) {
+                const Cursor<NT> &c = kw.cur;
+                int4 *un = reinterpret_cast<int4 *>(&in.unit);
+                const bool ragged = (c.tile + 1) * NT > c.w.len || have != all;
+                const int flags = (ragged || (c.tile + 1) * NT > c.w.before ? kMasked8 : 0) | (ragged ? kRagged8 : 0) |
+                                  (keys == 0 || c.tile == 0 ? kFirst8 : 0) | (keys + 1 == units || c.tile + 1 == c.tiles() ? kLast8 : 0);
+                un[0] = make_int4(c.b, c.h, c.rt, c.tile);
+                un[1] = make_int4(c.tiles(), c.w.before, c.w.len, c.live ? c.w.fresh : 0);
+                un[2] = make_int4(int(have), flags, 0, 0);
+                mbar_expect(smem_u32(&sh.full_i[at]), src.sum / D);  // a byte of words for D of codes
+                mbar_expect(smem_u32(&sh.full_k[s]), src.sum);
+            }
+            __syncwarp();
+            if (src.bytes && piece == 0) bulk_load(smem_u32(sh.k[s]) + gi * a.granule * D, src.at, src.bytes, smem_u32(&sh.full_k[s]));
+            if (src.bytes && piece == 1) bulk_load(smem_u32(in.word) + gi * a.granule, src.at, src.bytes, smem_u32(&sh.full_i[at]));
+            ++keys;
+            kw.advance(a, uend);
+            did = true;
+        }
+        if (values < most && __all_sync(0xFFFFFFFFu, values < kStages || mbar_test(&sh.empty_v[values % kStages], uint32_t(values / kStages - 1) & 1u))) {
+            const int s = values % kStages;
+            const Source8 src = vw.source(a, gi, 1, piece == 2 && gi < granules);
+            if (lane == 0) mbar_expect(smem_u32(&sh.full_v[s]), src.sum);
+            __syncwarp();
+            if (src.bytes) bulk_load(smem_u32(sh.v[s]) + gi * a.granule * D, src.at, src.bytes, smem_u32(&sh.full_v[s]));
+            ++values;
+            vw.advance(a, uend);
+            did = true;
+        }
+        if (did) {
+            patience.reset();
+        } else if (!__all_sync(0xFFFFFFFFu, patience.go_on())) {
+            atomicExch(a.status, int(SV_ERR_TIMEOUT));
+            break;
+        }
+    }
     for (int i = max(0, keys - kStages); i < keys; ++i)
         if (!mbar_wait(smem_u32(&sh.full_k[i % kStages]), uint32_t(i / kStages) & 1u) ||
             !mbar_wait(smem_u32(&sh.full_i[i % Sh::kInfos]), uint32_t(i / Sh::kInfos) & 1u))
@@ -240,22 +286,19 @@ __device__ __forceinline__ void issue_products8(const AttArgs &a, Att8Shared<D, 
     using Sh = Att8Shared<D, NR, NP>;
     constexpr int kStages = Sh::kStages, MB = Sh::MB;
     const uint32_t tmem = sh.tmem;
-    bool ok = true;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (ok && !mbar_wait(smem_u32(bar), parity)) {
-            ok = false;  // nothing more is issued; the other warps' waits give up too
-            atomicExch(a.status, int(SV_ERR_TIMEOUT));
-        }
-    };
-    int segment = -1;
+    int segment = -1, flags = 0;  // of the next scores' unit, once its keys are there
+    bool known = false;
     auto scores = [&](int n) {
         const int s = n % kStages;
-        wait(&sh.full_k[s], uint32_t(n / kStages) & 1u);
-        if (!ok) return;
-        const int flags = sh.info[n % Sh::kInfos].unit.masked;
-        if (flags & kFirst8) ++segment, wait(&sh.full_q[segment % Sh::kQ], uint32_t(segment / Sh::kQ) & 1u);
-        if (n >= 2) wait(&sh.free_s[n & 1], uint32_t((n >> 1) - 1) & 1u);
-        if (!ok) return;
+        if (!known) {
+            if (!mbar_test(&sh.full_k[s], uint32_t(n / kStages) & 1u)) return false;
+            flags = sh.info[n % Sh::kInfos].unit.masked;
+            if (flags & kFirst8) ++segment;
+            known = true;
+        }
+        if ((flags & kFirst8) && !mbar_test(&sh.full_q[segment % Sh::kQ], uint32_t(segment / Sh::kQ) & 1u)) return false;
+        if (n >= 2 && !mbar_test(&sh.free_s[n & 1], uint32_t((n >> 1) - 1) & 1u)) return false;
+        known = false;
         fence_after();
         constexpr uint32_t high = operand8_high(8 * D);
         const uint32_t d = tmem + (n & 1) * Sh::kScoreCols, k = operand8(smem_u32(sh.k[s]), 128);
@@ -275,13 +318,12 @@ __device__ __forceinline__ void issue_products8(const AttArgs &a, Att8Shared<D, 
         wide_commit(&sh.empty_k[s]);
         wide_commit(&sh.full_s[n & 1]);
         if (flags & kLast8) wide_commit(&sh.free_q[segment % Sh::kQ]);
+        return true;
     };
     auto products = [&](int n) {
         const int s = n % kStages;
-        wait(&sh.full_w[n & 1], uint32_t(n >> 1) & 1u);
-        wait(&sh.full_v[s], uint32_t(n / kStages) & 1u);
-        if (n >= 2) wait(&sh.free_o[n & 1], uint32_t((n >> 1) - 1) & 1u);
-        if (!ok) return;
+        if (!mbar_test(&sh.full_w[n & 1], uint32_t(n >> 1) & 1u) || !mbar_test(&sh.full_v[s], uint32_t(n / kStages) & 1u)) return false;
+        if (n >= 2 && !mbar_test(&sh.free_o[n & 1], uint32_t((n >> 1) - 1) & 1u)) return false;
         fence_after();
         constexpr int parts = Sh::kStackP ? 1 : NP, cols = Sh::kStackP ? NP * NR : NR;
         const uint32_t d = tmem + 2 * Sh::kScoreCols + (n & 1) * Sh::kOutCols;
@@ -296,83 +338,100 @@ __device__ __forceinline__ void issue_products8(const AttArgs &a, Att8Shared<D, 
                          kind8(cols, true), p > 0 || i > 0);
         wide_commit(&sh.empty_v[s]);
         wide_commit(&sh.full_o[n & 1]);
+        return true;
     };
-    scores(0);
-    for (int n = 1; n < units; ++n) scores(n), products(n - 1);
-    products(units - 1);
+    Patience patience;
+    for (int ns = 0, np = 0; np < units;) {
+        if (np < ns && products(np)) {
+            ++np, patience.reset();
+        } else if (ns < units && scores(ns)) {
+            ++ns, patience.reset();
+        } else if (!patience.go_on()) {  // nothing more is issued; the other warps' waits give up too
+            atomicExch(a.status, int(SV_ERR_TIMEOUT));
+            break;
+        }
+    }
     // nothing may be under way when the block ends
     wide_commit(&sh.done);
     if (!mbar_wait(smem_u32(&sh.done), 0)) atomicExch(a.status, int(SV_ERR_TIMEOUT));
 }
 
-// The query warps, 64 threads: each segment's rows, rotated, times a power of two that brings the row's largest number to 2^7 ..
-// 2^8, in parts.  A row with a NaN or an infinity is NaN throughout.
-template <int D, int NR, int NP>
-__device__ __forceinline__ void bring_queries8(const AttArgs &a, Att8Shared<D, NR, NP> &sh, const int *parent_s, uint32_t *see_s, Cursor<kTile8> &cur,
-                                               int ubegin, int uend, int tid) {
+// A segment's queries into place `at`, by the `threads` threads `tid`: rotated, times a power of two that brings the row's largest
+// number to 2^7 .. 2^8, in parts.  A row with a NaN or an infinity is NaN throughout.  `sync` is a barrier of these threads.
+template <int D, int NR, int NP, typename Sync>
+__device__ __forceinline__ void bring_queries8(const AttArgs &a, Att8Shared<D, NR, NP> &sh, const int *parent_s, uint32_t *see_s, const Cursor<kTile8> &cur,
+                                               int at, int tid, int threads, Sync sync) {
     using Sh = Att8Shared<D, NR, NP>;
-    constexpr int L = D / 8, P = 64 / L, SW = Sh::SW;
+    constexpr int L = D / 8, SW = Sh::SW;
     const int c = tid % L, d0 = c * 8;
+    const Unit un{cur.b, cur.h, cur.rt, cur.tile, cur.tiles(), cur.w.before, cur.w.len, cur.live ? cur.w.fresh : 0, 0, 0, {0, 0}};
+    uint8_t *q = sh.q[at];
+#pragma unroll 2
+    for (int r0 = 0; r0 < NR; r0 += threads / L) {
+        const int r = r0 + tid / L, row = un.rt * NR + r;
+        const int node = row / a.G, head = un.h * a.G + row - node * a.G;
+        const bool on = r < NR && node < un.fresh;
+        float x[8];
+        query_chunk(a, un, on ? node : 0, on ? head : 0, d0, x);  // (no branch: the rows' loads go out together)
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[i] = on ? x[i] : 0.f;
+            top = max(top, __float_as_uint(fabsf(x[i])));
+        }
+#pragma unroll
+        for (int o = L / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        if (r >= NR) continue;  // (whole rows: a row's lanes are of one mind)
+        const int e2 = top == 0 ? 0 : max(int(top >> 23) - 127 - 7, -110);
+        const bool odd = top >= 0x7F800000u;
+        const float shrink = power2(odd ? 0 : -e2);
+        uint32_t code[3][2] = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t p[3];
+            parts8(odd ? NAN : x[2 * i] * shrink, odd ? NAN : x[2 * i + 1] * shrink, p);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) code[k][i / 2] |= p[k] << (16 * (i & 1));
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            *reinterpret_cast<uint2 *>(q + kv8_code_byte(D, k * NR + r, d0)) = make_uint2(code[k][0], code[k][1]);
+        if (c == 0) sh.row_f[at][r] = a.scale * 1.4426950408889634f * power2(odd ? 0 : e2);
+    }
+    if (a.parent) {  // which rows see a new token
+        uint32_t *see = see_s + at * a.T * SW;
+        for (int i = tid; i < a.T * SW; i += threads) see[i] = 0;
+        sync();
+        if (tid < NR) {
+            const int node = (un.rt * NR + tid) / a.G;
+            for (int v = node < un.fresh ? node : -1; v >= 0;) {
+                atomicOr(see + v * SW + tid / 32, 1u << (tid & 31));
+                const int up = parent_s[v];
+                v = up < v ? up : -1;
+            }
+        }
+    }
+    fence_operands();
+}
+
+// The query warps, 64 threads: the segments after the share's first one.
+template <int D, int NR, int NP>
+__device__ __forceinline__ void bring_more_queries8(const AttArgs &a, Att8Shared<D, NR, NP> &sh, const int *parent_s, uint32_t *see_s,
+                                                    Cursor<kTile8> &cur, int ubegin, int uend, int tid) {
+    using Sh = Att8Shared<D, NR, NP>;
     int u = ubegin;
-    for (int segment = 0; u < uend; ++segment) {
+    for (int segment = 1;; ++segment) {
+        u += cur.tiles() - cur.tile;
+        if (u >= uend) return;
+        cur.tile = cur.tiles() - 1;
+        cur.next(a, NR, u);
         const int at = segment % Sh::kQ;
         bool ok = true;
         if (segment >= Sh::kQ) ok = mbar_wait(smem_u32(&sh.free_q[at]), uint32_t(segment / Sh::kQ - 1) & 1u);
         if (!ok) atomicExch(a.status, int(SV_ERR_TIMEOUT));
         if (group_or<3, 64>(!ok)) return;
-        const Unit un{cur.b, cur.h, cur.rt, cur.tile, cur.tiles(), cur.w.before, cur.w.len, cur.live ? cur.w.fresh : 0, 0, 0, {0, 0}};
-        uint8_t *q = sh.q[at];
-#pragma unroll 2
-        for (int r0 = 0; r0 < NR; r0 += P) {
-            const int r = r0 + tid / L, row = un.rt * NR + r;
-            const int node = row / a.G, head = un.h * a.G + row - node * a.G;
-            const bool on = node < un.fresh;
-            float x[8];
-            query_chunk(a, un, on ? node : 0, on ? head : 0, d0, x);  // (no branch: the rows' loads go out together)
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] = on ? x[i] : 0.f;
-                top = max(top, __float_as_uint(fabsf(x[i])));
-            }
-#pragma unroll
-            for (int o = L / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            const int e2 = top == 0 ? 0 : max(int(top >> 23) - 127 - 7, -110);
-            const bool odd = top >= 0x7F800000u;
-            const float shrink = power2(odd ? 0 : -e2);
-            uint32_t code[3][2] = {};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t p[3];
-                parts8(odd ? NAN : x[2 * i] * shrink, odd ? NAN : x[2 * i + 1] * shrink, p);
-#pragma unroll
-                for (int k = 0; k < 3; ++k) code[k][i / 2] |= p[k] << (16 * (i & 1));
-            }
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-                *reinterpret_cast<uint2 *>(q + kv8_code_byte(D, k * NR + r, d0)) = make_uint2(code[k][0], code[k][1]);
-            if (c == 0) sh.row_f[at][r] = a.scale * 1.4426950408889634f * power2(odd ? 0 : e2);
-        }
-        if (a.parent) {  // which rows see a new token
-            uint32_t *see = see_s + at * a.T * SW;
-            for (int i = tid; i < a.T * SW; i += 64) see[i] = 0;
-            group_or<3, 64>(false);
-            if (tid < NR) {
-                const int node = (un.rt * NR + tid) / a.G;
-                for (int v = node < un.fresh ? node : -1; v >= 0;) {
-                    atomicOr(see + v * SW + tid / 32, 1u << (tid & 31));
-                    const int up = parent_s[v];
-                    v = up < v ? up : -1;
-                }
-            }
-        }
-        fence_operands();
+        bring_queries8<D, NR, NP>(a, sh, parent_s, see_s, cur, at, tid, 64, [] { group_or<3, 64>(false); });
         mbar_arrive(smem_u32(&sh.full_q[at]));
-        u += cur.tiles() - cur.tile;
-        if (u < uend) {
-            cur.tile = cur.tiles() - 1;
-            cur.next(a, NR, u);
-        }
     }
 }
 
@@ -419,6 +478,13 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
     __syncthreads();
     fence_after();
     const int units = uend - ubegin;
+    // the first segment's queries, by all who would only wait for them
+    if (warp >= 2) {
+        constexpr int kAll = att8_threads(NR) - 64;
+        bring_queries8<D, NR, NP>(a, sh, parent_s, see_s, cur, 0, tid - 64, kAll, [] { group_or<6, kAll>(false); });
+        group_or<6, kAll>(false);
+        if (warp < 4) mbar_arrive(smem_u32(&sh.full_q[0]));
+    }
 
     if (warp == 0) {
         copy_tiles8<D, NR, NP>(a, sh, cur, ubegin, uend, lane);
@@ -426,7 +492,7 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
         if (lane == 0) issue_products8<D, NR, NP>(a, sh, units, nq);
         __syncwarp();
     } else if (warp < 4) {
-        bring_queries8<D, NR, NP>(a, sh, parent_s, see_s, cur, ubegin, uend, tid - 64);
+        bring_more_queries8<D, NR, NP>(a, sh, parent_s, see_s, cur, ubegin, uend, tid - 64);
     } else {
         const int wg = (warp - 4) / 4, quarter = warp & 3, token = quarter * 32 + lane;
         const int r0 = wg * RW;  // the group's first row
@@ -516,7 +582,7 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                 bool there = true;
                 if (flags & kMasked8) {
                     const int j = in.unit.tile * kTile8 + token, x = j - seg.before;  // among the new tokens
-                    there = j < seg.len && (in.unit.have >> (4 * (token >> granule_log2)) & 1u);
+                    there = j < seg.len && (in.unit.have >> (token >> granule_log2) & 1u);
                     see = there ? (1u << live) - 1 : 0u;
                     if (there && x >= 0) {
                         if (a.parent) {
