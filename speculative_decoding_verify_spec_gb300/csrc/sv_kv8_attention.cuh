@@ -39,8 +39,11 @@ __host__ __device__ constexpr int att8_groups(int NR) { return NR / kGroupRows8;
 __host__ __device__ constexpr int att8_threads(int NR) { return 128 + 128 * att8_groups(NR); }
 // Tiles in the rings, places for queries and weights, and blocks an SM: by shared memory and registers.
 __host__ __device__ constexpr int att8_stages(int D, int NR) { return D == 64 ? (NR == 16 ? 5 : NR == 32 ? 4 : 6) : D == 128 ? (NR <= 32 ? 2 : 3) : (NR == 16 ? 3 : 2); }
+__host__ __device__ constexpr int att8_value_stages(int D, int NR) {
+    return D == 256 ? (NR == 32 ? 3 : NR == 16 ? 3 : 2) : D == 128 && NR == 16 ? 3 : att8_stages(D, NR);
+}
 __host__ __device__ constexpr int att8_q_places(int D, int NR) { return D == 256 && NR >= 48 ? 1 : 2; }
-__host__ __device__ constexpr int att8_w_places(int D, int NR) { return NR >= 48 || (D == 256 && NR == 16) || (D == 128 && NR == 32) ? 1 : 2; }
+__host__ __device__ constexpr int att8_w_places(int D, int NR) { return NR >= 48 || D == 256 || (D == 128 && NR == 32) ? 1 : 2; }
 __host__ __device__ constexpr int att8_occupancy(int D, int NR) { return D == 256 || NR >= 48 ? 1 : 2; }
 // Rows a tile, by the rows that share a kv head: as few tiles of up to 64 as there have to be, and no larger than they need be.
 inline int att8_rows(int64_t rows) {
@@ -57,7 +60,7 @@ struct alignas(16) Info8 {
 
 template <int D, int NR, int NP>
 struct Att8Shared {
-    static constexpr int W = att8_groups(NR), RW = kGroupRows8, SW = (NR + 31) / 32, kStages = att8_stages(D, NR), kInfos = kStages + 2;
+    static constexpr int W = att8_groups(NR), RW = kGroupRows8, SW = (NR + 31) / 32, kStages = att8_stages(D, NR), kValues = att8_value_stages(D, NR), kInfos = kStages + 2;
     static constexpr int kQ = att8_q_places(D, NR), kP = att8_w_places(D, NR), MB = D == 256 ? 2 : 1;
     // Few rows: a product reads the cache's operand at its full width whatever the columns, so the parts are columns of
     // one product and are added up afterwards.
@@ -65,7 +68,7 @@ struct Att8Shared {
     static constexpr int kScoreCols = NR == 32 ? 32 : 64, kOutEach = NR >= 48 || (kStackP && NP == 3) ? 64 : 32, kOutCols = MB * kOutEach;
     static constexpr int kUsed = 2 * (kScoreCols + kOutCols), kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     alignas(1024) uint8_t k[kStages][kTile8 * D];
-    uint8_t v[kStages][kTile8 * D];       // (64 dimensions: a product's upper 64 rows read past the end, into w)
+    uint8_t v[kValues][kTile8 * D];       // (64 dimensions: a product's upper 64 rows read past the end, into w)
     uint8_t w[kP][NP * NR * kTile8];      // [part][16 rows][token][16 bytes]
     uint8_t q[kQ][3 * NR * D];            // [part][row], laid out as the keys
     Info8 info[kInfos];
@@ -75,7 +78,7 @@ struct Att8Shared {
     alignas(16) float4 move[W][4][2][RW / 2];  // of a row pair: -m, then 2^(m - M); every warp has its own
     // Each is waited for before what it tells of can come about once more, so that a phase's parity is enough: a unit's place in `info`
     // is taken again after the scores of two units later, which wait for the softmax to have read this one's.
-    alignas(8) uint64_t full_k[kStages], full_v[kStages], empty_k[kStages], empty_v[kStages], full_i[kInfos];
+    alignas(8) uint64_t full_k[kStages], full_v[kValues], empty_k[kStages], empty_v[kValues], full_i[kInfos];
     uint64_t full_s[2], free_s[2], full_o[2], free_o[2], full_w[2], full_q[kQ], free_q[kQ], done;
     uint32_t tmem;
 };
@@ -216,7 +219,7 @@ struct Walk8 {
 template <int D, int NR, int NP>
 __device__ __forceinline__ void copy_tiles8(const AttArgs &a, Att8Shared<D, NR, NP> &sh, Cursor<kTile8> &cur, int ubegin, int uend, int lane) {
     using Sh = Att8Shared<D, NR, NP>;
-    constexpr int NT = kTile8, kStages = Sh::kStages;
+    constexpr int NT = kTile8, kStages = Sh::kStages, kValues = Sh::kValues;
     const int gi = lane & 7, piece = lane >> 3, granules = NT / a.granule;  // lanes 0 .. 7 keys, 8 .. 15 words, 16 .. 23 values
     const uint32_t all = (1u << granules) - 1;
     const int units = uend - ubegin;
@@ -255,8 +258,8 @@ __device__ __forceinline__ void copy_tiles8(const AttArgs &a, Att8Shared<D, NR, 
             kw.advance(a, uend);
             did = true;
         }
-        if (values < most && __all_sync(0xFFFFFFFFu, values < kStages || mbar_test(&sh.empty_v[values % kStages], uint32_t(values / kStages - 1) & 1u))) {
-            const int s = values % kStages;
+        if (values < most && __all_sync(0xFFFFFFFFu, values < kValues || mbar_test(&sh.empty_v[values % kValues], uint32_t(values / kValues - 1) & 1u))) {
+            const int s = values % kValues;
             const Source8 src = vw.source(a, gi, 1, piece == 2 && gi < granules);
             if (lane == 0) mbar_expect(smem_u32(&sh.full_v[s]), src.sum);
             __syncwarp();
@@ -276,15 +279,15 @@ __device__ __forceinline__ void copy_tiles8(const AttArgs &a, Att8Shared<D, NR, 
         if (!mbar_wait(smem_u32(&sh.full_k[i % kStages]), uint32_t(i / kStages) & 1u) ||
             !mbar_wait(smem_u32(&sh.full_i[i % Sh::kInfos]), uint32_t(i / Sh::kInfos) & 1u))
             atomicExch(a.status, int(SV_ERR_TIMEOUT));
-    for (int i = max(0, values - kStages); i < values; ++i)
-        if (!mbar_wait(smem_u32(&sh.full_v[i % kStages]), uint32_t(i / kStages) & 1u)) atomicExch(a.status, int(SV_ERR_TIMEOUT));
+    for (int i = max(0, values - kValues); i < values; ++i)
+        if (!mbar_wait(smem_u32(&sh.full_v[i % kValues]), uint32_t(i / kValues) & 1u)) atomicExch(a.status, int(SV_ERR_TIMEOUT));
 }
 
 // The issuing thread.
 template <int D, int NR, int NP>
 __device__ __forceinline__ void issue_products8(const AttArgs &a, Att8Shared<D, NR, NP> &sh, int units, int nq) {
     using Sh = Att8Shared<D, NR, NP>;
-    constexpr int kStages = Sh::kStages, MB = Sh::MB;
+    constexpr int kStages = Sh::kStages, kValues = Sh::kValues, MB = Sh::MB;
     const uint32_t tmem = sh.tmem;
     int segment = -1, flags = 0;  // of the next scores' unit, once its keys are there
     bool known = false;
@@ -321,8 +324,8 @@ __device__ __forceinline__ void issue_products8(const AttArgs &a, Att8Shared<D, 
         return true;
     };
     auto products = [&](int n) {
-        const int s = n % kStages;
-        if (!mbar_test(&sh.full_w[n & 1], uint32_t(n >> 1) & 1u) || !mbar_test(&sh.full_v[s], uint32_t(n / kStages) & 1u)) return false;
+        const int s = n % kValues;
+        if (!mbar_test(&sh.full_w[n & 1], uint32_t(n >> 1) & 1u) || !mbar_test(&sh.full_v[s], uint32_t(n / kValues) & 1u)) return false;
         if (n >= 2 && !mbar_test(&sh.free_o[n & 1], uint32_t((n >> 1) - 1) & 1u)) return false;
         fence_after();
         constexpr int parts = Sh::kStackP ? 1 : NP, cols = Sh::kStackP ? NP * NR : NR;
@@ -414,17 +417,41 @@ __device__ __forceinline__ void bring_queries8(const AttArgs &a, Att8Shared<D, N
     fence_operands();
 }
 
+// A segment's queries and angles into the L2 cache: a block comes to a short segment before its queries' way from memory is over.
+template <int D, int NR>
+__device__ __forceinline__ void fetch_queries8(const AttArgs &a, const Cursor<kTile8> &cur, int tid, int threads) {
+    constexpr int kLines = D / 64;
+    auto fetch = [](const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); };
+    for (int i = tid; i < NR * kLines; i += threads) {
+        const int row = cur.rt * NR + i / kLines, node = row / a.G, head = row - node * a.G;
+        if (!cur.live || node >= cur.w.fresh) break;
+        fetch(a.q + cur.b * a.q_bs + node * a.q_ts + (cur.h * a.G + head) * a.q_hs + i % kLines * 64);
+        if (a.rot.cos && i % kLines == 0 && (head == 0 || i == 0)) {
+            const int64_t at = kv_rotation_row(a.rot, int64_t(cur.b) * a.T + node, cur.w.before, node);
+            for (int c = 0; c < a.rot.pairs; c += 32) fetch(a.rot.cos + at + c), fetch(a.rot.sin + at + c);
+        }
+    }
+}
+
 // The query warps, 64 threads: the segments after the share's first one.
 template <int D, int NR, int NP>
 __device__ __forceinline__ void bring_more_queries8(const AttArgs &a, Att8Shared<D, NR, NP> &sh, const int *parent_s, uint32_t *see_s,
                                                     Cursor<kTile8> &cur, int ubegin, int uend, int tid) {
     using Sh = Att8Shared<D, NR, NP>;
     int u = ubegin;
-    for (int segment = 1;; ++segment) {
-        u += cur.tiles() - cur.tile;
-        if (u >= uend) return;
-        cur.tile = cur.tiles() - 1;
-        cur.next(a, NR, u);
+    auto next = [&](Cursor<kTile8> &c) {  // to the segment that begins with unit u; false: the share is over
+        u += c.tiles() - c.tile;
+        if (u >= uend) return false;
+        c.tile = c.tiles() - 1;
+        c.next(a, NR, u);
+        return true;
+    };
+    if (!next(cur)) return;
+    fetch_queries8<D, NR>(a, cur, tid, 64);
+    Cursor<kTile8> ahead = cur;
+    for (int segment = 1; u < uend; ++segment) {
+        const bool more = next(ahead);
+        if (more) fetch_queries8<D, NR>(a, ahead, tid, 64);
         const int at = segment % Sh::kQ;
         bool ok = true;
         if (segment >= Sh::kQ) ok = mbar_wait(smem_u32(&sh.free_q[at]), uint32_t(segment / Sh::kQ - 1) & 1u);
@@ -432,13 +459,15 @@ __device__ __forceinline__ void bring_more_queries8(const AttArgs &a, Att8Shared
         if (group_or<3, 64>(!ok)) return;
         bring_queries8<D, NR, NP>(a, sh, parent_s, see_s, cur, at, tid, 64, [] { group_or<3, 64>(false); });
         mbar_arrive(smem_u32(&sh.full_q[at]));
+        if (!more) return;
+        cur = ahead;
     }
 }
 
 template <int D, int NR, int NP>
 __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_attention_kernel(const AttArgs a, int nq) {
     using Sh = Att8Shared<D, NR, NP>;
-    constexpr int W = Sh::W, RW = Sh::RW, MB = Sh::MB, kStages = Sh::kStages;
+    constexpr int W = Sh::W, RW = Sh::RW, MB = Sh::MB, kValues = Sh::kValues;
     extern __shared__ unsigned char raw0[];
     unsigned char *raw = raw0 + ((1024 - (smem_u32(raw0) & 1023)) & 1023);
     Sh &sh = *reinterpret_cast<Sh *>(raw);
@@ -449,9 +478,8 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
 
     griddep_launch_next();
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i)
-            mbar_init(smem_u32(&sh.full_k[i]), 1), mbar_init(smem_u32(&sh.full_v[i]), 1), mbar_init(smem_u32(&sh.empty_k[i]), 1),
-                mbar_init(smem_u32(&sh.empty_v[i]), 1);
+        for (int i = 0; i < Sh::kStages; ++i) mbar_init(smem_u32(&sh.full_k[i]), 1), mbar_init(smem_u32(&sh.empty_k[i]), 1);
+        for (int i = 0; i < kValues; ++i) mbar_init(smem_u32(&sh.full_v[i]), 1), mbar_init(smem_u32(&sh.empty_v[i]), 1);
         for (int i = 0; i < 2; ++i)
             mbar_init(smem_u32(&sh.full_s[i]), 1), mbar_init(smem_u32(&sh.free_s[i]), 4 * W), mbar_init(smem_u32(&sh.full_o[i]), 1),
                 mbar_init(smem_u32(&sh.free_o[i]), 4 * W), mbar_init(smem_u32(&sh.full_w[i]), 4 * W);
@@ -598,7 +626,7 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                     ks = (word.x | word.y) >> (token & 15) & 1u ? NAN : __uint_as_float(word.x & 0xFFFF0000u);
                     log2vs = float(e), inv = kv8_power(-e);
                 }
-                if (flags & kRagged8) wait(&sh.full_v[s], uint32_t(n / kStages) & 1u);
+                if (flags & kRagged8) wait(&sh.full_v[s], uint32_t(n / kValues) & 1u);
                 wait(&sh.full_s[n & 1], uint32_t(n >> 1) & 1u);
                 fence_after();
                 const Two ks2 = two(ks, ks), vs2 = two(log2vs, log2vs);
@@ -714,18 +742,28 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.full_w[n & 1]));
             if (!taken) take_up(n - 1);
-            if (++s == kStages) s = 0;
+            if (++s == kValues) s = 0;
             if (++at_info == Sh::kInfos) at_info = 0;
             if (!(flags & kLast8)) continue;
 
             // the segment's end
             take_up(n);
+            {  // the weights' sums over the warp: at each step a lane keeps half of the rows, in the end row lane / 2
+                float x[RW];
 #pragma unroll
-            for (int i = 0; i < RW / 2; ++i) {
-                float2 x = split(l[i]);
+                for (int i = 0; i < RW; ++i) x[i] = i & 1 ? split(l[i / 2]).y : split(l[i / 2]).x;
 #pragma unroll
-                for (int o = 16; o; o >>= 1) x.x += __shfl_xor_sync(0xFFFFFFFFu, x.x, o), x.y += __shfl_xor_sync(0xFFFFFFFFu, x.y, o);
-                if (lane == 0) *reinterpret_cast<float2 *>(&sh.sums[wg][quarter][2 * i]) = x;
+                for (int o = 16, rows = RW / 2; o > 1; o >>= 1, rows >>= 1) {
+                    const bool up = lane & o;
+#pragma unroll
+                    for (int i = 0; i < RW / 2; ++i)
+                        if (i < rows) {
+                            const float give = up ? x[i] : x[i + rows];
+                            x[i] = (up ? x[i + rows] : x[i]) + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+                        }
+                }
+                x[0] += __shfl_xor_sync(0xFFFFFFFFu, x[0], 1);
+                if (!(lane & 1)) sh.sums[wg][quarter][lane / 2] = x[0];
             }
             if (any(failed)) break;
             const bool whole = seg_lo >= ubegin && seg_lo + seg.tiles <= uend;
