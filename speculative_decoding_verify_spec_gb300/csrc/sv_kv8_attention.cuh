@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
         int seg_lo = 0, segment = -1, live = 0;  // live: rows of this group
         Two l[RW / 2], acc[MB][RW / 2];
         float M = -INFINITY;  // of row lane % 16 of the group
-        // the output of unit n, which is of the segment at hand
+        // the output of step n, which is of the segment at hand
         auto take_up = [&](int n) {
             wait(&sh.full_o[n & 1], uint32_t(n >> 1) & 1u);
             if (failed) return;
