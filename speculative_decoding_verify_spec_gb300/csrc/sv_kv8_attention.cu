@@ -4,33 +4,36 @@
 namespace sv {
 
 template <>
-cudaError_t launch_attention8_rows<64, 2>(const AttArgs &a, int nr, int nq, int grid, cudaStream_t s);
+cudaError_t launch_attention8_rows<64, 2>(const Att8Args &a, int grid, cudaStream_t s);
 template <>
-cudaError_t launch_attention8_rows<64, 3>(const AttArgs &a, int nr, int nq, int grid, cudaStream_t s);
+cudaError_t launch_attention8_rows<64, 3>(const Att8Args &a, int grid, cudaStream_t s);
 template <>
-cudaError_t launch_attention8_rows<128, 2>(const AttArgs &a, int nr, int nq, int grid, cudaStream_t s);
+cudaError_t launch_attention8_rows<128, 2>(const Att8Args &a, int grid, cudaStream_t s);
 template <>
-cudaError_t launch_attention8_rows<128, 3>(const AttArgs &a, int nr, int nq, int grid, cudaStream_t s);
+cudaError_t launch_attention8_rows<128, 3>(const Att8Args &a, int grid, cudaStream_t s);
 template <>
-cudaError_t launch_attention8_rows<256, 2>(const AttArgs &a, int nr, int nq, int grid, cudaStream_t s);
+cudaError_t launch_attention8_rows<256, 2>(const Att8Args &a, int grid, cudaStream_t s);
 template <>
-cudaError_t launch_attention8_rows<256, 3>(const AttArgs &a, int nr, int nq, int grid, cudaStream_t s);
+cudaError_t launch_attention8_rows<256, 3>(const Att8Args &a, int grid, cudaStream_t s);
 
 namespace {
 
 struct Att8Layout {
-    size_t desc, ml, acc, total;
+    size_t desc, ml, acc, parts, see, total;
     int grid;
 };
-Att8Layout att8_layout(int64_t rows, int D) {
+Att8Layout att8_layout(int B, int T, int H, int64_t rows, int D) {
     const int nr = att8_rows(rows);
+    const size_t row_tiles = size_t((rows + nr - 1) / nr);
     Att8Layout L;
     L.grid = kAttSMs * att8_occupancy(D, nr);
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     L.desc = 256;
     L.ml = up(L.desc + size_t(L.grid) * sizeof(AttDesc));
     L.acc = up(L.ml + size_t(2) * L.grid * nr * 8);
-    L.total = up(L.acc + size_t(2) * L.grid * nr * D * 4);
+    L.parts = up(L.acc + size_t(2) * L.grid * nr * D * 4);
+    L.see = up(L.parts + size_t(B) * H * row_tiles * query_bytes8(D, nr));
+    L.total = up(L.see + (T <= SV_MAX_TREE_NODES ? row_tiles * T * ((nr + 31) / 32) * 4 : 0));
     return L;
 }
 
@@ -41,7 +44,7 @@ extern "C" {
 
 size_t spec_kv8_attention_workspace_size(int B, int T, int heads, int kv_heads, int head_dim) {
     if (B <= 0 || T <= 0 || kv_heads < 1 || heads < kv_heads || heads % kv_heads || !sv::kv_head_dim_ok(head_dim)) return 0;
-    return sv::att8_layout(int64_t(T) * (heads / kv_heads), head_dim).total;
+    return sv::att8_layout(B, T, kv_heads, int64_t(T) * (heads / kv_heads), head_dim).total;
 }
 
 sv_status spec_kv8_attention(const void *q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,
@@ -66,7 +69,7 @@ sv_status spec_kv8_attention(const void *q, int64_t q_batch_stride, int64_t q_to
     if (reinterpret_cast<uintptr_t>(cache) % 16 || reinterpret_cast<uintptr_t>(q) % 2 || reinterpret_cast<uintptr_t>(out) % 16)
         return SV_ERR_INVALID_ARG;
     const int G = heads / kv_heads, nr = sv::att8_rows(int64_t(T) * G);
-    const sv::Att8Layout L = sv::att8_layout(int64_t(T) * G, head_dim);
+    const sv::Att8Layout L = sv::att8_layout(B, T, kv_heads, int64_t(T) * G, head_dim);
     if (!workspace || workspace_bytes < L.total || reinterpret_cast<uintptr_t>(workspace) % 16) return SV_ERR_WORKSPACE;
     char *ws = static_cast<char *>(workspace);
     const int64_t row_tiles = (int64_t(T) * G + nr - 1) / nr, tokens = int64_t(table_width) * page_size;
@@ -75,7 +78,9 @@ sv_status spec_kv8_attention(const void *q, int64_t q_batch_stride, int64_t q_to
     // no more blocks than the page tables have room for units: empty shares would only lengthen the joins
     const int64_t units = most * kv_heads * B;
     const int grid = units < L.grid ? int(units) : L.grid;
-    sv::AttArgs a{};
+    const int64_t query_blocks = (int64_t(B) * kv_heads * row_tiles * nr * (head_dim / 8) + sv::kQueryThreads8 - 1) / sv::kQueryThreads8;
+    if (query_blocks + row_tiles > 0x7FFFFFFF) return SV_ERR_INVALID_ARG;
+    sv::Att8Args a{};
     a.q = static_cast<const uint16_t *>(q);
     a.q_bs = q_batch_stride, a.q_ts = q_token_stride, a.q_hs = q_head_stride;
     a.bf16 = dtype == SV_KV_BF16;
@@ -94,16 +99,18 @@ sv_status spec_kv8_attention(const void *q, int64_t q_batch_stride, int64_t q_to
     a.desc = reinterpret_cast<sv::AttDesc *>(ws + L.desc);
     a.ml = reinterpret_cast<float2 *>(ws + L.ml);
     a.acc = reinterpret_cast<float *>(ws + L.acc);
+    a.nr = nr, a.see_words = (nr + 31) / 32, a.query_blocks = query_blocks;
+    a.parts = reinterpret_cast<uint8_t *>(ws + L.parts), a.see = reinterpret_cast<uint32_t *>(ws + L.see);
     // a bf16 query has 8 bits, which two parts hold; what the rotation makes of it, and an fp16 one, takes three
-    const int nq = cos || !a.bf16 ? 3 : 2;
+    a.nq = cos || !a.bf16 ? 3 : 2;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (head_dim == 64)
-        e = a.bf16 ? sv::launch_attention8_rows<64, 2>(a, nr, nq, grid, s) : sv::launch_attention8_rows<64, 3>(a, nr, nq, grid, s);
+        e = a.bf16 ? sv::launch_attention8_rows<64, 2>(a, grid, s) : sv::launch_attention8_rows<64, 3>(a, grid, s);
     else if (head_dim == 128)
-        e = a.bf16 ? sv::launch_attention8_rows<128, 2>(a, nr, nq, grid, s) : sv::launch_attention8_rows<128, 3>(a, nr, nq, grid, s);
+        e = a.bf16 ? sv::launch_attention8_rows<128, 2>(a, grid, s) : sv::launch_attention8_rows<128, 3>(a, grid, s);
     else
-        e = a.bf16 ? sv::launch_attention8_rows<256, 2>(a, nr, nq, grid, s) : sv::launch_attention8_rows<256, 3>(a, nr, nq, grid, s);
+        e = a.bf16 ? sv::launch_attention8_rows<256, 2>(a, grid, s) : sv::launch_attention8_rows<256, 3>(a, grid, s);
     return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 

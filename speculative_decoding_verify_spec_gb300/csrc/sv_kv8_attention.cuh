@@ -36,7 +36,7 @@ namespace sv {
 constexpr int kTile8 = 128;
 constexpr int kGroupRows8 = 16;  // query rows of a softmax group
 __host__ __device__ constexpr int att8_groups(int NR) { return NR / kGroupRows8; }
-__host__ __device__ constexpr int att8_threads(int NR) { return 128 + 128 * att8_groups(NR); }
+__host__ __device__ constexpr int att8_threads(int NR) { return 64 + 128 * att8_groups(NR); }
 // Tiles that a block takes at a time: two where a key head has many rows, whose softmax then has half as many barriers, waits and maxima.
 __host__ __device__ constexpr int att8_pair(int D, int NR) { return 1; }
 // Tiles in the rings, places for queries and weights, and blocks an SM: by shared memory and registers.
@@ -55,6 +55,17 @@ inline int att8_rows(int64_t rows) {
 
 enum : int { kMasked8 = 1, kRagged8 = 2, kFirst8 = 4, kLast8 = 8 };  // in Unit::masked: not every row sees every token; not every token is there; of a segment
 
+// Bytes of a segment's queries: three parts, laid out as the keys, and the rows' factors.
+__host__ __device__ constexpr int query_bytes8(int D, int NR) { return 3 * NR * D + 4 * NR; }
+
+struct Att8Args : AttArgs {
+    int nr, nq;            // rows a tile, parts of a query
+    int see_words;         // a new token's words in `see`
+    int64_t query_blocks;
+    uint8_t *parts;        // [B][H][row_tiles][query_bytes8]
+    uint32_t *see;         // [row_tiles][T][see_words]: the rows that see a new token of a tree
+};
+
 struct alignas(16) Info8 {
     Unit unit;
     uint32_t word[kTile8 / kKv8Block][4];
@@ -69,12 +80,15 @@ struct Att8Shared {
     static constexpr bool kStackQ = NR == 16 || (D == 256 && NR == 32), kStackP = NR == 16 || (D == 256 && NR == 32 && NP == 2);
     static constexpr int kScoreCols = kStackQ ? (NR == 16 ? 64 : 96) : NR == 32 ? 32 : 64, kOutEach = NR >= 48 || (kStackP && NP * NR > 32) ? 64 : 32, kOutCols = MB * kOutEach;
     static constexpr int kUsed = 2 * (TT * kScoreCols + kOutCols), kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
-    alignas(1024) uint8_t k[kStages][kTile8 * D];
+    alignas(128) uint8_t k[kStages][kTile8 * D];
     uint8_t v[kValues][kTile8 * D];       // (64 dimensions: a product's upper 64 rows read past the end, into w)
     uint8_t w[kP][TT * NP * NR * kTile8];  // [tile][part][16 rows][token][16 bytes]
-    uint8_t q[kQ][3 * NR * D];            // [part][row], laid out as the keys
+    struct Queries {
+        uint8_t part[3][NR * D];
+        float factor[NR];                 // log2(e) scale times the power of two taken out of the row
+    };
+    Queries q[kQ];
     Info8 info[kInfos];
-    alignas(16) float row_f[kQ][NR];      // log2(e) scale times the power of two taken out of the row
     alignas(16) float red[W][2][4][RW];        // maxima of a warp's 32 tokens
     alignas(16) float sums[W][4][RW];
     alignas(16) float4 move[W][4][2][RW / 2];  // of a row pair: -m, then 2^(m - M); every warp has its own
@@ -188,7 +202,7 @@ struct Walk8 {
     Cursor<kTile8> cur;
     int u, pi = 0, slot = 0;
     bool placed = false;
-    __device__ __forceinline__ Source8 source(const AttArgs &a, int gi, int piece, bool busy) {
+    __device__ __forceinline__ Source8 source(const Att8Args &a, int gi, int piece, bool busy) {
         const int tok = cur.tile * kTile8 + gi * a.granule;
         if (!placed) pi = tok / a.page, slot = tok - pi * a.page, placed = true;
         const bool inside = busy && cur.live && tok < cur.w.len;
@@ -204,7 +218,7 @@ struct Walk8 {
         r.have = __ballot_sync(0xFFFFFFFFu, here);
         return r;
     }
-    __device__ __forceinline__ void advance(const AttArgs &a, int uend) {
+    __device__ __forceinline__ void advance(const Att8Args &a, int uend) {
         ++u;
         if (cur.tile + 1 < cur.tiles()) {
             ++cur.tile;
@@ -217,24 +231,45 @@ struct Walk8 {
     }
 };
 
-// The copying warp.  Keys and words, and values, each go as far ahead as their rings have room.  Returns when all that it has begun is there.
+// The copying warp.  Keys and words, values, and segments' queries each go as far ahead as their rings have room.  Returns when all that it has begun is there.
 template <int D, int NR, int NP>
-__device__ __forceinline__ void copy_tiles8(const AttArgs &a, Att8Shared<D, NR, NP> &sh, Cursor<kTile8> &cur, int ubegin, int uend, int lane) {
+__device__ __forceinline__ void copy_tiles8(const Att8Args &a, Att8Shared<D, NR, NP> &sh, Cursor<kTile8> &cur, int ubegin, int uend, int lane) {
     using Sh = Att8Shared<D, NR, NP>;
     constexpr int NT = kTile8, kStages = Sh::kStages, kValues = Sh::kValues;
     const int gi = lane & 7, piece = lane >> 3, granules = NT / a.granule;  // lanes 0 .. 7 keys, 8 .. 15 words, 16 .. 23 values
     const uint32_t all = (1u << granules) - 1;
     const int units = uend - ubegin;
     int keys = 0, values = 0;  // begun
+    int queries = 0, qu = ubegin;  // segments whose queries are begun, and the unit with which the next one begins
     Walk8<D, NR> kw{cur, ubegin}, vw{cur, ubegin};
+    Cursor<kTile8> qc = cur;
+    const uint32_t part_bytes = uint32_t(a.nq) * NR * D;
     Patience patience;
 #ifdef SV_CHECKS
     const int most = g_kv_lose < 0 ? units : min(units, g_kv_lose);
 #else
     const int most = units;
 #endif
-    while (keys < most || values < most) {
+    while (keys < most || values < most || (qu < uend && most == units)) {
         bool did = false;
+        if (qu < uend && __all_sync(0xFFFFFFFFu, queries < Sh::kQ || mbar_test(&sh.free_q[queries % Sh::kQ], uint32_t(queries / Sh::kQ - 1) & 1u))) {
+            const int at = queries % Sh::kQ;
+            if (lane == 0) {
+                const uint8_t *src = a.parts + ((int64_t(qc.b) * a.H + qc.h) * a.row_tiles + qc.rt) * query_bytes8(D, NR);
+                const uint32_t bar = smem_u32(&sh.full_q[at]);
+                mbar_expect(bar, part_bytes + 4 * NR);
+                bulk_load(smem_u32(sh.q[at].part), src, part_bytes, bar);
+                bulk_load(smem_u32(sh.q[at].factor), src + 3 * NR * D, 4 * NR, bar);
+            }
+            __syncwarp();
+            ++queries;
+            qu += qc.tiles() - qc.tile;
+            if (qu < uend) {
+                qc.tile = qc.tiles() - 1;
+                qc.next(a, NR, qu);
+            }
+            did = true;
+        }
         // (a warp looks as one: the lanes' looks may differ)
         if (keys < most && __all_sync(0xFFFFFFFFu, keys < kStages || mbar_test(&sh.empty_k[keys % kStages], uint32_t(keys / kStages - 1) & 1u))) {
             const int s = keys % kStages, at = keys % Sh::kInfos;
@@ -281,13 +316,15 @@ __device__ __forceinline__ void copy_tiles8(const AttArgs &a, Att8Shared<D, NR, 
         if (!mbar_wait(smem_u32(&sh.full_k[i % kStages]), uint32_t(i / kStages) & 1u) ||
             !mbar_wait(smem_u32(&sh.full_i[i % Sh::kInfos]), uint32_t(i / Sh::kInfos) & 1u))
             atomicExch(a.status, int(SV_ERR_TIMEOUT));
+    for (int i = max(0, queries - Sh::kQ); i < queries; ++i)
+        if (!mbar_wait(smem_u32(&sh.full_q[i % Sh::kQ]), uint32_t(i / Sh::kQ) & 1u)) atomicExch(a.status, int(SV_ERR_TIMEOUT));
     for (int i = max(0, values - kValues); i < values; ++i)
         if (!mbar_wait(smem_u32(&sh.full_v[i % kValues]), uint32_t(i / kValues) & 1u)) atomicExch(a.status, int(SV_ERR_TIMEOUT));
 }
 
 // The issuing thread.
 template <int D, int NR, int NP>
-__device__ __forceinline__ void issue_products8(const AttArgs &a, Att8Shared<D, NR, NP> &sh, int units, int nq) {
+__device__ __forceinline__ void issue_products8(const Att8Args &a, Att8Shared<D, NR, NP> &sh, int units, int nq) {
     using Sh = Att8Shared<D, NR, NP>;
     constexpr int kStages = Sh::kStages, kValues = Sh::kValues, MB = Sh::MB;
     const uint32_t tmem = sh.tmem;
@@ -312,7 +349,7 @@ __device__ __forceinline__ void issue_products8(const AttArgs &a, Att8Shared<D, 
         fence_after();
         constexpr uint32_t high = operand8_high(8 * D);
         const uint32_t d = tmem + ((step & 1) * Sh::TT + half) * Sh::kScoreCols, k = operand8(smem_u32(sh.k[s]), 128);
-        uint32_t q = operand8(smem_u32(sh.q[segment % Sh::kQ]), 128);
+        uint32_t q = operand8(smem_u32(sh.q[segment % Sh::kQ].part), 128);
         if constexpr (Sh::kStackQ) {
             const uint32_t kind = kind8(NR, false) + uint32_t((nq - 1) * NR / 8) * (1u << 17);
 #pragma unroll
@@ -379,120 +416,85 @@ __device__ __forceinline__ void issue_products8(const AttArgs &a, Att8Shared<D, 
     if (!mbar_wait(smem_u32(&sh.done), 0)) atomicExch(a.status, int(SV_ERR_TIMEOUT));
 }
 
-// A segment's queries into place `at`, by the `threads` threads `tid`: rotated, times a power of two that brings the row's largest
-// number to 2^7 .. 2^8, in parts.  A row with a NaN or an infinity is NaN throughout.  `sync` is a barrier of these threads.
-template <int D, int NR, int NP, typename Sync>
-__device__ __forceinline__ void bring_queries8(const AttArgs &a, Att8Shared<D, NR, NP> &sh, const int *parent_s, uint32_t *see_s, const Cursor<kTile8> &cur,
-                                               int at, int tid, int threads, Sync sync) {
-    using Sh = Att8Shared<D, NR, NP>;
-    constexpr int L = D / 8, SW = Sh::SW;
-    const int c = tid % L, d0 = c * 8;
-    const Unit un{cur.b, cur.h, cur.rt, cur.tile, cur.tiles(), cur.w.before, cur.w.len, cur.live ? cur.w.fresh : 0, 0, 0, {0, 0}};
-    uint8_t *q = sh.q[at];
-#pragma unroll 2
-    for (int r0 = 0; r0 < NR; r0 += threads / L) {
-        const int r = r0 + tid / L, row = un.rt * NR + r;
-        const int node = row / a.G, head = un.h * a.G + row - node * a.G;
-        const bool on = r < NR && node < un.fresh;
-        float x[8];
-        query_chunk(a, un, on ? node : 0, on ? head : 0, d0, x);  // (no branch: the rows' loads go out together)
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = on ? x[i] : 0.f;
-            top = max(top, __float_as_uint(fabsf(x[i])));
-        }
-#pragma unroll
-        for (int o = L / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        if (r >= NR) continue;  // (whole rows: a row's lanes are of one mind)
-        const int e2 = top == 0 ? 0 : max(int(top >> 23) - 127 - 7, -110);
-        const bool odd = top >= 0x7F800000u;
-        const float shrink = power2(odd ? 0 : -e2);
-        uint32_t code[3][2] = {};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t p[3];
-            parts8(odd ? NAN : x[2 * i] * shrink, odd ? NAN : x[2 * i + 1] * shrink, p);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) code[k][i / 2] |= p[k] << (16 * (i & 1));
-        }
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-            *reinterpret_cast<uint2 *>(q + kv8_code_byte(D, k * NR + r, d0)) = make_uint2(code[k][0], code[k][1]);
-        if (c == 0) sh.row_f[at][r] = a.scale * 1.4426950408889634f * power2(odd ? 0 : e2);
-    }
-    if (a.parent) {  // which rows see a new token
-        uint32_t *see = see_s + at * a.T * SW;
-        for (int i = tid; i < a.T * SW; i += threads) see[i] = 0;
-        sync();
-        if (tid < NR) {
-            const int node = (un.rt * NR + tid) / a.G;
-            for (int v = node < un.fresh ? node : -1; v >= 0;) {
-                atomicOr(see + v * SW + tid / 32, 1u << (tid & 31));
-                const int up = parent_s[v];
+// The queries in parts, for all segments (sequence, kv head, row tile): each row rotated, times a power of two that brings its largest number to
+// 2^7 .. 2^8.  A row with a NaN or an infinity is NaN throughout.  D / 8 lanes a row.  The blocks behind those have a row tile each
+// of a tree's words (which rows see a new token).  A kernel of its own: two warps of the attention's blocks took 20 us a segment for it, beside
+// instructions that the softmax then had to fetch again.
+constexpr int kQueryThreads8 = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kQueryThreads8) kv8_queries_kernel(const Att8Args a) {
+    constexpr int L = D / 8;
+    extern __shared__ uint32_t see_s[];
+    const int tid = threadIdx.x;
+    griddep_launch_next();
+    griddep_wait();
+    if (int64_t(blockIdx.x) >= a.query_blocks) {
+        const int rt = int(blockIdx.x - a.query_blocks), words = a.T * a.see_words;
+        for (int i = tid; i < words; i += kQueryThreads8) see_s[i] = 0;
+        __syncthreads();
+        if (tid < a.nr) {
+            const int64_t node = (int64_t(rt) * a.nr + tid) / a.G;
+            for (int v = node < a.T ? int(node) : -1; v >= 0;) {
+                atomicOr(see_s + v * a.see_words + tid / 32, 1u << (tid & 31));
+                const int up = __ldg(a.parent + v);
                 v = up < v ? up : -1;
             }
         }
+        __syncthreads();
+        for (int i = tid; i < words; i += kQueryThreads8) a.see[int64_t(rt) * words + i] = see_s[i];
+        return;
     }
-    fence_operands();
-}
-
-// A segment's queries and angles into the L2 cache: a block comes to a short segment before its queries' way from memory is over.
-template <int D, int NR>
-__device__ __forceinline__ void fetch_queries8(const AttArgs &a, const Cursor<kTile8> &cur, int tid, int threads) {
-    constexpr int kLines = D / 64;
-    auto fetch = [](const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); };
-    for (int i = tid; i < NR * kLines; i += threads) {
-        const int row = cur.rt * NR + i / kLines, node = row / a.G, head = row - node * a.G;
-        if (!cur.live || node >= cur.w.fresh) break;
-        fetch(a.q + cur.b * a.q_bs + node * a.q_ts + (cur.h * a.G + head) * a.q_hs + i % kLines * 64);
-        if (a.rot.cos && i % kLines == 0 && (head == 0 || i == 0)) {
-            const int64_t at = kv_rotation_row(a.rot, int64_t(cur.b) * a.T + node, cur.w.before, node);
-            for (int c = 0; c < a.rot.pairs; c += 32) fetch(a.rot.cos + at + c), fetch(a.rot.sin + at + c);
-        }
+    const int64_t row = (int64_t(blockIdx.x) * kQueryThreads8 + tid) / L;
+    const int64_t tile = row / a.nr;
+    const int r = int(row - tile * a.nr), c = tid % L, d0 = c * 8;
+    const bool inside = tile < int64_t(a.B) * a.H * a.row_tiles;
+    Unit un{};
+    int node = 0, head = 0;
+    bool on = false;
+    if (inside) {
+        const int64_t bh = tile / a.row_tiles;
+        un.rt = int(tile - bh * a.row_tiles), un.b = int(bh / a.H), un.h = int(bh - int64_t(un.b) * a.H);
+        kv_lengths(a.start, a.new_lens, un.b, a.T, int64_t(a.width) * a.page, un.before, un.fresh);
+        const int at = un.rt * a.nr + r;
+        node = at / a.G, head = un.h * a.G + at - node * a.G;
+        on = node < un.fresh;
     }
-}
-
-// The query warps, 64 threads: the segments after the share's first one.
-template <int D, int NR, int NP>
-__device__ __forceinline__ void bring_more_queries8(const AttArgs &a, Att8Shared<D, NR, NP> &sh, const int *parent_s, uint32_t *see_s,
-                                                    Cursor<kTile8> &cur, int ubegin, int uend, int tid) {
-    using Sh = Att8Shared<D, NR, NP>;
-    int u = ubegin;
-    auto next = [&](Cursor<kTile8> &c) {  // to the segment that begins with unit u; false: the share is over
-        u += c.tiles() - c.tile;
-        if (u >= uend) return false;
-        c.tile = c.tiles() - 1;
-        c.next(a, NR, u);
-        return true;
-    };
-    if (!next(cur)) return;
-    fetch_queries8<D, NR>(a, cur, tid, 64);
-    Cursor<kTile8> ahead = cur;
-    for (int segment = 1; u < uend; ++segment) {
-        const bool more = next(ahead);
-        if (more) fetch_queries8<D, NR>(a, ahead, tid, 64);
-        const int at = segment % Sh::kQ;
-        bool ok = true;
-        if (segment >= Sh::kQ) ok = mbar_wait(smem_u32(&sh.free_q[at]), uint32_t(segment / Sh::kQ - 1) & 1u);
-        if (!ok) atomicExch(a.status, int(SV_ERR_TIMEOUT));
-        if (group_or<3, 64>(!ok)) return;
-        bring_queries8<D, NR, NP>(a, sh, parent_s, see_s, cur, at, tid, 64, [] { group_or<3, 64>(false); });
-        mbar_arrive(smem_u32(&sh.full_q[at]));
-        if (!more) return;
-        cur = ahead;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    if (on) query_chunk(a, un, node, head, d0, x);
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(fabsf(x[i])));
+#pragma unroll
+    for (int o = L / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if (!inside) return;
+    const int e2 = top == 0 ? 0 : max(int(top >> 23) - 127 - 7, -110);
+    const bool odd = top >= 0x7F800000u;
+    const float shrink = power2(odd ? 0 : -e2);
+    uint32_t code[3][2] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t p[3];
+        parts8(odd ? NAN : x[2 * i] * shrink, odd ? NAN : x[2 * i + 1] * shrink, p);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) code[k][i / 2] |= p[k] << (16 * (i & 1));
     }
+    uint8_t *q = a.parts + tile * query_bytes8(D, a.nr);
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        if (k < a.nq) *reinterpret_cast<uint2 *>(q + kv8_code_byte(D, k * a.nr + r, d0)) = make_uint2(code[k][0], code[k][1]);
+    if (c == 0) reinterpret_cast<float *>(q + 3 * a.nr * D)[r] = a.scale * 1.4426950408889634f * power2(odd ? 0 : e2);
 }
 
 template <int D, int NR, int NP>
-__global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_attention_kernel(const AttArgs a, int nq) {
+__global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_attention_kernel(const Att8Args a) {
     using Sh = Att8Shared<D, NR, NP>;
     constexpr int W = Sh::W, RW = Sh::RW, MB = Sh::MB, TT = Sh::TT, kValues = Sh::kValues;
     extern __shared__ unsigned char raw0[];
-    unsigned char *raw = raw0 + ((1024 - (smem_u32(raw0) & 1023)) & 1023);
+    unsigned char *raw = raw0 + ((128 - (smem_u32(raw0) & 127)) & 127);
     Sh &sh = *reinterpret_cast<Sh *>(raw);
-    int *parent_s = reinterpret_cast<int *>(raw + sizeof(Sh));
-    uint32_t *see_s = reinterpret_cast<uint32_t *>(parent_s + (a.parent ? a.T : 0));  // [kQ][T][SW]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ncta = int(gridDim.x), cta = int(blockIdx.x);
 
@@ -503,15 +505,13 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
         for (int i = 0; i < 2; ++i)
             mbar_init(smem_u32(&sh.full_s[i]), 1), mbar_init(smem_u32(&sh.free_s[i]), 4 * W), mbar_init(smem_u32(&sh.full_o[i]), 1),
                 mbar_init(smem_u32(&sh.free_o[i]), 4 * W), mbar_init(smem_u32(&sh.full_w[i]), 4 * W);
-        for (int i = 0; i < Sh::kQ; ++i) mbar_init(smem_u32(&sh.full_q[i]), 64), mbar_init(smem_u32(&sh.free_q[i]), 4 * W + 1);
+        for (int i = 0; i < Sh::kQ; ++i) mbar_init(smem_u32(&sh.full_q[i]), 1), mbar_init(smem_u32(&sh.free_q[i]), 4 * W + 1);
         for (int i = 0; i < Sh::kInfos; ++i) mbar_init(smem_u32(&sh.full_i[i]), 1);
         mbar_init(smem_u32(&sh.done), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     griddep_wait();
     if (cta == 0 && tid == 0) *a.status = SV_OK;
-    if (a.parent)
-        for (int i = tid; i < a.T; i += att8_threads(NR)) parent_s[i] = a.parent[i];
     Cursor<kTile8> cur;
     int total, ubegin, uend;
     if (!find_share<kTile8>(a, NR, lane, cta, ncta, cur, total, ubegin, uend)) {
@@ -526,23 +526,13 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
     __syncthreads();
     fence_after();
     const int units = uend - ubegin;
-    // the first segment's queries, by all who would only wait for them
-    if (warp >= 2) {
-        constexpr int kAll = att8_threads(NR) - 64;
-        bring_queries8<D, NR, NP>(a, sh, parent_s, see_s, cur, 0, tid - 64, kAll, [] { group_or<6, kAll>(false); });
-        group_or<6, kAll>(false);
-        if (warp < 4) mbar_arrive(smem_u32(&sh.full_q[0]));
-    }
-
     if (warp == 0) {
         copy_tiles8<D, NR, NP>(a, sh, cur, ubegin, uend, lane);
     } else if (warp == 1) {
-        if (lane == 0) issue_products8<D, NR, NP>(a, sh, units, nq);
+        if (lane == 0) issue_products8<D, NR, NP>(a, sh, units, a.nq);
         __syncwarp();
-    } else if (warp < 4) {
-        bring_more_queries8<D, NR, NP>(a, sh, parent_s, see_s, cur, ubegin, uend, tid - 64);
     } else {
-        const int wg = (warp - 4) / 4, quarter = warp & 3, token = quarter * 32 + lane;
+        const int wg = (warp - 2) / 4, quarter = warp & 3, nq = a.nq, token = quarter * 32 + lane;
         const int r0 = wg * RW;  // the group's first row
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
         const uint32_t tmem_s = sh.tmem + lanes + r0, tmem_o = sh.tmem + lanes + 2 * TT * Sh::kScoreCols + r0;
@@ -646,7 +636,7 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                         see[h] = there ? (1u << live) - 1 : 0u;
                         if (there && x >= 0) {
                             if (a.parent) {
-                                see[h] &= see_s[(at * a.T + x) * Sh::SW + wg / 2] >> (16 * (wg & 1));
+                                see[h] &= __ldcg(a.see + (int64_t(seg.rt) * a.T + x) * Sh::SW + wg / 2) >> (16 * (wg & 1));
                             } else {
                                 see[h] &= 0xFFFFu << min(max(x * a.G - seg.rt * NR - r0, 0), 16);  // not the rows of earlier tokens
                             }
@@ -687,7 +677,7 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                         for (int p = 0; p < parts; ++p) tmem_here(x[h][p]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float2 f = *reinterpret_cast<const float2 *>(&sh.row_f[at][r0 + 8 * c + 2 * j]);
+                        const float2 f = *reinterpret_cast<const float2 *>(&sh.q[at].factor[r0 + 8 * c + 2 * j]);
 #pragma unroll
                         for (int h = 0; h < TT; ++h) {
                             Two y = two(x[h][0][2 * j], x[h][0][2 * j + 1]);
@@ -847,7 +837,7 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                 }
                 if (++head == a.G) head = 0, ++node;
             }
-            if (tid == 128 && seg_lo <= ubegin)  // the share's first segment
+            if (tid == 64 && seg_lo <= ubegin)  // the share's first segment
                 a.desc[cta] = describe(total, cta, ncta, ubegin, seg_lo, seg_lo + seg.tiles, seg.b, seg.h, seg.rt, seg.fresh);
         }
     }
@@ -858,32 +848,40 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(Sh::kCols));
 }
 
+template <int D>
+cudaError_t launch_queries8(const Att8Args &a, cudaStream_t s) {
+    const size_t smem = a.parent ? size_t(a.T) * a.see_words * 4 : 0;  // at most 8 KB
+    const unsigned blocks = unsigned(a.query_blocks + (a.parent ? a.row_tiles : 0));
+    return launch_after(kv8_queries_kernel<D>, blocks, unsigned(kQueryThreads8), smem, s, a);
+}
+
 template <int D, int NR, int NP>
-cudaError_t launch_attention8(const AttArgs &a, int nq, int grid, cudaStream_t s) {
+cudaError_t launch_attention8(const Att8Args &a, int grid, cudaStream_t s) {
     using Sh = Att8Shared<D, NR, NP>;
-    constexpr size_t fixed = sizeof(Sh) + 1024;
-    static_assert(fixed + (NR == 64 ? SV_MAX_TREE_NODES : NR) * 4 * (1 + Sh::kQ * Sh::SW) <= 227 * 1024, "the largest tree");
-    static_assert((fixed + 1024) * att8_occupancy(D, NR) <= 228 * 1024 && Sh::kUsed <= Sh::kCols && Sh::kCols * att8_occupancy(D, NR) <= 512, "");
-    const size_t smem = fixed + (a.parent ? size_t(a.T) * 4 * (1 + Sh::kQ * Sh::SW) : 0);
+    constexpr size_t smem = sizeof(Sh) + 128;
+    static_assert(smem <= 227 * 1024 && (smem + 1024) * att8_occupancy(D, NR) <= 228 * 1024, "");
+    static_assert(sizeof(typename Sh::Queries) == query_bytes8(D, NR) && Sh::kUsed <= Sh::kCols && Sh::kCols * att8_occupancy(D, NR) <= 512, "");
     static std::atomic<int> allowed[64];
     cudaError_t e = allow_shared(kv8_attention_kernel<D, NR, NP>, int(smem), allowed);
     if (e != cudaSuccess) return e;
-    e = launch_after(kv8_attention_kernel<D, NR, NP>, unsigned(grid), unsigned(att8_threads(NR)), smem, s, a, nq);
+    e = launch_after(kv8_attention_kernel<D, NR, NP>, unsigned(grid), unsigned(att8_threads(NR)), smem, s, a);
     if (e != cudaSuccess) return e;
     return launch_join<D>(a, grid, NR, s);
 }
 
 // The kernels of a head dimension and number of weights' parts, each in its own translation unit.
 template <int D, int NP>
-cudaError_t launch_attention8_rows(const AttArgs &a, int nr, int nq, int grid, cudaStream_t s);
+cudaError_t launch_attention8_rows(const Att8Args &a, int grid, cudaStream_t s);
 
 #define SV_KV8_ATTENTION_INSTANTIATE(D, NP)                                                                   \
     template <>                                                                                              \
-    cudaError_t launch_attention8_rows<D, NP>(const AttArgs &a, int nr, int nq, int grid, cudaStream_t s) {    \
-        return nr == 16 ? launch_attention8<D, 16, NP>(a, nq, grid, s)                                         \
-               : nr == 32 ? launch_attention8<D, 32, NP>(a, nq, grid, s)                                       \
-               : nr == 48 ? launch_attention8<D, 48, NP>(a, nq, grid, s)                                       \
-                          : launch_attention8<D, 64, NP>(a, nq, grid, s);                                      \
+    cudaError_t launch_attention8_rows<D, NP>(const Att8Args &a, int grid, cudaStream_t s) {    \
+        cudaError_t e = launch_queries8<D>(a, s);                                                              \
+        if (e != cudaSuccess) return e;                                                                       \
+        return a.nr == 16   ? launch_attention8<D, 16, NP>(a, grid, s)                                         \
+               : a.nr == 32 ? launch_attention8<D, 32, NP>(a, grid, s)                                         \
+               : a.nr == 48 ? launch_attention8<D, 48, NP>(a, grid, s)                                         \
+                            : launch_attention8<D, 64, NP>(a, grid, s);                                        \
     }
 
 }  // namespace sv
