@@ -178,6 +178,15 @@ __device__ __forceinline__ bool mbar_test(const uint64_t *bar, uint32_t parity) 
         : "memory");
     return ok != 0;
 }
+// Asleep until a phase is over, or some 200 ns.
+__device__ __forceinline__ void mbar_doze(const uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(200)
+        : "memory");
+}
 // Between two looks at several barriers: false when nothing has come for as long as a wait may take.
 struct Patience {
     uint64_t since = 0;
@@ -185,9 +194,7 @@ struct Patience {
     __device__ __forceinline__ void reset() { looks = 0; }
     __device__ __forceinline__ bool go_on() {
         if (looks++ == 0) since = global_ns();
-        if ((looks & 63) == 0 && global_ns() - since > kCopyLimitNs) return false;
-        if (looks > 8) __nanosleep(20);
-        return true;
+        return (looks & 63) != 0 || global_ns() - since <= kCopyLimitNs;
     }
 };
 
@@ -310,6 +317,8 @@ __device__ __forceinline__ void copy_tiles8(const Att8Args &a, Att8Shared<D, NR,
         } else if (!__all_sync(0xFFFFFFFFu, patience.go_on())) {
             atomicExch(a.status, int(SV_ERR_TIMEOUT));
             break;
+        } else {
+            __nanosleep(100);  // (looks take instruction slots from the softmax)
         }
     }
     for (int i = max(0, keys - kStages); i < keys; ++i)
@@ -409,6 +418,10 @@ __device__ __forceinline__ void issue_products8(const Att8Args &a, Att8Shared<D,
         } else if (!patience.go_on()) {  // nothing more is issued; the other warps' waits give up too
             atomicExch(a.status, int(SV_ERR_TIMEOUT));
             break;
+        } else if (done < step) {  // asleep until what comes next is likely there
+            mbar_doze(&sh.full_w[done & 1], uint32_t(done >> 1) & 1u);
+        } else {
+            mbar_doze(&sh.full_k[ns % kStages], uint32_t(ns / kStages) & 1u);
         }
     }
     // nothing may be under way when the block ends
