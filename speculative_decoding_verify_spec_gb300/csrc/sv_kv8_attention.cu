@@ -1,5 +1,5 @@
 // sv_kv8_attention.cu -- the C entry of the attention over the 8-bit paged cache: argument checks and workspace layout.
-#include "sv_kv8_attention.cuh"
+#include "sv_kv8_wide.cuh"
 
 namespace sv {
 
@@ -16,24 +16,45 @@ cudaError_t launch_attention8_rows<256, 2>(const Att8Args &a, int grid, cudaStre
 template <>
 cudaError_t launch_attention8_rows<256, 3>(const Att8Args &a, int grid, cudaStream_t s);
 
+template <>
+cudaError_t launch_wide8_of<64, 2>(const Att8Args &a, int grid, cudaStream_t s);
+template <>
+cudaError_t launch_wide8_of<64, 3>(const Att8Args &a, int grid, cudaStream_t s);
+template <>
+cudaError_t launch_wide8_of<128, 2>(const Att8Args &a, int grid, cudaStream_t s);
+template <>
+cudaError_t launch_wide8_of<128, 3>(const Att8Args &a, int grid, cudaStream_t s);
+template <>
+cudaError_t launch_wide8_of<256, 2>(const Att8Args &a, int grid, cudaStream_t s);
+template <>
+cudaError_t launch_wide8_of<256, 3>(const Att8Args &a, int grid, cudaStream_t s);
+
 namespace {
+
+// More rows than this a kv head go to the kernel for many rows.
+constexpr int kNarrowRows8 = 16;
 
 struct Att8Layout {
     size_t desc, ml, acc, parts, see, total;
-    int grid;
+    int grid, nr, tile, see_words;  // blocks at most, rows and tokens a tile
+    bool wide;
 };
 Att8Layout att8_layout(int B, int T, int H, int64_t rows, int D) {
-    const int nr = att8_rows(rows);
-    const size_t row_tiles = size_t((rows + nr - 1) / nr);
     Att8Layout L;
-    L.grid = kAttSMs * att8_occupancy(D, nr);
+    L.wide = rows > kNarrowRows8;
+    L.nr = L.wide ? kWideRows8 : att8_rows(rows);
+    L.tile = L.wide ? wide8_tile(D) : kTile8;
+    L.grid = kAttSMs * (L.wide ? 1 : att8_occupancy(D, L.nr));
+    L.see_words = L.wide ? (T + 31) / 32 : (L.nr + 31) / 32;
+    const int nr = L.nr;
+    const size_t row_tiles = size_t((rows + nr - 1) / nr);
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     L.desc = 256;
     L.ml = up(L.desc + size_t(L.grid) * sizeof(AttDesc));
     L.acc = up(L.ml + size_t(2) * L.grid * nr * 8);
     L.parts = up(L.acc + size_t(2) * L.grid * nr * D * 4);
     L.see = up(L.parts + size_t(B) * H * row_tiles * query_bytes8(D, nr));
-    L.total = up(L.see + (T <= SV_MAX_TREE_NODES ? row_tiles * T * ((nr + 31) / 32) * 4 : 0));
+    L.total = up(L.see + (T <= SV_MAX_TREE_NODES ? row_tiles * (L.wide ? nr : T) * L.see_words * 4 : 0));
     return L;
 }
 
@@ -68,12 +89,13 @@ sv_status spec_kv8_attention(const void *q, int64_t q_batch_stride, int64_t q_to
     if (!q || !out || !start || (table_width > 0 && !page_table) || (num_pages > 0 && !cache)) return SV_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(cache) % 16 || reinterpret_cast<uintptr_t>(q) % 2 || reinterpret_cast<uintptr_t>(out) % 16)
         return SV_ERR_INVALID_ARG;
-    const int G = heads / kv_heads, nr = sv::att8_rows(int64_t(T) * G);
+    const int G = heads / kv_heads;
     const sv::Att8Layout L = sv::att8_layout(B, T, kv_heads, int64_t(T) * G, head_dim);
     if (!workspace || workspace_bytes < L.total || reinterpret_cast<uintptr_t>(workspace) % 16) return SV_ERR_WORKSPACE;
     char *ws = static_cast<char *>(workspace);
+    const int nr = L.nr;
     const int64_t row_tiles = (int64_t(T) * G + nr - 1) / nr, tokens = int64_t(table_width) * page_size;
-    const int64_t most = row_tiles * (tokens / sv::kTile8 + 1);  // units of a sequence and head
+    const int64_t most = row_tiles * (tokens / L.tile + 1);  // units of a sequence and head
     if (most > 0x7FFFFFFF / kv_heads || most * kv_heads > 0x7FFFFFFF / B) return SV_ERR_INVALID_ARG;
     // no more blocks than the page tables have room for units: empty shares would only lengthen the joins
     const int64_t units = most * kv_heads * B;
@@ -87,7 +109,7 @@ sv_status spec_kv8_attention(const void *q, int64_t q_batch_stride, int64_t q_to
     a.B = B, a.T = T, a.H = kv_heads, a.G = G;
     a.cache = static_cast<const uint8_t *>(cache), a.num_pages = num_pages, a.page = page_size, a.width = table_width;
     a.granule = 16;
-    while (a.granule < sv::kTile8 && page_size % (2 * a.granule) == 0) a.granule *= 2;
+    while (a.granule < L.tile && page_size % (2 * a.granule) == 0) a.granule *= 2;
     a.vec = (q_batch_stride | q_token_stride | q_head_stride) % 8 == 0 && reinterpret_cast<uintptr_t>(q) % 16 == 0;
     a.rot_vec = cos && pairs % 4 == 0 && (reinterpret_cast<uintptr_t>(cos) | reinterpret_cast<uintptr_t>(sin)) % 16 == 0;
     a.table = page_table, a.start = start, a.new_lens = new_lens, a.parent = parent;
@@ -99,13 +121,18 @@ sv_status spec_kv8_attention(const void *q, int64_t q_batch_stride, int64_t q_to
     a.desc = reinterpret_cast<sv::AttDesc *>(ws + L.desc);
     a.ml = reinterpret_cast<float2 *>(ws + L.ml);
     a.acc = reinterpret_cast<float *>(ws + L.acc);
-    a.nr = nr, a.see_words = (nr + 31) / 32, a.query_blocks = query_blocks;
+    a.nr = nr, a.wide = L.wide, a.see_words = L.see_words, a.query_blocks = query_blocks;
     a.parts = reinterpret_cast<uint8_t *>(ws + L.parts), a.see = reinterpret_cast<uint32_t *>(ws + L.see);
     // a bf16 query has 8 bits, which two parts hold; what the rotation makes of it, and an fp16 one, takes three
     a.nq = cos || !a.bf16 ? 3 : 2;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (head_dim == 64)
+    if (L.wide)
+        e = head_dim == 64    ? a.bf16 ? sv::launch_wide8_of<64, 2>(a, grid, s) : sv::launch_wide8_of<64, 3>(a, grid, s)
+            : head_dim == 128 ? a.bf16 ? sv::launch_wide8_of<128, 2>(a, grid, s) : sv::launch_wide8_of<128, 3>(a, grid, s)
+            : a.bf16          ? sv::launch_wide8_of<256, 2>(a, grid, s)
+                              : sv::launch_wide8_of<256, 3>(a, grid, s);
+    else if (head_dim == 64)
         e = a.bf16 ? sv::launch_attention8_rows<64, 2>(a, grid, s) : sv::launch_attention8_rows<64, 3>(a, grid, s);
     else if (head_dim == 128)
         e = a.bf16 ? sv::launch_attention8_rows<128, 2>(a, grid, s) : sv::launch_attention8_rows<128, 3>(a, grid, s);

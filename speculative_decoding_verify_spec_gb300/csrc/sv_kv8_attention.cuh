@@ -60,10 +60,11 @@ __host__ __device__ constexpr int query_bytes8(int D, int NR) { return 3 * NR * 
 
 struct Att8Args : AttArgs {
     int nr, nq;            // rows a tile, parts of a query
-    int see_words;         // a new token's words in `see`
+    int wide;              // the kernel for many rows
+    int see_words;         // a new token's words in `see`; of the kernel for many rows: a row's
     int64_t query_blocks;
     uint8_t *parts;        // [B][H][row_tiles][query_bytes8]
-    uint32_t *see;         // [row_tiles][T][see_words]: the rows that see a new token of a tree
+    uint32_t *see;         // [row_tiles][T][see_words]: the rows that see a new token of a tree; or [row_tiles][nr][see_words], the other way round
 };
 
 struct alignas(16) Info8 {
@@ -73,7 +74,7 @@ struct alignas(16) Info8 {
 
 template <int D, int NR, int NP>
 struct Att8Shared {
-    static constexpr int W = att8_groups(NR), RW = kGroupRows8, SW = (NR + 31) / 32, kStages = att8_stages(D, NR), kValues = att8_value_stages(D, NR), TT = att8_pair(D, NR), kInfos = kStages + 2 * TT;
+    static constexpr int kDims = D, kRows = NR, kTile = kTile8, W = att8_groups(NR), RW = kGroupRows8, SW = (NR + 31) / 32, kStages = att8_stages(D, NR), kValues = att8_value_stages(D, NR), TT = att8_pair(D, NR), kInfos = kStages + 2 * TT;
     static constexpr int kQ = att8_q_places(D, NR), kP = att8_w_places(D, NR), MB = D == 256 ? 2 : 1;
     // Few rows: a product reads the cache's operand at its full width whatever the columns, so the parts are columns of
     // one product and are added up afterwards.
@@ -204,13 +205,14 @@ struct Source8 {
     uint32_t bytes, sum, have;  // this lane's bytes, those of all granules (of codes), bit 4 g: granule g is there
 };
 // The units of the share in turn, each with a lane's piece (0: keys, 1: values, 2: words).
-template <int D, int NR>
+template <typename Sh>
 struct Walk8 {
-    Cursor<kTile8> cur;
+    Cursor<Sh::kTile> cur;
     int u, pi = 0, slot = 0;
     bool placed = false;
     __device__ __forceinline__ Source8 source(const Att8Args &a, int gi, int piece, bool busy) {
-        const int tok = cur.tile * kTile8 + gi * a.granule;
+        constexpr int D = Sh::kDims;
+        const int tok = cur.tile * Sh::kTile + gi * a.granule;
         if (!placed) pi = tok / a.page, slot = tok - pi * a.page, placed = true;
         const bool inside = busy && cur.live && tok < cur.w.len;
         const int pg = inside ? __ldg(a.table + int64_t(cur.b) * a.width + pi) : -1;
@@ -229,27 +231,26 @@ struct Walk8 {
         ++u;
         if (cur.tile + 1 < cur.tiles()) {
             ++cur.tile;
-            slot += kTile8;
+            slot += Sh::kTile;
             while (slot >= a.page) slot -= a.page, ++pi;
         } else if (u < uend) {
-            cur.next(a, NR, u);
+            cur.next(a, Sh::kRows, u);
             placed = false;
         }
     }
 };
 
 // The copying warp.  Keys and words, values, and segments' queries each go as far ahead as their rings have room.  Returns when all that it has begun is there.
-template <int D, int NR, int NP>
-__device__ __forceinline__ void copy_tiles8(const Att8Args &a, Att8Shared<D, NR, NP> &sh, Cursor<kTile8> &cur, int ubegin, int uend, int lane) {
-    using Sh = Att8Shared<D, NR, NP>;
-    constexpr int NT = kTile8, kStages = Sh::kStages, kValues = Sh::kValues;
+template <typename Sh>
+__device__ __forceinline__ void copy_tiles8(const Att8Args &a, Sh &sh, Cursor<Sh::kTile> &cur, int ubegin, int uend, int lane) {
+    constexpr int NT = Sh::kTile, D = Sh::kDims, NR = Sh::kRows, kStages = Sh::kStages, kValues = Sh::kValues;
     const int gi = lane & 7, piece = lane >> 3, granules = NT / a.granule;  // lanes 0 .. 7 keys, 8 .. 15 words, 16 .. 23 values
     const uint32_t all = (1u << granules) - 1;
     const int units = uend - ubegin;
     int keys = 0, values = 0;  // begun
     int queries = 0, qu = ubegin;  // segments whose queries are begun, and the unit with which the next one begins
-    Walk8<D, NR> kw{cur, ubegin}, vw{cur, ubegin};
-    Cursor<kTile8> qc = cur;
+    Walk8<Sh> kw{cur, ubegin}, vw{cur, ubegin};
+    Cursor<NT> qc = cur;
     const uint32_t part_bytes = uint32_t(a.nq) * NR * D;
     Patience patience;
 #ifdef SV_CHECKS
@@ -443,13 +444,16 @@ __global__ void __launch_bounds__(kQueryThreads8) kv8_queries_kernel(const Att8A
     griddep_launch_next();
     griddep_wait();
     if (int64_t(blockIdx.x) >= a.query_blocks) {
-        const int rt = int(blockIdx.x - a.query_blocks), words = a.T * a.see_words;
+        const int rt = int(blockIdx.x - a.query_blocks), words = (a.wide ? a.nr : a.T) * a.see_words;
         for (int i = tid; i < words; i += kQueryThreads8) see_s[i] = 0;
         __syncthreads();
         if (tid < a.nr) {
             const int64_t node = (int64_t(rt) * a.nr + tid) / a.G;
             for (int v = node < a.T ? int(node) : -1; v >= 0;) {
-                atomicOr(see_s + v * a.see_words + tid / 32, 1u << (tid & 31));
+                if (a.wide)
+                    see_s[tid * a.see_words + v / 32] |= 1u << (v & 31);
+                else
+                    atomicOr(see_s + v * a.see_words + tid / 32, 1u << (tid & 31));
                 const int up = __ldg(a.parent + v);
                 v = up < v ? up : -1;
             }
@@ -479,7 +483,10 @@ __global__ void __launch_bounds__(kQueryThreads8) kv8_queries_kernel(const Att8A
     if (on) query_chunk(a, un, node, head, d0, x);
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(fabsf(x[i])));
+    for (int i = 0; i < 8; ++i) {
+        x[i] = a.scale == 0.f ? x[i] * 0.f : a.scale < 0.f ? -x[i] : x[i];  // (factors are above 0)
+        top = max(top, __float_as_uint(fabsf(x[i])));
+    }
 #pragma unroll
     for (int o = L / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     if (!inside) return;
@@ -498,7 +505,8 @@ __global__ void __launch_bounds__(kQueryThreads8) kv8_queries_kernel(const Att8A
 #pragma unroll
     for (int k = 0; k < 3; ++k)
         if (k < a.nq) *reinterpret_cast<uint2 *>(q + kv8_code_byte(D, k * a.nr + r, d0)) = make_uint2(code[k][0], code[k][1]);
-    if (c == 0) reinterpret_cast<float *>(q + 3 * a.nr * D)[r] = a.scale * 1.4426950408889634f * power2(odd ? 0 : e2);
+    if (c == 0) reinterpret_cast<float *>(q + 3 * a.nr * D)[r] =
+            a.scale == 0.f ? 1.f : fmaxf(fabsf(a.scale) * 1.4426950408889634f * power2(odd ? 0 : e2), 1.2e-38f);
 }
 
 template <int D, int NR, int NP>
@@ -540,7 +548,7 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
     fence_after();
     const int units = uend - ubegin;
     if (warp == 0) {
-        copy_tiles8<D, NR, NP>(a, sh, cur, ubegin, uend, lane);
+        copy_tiles8(a, sh, cur, ubegin, uend, lane);
     } else if (warp == 1) {
         if (lane == 0) issue_products8<D, NR, NP>(a, sh, units, a.nq);
         __syncwarp();
@@ -863,7 +871,7 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
 
 template <int D>
 cudaError_t launch_queries8(const Att8Args &a, cudaStream_t s) {
-    const size_t smem = a.parent ? size_t(a.T) * a.see_words * 4 : 0;  // at most 8 KB
+    const size_t smem = a.parent ? size_t(a.wide ? a.nr : a.T) * a.see_words * 4 : 0;  // at most 17 KB
     const unsigned blocks = unsigned(a.query_blocks + (a.parent ? a.row_tiles : 0));
     return launch_after(kv8_queries_kernel<D>, blocks, unsigned(kQueryThreads8), smem, s, a);
 }

@@ -1,0 +1,396 @@
+// sv_kv8_wide.cuh -- the attention over the 8-bit paged cache for many query rows a kv head (drafts, token trees): 128 rows
+// a tile, a thread of the softmax has one row.
+//
+// The sums are those of sv_kv8_attention.cuh, and so are the queries' parts, the copying warp, the list of units and the join.  Here
+// the rows are the products' 128-row operand and the cache's bytes the other one:
+//   S [128 rows x tokens] = q [128 x D]  times  K codes^T         D / 32 steps a part of q
+//   O [128 rows x D]      = w [128 x tokens]  times  V codes      a step for 32 tokens and part of w
+// so that a row's maximum and sum need no reduction over lanes, a block of 16 tokens has its scales in registers, and m is taken out in the
+// multiplication that scales a score.  Sixteen warps: four groups of 128 threads have the 128 rows each, and a quarter of
+// the tile's tokens and of the output's dimensions.  As there, every tile has its own m and output, which is added up in registers.
+#pragma once
+
+#include "sv_kv8_attention.cuh"
+
+namespace sv {
+
+constexpr int kWideRows8 = 128, kWideGroups8 = 4, kWideThreads8 = 64 + 128 * kWideGroups8;
+__host__ __device__ constexpr int wide8_tile(int D) { return D == 256 ? 64 : 128; }  // by shared memory
+
+template <int D, int NP>
+struct Wide8Shared {
+    static constexpr int kDims = D, kRows = kWideRows8, kTile = wide8_tile(D);
+    static constexpr int kStages = D == 64 ? 4 : 3, kValues = kStages, kInfos = kStages + 2, kQ = D == 64 ? 2 : 1;
+    static constexpr int kO = D == 256 ? 1 : 2;  // outputs in tensor memory
+    static constexpr int kUsed = 2 * kTile + kO * D, kCols = kUsed <= 256 ? 256 : 512;
+    alignas(128) uint8_t k[kStages][kTile * D];
+    uint8_t v[kValues][kTile * D];
+    uint8_t w[NP][kRows * kTile];  // [part][16 tokens][row][16 bytes]
+    struct Queries {
+        uint8_t part[3][kRows * D];
+        float factor[kRows];
+    };
+    Queries q[kQ];
+    Info8 info[kInfos];
+    float red[2][kWideGroups8][kRows], sums[kWideGroups8][kRows];
+    alignas(8) uint64_t full_k[kStages], full_v[kValues], empty_k[kStages], empty_v[kValues], full_i[kInfos];
+    uint64_t full_s[2], free_s[2], full_o[kO], free_o[kO], full_w[2], full_q[kQ], free_q[kQ], done;
+    uint32_t tmem;
+};
+
+// The issuing thread.
+template <int D, int NP>
+__device__ __forceinline__ void issue_wide8(const Att8Args &a, Wide8Shared<D, NP> &sh, int units) {
+    using Sh = Wide8Shared<D, NP>;
+    constexpr int kStages = Sh::kStages, kValues = Sh::kValues, NT = Sh::kTile;
+    const uint32_t tmem = sh.tmem;
+    int segment = -1, flags = 0;  // of the next scores' unit, once its keys are there
+    bool known = false;
+    auto scores = [&](int n) {
+        const int s = n % kStages;
+        if (!known) {
+            if (!mbar_test(&sh.full_k[s], uint32_t(n / kStages) & 1u)) return false;
+            flags = sh.info[n % Sh::kInfos].unit.masked;
+            if (flags & kFirst8) ++segment;
+            known = true;
+        }
+        if ((flags & kFirst8) && !mbar_test(&sh.full_q[segment % Sh::kQ], uint32_t(segment / Sh::kQ) & 1u)) return false;
+        if (n >= 2 && !mbar_test(&sh.free_s[n & 1], uint32_t((n >> 1) - 1) & 1u)) return false;
+        known = false;
+        fence_after();
+        constexpr uint32_t high = operand8_high(8 * D);
+        const uint32_t d = tmem + (n & 1) * NT, k = operand8(smem_u32(sh.k[s]), 128);
+        uint32_t q = operand8(smem_u32(sh.q[segment % Sh::kQ].part), 128);
+#pragma unroll
+        for (int p = 0; p < 3; ++p, q += kWideRows8 * D / 16)
+            if (p < 2 || a.nq > 2) {
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) mma8(d, q + i * 16, high, k + i * 16, high, kind8(NT, false), p > 0 || i > 0);
+            }
+        wide_commit(&sh.empty_k[s]);
+        wide_commit(&sh.full_s[n & 1]);
+        if (flags & kLast8) wide_commit(&sh.free_q[segment % Sh::kQ]);
+        return true;
+    };
+    auto products = [&](int n) {
+        const int s = n % kValues, at = n % Sh::kO;
+        if (!mbar_test(&sh.full_w[n & 1], uint32_t(n >> 1) & 1u) || !mbar_test(&sh.full_v[s], uint32_t(n / kValues) & 1u)) return false;
+        if (n >= Sh::kO && !mbar_test(&sh.free_o[at], uint32_t(n / Sh::kO - 1) & 1u)) return false;
+        fence_after();
+        const uint32_t d = tmem + 2 * NT + at * D, v = operand8(smem_u32(sh.v[s]), 8 * D), w = operand8(smem_u32(sh.w), 2048);
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+            for (int i = 0; i < NT / 32; ++i)
+                mma8(d, w + (p * kWideRows8 * NT + i * 4096) / 16, operand8_high(128), v + i * 2 * D, operand8_high(128),
+                     kind8(D, false) | 1u << 16, p > 0 || i > 0);  // (the values have their rows contiguous)
+        wide_commit(&sh.empty_v[s]);
+        wide_commit(&sh.full_o[at]);
+        return true;
+    };
+    Patience patience;
+    for (int ns = 0, np = 0; np < units;) {
+        if (np < ns && products(np)) {
+            ++np, patience.reset();
+        } else if (ns < units && scores(ns)) {
+            ++ns, patience.reset();
+        } else if (!patience.go_on()) {  // nothing more is issued; the other warps' waits give up too
+            atomicExch(a.status, int(SV_ERR_TIMEOUT));
+            break;
+        } else if (np < ns) {  // asleep until what comes next is likely there
+            mbar_doze(&sh.full_w[np & 1], uint32_t(np >> 1) & 1u);
+        } else {
+            mbar_doze(&sh.full_k[ns % kStages], uint32_t(ns / kStages) & 1u);
+        }
+    }
+    // nothing may be under way when the block ends
+    wide_commit(&sh.done);
+    if (!mbar_wait(smem_u32(&sh.done), 0)) atomicExch(a.status, int(SV_ERR_TIMEOUT));
+}
+
+template <int D, int NP>
+__global__ void __launch_bounds__(kWideThreads8, 1) kv8_wide_kernel(const Att8Args a) {
+    using Sh = Wide8Shared<D, NP>;
+    constexpr int NT = Sh::kTile, NR = kWideRows8, kValues = Sh::kValues, TW = NT / kWideGroups8, CW = D / kWideGroups8;  // a thread's tokens and dimensions
+    extern __shared__ unsigned char raw0[];
+    Sh &sh = *reinterpret_cast<Sh *>(raw0 + ((128 - (smem_u32(raw0) & 127)) & 127));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ncta = int(gridDim.x), cta = int(blockIdx.x);
+
+    griddep_launch_next();
+    if (tid == 0) {
+        for (int i = 0; i < Sh::kStages; ++i) mbar_init(smem_u32(&sh.full_k[i]), 1), mbar_init(smem_u32(&sh.empty_k[i]), 1);
+        for (int i = 0; i < kValues; ++i) mbar_init(smem_u32(&sh.full_v[i]), 1), mbar_init(smem_u32(&sh.empty_v[i]), 1);
+        for (int i = 0; i < 2; ++i)
+            mbar_init(smem_u32(&sh.full_s[i]), 1), mbar_init(smem_u32(&sh.free_s[i]), 16), mbar_init(smem_u32(&sh.full_w[i]), 16);
+        for (int i = 0; i < Sh::kO; ++i) mbar_init(smem_u32(&sh.full_o[i]), 1), mbar_init(smem_u32(&sh.free_o[i]), 16);
+        for (int i = 0; i < Sh::kQ; ++i) mbar_init(smem_u32(&sh.full_q[i]), 1), mbar_init(smem_u32(&sh.free_q[i]), 17);
+        for (int i = 0; i < Sh::kInfos; ++i) mbar_init(smem_u32(&sh.full_i[i]), 1);
+        mbar_init(smem_u32(&sh.done), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    griddep_wait();
+    if (cta == 0 && tid == 0) *a.status = SV_OK;
+    Cursor<NT> cur;
+    int total, ubegin, uend;
+    if (!find_share<NT>(a, NR, lane, cta, ncta, cur, total, ubegin, uend)) {
+        if (tid == 0) a.desc[cta] = AttDesc{0, 0, 0, 0, 0, 0, 0, 0};
+        return;
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "r"(Sh::kCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        fence_before();
+    }
+    __syncthreads();
+    fence_after();
+    const int units = uend - ubegin;
+
+    if (warp == 0) {
+        copy_tiles8(a, sh, cur, ubegin, uend, lane);
+    } else if (warp == 1) {
+        if (lane == 0) issue_wide8<D, NP>(a, sh, units);
+        __syncwarp();
+    } else {
+        const int group = (warp - 2) / 4, quarter = warp & 3, r = quarter * 32 + lane;  // this thread's row
+        const uint32_t lanes = uint32_t(quarter * 32) << 16;
+        const uint32_t tmem_s = sh.tmem + lanes + group * TW, tmem_o = sh.tmem + lanes + 2 * NT + group * CW;
+        int granule_log2 = 4;
+        while (1 << granule_log2 < a.granule) ++granule_log2;
+        bool failed = false;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (!warp_wait(bar, parity) && !failed) {
+                failed = true;
+                atomicExch(a.status, int(SV_ERR_TIMEOUT));
+            }
+        };
+        Unit seg{};
+        int seg_lo = 0, segment = -1, node = -1;
+        bool warp_on = false;  // some row of the warp is live
+        float factor = 1.f, M = -INFINITY, l = 0.f, f_last = 1.f;
+        Two acc[CW / 2];
+        // the output of unit n, which is of the segment at hand
+        auto take_up = [&](int n, float f) {
+            wait(&sh.full_o[n % Sh::kO], uint32_t(n / Sh::kO) & 1u);
+            if (failed) return;
+            fence_after();
+            if (warp_on) {
+#pragma unroll
+                for (int c = 0; c < CW; c += 16) {
+                    float o[2][8];
+                    tmem_get8(o[0], tmem_o + n % Sh::kO * D + c), tmem_get8(o[1], tmem_o + n % Sh::kO * D + c + 8);
+                    tmem_loaded();
+                    tmem_here(o[0]), tmem_here(o[1]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[c / 2 + j] = fma2(two(o[j / 4][2 * (j % 4)], o[j / 4][2 * (j % 4) + 1]), two(f, f), acc[c / 2 + j]);
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.free_o[n % Sh::kO]));
+        };
+
+        for (int n = 0; n < units; ++n) {
+            const Info8 &in = sh.info[n % Sh::kInfos];
+            wait(&sh.full_i[n % Sh::kInfos], uint32_t(n / Sh::kInfos) & 1u);
+            int flags = 0;
+            float s[TW], scale[TW / 16], shift[TW / 16], inv[TW / 16];
+            uint32_t see = 0xFFFFFFFFu;
+            if (!failed) {
+                flags = in.unit.masked;
+                if (flags & kFirst8) {
+                    seg = in.unit;
+                    ++segment;
+                    seg_lo = ubegin + n - seg.tile;
+                    node = (seg.rt * NR + r) / a.G;
+                    if (node >= seg.fresh) node = -1;
+                    warp_on = __any_sync(0xFFFFFFFFu, node >= 0);
+                    M = -INFINITY, l = 0.f;
+#pragma unroll
+                    for (int j = 0; j < CW / 2; ++j) acc[j] = 0;
+                    wait(&sh.full_q[segment % Sh::kQ], uint32_t(segment / Sh::kQ) & 1u);
+                    factor = sh.q[segment % Sh::kQ].factor[r];
+                }
+                const int tok0 = in.unit.tile * NT + group * TW;  // this thread's first token
+                if (flags & kMasked8) {  // which of its tokens the row sees
+                    uint32_t there = 0;
+#pragma unroll
+                    for (int b = 0; b < TW; b += 16) {  // (granules are 16 tokens at least)
+                        const int left = seg.len - (tok0 + b);
+                        if (left > 0 && (in.unit.have >> ((group * TW + b) >> granule_log2) & 1u)) there |= (left >= 16 ? 0xFFFFu : (1u << left) - 1) << b;
+                    }
+                    const int x = tok0 - seg.before;  // the first one among the new tokens
+                    if (x > -TW && node >= 0) {
+                        if (a.parent) {
+                            const uint32_t *words = a.see + (int64_t(seg.rt) * NR + r) * a.see_words;
+                            const int w = max(x, 0) >> 5;
+                            const uint32_t low = w < a.see_words ? __ldcg(words + w) : 0u, high = w + 1 < a.see_words ? __ldcg(words + w + 1) : 0u;
+                            see = x >= 0 ? __funnelshift_r(low, high, x & 31) : low << -x | ((1u << -x) - 1);
+                        } else {
+                            const int count = node + 1 - x;
+                            see = count >= 32 ? 0xFFFFFFFFu : count <= 0 ? 0u : (1u << count) - 1;
+                        }
+                    }
+                    see &= there;
+                    if (flags & kRagged8) wait(&sh.full_v[n % kValues], uint32_t(n / kValues) & 1u);
+                }
+                wait(&sh.full_s[n & 1], uint32_t(n >> 1) & 1u);
+                fence_after();
+                float most = -INFINITY;
+                if (warp_on) {
+#pragma unroll
+                    for (int c = 0; c < TW; c += 8) tmem_get8(*reinterpret_cast<float(*)[8]>(s + c), tmem_s + (n & 1) * NT + c);
+                    tmem_loaded();
+#pragma unroll
+                    for (int c = 0; c < TW; c += 8) tmem_here(*reinterpret_cast<float(*)[8]>(s + c));
+#pragma unroll
+                    for (int b = 0; b < TW / 16; ++b) {
+                        uint2 word = *reinterpret_cast<const uint2 *>(in.word[group * (TW / 16) + b]);
+                        // (what is not there has no scale; its tokens are not seen)
+                        if ((flags & kRagged8) && (tok0 + 16 * b >= seg.len || !(in.unit.have >> ((group * TW + 16 * b) >> granule_log2) & 1u))) word = make_uint2(0x3F800000u, 0x3F800000u);
+                        const int e = kv8_exponent(word.y);
+                        scale[b] = fmaxf(factor * __uint_as_float(word.x & 0xFFFF0000u), 1.2e-38f), shift[b] = float(e), inv[b] = kv8_power(-e);
+                        const uint32_t bad = (word.x | word.y) & 0xFFFFu;
+                        if (bad) {  // (of the whole warp; rare)
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                if (bad >> j & 1u) s[16 * b + j] = NAN;
+                        }
+                        if (flags & kMasked8) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                if (!(see >> (16 * b + j) & 1u)) s[16 * b + j] = -INFINITY;
+                        }
+                        float top = s[16 * b];
+#pragma unroll
+                        for (int j = 1; j < 16; ++j) top = fmaxf(top, s[16 * b + j]);
+                        most = fmaxf(most, fmaf(top, scale[b], shift[b]));
+                    }
+                    sh.red[n & 1][group][r] = most;
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) {  // the scores and what is known of the unit are read
+                    mbar_arrive(smem_u32(&sh.free_s[n & 1]));
+                    if (flags & kLast8) mbar_arrive(smem_u32(&sh.free_q[segment % Sh::kQ]));
+                }
+            }
+            if (group_or<1, 128 * kWideGroups8>(failed)) break;
+            const bool first = (flags & kFirst8) != 0, last = (flags & kLast8) != 0;
+            float f = 1.f;
+            if (!first) wait(&sh.full_o[(n - 1) % Sh::kO], uint32_t((n - 1) / Sh::kO) & 1u);  // the last unit's weights are in the place of these
+            if (warp_on && !failed) {
+                const float(*red)[NR] = sh.red[n & 1];
+                const float m = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r]));
+                const float whole = rintf(m);
+                float g = 1.f, minus = m == INFINITY ? -INFINITY : 0.f;
+                if (fabsf(whole) < INFINITY) {
+                    if (M == -INFINITY) M = whole;
+                    if (whole > M + 60.f) g = ex2(fmaxf(M - whole, -126.f)), M = whole;
+                    f = ex2(fmaxf(whole - M, -127.f));
+                    minus = float(kKv8Top) - whole;
+                }
+                if (__any_sync(0xFFFFFFFFu, g != 1.f)) {  // (rare; the last unit's output, not taken up yet, is to move too)
+                    l *= g, f_last *= g;
+#pragma unroll
+                    for (int j = 0; j < CW / 2; ++j) acc[j] = mul2(acc[j], two(g, g));
+                }
+#pragma unroll
+                for (int b = 0; b < TW / 16; ++b) {
+                    const Two a2 = two(scale[b], scale[b]), b2 = two(shift[b] + minus, shift[b] + minus);
+                    Two sum = 0;
+                    uint32_t code[NP][4];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 x = split(fma2(two(s[16 * b + 2 * j], s[16 * b + 2 * j + 1]), a2, b2));
+                        const float w0 = ex2(x.x), w1 = ex2(x.y);
+                        sum = add2(sum, two(w0, w1));
+                        uint32_t p[NP];
+                        parts8(w0, w1, p);
+#pragma unroll
+                        for (int k = 0; k < NP; ++k) code[k][j / 2] = j & 1 ? code[k][j / 2] | p[k] << 16 : p[k];
+                    }
+#pragma unroll
+                    for (int k = 0; k < NP; ++k)
+                        *reinterpret_cast<uint4 *>(sh.w[k] + (group * (TW / 16) + b) * 2048 + r * 16) = make_uint4(code[k][0], code[k][1], code[k][2], code[k][3]);
+                    const float2 both = split(sum);
+                    l = fmaf((both.x + both.y) * inv[b], f, l);
+                }
+            }
+            if (!failed) {
+                const int token = tid - 64;  // a code that is not there may be a NaN, which no weight of 0 takes away
+                if ((flags & kRagged8) && token < NT && (in.unit.tile * NT + token >= seg.len || !(in.unit.have >> (token >> granule_log2) & 1u))) {
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) *reinterpret_cast<uint4 *>(sh.v[n % kValues] + kv8_code_byte(D, token, 16 * j)) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            fence_operands();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.full_w[n & 1]));
+            // the last unit's output, and at the segment's end this one's
+#pragma unroll 1
+            for (int j = first ? n : n - 1; j <= (last ? n : n - 1); ++j) take_up(j, j == n ? f : f_last);
+            f_last = f;
+            if (!last) continue;
+
+            // the segment's end
+            sh.sums[group][r] = l;
+            if (group_or<1, 128 * kWideGroups8>(failed)) break;
+            const bool whole = seg_lo >= ubegin && seg_lo + seg.tiles <= uend;
+            const int64_t slot = 2 * cta + (seg_lo > ubegin ? 1 : 0);
+            const float sum = (sh.sums[0][r] + sh.sums[1][r]) + (sh.sums[2][r] + sh.sums[3][r]);
+            const float part = node < 0 || sum == 0.f ? 0.f : 1.f / sum;
+            const int row = seg.rt * NR + r, at = row / a.G;
+            if (whole) {
+                if (at < a.T) {
+                    uint16_t *out = a.out + ((seg.b * int64_t(a.T) + at) * a.H * a.G + seg.h * a.G + row - at * a.G) * D + group * CW;
+#pragma unroll
+                    for (int c = 0; c < CW; c += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 x = split(acc[c / 2 + j]);
+                            w[j] = uint32_t(kv_from_float(part == 0.f ? 0.f : x.x * part, a.bf16)) | uint32_t(kv_from_float(part == 0.f ? 0.f : x.y * part, a.bf16)) << 16;
+                        }
+                        *reinterpret_cast<uint4 *>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            } else if (SV_IN(slot, 2 * ncta)) {
+                float4 *dst = reinterpret_cast<float4 *>(a.acc + (slot * NR + r) * D + group * CW);
+#pragma unroll
+                for (int c = 0; c < CW; c += 4) {
+                    const float2 x = split(acc[c / 2]), y = split(acc[c / 2 + 1]);
+                    dst[c / 4] = make_float4(x.x, x.y, y.x, y.y);
+                }
+                if (group == 0) a.ml[slot * NR + r] = make_float2(M, sum);
+            }
+            if (tid == 64 && seg_lo <= ubegin)  // the share's first segment
+                a.desc[cta] = describe(total, cta, ncta, ubegin, seg_lo, seg_lo + seg.tiles, seg.b, seg.h, seg.rt, seg.fresh);
+        }
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(Sh::kCols));
+}
+
+template <int D, int NP>
+cudaError_t launch_wide8(const Att8Args &a, int grid, cudaStream_t s) {
+    using Sh = Wide8Shared<D, NP>;
+    constexpr size_t smem = sizeof(Sh) + 128;
+    static_assert(smem <= 227 * 1024 && sizeof(typename Sh::Queries) == query_bytes8(D, kWideRows8) && Sh::kUsed <= 512, "");
+    static std::atomic<int> allowed[64];
+    cudaError_t e = launch_queries8<D>(a, s);
+    if (e != cudaSuccess) return e;
+    e = allow_shared(kv8_wide_kernel<D, NP>, int(smem), allowed);
+    if (e != cudaSuccess) return e;
+    e = launch_after(kv8_wide_kernel<D, NP>, unsigned(grid), unsigned(kWideThreads8), smem, s, a);
+    if (e != cudaSuccess) return e;
+    return launch_join<D>(a, grid, kWideRows8, s);
+}
+
+template <int D, int NP>
+cudaError_t launch_wide8_of(const Att8Args &a, int grid, cudaStream_t s);
+
+}  // namespace sv
