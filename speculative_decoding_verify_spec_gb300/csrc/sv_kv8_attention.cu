@@ -32,7 +32,7 @@ cudaError_t launch_wide8_of<256, 3>(const Att8Args &a, int grid, cudaStream_t s)
 namespace {
 
 // More rows than this a kv head go to the kernel for many rows.
-constexpr int kNarrowRows8 = 16;
+constexpr int kNarrowRows8 = 64;
 
 struct Att8Layout {
     size_t desc, ml, acc, parts, see, total;

@@ -37,8 +37,6 @@ constexpr int kTile8 = 128;
 constexpr int kGroupRows8 = 16;  // query rows of a softmax group
 __host__ __device__ constexpr int att8_groups(int NR) { return NR / kGroupRows8; }
 __host__ __device__ constexpr int att8_threads(int NR) { return 64 + 128 * att8_groups(NR); }
-// Tiles that a block takes at a time: two where a key head has many rows, whose softmax then has half as many barriers, waits and maxima.
-__host__ __device__ constexpr int att8_pair(int D, int NR) { return 1; }
 // Tiles in the rings, places for queries and weights, and blocks an SM: by shared memory and registers.
 __host__ __device__ constexpr int att8_stages(int D, int NR) { return D == 64 ? (NR == 16 ? 5 : NR == 32 ? 4 : 6) : D == 128 ? (NR <= 32 ? 2 : 3) : (NR == 16 ? 3 : 2); }
 __host__ __device__ constexpr int att8_value_stages(int D, int NR) {
@@ -74,16 +72,16 @@ struct alignas(16) Info8 {
 
 template <int D, int NR, int NP>
 struct Att8Shared {
-    static constexpr int kDims = D, kRows = NR, kTile = kTile8, W = att8_groups(NR), RW = kGroupRows8, SW = (NR + 31) / 32, kStages = att8_stages(D, NR), kValues = att8_value_stages(D, NR), TT = att8_pair(D, NR), kInfos = kStages + 2 * TT;
+    static constexpr int kDims = D, kRows = NR, kTile = kTile8, W = att8_groups(NR), RW = kGroupRows8, SW = (NR + 31) / 32, kStages = att8_stages(D, NR), kValues = att8_value_stages(D, NR), kInfos = kStages + 2;
     static constexpr int kQ = att8_q_places(D, NR), kP = att8_w_places(D, NR), MB = D == 256 ? 2 : 1;
     // Few rows: a product reads the cache's operand at its full width whatever the columns, so the parts are columns of
     // one product and are added up afterwards.
     static constexpr bool kStackQ = NR == 16 || (D == 256 && NR == 32), kStackP = NR == 16 || (D == 256 && NR == 32 && NP == 2);
     static constexpr int kScoreCols = kStackQ ? (NR == 16 ? 64 : 96) : NR == 32 ? 32 : 64, kOutEach = NR >= 48 || (kStackP && NP * NR > 32) ? 64 : 32, kOutCols = MB * kOutEach;
-    static constexpr int kUsed = 2 * (TT * kScoreCols + kOutCols), kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+    static constexpr int kUsed = 2 * (kScoreCols + kOutCols), kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     alignas(128) uint8_t k[kStages][kTile8 * D];
     uint8_t v[kValues][kTile8 * D];       // (64 dimensions: a product's upper 64 rows read past the end, into w)
-    uint8_t w[kP][TT * NP * NR * kTile8];  // [tile][part][16 rows][token][16 bytes]
+    uint8_t w[kP][NP * NR * kTile8];      // [part][16 rows][token][16 bytes]
     struct Queries {
         uint8_t part[3][NR * D];
         float factor[NR];                 // log2(e) scale times the power of two taken out of the row
@@ -94,7 +92,7 @@ struct Att8Shared {
     alignas(16) float sums[W][4][RW];
     alignas(16) float4 move[W][4][2][RW / 2];  // of a row pair: -m, then 2^(m - M); every warp has its own
     // Each is waited for before what it tells of can come about once more, so that a phase's parity is enough: a unit's place in `info`
-    // is taken again after the scores of two steps later (a step is a unit, or two of a segment), which wait for the softmax to have read this one's.
+    // is taken again after the scores of two units later, which wait for the softmax to have read this one's.
     alignas(8) uint64_t full_k[kStages], full_v[kValues], empty_k[kStages], empty_v[kValues], full_i[kInfos];
     uint64_t full_s[2], free_s[2], full_o[2], free_o[2], full_w[2], full_q[kQ], free_q[kQ], done;
     uint32_t tmem;
@@ -340,25 +338,20 @@ __device__ __forceinline__ void issue_products8(const Att8Args &a, Att8Shared<D,
     const uint32_t tmem = sh.tmem;
     int segment = -1, flags = 0;  // of the next scores' unit, once its keys are there
     bool known = false;
-    int ns = 0, step = 0, half = 0;        // the next scores' unit, its step, and whether it is the step's second one
-    int np = 0, done = 0;                  // the next products' first unit and step
-    uint32_t pairs = 0;                    // bit i % 4: step i has two units
-    auto scores = [&] {
-        const int s = ns % kStages;
+    auto scores = [&](int n) {
+        const int s = n % kStages;
         if (!known) {
-            if (!mbar_test(&sh.full_k[s], uint32_t(ns / kStages) & 1u)) return false;
-            flags = sh.info[ns % Sh::kInfos].unit.masked;
+            if (!mbar_test(&sh.full_k[s], uint32_t(n / kStages) & 1u)) return false;
+            flags = sh.info[n % Sh::kInfos].unit.masked;
             if (flags & kFirst8) ++segment;
             known = true;
         }
-        if (half == 0) {
-            if ((flags & kFirst8) && !mbar_test(&sh.full_q[segment % Sh::kQ], uint32_t(segment / Sh::kQ) & 1u)) return false;
-            if (step >= 2 && !mbar_test(&sh.free_s[step & 1], uint32_t((step >> 1) - 1) & 1u)) return false;
-        }
+        if ((flags & kFirst8) && !mbar_test(&sh.full_q[segment % Sh::kQ], uint32_t(segment / Sh::kQ) & 1u)) return false;
+        if (n >= 2 && !mbar_test(&sh.free_s[n & 1], uint32_t((n >> 1) - 1) & 1u)) return false;
         known = false;
         fence_after();
         constexpr uint32_t high = operand8_high(8 * D);
-        const uint32_t d = tmem + ((step & 1) * Sh::TT + half) * Sh::kScoreCols, k = operand8(smem_u32(sh.k[s]), 128);
+        const uint32_t d = tmem + (n & 1) * Sh::kScoreCols, k = operand8(smem_u32(sh.k[s]), 128);
         uint32_t q = operand8(smem_u32(sh.q[segment % Sh::kQ].part), 128);
         if constexpr (Sh::kStackQ) {
             const uint32_t kind = kind8(NR, false) + uint32_t((nq - 1) * NR / 8) * (1u << 17);
@@ -373,54 +366,41 @@ __device__ __forceinline__ void issue_products8(const Att8Args &a, Att8Shared<D,
                 }
         }
         wide_commit(&sh.empty_k[s]);
-        ++ns;
-        if (Sh::TT == 2 && half == 0 && !(flags & kLast8)) {
-            half = 1;
-            return true;
-        }
-        pairs = (pairs & ~(1u << (step & 3))) | uint32_t(half) << (step & 3);
-        wide_commit(&sh.full_s[step & 1]);
+        wide_commit(&sh.full_s[n & 1]);
         if (flags & kLast8) wide_commit(&sh.free_q[segment % Sh::kQ]);
-        ++step, half = 0;
         return true;
     };
-    auto products = [&] {
-        const bool two_units = Sh::TT == 2 && (pairs >> (done & 3) & 1u);
-        const int s = np % kValues, s2 = (np + 1) % kValues;
-        if (!mbar_test(&sh.full_w[done & 1], uint32_t(done >> 1) & 1u) || !mbar_test(&sh.full_v[s], uint32_t(np / kValues) & 1u)) return false;
-        if (two_units && !mbar_test(&sh.full_v[s2], uint32_t((np + 1) / kValues) & 1u)) return false;
-        if (done >= 2 && !mbar_test(&sh.free_o[done & 1], uint32_t((done >> 1) - 1) & 1u)) return false;
+    auto products = [&](int n) {
+        const int s = n % kValues;
+        if (!mbar_test(&sh.full_w[n & 1], uint32_t(n >> 1) & 1u) || !mbar_test(&sh.full_v[s], uint32_t(n / kValues) & 1u)) return false;
+        if (n >= 2 && !mbar_test(&sh.free_o[n & 1], uint32_t((n >> 1) - 1) & 1u)) return false;
         fence_after();
         constexpr int parts = Sh::kStackP ? 1 : NP, cols = Sh::kStackP ? NP * NR : NR;
-        const uint32_t d = tmem + 2 * Sh::TT * Sh::kScoreCols + (done & 1) * Sh::kOutCols;
-        const uint32_t w = operand8(smem_u32(sh.w[done % Sh::kP]), 128);
-        auto unit = [&](int place, uint32_t w, bool first) {
-            const uint32_t v = operand8(smem_u32(sh.v[place]), 8 * D);
+        const uint32_t d = tmem + 2 * Sh::kScoreCols + (n & 1) * Sh::kOutCols;
+        const uint32_t v = operand8(smem_u32(sh.v[s]), 8 * D), w = operand8(smem_u32(sh.w[n % Sh::kP]), 128);
 #pragma unroll
-            for (int mb = 0; mb < MB; ++mb)
+        for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-                for (int p = 0; p < parts; ++p)
+            for (int p = 0; p < parts; ++p)
 #pragma unroll
-                    for (int i = 0; i < kTile8 / 32; ++i)
-                        mma8(d + mb * Sh::kOutEach, v + mb * 64 + i * 2 * D, operand8_high(128), w + p * NR * kTile8 / 16 + i * 32, operand8_high(2048),
-                             kind8(cols, true), !first || p > 0 || i > 0);
-            wide_commit(&sh.empty_v[place]);
-        };
-        unit(s, w, true);
-        if (two_units) unit(s2, w + NP * NR * kTile8 / 16, false);
-        wide_commit(&sh.full_o[done & 1]);
-        np += two_units ? 2 : 1, ++done;
+                for (int i = 0; i < kTile8 / 32; ++i)
+                    mma8(d + mb * Sh::kOutEach, v + mb * 64 + i * 2 * D, operand8_high(128), w + p * NR * kTile8 / 16 + i * 32, operand8_high(2048),
+                         kind8(cols, true), p > 0 || i > 0);
+        wide_commit(&sh.empty_v[s]);
+        wide_commit(&sh.full_o[n & 1]);
         return true;
     };
     Patience patience;
-    while (np < units) {
-        if ((done < step && products()) || (ns < units && scores())) {
-            patience.reset();
+    for (int ns = 0, np = 0; np < units;) {
+        if (np < ns && products(np)) {
+            ++np, patience.reset();
+        } else if (ns < units && scores(ns)) {
+            ++ns, patience.reset();
         } else if (!patience.go_on()) {  // nothing more is issued; the other warps' waits give up too
             atomicExch(a.status, int(SV_ERR_TIMEOUT));
             break;
-        } else if (done < step) {  // asleep until what comes next is likely there
-            mbar_doze(&sh.full_w[done & 1], uint32_t(done >> 1) & 1u);
+        } else if (np < ns) {  // asleep until what comes next is likely there
+            mbar_doze(&sh.full_w[np & 1], uint32_t(np >> 1) & 1u);
         } else {
             mbar_doze(&sh.full_k[ns % kStages], uint32_t(ns / kStages) & 1u);
         }
@@ -512,7 +492,7 @@ __global__ void __launch_bounds__(kQueryThreads8) kv8_queries_kernel(const Att8A
 template <int D, int NR, int NP>
 __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_attention_kernel(const Att8Args a) {
     using Sh = Att8Shared<D, NR, NP>;
-    constexpr int W = Sh::W, RW = Sh::RW, MB = Sh::MB, TT = Sh::TT, kValues = Sh::kValues;
+    constexpr int W = Sh::W, RW = Sh::RW, MB = Sh::MB, kValues = Sh::kValues;
     extern __shared__ unsigned char raw0[];
     unsigned char *raw = raw0 + ((128 - (smem_u32(raw0) & 127)) & 127);
     Sh &sh = *reinterpret_cast<Sh *>(raw);
@@ -556,7 +536,7 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
         const int wg = (warp - 2) / 4, quarter = warp & 3, nq = a.nq, token = quarter * 32 + lane;
         const int r0 = wg * RW;  // the group's first row
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
-        const uint32_t tmem_s = sh.tmem + lanes + r0, tmem_o = sh.tmem + lanes + 2 * TT * Sh::kScoreCols + r0;
+        const uint32_t tmem_s = sh.tmem + lanes + r0, tmem_o = sh.tmem + lanes + 2 * Sh::kScoreCols + r0;
         const bool writes = D >= 128 || quarter < 2;  // has a dimension
         int granule_log2 = 4;
         while (1 << granule_log2 < a.granule) ++granule_log2;
@@ -577,7 +557,7 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
         int seg_lo = 0, segment = -1, live = 0;  // live: rows of this group
         Two l[RW / 2], acc[MB][RW / 2];
         float M = -INFINITY;  // of row lane % 16 of the group
-        // the output of step n, which is of the segment at hand
+        // the output of unit n, which is of the segment at hand
         auto take_up = [&](int n) {
             wait(&sh.full_o[n & 1], uint32_t(n >> 1) & 1u);
             if (failed) return;
@@ -616,17 +596,15 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
             if (lane == 0) mbar_arrive(smem_u32(&sh.free_o[n & 1]));
         };
 
-        // A step takes unit n, and the next one too if TT is 2 and the segment goes on.
-        for (int n = 0, i = 0; n < units; ++i) {
+        for (int n = 0; n < units; ++n) {
+            const Info8 &in = sh.info[n % Sh::kInfos];
             wait(&sh.full_i[n % Sh::kInfos], uint32_t(n / Sh::kInfos) & 1u);
-            int flags = 0, count = 1;
-            float t[TT][RW], inv[TT];  // inv: 1 / s', 0: not there
-#pragma unroll
-            for (int h = 0; h < TT; ++h) inv[h] = 0.f;
+            int flags = 0;
+            float t[RW], inv = 0.f;  // inv: 1 / s', 0: not there
             if (!failed) {
-                flags = sh.info[n % Sh::kInfos].unit.masked;
+                flags = in.unit.masked;
                 if (flags & kFirst8) {
-                    seg = sh.info[n % Sh::kInfos].unit;
+                    seg = in.unit;
                     ++segment;
                     seg_lo = ubegin + n - seg.tile;
                     live = min(max(seg.fresh * a.G - seg.rt * NR - r0, 0), RW);
@@ -635,107 +613,82 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                     for (int j = 0; j < RW / 2; ++j) l[j] = acc[0][j] = acc[MB - 1][j] = 0;
                     wait(&sh.full_q[segment % Sh::kQ], uint32_t(segment / Sh::kQ) & 1u);
                 }
-                if (TT == 2 && !(flags & kLast8)) {
-                    wait(&sh.full_i[(n + 1) % Sh::kInfos], uint32_t((n + 1) / Sh::kInfos) & 1u);
-                    if (!failed) {
-                        count = 2;
-                        flags |= sh.info[(n + 1) % Sh::kInfos].unit.masked & (kLast8 | kMasked8 | kRagged8);
-                    }
-                }
-                // the scale of this thread's tokens, and the rows that see them
+                // the scale of this thread's token, and the rows that see it
                 const int at = segment % Sh::kQ;
-                float ks[TT], log2vs[TT];
-                uint32_t see[TT];
-#pragma unroll
-                for (int h = 0; h < TT; ++h) {
-                    const Info8 &in = sh.info[(n + h) % Sh::kInfos];
-                    bool there = h < count;
-                    see[h] = there ? 0xFFFFu : 0u;
-                    if ((flags & kMasked8) && there) {
-                        const int j = in.unit.tile * kTile8 + token, x = j - seg.before;  // among the new tokens
-                        there = j < seg.len && (in.unit.have >> (token >> granule_log2) & 1u);
-                        see[h] = there ? (1u << live) - 1 : 0u;
-                        if (there && x >= 0) {
-                            if (a.parent) {
-                                see[h] &= __ldcg(a.see + (int64_t(seg.rt) * a.T + x) * Sh::SW + wg / 2) >> (16 * (wg & 1));
-                            } else {
-                                see[h] &= 0xFFFFu << min(max(x * a.G - seg.rt * NR - r0, 0), 16);  // not the rows of earlier tokens
-                            }
+                float ks = 0.f, log2vs = 0.f;
+                uint32_t see = 0xFFFFu;
+                bool there = true;
+                if (flags & kMasked8) {
+                    const int j = in.unit.tile * kTile8 + token, x = j - seg.before;  // among the new tokens
+                    there = j < seg.len && (in.unit.have >> (token >> granule_log2) & 1u);
+                    see = there ? (1u << live) - 1 : 0u;
+                    if (there && x >= 0) {
+                        if (a.parent) {
+                            see &= __ldcg(a.see + (int64_t(seg.rt) * a.T + x) * Sh::SW + wg / 2) >> (16 * (wg & 1));
+                        } else {
+                            see &= 0xFFFFu << min(max(x * a.G - seg.rt * NR - r0, 0), 16);  // not the rows of earlier tokens
                         }
                     }
-                    ks[h] = log2vs[h] = 0.f;
-                    if (there) {
-                        const uint2 word = *reinterpret_cast<const uint2 *>(in.word[token / kKv8Block]);
-                        const int e = kv8_exponent(word.y);
-                        ks[h] = (word.x | word.y) >> (token & 15) & 1u ? NAN : __uint_as_float(word.x & 0xFFFF0000u);
-                        log2vs[h] = float(e), inv[h] = kv8_power(-e);
-                    }
                 }
-                if (flags & kRagged8) {
-                    wait(&sh.full_v[n % kValues], uint32_t(n / kValues) & 1u);
-                    if (count > 1) wait(&sh.full_v[(n + 1) % kValues], uint32_t((n + 1) / kValues) & 1u);
+                if (there) {
+                    const uint2 word = *reinterpret_cast<const uint2 *>(in.word[token / kKv8Block]);
+                    const int e = kv8_exponent(word.y);
+                    ks = (word.x | word.y) >> (token & 15) & 1u ? NAN : __uint_as_float(word.x & 0xFFFF0000u);
+                    log2vs = float(e), inv = kv8_power(-e);
                 }
-                wait(&sh.full_s[i & 1], uint32_t(i >> 1) & 1u);
+                if (flags & kRagged8) wait(&sh.full_v[n % kValues], uint32_t(n / kValues) & 1u);
+                wait(&sh.full_s[n & 1], uint32_t(n >> 1) & 1u);
                 fence_after();
-                const uint32_t s_at = tmem_s + (i & 1) * TT * Sh::kScoreCols;
+                const Two ks2 = two(ks, ks), vs2 = two(log2vs, log2vs);
+                const uint32_t s_at = tmem_s + (n & 1) * Sh::kScoreCols;
                 constexpr int parts = Sh::kStackQ ? 3 : 1;
 #pragma unroll
                 for (int c = 0; c < RW / 8; ++c) {
                     if (8 * c >= live) continue;
-                    float x[TT][parts][8], most[8];
-#pragma unroll
-                    for (int h = 0; h < TT; ++h) {  // (of a second unit that is not there: what lies in its place, and is not used)
-                        tmem_get8(x[h][0], s_at + h * Sh::kScoreCols + 8 * c);
-                        if constexpr (parts > 1) {
-                            tmem_get8(x[h][1], s_at + h * Sh::kScoreCols + NR + 8 * c);
-                            tmem_get8(x[h][2], s_at + h * Sh::kScoreCols + (nq > 2 ? 2 * NR : NR) + 8 * c);
-                        }
+                    float x[parts][8], most[8];
+                    tmem_get8(x[0], s_at + 8 * c);
+                    if constexpr (parts > 1) {
+                        tmem_get8(x[1], s_at + NR + 8 * c);
+                        tmem_get8(x[2], s_at + (nq > 2 ? 2 * NR : NR) + 8 * c);
                     }
                     tmem_loaded();
 #pragma unroll
-                    for (int h = 0; h < TT; ++h)
-#pragma unroll
-                        for (int p = 0; p < parts; ++p) tmem_here(x[h][p]);
+                    for (int p = 0; p < parts; ++p) tmem_here(x[p]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float2 f = *reinterpret_cast<const float2 *>(&sh.q[at].factor[r0 + 8 * c + 2 * j]);
-#pragma unroll
-                        for (int h = 0; h < TT; ++h) {
-                            Two y = two(x[h][0][2 * j], x[h][0][2 * j + 1]);
-                            if constexpr (parts > 1) {
-                                const Two z = two(x[h][1][2 * j], x[h][1][2 * j + 1]);
-                                y = add2(y, nq > 2 ? add2(z, two(x[h][2][2 * j], x[h][2][2 * j + 1])) : z);
-                            }
-                            const float2 u = split(fma2(mul2(y, two(f.x, f.y)), two(ks[h], ks[h]), two(log2vs[h], log2vs[h])));
-                            t[h][8 * c + 2 * j] = u.x, t[h][8 * c + 2 * j + 1] = u.y;
+                        Two y = two(x[0][2 * j], x[0][2 * j + 1]);
+                        if constexpr (parts > 1) {
+                            const Two z = two(x[1][2 * j], x[1][2 * j + 1]);
+                            y = add2(y, nq > 2 ? add2(z, two(x[2][2 * j], x[2][2 * j + 1])) : z);
                         }
+                        const float2 u = split(fma2(mul2(y, two(f.x, f.y)), ks2, vs2));
+                        t[8 * c + 2 * j] = u.x, t[8 * c + 2 * j + 1] = u.y;
                     }
-                    if ((flags & kMasked8) || count < TT) {
+                    if (flags & kMasked8) {
 #pragma unroll
-                        for (int h = 0; h < TT; ++h)
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (!(see[h] >> (8 * c + j) & 1u)) t[h][8 * c + j] = -INFINITY;
+                        for (int j = 0; j < 8; ++j)
+                            if (!(see >> (8 * c + j) & 1u)) t[8 * c + j] = -INFINITY;
                         __syncwarp();
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) most[j] = warp_largest(TT == 2 ? fmaxf(t[0][8 * c + j], t[TT - 1][8 * c + j]) : t[0][8 * c + j]);
+                    for (int j = 0; j < 8; ++j) most[j] = warp_largest(t[8 * c + j]);
                     if (lane == 0) {
-                        float4 *to = reinterpret_cast<float4 *>(&sh.red[wg][i & 1][quarter][8 * c]);
+                        float4 *to = reinterpret_cast<float4 *>(&sh.red[wg][n & 1][quarter][8 * c]);
                         to[0] = make_float4(most[0], most[1], most[2], most[3]), to[1] = make_float4(most[4], most[5], most[6], most[7]);
                     }
                 }
                 fence_before();
                 __syncwarp();
-                if (lane == 0) {  // the scores and what is known of the units are read
-                    mbar_arrive(smem_u32(&sh.free_s[i & 1]));
+                if (lane == 0) {  // the scores and what is known of the unit are read
+                    mbar_arrive(smem_u32(&sh.free_s[n & 1]));
                     if (flags & kLast8) mbar_arrive(smem_u32(&sh.free_q[at]));
                 }
             }
             if (any(failed)) break;
             {  // each warp for itself: m, and what it makes of M (lane: row)
                 const int row = lane & 15;
-                const float(*red)[RW] = sh.red[wg][i & 1];
+                const float(*red)[RW] = sh.red[wg][n & 1];
                 const float m = fmaxf(fmaxf(red[0][row], red[1][row]), fmaxf(red[2][row], red[3][row]));
                 const float whole = rintf(m);
                 float f = 1.f, g = 1.f, minus = m == INFINITY ? -INFINITY : 0.f;
@@ -745,10 +698,10 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                     f = ex2(fmaxf(whole - M, -127.f));
                     minus = float(kKv8Top) - whole;
                 }
-                float *mv = reinterpret_cast<float *>(&sh.move[wg][quarter][i & 1][row / 2]);
+                float *mv = reinterpret_cast<float *>(&sh.move[wg][quarter][n & 1][row / 2]);
                 if (lane < 16) mv[row & 1] = minus, mv[2 + (row & 1)] = f;
-                if (__any_sync(0xFFFFFFFFu, g != 1.f)) {  // (rare; the last step's output, not taken up yet, is to move too)
-                    if (lane < 16) reinterpret_cast<float *>(&sh.move[wg][quarter][(i & 1) ^ 1][row / 2])[2 + (row & 1)] *= g;
+                if (__any_sync(0xFFFFFFFFu, g != 1.f)) {  // (rare; the last unit's output, not taken up yet, is to move too)
+                    if (lane < 16) reinterpret_cast<float *>(&sh.move[wg][quarter][(n & 1) ^ 1][row / 2])[2 + (row & 1)] *= g;
 #pragma unroll
                     for (int j = 0; j < RW / 2; ++j) {
                         const Two g2 = two(__shfl_sync(0xFFFFFFFFu, g, 2 * j), __shfl_sync(0xFFFFFFFFu, g, 2 * j + 1));
@@ -760,57 +713,45 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                 __syncwarp();
             }
             // the weights
-            uint32_t code[TT][NP][4];
+            uint32_t code[NP][4];
+            const Two inv2 = two(inv, inv);
 #pragma unroll
             for (int c = 0; c < RW / 8; ++c) {
 #pragma unroll
-                for (int h = 0; h < TT; ++h)
-#pragma unroll
-                    for (int k = 0; k < NP; ++k) code[h][k][2 * c] = code[h][k][2 * c + 1] = 0;
+                for (int k = 0; k < NP; ++k) code[k][2 * c] = code[k][2 * c + 1] = 0;
                 if (8 * c >= live) continue;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float4 mv = sh.move[wg][quarter][i & 1][4 * c + j];
-                    Two sum = 0;
+                    const float4 mv = sh.move[wg][quarter][n & 1][4 * c + j];
+                    const float2 x = split(add2(two(t[8 * c + 2 * j], t[8 * c + 2 * j + 1]), two(mv.x, mv.y)));
+                    const float w0 = ex2(x.x), w1 = ex2(x.y);
+                    l[4 * c + j] = fma2(mul2(two(w0, w1), inv2), two(mv.z, mv.w), l[4 * c + j]);
+                    uint32_t p[NP];
+                    parts8(w0, w1, p);
 #pragma unroll
-                    for (int h = 0; h < TT; ++h) {
-                        const float2 x = split(add2(two(t[h][8 * c + 2 * j], t[h][8 * c + 2 * j + 1]), two(mv.x, mv.y)));
-                        const float w0 = ex2(x.x), w1 = ex2(x.y);
-                        sum = h ? fma2(two(w0, w1), two(inv[h], inv[h]), sum) : mul2(two(w0, w1), two(inv[h], inv[h]));
-                        uint32_t p[NP];
-                        parts8(w0, w1, p);
-#pragma unroll
-                        for (int k = 0; k < NP; ++k) code[h][k][2 * c + j / 2] |= p[k] << (16 * (j & 1));
-                    }
-                    l[4 * c + j] = fma2(sum, two(mv.z, mv.w), l[4 * c + j]);
+                    for (int k = 0; k < NP; ++k) code[k][2 * c + j / 2] |= p[k] << (16 * (j & 1));
                 }
             }
             const bool first = (flags & kFirst8) != 0, last = (flags & kLast8) != 0;
-            if (Sh::kP == 1 && !first) wait(&sh.full_o[(i & 1) ^ 1], uint32_t((i - 1) >> 1) & 1u);  // its weights are in this place
+            if (Sh::kP == 1 && !first) wait(&sh.full_o[(n & 1) ^ 1], uint32_t((n - 1) >> 1) & 1u);  // its weights are in this place
             if (!failed) {
-                uint8_t *to = sh.w[i % Sh::kP] + wg * 2048 + token * 16;
+                uint8_t *to = sh.w[n % Sh::kP] + wg * 2048 + token * 16;
+                if (live > 0) {
 #pragma unroll
-                for (int h = 0; h < TT; ++h) {
-                    if (h >= count) continue;
-                    if (live > 0) {
+                    for (int k = 0; k < NP; ++k) *reinterpret_cast<uint4 *>(to + k * NR * kTile8) = make_uint4(code[k][0], code[k][1], code[k][2], code[k][3]);
+                }
+                if ((flags & kRagged8) && wg == 0 && inv == 0.f) {  // a code that is not there may be a NaN, which no weight of 0 takes away
+                    uint8_t *v = sh.v[n % kValues];
 #pragma unroll
-                        for (int k = 0; k < NP; ++k)
-                            *reinterpret_cast<uint4 *>(to + (h * NP + k) * NR * kTile8) = make_uint4(code[h][k][0], code[h][k][1], code[h][k][2], code[h][k][3]);
-                    }
-                    if ((flags & kRagged8) && wg == 0 && inv[h] == 0.f) {  // a code that is not there may be a NaN, which no weight of 0 takes away
-                        uint8_t *v = sh.v[(n + h) % kValues];
-#pragma unroll
-                        for (int j = 0; j < D / 16; ++j) *reinterpret_cast<uint4 *>(v + kv8_code_byte(D, token, 16 * j)) = make_uint4(0, 0, 0, 0);
-                    }
+                    for (int j = 0; j < D / 16; ++j) *reinterpret_cast<uint4 *>(v + kv8_code_byte(D, token, 16 * j)) = make_uint4(0, 0, 0, 0);
                 }
             }
             fence_operands();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.full_w[i & 1]));
-            n += count;
-            // the last step's output, and at the segment's end this one's
+            if (lane == 0) mbar_arrive(smem_u32(&sh.full_w[n & 1]));
+            // the last unit's output, and at the segment's end this one's
 #pragma unroll 1
-            for (int j = first ? i : i - 1; j <= (last ? i : i - 1); ++j) take_up(j);
+            for (int j = first ? n : n - 1; j <= (last ? n : n - 1); ++j) take_up(j);
             if (!last) continue;
 
             // the segment's end

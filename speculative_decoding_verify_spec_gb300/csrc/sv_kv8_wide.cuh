@@ -251,15 +251,13 @@ __global__ void __launch_bounds__(kWideThreads8, 1) kv8_wide_kernel(const Att8Ar
                         const int e = kv8_exponent(word.y);
                         scale[b] = fmaxf(factor * __uint_as_float(word.x & 0xFFFF0000u), 1.2e-38f), shift[b] = float(e), inv[b] = kv8_power(-e);
                         const uint32_t bad = (word.x | word.y) & 0xFFFFu;
-                        if (bad) {  // (of the whole warp; rare)
+                        if ((flags & kMasked8) || bad) {  // (the same for the whole warp)
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
+                            for (int j = 0; j < 16; ++j) {
                                 if (bad >> j & 1u) s[16 * b + j] = NAN;
-                        }
-                        if (flags & kMasked8) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
                                 if (!(see >> (16 * b + j) & 1u)) s[16 * b + j] = -INFINITY;
+                            }
+                            __syncwarp();  // (a branch, not 64 selections in every unit)
                         }
                         float top = s[16 * b];
 #pragma unroll
