@@ -1,11 +1,11 @@
 // sv_kv8_append.cu -- the new tokens' keys and values into the 8-bit paged cache, the position rotation of the keys
 // applied on the way.
 //
-// A block of 16 slots has one scale, so a warp takes a block of one sequence and head, its keys or its values: it loads
-// the new tokens' vectors, rotates keys, reduces the largest magnitude over the warp, and from it has the scale (a power of two) and the
-// codes; the block's older codes are read only if the scale grows.  Lane l has slot l % 8 of a group of eight, and pairs of
-// 16-dimension pieces: a piece of eight slots is 128 contiguous bytes of the cache, and the two pieces of a pair are those
-// that the rotation joins, so that an angle is loaded once for both.
+// A block of 16 slots has one scale, so D / 64 warps take a block of one sequence and head, its keys or its values: they load
+// the new tokens' vectors, rotate keys, reduce the largest magnitude, and from it have the scale (a power of two) and the
+// codes; the block's older codes are read only if the scale grows.  A lane has a slot and two pieces of 16 dimensions: a piece of eight
+// slots is 128 contiguous bytes of the cache, and the two pieces are those that the rotation joins, so that an angle is loaded
+// once for both.  The rotated numbers stay in registers from the reduction to the codes.
 //
 // The result is that of the exact rule.  fp32 leaves a rotated key off by at most 2^-23 (|a cos| + |b sin|), and with D the
 // largest such bound of the block, a scale or a code is settled if x - D and x + D have the same one.  What is left (a code in
@@ -157,15 +157,13 @@ __device__ __noinline__ uint32_t code_exactly(double x) {
 
 template <int D, Layout8 kLayout, bool kBF16>
 __global__ void __launch_bounds__(kApp8Threads) kv8_append_kernel(const Append8Args a) {
-    // passes over (group of eight slots, unit of two pieces): four groups-of-lanes at a time
-    constexpr int U = D / 32, N = D / 32;  // units a row; passes: 2 groups x U units / 4 lanes' worth x 2
-    constexpr int kPass = 2 * U / 4;
-    static_assert(kPass >= 1 && N >= kPass, "");
-    const uint32_t item = blockIdx.x * (kApp8Threads / 32) + threadIdx.x / 32;
-    const int lane = threadIdx.x & 31;
+    constexpr int W = D / 64, kItems = kApp8Threads / 32 / W;  // warps of a block of slots, and those blocks of a thread block
+    __shared__ uint32_t red[kItems][2][W], bad_s[kItems];
+    __shared__ int e_s[kItems];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, part = warp % W, mine = warp / W;
+    const uint32_t item0 = blockIdx.x * kItems + mine, item = item0 < a.items ? item0 : a.items - 1;
     griddep_launch_next();
     griddep_wait();
-    if (item >= a.items) return;
     const int values = int(item & 1u);
     const uint32_t bjh = item >> 1, bj = bjh / uint32_t(a.H), h = bjh - bj * uint32_t(a.H), b = bj / a.blocks;
     const int64_t capacity = int64_t(a.width) * a.page;
@@ -174,19 +172,40 @@ __global__ void __launch_bounds__(kApp8Threads) kv8_append_kernel(const Append8A
     const int64_t first = int64_t(before / kKv8Block) * kKv8Block + int64_t(bj - b * a.blocks) * kKv8Block;  // the block's first slot
     // the block's slots from `lo` on are tokens t0 + slot; those below `end` are new
     const int64_t t0 = first - before;
-    const int lo = t0 < 0 ? int(-t0) : 0;
+    const int lo = item0 < a.items ? (t0 < 0 ? int(-t0) : 0) : kKv8Block;  // (past the last item: nothing)
     const int end = int(fresh - t0 < 0 ? 0 : (fresh - t0 < kKv8Block ? fresh - t0 : kKv8Block));
     uint16_t *held = values ? a.v_values : a.k_values;
-    if (end <= lo && (!held || t0 + lo >= a.T)) return;
     const uint16_t *in = values ? a.v + b * a.v_bs + h * a.v_hs : a.k + b * a.k_bs + h * a.k_hs;
-    const int64_t ts = values ? a.v_ts : a.k_ts;
     Rotation rot = a.rot;
-    if (values) rot.cos = nullptr;
+    if (values) rot.cos = nullptr, rot.pairs = 0;
     int pg = -1, s0 = 0;  // page, and the block's first slot in it
     if (first < capacity && end > lo) {
         const uint32_t pi = uint32_t(first) / uint32_t(a.page);
         s0 = int(uint32_t(first) - pi * uint32_t(a.page));
         pg = __ldg(a.table + int64_t(b) * a.width + pi);
+    }
+    // this lane's slot and its two pieces of the row
+    const int slot = D == 64 ? lane & 15 : (lane & 7) + (part & 1) * 8;
+    const int unit = D == 64 ? lane >> 4 : (lane >> 3) + part / 2 * 4;
+    int p, q;
+    pieces_of<D, kLayout>(rot.pairs, unit, p, q);
+    const int64_t t = t0 + slot;
+    const bool live = slot >= lo && slot < end;
+    const uint16_t *row = in + t * (values ? a.v_ts : a.k_ts);
+    float x[2][16], largest = 0.f, most = 0.f;
+    int64_t angles = 0;
+    bool fine = true;
+    if (live) {
+        uint32_t raw[2][8];
+        load_piece<kLayout>(row + p * 16, raw[0]), load_piece<kLayout>(row + q * 16, raw[1]);
+        if (rot.cos) angles = kv_rotation_row(rot, int64_t(b) * a.T + t, before, int(t));
+        rotated<kLayout, kBF16>(rot, row, angles, p, q, raw, x, most);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) largest = fmaxf(largest, fmaxf(fabsf(x[0][j]), fabsf(x[1][j])));
+        float sum = 0.f;  // finite if every number is
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum += fabsf(x[0][j]) * 0.f + fabsf(x[1][j]) * 0.f;
+        fine = sum == 0.f && most < INFINITY;
     }
     const bool here = pg >= 0 && pg < a.num_pages && SV_IN(kv8_code_byte(D, s0 + kKv8Block - 1, D - 1), a.page * D);
     uint8_t *base = here ? a.cache + (int64_t(pg) * a.H + h) * kv8_page_bytes(a.page, D) : nullptr;
@@ -195,93 +214,56 @@ __global__ void __launch_bounds__(kApp8Threads) kv8_append_kernel(const Append8A
     uint32_t old = 0;
     if (here && lo > 0) old = __ldcg(word);
 
-    // this lane's places: pass i has slot of a group and unit of a row
-    auto slot_of = [&](int i) { return D == 64 ? lane & 15 : (lane & 7) + (i / (kPass / 2 > 0 ? kPass / 2 : 1)) * 8; };
-    auto unit_of = [&](int i) { return D == 64 ? lane >> 4 : (lane >> 3) + i % (kPass / 2 > 0 ? kPass / 2 : 1) * 4; };
-    uint32_t raw[kPass][2][8];
-    float largest = 0.f, most = 0.f;
-    bool fine = true;
-#pragma unroll
-    for (int i = 0; i < kPass; ++i) {
-        const int slot = slot_of(i);
-        const bool live = slot >= lo && slot < end;
-        int p, q;
-        pieces_of<D, kLayout>(rot.cos ? rot.pairs : 0, unit_of(i), p, q);
-        if (live) {
-            const uint16_t *row = in + (t0 + slot) * ts;
-            load_piece<kLayout>(row + p * 16, raw[i][0]), load_piece<kLayout>(row + q * 16, raw[i][1]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) raw[i][0][j] = raw[i][1][j] = 0;
-        }
+    uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(largest)), bound = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
+    if (W > 1) {
+        if (lane == 0) red[mine][0][part] = top, red[mine][1][part] = bound;
     }
+    if (threadIdx.x < kItems) bad_s[threadIdx.x] = 0, e_s[threadIdx.x] = -1022;
+    const bool odd = __syncthreads_or(!fine);  // (some number here is not finite, or not in 32 bits: all in 64)
+    if (W > 1) {
 #pragma unroll
-    for (int i = 0; i < kPass; ++i) {
-        const int slot = slot_of(i);
-        if (slot < lo || slot >= end) continue;
-        int p, q;
-        pieces_of<D, kLayout>(rot.cos ? rot.pairs : 0, unit_of(i), p, q);
-        const int64_t t = t0 + slot;
-        float x[2][16];
-        rotated<kLayout, kBF16>(rot, in + t * ts, rot.cos ? kv_rotation_row(rot, int64_t(b) * a.T + t, before, int(t)) : 0, p, q, raw[i], x, most);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            largest = fmaxf(largest, fmaxf(fabsf(x[0][j]), fabsf(x[1][j])));
-            fine &= fabsf(x[0][j]) < INFINITY && fabsf(x[1][j]) < INFINITY;
-        }
+        for (int i = 0; i < W; ++i) top = max(top, red[mine][0][i]), bound = max(bound, red[mine][1][i]);
     }
-    largest = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(largest)));
-    most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)));
-    const float off = most * 2.4e-7f;  // 2^-22 and a little: two roundings, and those of the sums that make `most`
-    int e = ceil_exponent(fmaxf(largest - off, 0.f));
+    const float off = __uint_as_float(bound) * 2.4e-7f;  // 2^-22 and a little: two roundings, and those of the sums that make `most`
+    int e = ceil_exponent(fmaxf(__uint_as_float(top) - off, 0.f));
     uint32_t bad = 0;  // slots with a NaN or an infinity
-    const bool odd = !__all_sync(0xFFFFFFFFu, fine && most < INFINITY);
-    if (odd || e != ceil_exponent(largest + off)) {
+    if (__syncthreads_or(odd || e != ceil_exponent(__uint_as_float(top) + off))) {
         // in 64 bits: first which vectors are to be left out, then the largest magnitude of the others
         for (int round = 0; round < 2; ++round) {
             e = -1022;
+            if (live && !(bad >> slot & 1u)) {
+                bool out = false;
 #pragma unroll 1
-            for (int i = 0; i < kPass; ++i) {
-                const int slot = slot_of(i);
-                if (slot < lo || slot >= end || (bad >> slot & 1u)) continue;
-                int p, q;
-                pieces_of<D, kLayout>(rot.cos ? rot.pairs : 0, unit_of(i), p, q);
-                const int64_t t = t0 + slot, angles = rot.cos ? kv_rotation_row(rot, int64_t(b) * a.T + t, before, int(t)) : 0;
                 for (int j = 0; j < 32; ++j) {
-                    const double x = rotated_exactly<kBF16>(rot, in + t * ts, angles, (j < 16 ? p : q) * 16 + j % 16);
-                    if (!(fabs(x) < INFINITY)) bad |= 1u << slot;
-                    else e = max(e, ceil_exponent(x));
+                    const double y = rotated_exactly<kBF16>(rot, row, angles, (j < 16 ? p : q) * 16 + j % 16);
+                    if (!(fabs(y) < INFINITY)) out = true;
+                    else e = max(e, ceil_exponent(y));
                 }
+                if (out) atomicOr(&bad_s[mine], 1u << slot);
+                if (round == 1) atomicMax(&e_s[mine], e);
             }
-            bad = __reduce_or_sync(0xFFFFFFFFu, bad);
+            __syncthreads();
+            bad = bad_s[mine];
         }
-        e = __reduce_max_sync(0xFFFFFFFFu, e);
+        e = e_s[mine];
     }
     e = min(max(e - kKv8Top, kKv8Least), kKv8Most);
     if (here && lo > 0) e = max(e, kv8_exponent(old));
     const float inv = kv8_power(-e), scale = kv8_power(e), doff = off * inv;
 
+    if (slot >= lo && t < a.T) {
+        const bool nan = bad >> slot & 1u;
 #pragma unroll
-    for (int i = 0; i < kPass; ++i) {
-        const int slot = slot_of(i);
-        const int64_t t = t0 + slot;
-        if (slot < lo || t >= a.T) continue;
-        int p, q;
-        pieces_of<D, kLayout>(rot.cos ? rot.pairs : 0, unit_of(i), p, q);
-        const bool live = slot < end, nan = bad >> slot & 1u;
-        uint32_t c[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-        if (live && !nan) {
-            float x[2][16], unused = 0.f;
-            const int64_t angles = rot.cos ? kv_rotation_row(rot, int64_t(b) * a.T + t, before, int(t)) : 0;
-            rotated<kLayout, kBF16>(rot, in + t * ts, angles, p, q, raw[i], x, unused);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 2; ++k) {
+            uint32_t c[4] = {0, 0, 0, 0};
+            const int piece = k ? q : p;
+            if (live && !nan) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float y[4];
 #pragma unroll
                     for (int n = 0; n < 4; ++n) y[n] = x[k][4 * j + n] * inv;
-                    const int d = (k ? q : p) * 16 + 4 * j;
+                    const int d = piece * 16 + 4 * j;
                     const bool turned = rot.cos && d < 2 * rot.pairs;
                     const float o = turned ? doff : 0.f;
                     uint32_t w = kv8_codes(y[0] - o, y[1] - o) | kv8_codes(y[2] - o, y[3] - o) << 16;
@@ -289,34 +271,29 @@ __global__ void __launch_bounds__(kApp8Threads) kv8_append_kernel(const Append8A
                         const uint32_t u = kv8_codes(y[0] + o, y[1] + o) | kv8_codes(y[2] + o, y[3] + o) << 16;
                         if (w != u || odd) {
                             uint32_t r = 0;
+#pragma unroll 1
                             for (int n = 0; n < 4; ++n) {
-                                uint32_t c = w >> (8 * n) & 255u;
-                                if (odd || c != (u >> (8 * n) & 255u))
-                                    c = code_exactly(rotated_exactly<kBF16>(rot, in + t * ts, angles, d + n) * double(inv));
-                                r |= c << (8 * n);
+                                uint32_t one = w >> (8 * n) & 255u;
+                                if (odd || one != (u >> (8 * n) & 255u))
+                                    one = code_exactly(rotated_exactly<kBF16>(rot, row, angles, d + n) * double(inv));
+                                r |= one << (8 * n);
                             }
                             w = r;
                         }
                     }
-                    c[k][j] = kv8_no_minus_zero(w);
+                    c[j] = kv8_no_minus_zero(w);
                 }
-        }
-        if (live && here) {
-            *reinterpret_cast<uint4 *>(codes + kv8_code_byte(D, s0 + slot, p * 16)) = make_uint4(c[0][0], c[0][1], c[0][2], c[0][3]);
-            *reinterpret_cast<uint4 *>(codes + kv8_code_byte(D, s0 + slot, q * 16)) = make_uint4(c[1][0], c[1][1], c[1][2], c[1][3]);
-        }
-        if (held) {
-            uint16_t *dst = held + ((int64_t(b) * a.T + t) * a.H + h) * D;
-            const float s = nan ? NAN : scale;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            }
+            if (live && here) *reinterpret_cast<uint4 *>(codes + kv8_code_byte(D, s0 + slot, piece * 16)) = make_uint4(c[0], c[1], c[2], c[3]);
+            if (held) {
+                const float s = nan ? NAN : scale;
                 uint32_t o[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 u = kv8_numbers(c[k][j]), v = kv8_numbers(c[k][j] >> 16);
+                    const float2 u = kv8_numbers(c[j]), v = kv8_numbers(c[j] >> 16);
                     o[2 * j] = kv8_pack<kBF16>(u.x * s, u.y * s), o[2 * j + 1] = kv8_pack<kBF16>(v.x * s, v.y * s);
                 }
-                uint4 *to = reinterpret_cast<uint4 *>(dst + (k ? q : p) * 16);
+                uint4 *to = reinterpret_cast<uint4 *>(held + ((int64_t(b) * a.T + t) * a.H + h) * D + piece * 16);
                 to[0] = make_uint4(o[0], o[1], o[2], o[3]), to[1] = make_uint4(o[4], o[5], o[6], o[7]);
             }
         }
@@ -325,26 +302,27 @@ __global__ void __launch_bounds__(kApp8Threads) kv8_append_kernel(const Append8A
     if (lo > 0 && e > kv8_exponent(old)) {  // the older codes, to the new scale
         const float shrink = kv8_power(max(kv8_exponent(old) - e, -100));
 #pragma unroll 1
-        for (int i = lane; i < kKv8Block * (D / 16); i += 32) {
-            const int slot = i & 15, piece = i >> 4;
-            if (slot >= lo) continue;
-            uint4 *at = reinterpret_cast<uint4 *>(codes + kv8_code_byte(D, s0 + slot, piece * 16));
+        for (int i = part * 32 + lane; i < kKv8Block * (D / 16); i += 32 * W) {
+            const int sl = i & 15, piece = i >> 4;
+            if (sl >= lo) continue;
+            uint4 *at = reinterpret_cast<uint4 *>(codes + kv8_code_byte(D, s0 + sl, piece * 16));
             const uint4 was = __ldcg(at);
             uint32_t w[4] = {was.x, was.y, was.z, was.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 x = kv8_numbers(w[j]), y = kv8_numbers(w[j] >> 16);
-                w[j] = kv8_no_minus_zero(kv8_codes(x.x * shrink, x.y * shrink) | kv8_codes(y.x * shrink, y.y * shrink) << 16);
+                const float2 u = kv8_numbers(w[j]), v = kv8_numbers(w[j] >> 16);
+                w[j] = kv8_no_minus_zero(kv8_codes(u.x * shrink, u.y * shrink) | kv8_codes(v.x * shrink, v.y * shrink) << 16);
             }
             *at = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
-    if (lane == 0) *word = (__float_as_uint(scale) & 0xFFFF0000u) | (old & ((1u << lo) - 1)) | bad;
+    if (lane == 0 && part == 0) *word = (__float_as_uint(scale) & 0xFFFF0000u) | (old & ((1u << lo) - 1)) | bad;
 }
 
 template <int D>
 cudaError_t launch_append8(const Append8Args &a, Layout8 layout, bool bf16, cudaStream_t s) {
-    const unsigned blocks = (a.items + kApp8Threads / 32 - 1) / (kApp8Threads / 32);
+    constexpr unsigned kItems = kApp8Threads / 32 / (D / 64);
+    const unsigned blocks = (a.items + kItems - 1) / kItems;
     auto go = [&](auto kernel) { return launch_after(kernel, blocks, unsigned(kApp8Threads), 0, s, a); };
     switch (layout) {
     case kHalves8: return bf16 ? go(kv8_append_kernel<D, kHalves8, true>) : go(kv8_append_kernel<D, kHalves8, false>);
