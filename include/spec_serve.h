@@ -207,7 +207,7 @@ int64_t spec_kv8_code_offset(int page_size, int head_dim, int values, int token,
 int64_t spec_kv_code_offset(int page_size, int head_dim, int values, int token, int dim);
 
 /*
- * Test hook of the bounds-checked build: from now on no thread block of spec_kv_attention gets the
+ * Test hook of the bounds-checked build: from now on no thread block of spec_kv_attention or spec_kv8_attention gets the
  * unit-th piece of the cache (from 0) that it is to read, or any after it; -1: all do.  The waits for
  * them run out after a second each, the call ends with SV_ERR_TIMEOUT in its workspace, and its output
  * is of no use.  SV_ERR_UNSUPPORTED in the normal build.

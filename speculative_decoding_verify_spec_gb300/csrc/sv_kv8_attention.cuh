@@ -519,6 +519,8 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
         if (tid == 0) a.desc[cta] = AttDesc{0, 0, 0, 0, 0, 0, 0, 0};
         return;
     }
+    if (tid == 0)  // the share's first segment (at once: the join reads this whether or not a wait gives up)
+        a.desc[cta] = describe(total, cta, ncta, ubegin, ubegin - cur.tile, ubegin - cur.tile + cur.tiles(), cur.b, cur.h, cur.rt, cur.live ? cur.w.fresh : 0);
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "r"(Sh::kCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -799,8 +801,6 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                 }
                 if (++head == a.G) head = 0, ++node;
             }
-            if (tid == 64 && seg_lo <= ubegin)  // the share's first segment
-                a.desc[cta] = describe(total, cta, ncta, ubegin, seg_lo, seg_lo + seg.tiles, seg.b, seg.h, seg.rt, seg.fresh);
         }
     }
     __syncwarp();
