@@ -1,13 +1,13 @@
 """One speculative decoding loop, every step of it in the library's kernels but the matrix products.
 
 A toy two-layer model (random weights) decodes a batch greedily: prompt-lookup drafts from the
-history (spec_ngram_draft), the drafts' keys and values into the 4-bit paged cache with their
-rotation (spec_kv_append), their attention over it (spec_kv_attention), a repetition penalty and
-a mask of allowed tokens on the logits (spec_logit_adjust), and the verification
-(spec_verify_greedy).  A rejected draft needs no clean-up: the next step's tokens are appended
-over its slots.
+history (spec_ngram_draft), the drafts' keys and values into the paged cache held in 4 bits (or 8)
+with their rotation (spec_kv_append, spec_kv8_append), their attention over it (spec_kv_attention,
+spec_kv8_attention), a repetition penalty and a mask of allowed tokens on the logits
+(spec_logit_adjust), and the verification (spec_verify_greedy).  A rejected draft needs no
+clean-up: the next step's tokens are appended over its slots.
 
-    python examples/verify_step.py
+    python examples/verify_step.py [bits]
 """
 from __future__ import annotations
 
@@ -24,7 +24,11 @@ import speculative_decoding_verify_spec_gb300 as sv  # noqa: E402
 class Model:
     """Two layers of grouped-query attention over the paged cache, and an output head."""
 
-    def __init__(self, vocab=256, heads=8, kv_heads=2, head_dim=64, layers=2, max_len=512, batch=4, page=16, seed=0):
+    def __init__(self, vocab=256, heads=8, kv_heads=2, head_dim=64, layers=2, max_len=512, batch=4, page=16, seed=0, bits=4):
+        self.append, self.attention, page_bytes = {
+            4: (sv.spec_kv_append, sv.spec_kv_attention, sv.spec_kv_page_bytes),
+            8: (sv.spec_kv8_append, sv.spec_kv8_attention, sv.spec_kv8_page_bytes),
+        }[bits]
         g = torch.Generator(device="cuda").manual_seed(seed)
         width = heads * head_dim
         rand = lambda *s: (torch.randn(s, generator=g, device="cuda") * s[0] ** -0.5).to(torch.bfloat16)  # noqa: E731
@@ -35,7 +39,7 @@ class Model:
         self.cos, self.sin = angle.cos(), angle.sin()
         pages = max_len // page
         self.table = torch.randperm(batch * pages, generator=g, device="cuda").to(torch.int32).reshape(batch, pages)
-        size = sv.spec_kv_page_bytes(page, head_dim)
+        size = page_bytes(page, head_dim)
         self.caches = [torch.empty((batch * pages, kv_heads, size), dtype=torch.uint8, device="cuda") for _ in range(layers)]
 
     def __call__(self, tokens, start):
@@ -46,8 +50,8 @@ class Model:
         for (w_in, w_out), cache in zip(self.layers, self.caches):
             qkv = (x @ w_in).split([q, k, k], -1)
             qh, kh, vh = (t.unflatten(-1, (-1, self.head_dim)) for t in qkv)
-            sv.spec_kv_append(kh, vh, cache, self.table, start, **rotation)
-            x = x + sv.spec_kv_attention(qh, cache, self.table, start, **rotation).flatten(-2) @ w_out
+            self.append(kh, vh, cache, self.table, start, **rotation)
+            x = x + self.attention(qh, cache, self.table, start, **rotation).flatten(-2) @ w_out
         return x @ self.head
 
 
@@ -79,7 +83,7 @@ def decode(model, prompt, steps, gamma, repetition=1.2, allowed_words=None):
 
 
 def main():
-    model = Model()
+    model = Model(bits=int(sys.argv[1]) if len(sys.argv) > 1 else 4)
     prompt = torch.arange(12, dtype=torch.int32, device="cuda").repeat(4, 2) + 7 * torch.arange(4, dtype=torch.int32, device="cuda")[:, None]
     history, lengths = decode(model, prompt, steps=20, gamma=4)
     for row, n in zip(history.tolist(), lengths.tolist()):

@@ -85,7 +85,8 @@ def test_largest_tree(D, G, dtype, rope):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("D,T,G", [(64, 1, 8), (64, 64, 4), (128, 1, 4), (128, 9, 4), (128, 40, 2), (256, 1, 8), (256, 9, 4), (256, 20, 3)])
+@pytest.mark.parametrize("D,T,G", [(64, 1, 8), (64, 9, 4), (64, 16, 4), (64, 64, 4), (128, 1, 4), (128, 4, 5), (128, 9, 4), (128, 16, 4), (128, 40, 2), (256, 1, 8),
+                                   (256, 6, 4), (256, 9, 4), (256, 20, 3), (256, 33, 4)])
 def test_many_units_a_block(D, T, G, dtype):
     """Lengths of all kinds, so that a block's share holds several segments and the ends of others, and long ones that many share."""
     g = torch.Generator().manual_seed(D + T)
@@ -103,7 +104,7 @@ def test_many_units_a_block(D, T, G, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("D,T,G", [(64, 1, 4), (128, 9, 4), (256, 6, 4)])
+@pytest.mark.parametrize("D,T,G", [(64, 1, 4), (128, 9, 4), (256, 6, 4), (64, 17, 4), (128, 33, 2), (256, 70, 1)])
 def test_one_long_context(D, T, G, dtype):
     """A sink at the start, whose weight is far above the others' together in a tile, and growing scores, so that maxima move."""
     g = torch.Generator().manual_seed(D)
@@ -113,7 +114,8 @@ def test_one_long_context(D, T, G, dtype):
     q = torch.randn((1, T, H * G, D), generator=g)
     k = torch.randn((1, 1, H, D), generator=g)
     at = torch.zeros(1, dtype=torch.int32, device=DEV)
-    sv.spec_kv8_append(dev(3 * q[:, :1, ::G].to(torch.bfloat16)), dev(k.to(torch.bfloat16)), cache, table, at)  # the sink: scores of about 3 sqrt(D)
+    sink = 3 * q[:, :1, ::G]  # scores of about 3 sqrt(D) from the first token's first head; keys after it are held as they were
+    sv.spec_kv8_append(dev(sink.to(torch.bfloat16)), dev(k.to(torch.bfloat16)), cache, table, at)
     q = q.to(DT[dtype])
     st = torch.tensor([L], dtype=torch.int32)
     check(q, cache, table, st, None, page)
@@ -145,7 +147,7 @@ def test_bad_pages_and_lengths():
     assert (out[4] == 0).all() and (out[5] == 0).all()
 
 
-@pytest.mark.parametrize("T,G", [(8, 1), (8, 4), (8, 16)])
+@pytest.mark.parametrize("T,G", [(8, 1), (8, 4), (8, 8), (8, 16)])
 @pytest.mark.parametrize("what", ["key", "value"])
 def test_masked_nan_does_not_spread(T, G, what):
     """A NaN token is seen by its descendants alone; the others keep their results."""
