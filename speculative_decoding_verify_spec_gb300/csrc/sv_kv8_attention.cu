@@ -44,7 +44,7 @@ Att8Layout att8_layout(int B, int T, int H, int64_t rows, int D) {
     L.wide = rows > kNarrowRows8;
     L.nr = L.wide ? kWideRows8 : att8_rows(rows);
     L.tile = L.wide ? wide8_tile(D) : kTile8;
-    L.grid = kAttSMs * (L.wide ? 1 : att8_occupancy(D, L.nr));
+    L.grid = kAttSMs * (L.wide ? wide8_occupancy(D) : att8_occupancy(D, L.nr));
     L.see_words = L.wide ? (T + 31) / 32 : (L.nr + 31) / 32;
     const int nr = L.nr;
     const size_t row_tiles = size_t((rows + nr - 1) / nr);

@@ -6,23 +6,28 @@
 //   S [128 rows x tokens] = q [128 x D]  times  K codes^T         D / 32 steps a part of q
 //   O [128 rows x D]      = w [128 x tokens]  times  V codes      a step for 32 tokens and part of w
 // so that a row's maximum and sum need no reduction over lanes, a block of 16 tokens has its scales in registers, and m is taken out in the
-// multiplication that scales a score.  Sixteen warps: four groups of 128 threads have the 128 rows each, and a quarter of
-// the tile's tokens and of the output's dimensions.  As there, every tile has its own m and output, which is added up in registers.
+// multiplication that scales a score.  Two or four groups of 128 threads have the 128 rows each, and their share of
+// the tile's tokens and of the output's dimensions.  The scores are read from tensor memory twice, for the maximum and for the weights, 16 tokens
+// at a time, instead of kept.  As there, every tile has its own m and output, which is added up in registers.
 #pragma once
 
 #include "sv_kv8_attention.cuh"
 
 namespace sv {
 
-constexpr int kWideRows8 = 128, kWideGroups8 = 4, kWideThreads8 = 64 + 128 * kWideGroups8;
+constexpr int kWideRows8 = 128;
+// Softmax groups of a block and blocks an SM: two blocks hide each other's waits where registers and shared memory admit them.
+__host__ __device__ constexpr int wide8_groups(int D) { return D == 64 ? 2 : 4; }
+__host__ __device__ constexpr int wide8_occupancy(int D) { return D == 64 ? 2 : 1; }
+__host__ __device__ constexpr int wide8_threads(int D) { return 64 + 128 * wide8_groups(D); }
 __host__ __device__ constexpr int wide8_tile(int D) { return D == 256 ? 64 : 128; }  // by shared memory
 
 template <int D, int NP>
 struct Wide8Shared {
     static constexpr int kDims = D, kRows = kWideRows8, kTile = wide8_tile(D);
-    static constexpr int kStages = D == 64 ? 4 : 3, kValues = kStages, kInfos = kStages + 2, kQ = D == 64 ? 2 : 1;
-    static constexpr int kO = D == 256 ? 1 : 2;  // outputs in tensor memory
-    static constexpr int kUsed = 2 * kTile + kO * D, kCols = kUsed <= 256 ? 256 : 512;
+    static constexpr int kStages = D == 64 ? 2 : 3, kValues = kStages, kInfos = kStages + 2, kQ = 1, kGroups = wide8_groups(D);
+    static constexpr int kS = D == 64 ? 1 : 2, kO = D == 256 ? 1 : 2;  // scores and outputs in tensor memory
+    static constexpr int kUsed = kS * kTile + kO * D, kCols = kUsed <= 256 ? 256 : 512;
     alignas(128) uint8_t k[kStages][kTile * D];
     uint8_t v[kValues][kTile * D];
     uint8_t w[NP][kRows * kTile];  // [part][16 tokens][row][16 bytes]
@@ -32,9 +37,9 @@ struct Wide8Shared {
     };
     Queries q[kQ];
     Info8 info[kInfos];
-    float red[2][kWideGroups8][kRows], sums[kWideGroups8][kRows];
+    float red[2][kGroups][kRows], sums[kGroups][kRows];
     alignas(8) uint64_t full_k[kStages], full_v[kValues], empty_k[kStages], empty_v[kValues], full_i[kInfos];
-    uint64_t full_s[2], free_s[2], full_o[kO], free_o[kO], full_w[2], full_q[kQ], free_q[kQ], done;
+    uint64_t full_s[kS], free_s[kS], full_o[kO], free_o[kO], full_w[2], full_q[kQ], free_q[kQ], done;
     uint32_t tmem;
 };
 
@@ -55,11 +60,11 @@ __device__ __forceinline__ void issue_wide8(const Att8Args &a, Wide8Shared<D, NP
             known = true;
         }
         if ((flags & kFirst8) && !mbar_test(&sh.full_q[segment % Sh::kQ], uint32_t(segment / Sh::kQ) & 1u)) return false;
-        if (n >= 2 && !mbar_test(&sh.free_s[n & 1], uint32_t((n >> 1) - 1) & 1u)) return false;
+        if (n >= Sh::kS && !mbar_test(&sh.free_s[n % Sh::kS], uint32_t(n / Sh::kS - 1) & 1u)) return false;
         known = false;
         fence_after();
         constexpr uint32_t high = operand8_high(8 * D);
-        const uint32_t d = tmem + (n & 1) * NT, k = operand8(smem_u32(sh.k[s]), 128);
+        const uint32_t d = tmem + n % Sh::kS * NT, k = operand8(smem_u32(sh.k[s]), 128);
         uint32_t q = operand8(smem_u32(sh.q[segment % Sh::kQ].part), 128);
 #pragma unroll
         for (int p = 0; p < 3; ++p, q += kWideRows8 * D / 16)
@@ -68,7 +73,7 @@ __device__ __forceinline__ void issue_wide8(const Att8Args &a, Wide8Shared<D, NP
                 for (int i = 0; i < D / 32; ++i) mma8(d, q + i * 16, high, k + i * 16, high, kind8(NT, false), p > 0 || i > 0);
             }
         wide_commit(&sh.empty_k[s]);
-        wide_commit(&sh.full_s[n & 1]);
+        wide_commit(&sh.full_s[n % Sh::kS]);
         if (flags & kLast8) wide_commit(&sh.free_q[segment % Sh::kQ]);
         return true;
     };
@@ -77,7 +82,7 @@ __device__ __forceinline__ void issue_wide8(const Att8Args &a, Wide8Shared<D, NP
         if (!mbar_test(&sh.full_w[n & 1], uint32_t(n >> 1) & 1u) || !mbar_test(&sh.full_v[s], uint32_t(n / kValues) & 1u)) return false;
         if (n >= Sh::kO && !mbar_test(&sh.free_o[at], uint32_t(n / Sh::kO - 1) & 1u)) return false;
         fence_after();
-        const uint32_t d = tmem + 2 * NT + at * D, v = operand8(smem_u32(sh.v[s]), 8 * D), w = operand8(smem_u32(sh.w), 2048);
+        const uint32_t d = tmem + Sh::kS * NT + at * D, v = operand8(smem_u32(sh.v[s]), 8 * D), w = operand8(smem_u32(sh.w), 2048);
 #pragma unroll
         for (int p = 0; p < NP; ++p)
 #pragma unroll
@@ -109,9 +114,9 @@ __device__ __forceinline__ void issue_wide8(const Att8Args &a, Wide8Shared<D, NP
 }
 
 template <int D, int NP>
-__global__ void __launch_bounds__(kWideThreads8, 1) kv8_wide_kernel(const Att8Args a) {
+__global__ void __launch_bounds__(wide8_threads(D), wide8_occupancy(D)) kv8_wide_kernel(const Att8Args a) {
     using Sh = Wide8Shared<D, NP>;
-    constexpr int NT = Sh::kTile, NR = kWideRows8, kValues = Sh::kValues, TW = NT / kWideGroups8, CW = D / kWideGroups8;  // a thread's tokens and dimensions
+    constexpr int NT = Sh::kTile, NR = kWideRows8, kValues = Sh::kValues, kGroups = Sh::kGroups, TW = NT / kGroups, CW = D / kGroups;  // a thread's tokens and dimensions
     extern __shared__ unsigned char raw0[];
     Sh &sh = *reinterpret_cast<Sh *>(raw0 + ((128 - (smem_u32(raw0) & 127)) & 127));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -121,10 +126,11 @@ __global__ void __launch_bounds__(kWideThreads8, 1) kv8_wide_kernel(const Att8Ar
     if (tid == 0) {
         for (int i = 0; i < Sh::kStages; ++i) mbar_init(smem_u32(&sh.full_k[i]), 1), mbar_init(smem_u32(&sh.empty_k[i]), 1);
         for (int i = 0; i < kValues; ++i) mbar_init(smem_u32(&sh.full_v[i]), 1), mbar_init(smem_u32(&sh.empty_v[i]), 1);
-        for (int i = 0; i < 2; ++i)
-            mbar_init(smem_u32(&sh.full_s[i]), 1), mbar_init(smem_u32(&sh.free_s[i]), 16), mbar_init(smem_u32(&sh.full_w[i]), 16);
-        for (int i = 0; i < Sh::kO; ++i) mbar_init(smem_u32(&sh.full_o[i]), 1), mbar_init(smem_u32(&sh.free_o[i]), 16);
-        for (int i = 0; i < Sh::kQ; ++i) mbar_init(smem_u32(&sh.full_q[i]), 1), mbar_init(smem_u32(&sh.free_q[i]), 17);
+        constexpr int kWarps = 4 * kGroups;
+        for (int i = 0; i < Sh::kS; ++i) mbar_init(smem_u32(&sh.full_s[i]), 1), mbar_init(smem_u32(&sh.free_s[i]), kWarps);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.full_w[i]), kWarps);
+        for (int i = 0; i < Sh::kO; ++i) mbar_init(smem_u32(&sh.full_o[i]), 1), mbar_init(smem_u32(&sh.free_o[i]), kWarps);
+        for (int i = 0; i < Sh::kQ; ++i) mbar_init(smem_u32(&sh.full_q[i]), 1), mbar_init(smem_u32(&sh.free_q[i]), kWarps + 1);
         for (int i = 0; i < Sh::kInfos; ++i) mbar_init(smem_u32(&sh.full_i[i]), 1);
         mbar_init(smem_u32(&sh.done), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -156,7 +162,7 @@ __global__ void __launch_bounds__(kWideThreads8, 1) kv8_wide_kernel(const Att8Ar
     } else {
         const int group = (warp - 2) / 4, quarter = warp & 3, r = quarter * 32 + lane;  // this thread's row
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
-        const uint32_t tmem_s = sh.tmem + lanes + group * TW, tmem_o = sh.tmem + lanes + 2 * NT + group * CW;
+        const uint32_t tmem_s = sh.tmem + lanes + group * TW, tmem_o = sh.tmem + lanes + Sh::kS * NT + group * CW;
         int granule_log2 = 4;
         while (1 << granule_log2 < a.granule) ++granule_log2;
         bool failed = false;
@@ -196,8 +202,33 @@ __global__ void __launch_bounds__(kWideThreads8, 1) kv8_wide_kernel(const Att8Ar
             const Info8 &in = sh.info[n % Sh::kInfos];
             wait(&sh.full_i[n % Sh::kInfos], uint32_t(n / Sh::kInfos) & 1u);
             int flags = 0;
-            float s[TW], scale[TW / 16], shift[TW / 16], inv[TW / 16];
-            uint32_t see = 0xFFFFFFFFu;
+            uint32_t see[(TW + 31) / 32];
+#pragma unroll
+            for (int i = 0; i < (TW + 31) / 32; ++i) see[i] = 0xFFFFFFFFu;
+            const uint32_t s_at = tmem_s + n % Sh::kS * NT;
+            // 16 tokens' scores, as they are to be seen, and their scales: t = score * scale + shift, w / s' = w * inv
+            auto scores = [&](int b, float (&s)[16], float &scale, float &shift, float &inv) {
+                tmem_get8(*reinterpret_cast<float(*)[8]>(s), s_at + 16 * b), tmem_get8(*reinterpret_cast<float(*)[8]>(s + 8), s_at + 16 * b + 8);
+                const int token = group * TW + 16 * b;  // in the tile
+                uint2 word = *reinterpret_cast<const uint2 *>(in.word[token / kKv8Block]);
+                // (what is not there has no scale; its tokens are not seen)
+                if ((flags & kRagged8) && (in.unit.tile * NT + token >= seg.len || !(in.unit.have >> (token >> granule_log2) & 1u)))
+                    word = make_uint2(0x3F800000u, 0x3F800000u);
+                const int e = kv8_exponent(word.y);
+                scale = fmaxf(factor * __uint_as_float(word.x & 0xFFFF0000u), 1.2e-38f), shift = float(e), inv = kv8_power(-e);
+                const uint32_t bad = (word.x | word.y) & 0xFFFFu;
+                tmem_loaded();
+                tmem_here(*reinterpret_cast<float(*)[8]>(s)), tmem_here(*reinterpret_cast<float(*)[8]>(s + 8));
+                if ((flags & kMasked8) || bad) {  // (the same for the whole warp)
+                    const uint32_t seen = (TW > 32 && b >= 2 ? see[(TW + 31) / 32 - 1] : see[0]) >> (16 * (b & 1));
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (bad >> j & 1u) s[j] = NAN;
+                        if (!(seen >> j & 1u)) s[j] = -INFINITY;
+                    }
+                    __syncwarp();  // (a branch, not 32 selections in every block)
+                }
+            };
             if (!failed) {
                 flags = in.unit.masked;
                 if (flags & kFirst8) {
@@ -213,75 +244,56 @@ __global__ void __launch_bounds__(kWideThreads8, 1) kv8_wide_kernel(const Att8Ar
                     wait(&sh.full_q[segment % Sh::kQ], uint32_t(segment / Sh::kQ) & 1u);
                     factor = sh.q[segment % Sh::kQ].factor[r];
                 }
-                const int tok0 = in.unit.tile * NT + group * TW;  // this thread's first token
                 if (flags & kMasked8) {  // which of its tokens the row sees
-                    uint32_t there = 0;
 #pragma unroll
-                    for (int b = 0; b < TW; b += 16) {  // (granules are 16 tokens at least)
-                        const int left = seg.len - (tok0 + b);
-                        if (left > 0 && (in.unit.have >> ((group * TW + b) >> granule_log2) & 1u)) there |= (left >= 16 ? 0xFFFFu : (1u << left) - 1) << b;
-                    }
-                    const int x = tok0 - seg.before;  // the first one among the new tokens
-                    if (x > -TW && node >= 0) {
-                        if (a.parent) {
-                            const uint32_t *words = a.see + (int64_t(seg.rt) * NR + r) * a.see_words;
-                            const int w = max(x, 0) >> 5;
-                            const uint32_t low = w < a.see_words ? __ldcg(words + w) : 0u, high = w + 1 < a.see_words ? __ldcg(words + w + 1) : 0u;
-                            see = x >= 0 ? __funnelshift_r(low, high, x & 31) : low << -x | ((1u << -x) - 1);
-                        } else {
-                            const int count = node + 1 - x;
-                            see = count >= 32 ? 0xFFFFFFFFu : count <= 0 ? 0u : (1u << count) - 1;
+                    for (int i = 0; i < (TW + 31) / 32; ++i) {
+                        const int in_tile = group * TW + 32 * i, tok0 = in.unit.tile * NT + in_tile;  // the first of up to 32 tokens
+                        uint32_t there = 0, row = 0xFFFFFFFFu;
+#pragma unroll
+                        for (int b = 0; b < (TW < 32 ? TW : 32); b += 16) {  // (granules are 16 tokens at least)
+                            const int left = seg.len - (tok0 + b);
+                            if (left > 0 && (in.unit.have >> ((in_tile + b) >> granule_log2) & 1u)) there |= (left >= 16 ? 0xFFFFu : (1u << left) - 1) << b;
                         }
+                        const int x = tok0 - seg.before;  // the first one among the new tokens
+                        if (x > -32 && node >= 0) {
+                            if (a.parent) {
+                                const uint32_t *words = a.see + (int64_t(seg.rt) * NR + r) * a.see_words;
+                                const int w = max(x, 0) >> 5;
+                                const uint32_t low = w < a.see_words ? __ldcg(words + w) : 0u, high = w + 1 < a.see_words ? __ldcg(words + w + 1) : 0u;
+                                row = x >= 0 ? __funnelshift_r(low, high, x & 31) : low << -x | ((1u << -x) - 1);
+                            } else {
+                                const int count = node + 1 - x;
+                                row = count >= 32 ? 0xFFFFFFFFu : count <= 0 ? 0u : (1u << count) - 1;
+                            }
+                        }
+                        see[i] = row & there;
                     }
-                    see &= there;
                     if (flags & kRagged8) wait(&sh.full_v[n % kValues], uint32_t(n / kValues) & 1u);
                 }
-                wait(&sh.full_s[n & 1], uint32_t(n >> 1) & 1u);
+                wait(&sh.full_s[n % Sh::kS], uint32_t(n / Sh::kS) & 1u);
                 fence_after();
-                float most = -INFINITY;
                 if (warp_on) {
-#pragma unroll
-                    for (int c = 0; c < TW; c += 8) tmem_get8(*reinterpret_cast<float(*)[8]>(s + c), tmem_s + (n & 1) * NT + c);
-                    tmem_loaded();
-#pragma unroll
-                    for (int c = 0; c < TW; c += 8) tmem_here(*reinterpret_cast<float(*)[8]>(s + c));
-#pragma unroll
+                    float most = -INFINITY;
+#pragma unroll 2
                     for (int b = 0; b < TW / 16; ++b) {
-                        uint2 word = *reinterpret_cast<const uint2 *>(in.word[group * (TW / 16) + b]);
-                        // (what is not there has no scale; its tokens are not seen)
-                        if ((flags & kRagged8) && (tok0 + 16 * b >= seg.len || !(in.unit.have >> ((group * TW + 16 * b) >> granule_log2) & 1u))) word = make_uint2(0x3F800000u, 0x3F800000u);
-                        const int e = kv8_exponent(word.y);
-                        scale[b] = fmaxf(factor * __uint_as_float(word.x & 0xFFFF0000u), 1.2e-38f), shift[b] = float(e), inv[b] = kv8_power(-e);
-                        const uint32_t bad = (word.x | word.y) & 0xFFFFu;
-                        if ((flags & kMasked8) || bad) {  // (the same for the whole warp)
+                        float s[16], scale, shift, inv;
+                        scores(b, s, scale, shift, inv);
+                        float top = s[0];
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                if (bad >> j & 1u) s[16 * b + j] = NAN;
-                                if (!(see >> (16 * b + j) & 1u)) s[16 * b + j] = -INFINITY;
-                            }
-                            __syncwarp();  // (a branch, not 64 selections in every unit)
-                        }
-                        float top = s[16 * b];
-#pragma unroll
-                        for (int j = 1; j < 16; ++j) top = fmaxf(top, s[16 * b + j]);
-                        most = fmaxf(most, fmaf(top, scale[b], shift[b]));
+                        for (int j = 1; j < 16; ++j) top = fmaxf(top, s[j]);
+                        most = fmaxf(most, fmaf(top, scale, shift));
                     }
                     sh.red[n & 1][group][r] = most;
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) {  // the scores and what is known of the unit are read
-                    mbar_arrive(smem_u32(&sh.free_s[n & 1]));
-                    if (flags & kLast8) mbar_arrive(smem_u32(&sh.free_q[segment % Sh::kQ]));
-                }
             }
-            if (group_or<1, 128 * kWideGroups8>(failed)) break;
+            if (group_or<1, 128 * kGroups>(failed)) break;
             const bool first = (flags & kFirst8) != 0, last = (flags & kLast8) != 0;
             float f = 1.f;
             if (!first) wait(&sh.full_o[(n - 1) % Sh::kO], uint32_t((n - 1) / Sh::kO) & 1u);  // the last unit's weights are in the place of these
             if (warp_on && !failed) {
-                const float(*red)[NR] = sh.red[n & 1];
-                const float m = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r]));
+                float m = sh.red[n & 1][0][r];
+#pragma unroll
+                for (int i = 1; i < kGroups; ++i) m = fmaxf(m, sh.red[n & 1][i][r]);
                 const float whole = rintf(m);
                 float g = 1.f, minus = m == INFINITY ? -INFINITY : 0.f;
                 if (fabsf(whole) < INFINITY) {
@@ -295,14 +307,16 @@ __global__ void __launch_bounds__(kWideThreads8, 1) kv8_wide_kernel(const Att8Ar
 #pragma unroll
                     for (int j = 0; j < CW / 2; ++j) acc[j] = mul2(acc[j], two(g, g));
                 }
-#pragma unroll
+#pragma unroll 2
                 for (int b = 0; b < TW / 16; ++b) {
-                    const Two a2 = two(scale[b], scale[b]), b2 = two(shift[b] + minus, shift[b] + minus);
+                    float s[16], scale, shift, inv;
+                    scores(b, s, scale, shift, inv);
+                    const Two a2 = two(scale, scale), b2 = two(shift + minus, shift + minus);
                     Two sum = 0;
                     uint32_t code[NP][4];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const float2 x = split(fma2(two(s[16 * b + 2 * j], s[16 * b + 2 * j + 1]), a2, b2));
+                        const float2 x = split(fma2(two(s[2 * j], s[2 * j + 1]), a2, b2));
                         const float w0 = ex2(x.x), w1 = ex2(x.y);
                         sum = add2(sum, two(w0, w1));
                         uint32_t p[NP];
@@ -314,7 +328,7 @@ __global__ void __launch_bounds__(kWideThreads8, 1) kv8_wide_kernel(const Att8Ar
                     for (int k = 0; k < NP; ++k)
                         *reinterpret_cast<uint4 *>(sh.w[k] + (group * (TW / 16) + b) * 2048 + r * 16) = make_uint4(code[k][0], code[k][1], code[k][2], code[k][3]);
                     const float2 both = split(sum);
-                    l = fmaf((both.x + both.y) * inv[b], f, l);
+                    l = fmaf((both.x + both.y) * inv, f, l);
                 }
             }
             if (!failed) {
@@ -323,6 +337,12 @@ __global__ void __launch_bounds__(kWideThreads8, 1) kv8_wide_kernel(const Att8Ar
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) *reinterpret_cast<uint4 *>(sh.v[n % kValues] + kv8_code_byte(D, token, 16 * j)) = make_uint4(0, 0, 0, 0);
                 }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) {  // the scores and what is known of the unit are read
+                mbar_arrive(smem_u32(&sh.free_s[n % Sh::kS]));
+                if (last) mbar_arrive(smem_u32(&sh.free_q[segment % Sh::kQ]));
             }
             fence_operands();
             __syncwarp();
@@ -335,10 +355,12 @@ __global__ void __launch_bounds__(kWideThreads8, 1) kv8_wide_kernel(const Att8Ar
 
             // the segment's end
             sh.sums[group][r] = l;
-            if (group_or<1, 128 * kWideGroups8>(failed)) break;
+            if (group_or<1, 128 * kGroups>(failed)) break;
             const bool whole = seg_lo >= ubegin && seg_lo + seg.tiles <= uend;
             const int64_t slot = 2 * cta + (seg_lo > ubegin ? 1 : 0);
-            const float sum = (sh.sums[0][r] + sh.sums[1][r]) + (sh.sums[2][r] + sh.sums[3][r]);
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) sum += sh.sums[i][r];
             const float part = node < 0 || sum == 0.f ? 0.f : 1.f / sum;
             const int row = seg.rt * NR + r, at = row / a.G;
             if (whole) {
@@ -377,13 +399,13 @@ template <int D, int NP>
 cudaError_t launch_wide8(const Att8Args &a, int grid, cudaStream_t s) {
     using Sh = Wide8Shared<D, NP>;
     constexpr size_t smem = sizeof(Sh) + 128;
-    static_assert(smem <= 227 * 1024 && sizeof(typename Sh::Queries) == query_bytes8(D, kWideRows8) && Sh::kUsed <= 512, "");
+    static_assert((smem + 1024) * wide8_occupancy(D) <= 228 * 1024 && Sh::kCols * wide8_occupancy(D) <= 512 && sizeof(typename Sh::Queries) == query_bytes8(D, kWideRows8) && Sh::kUsed <= 512, "");
     static std::atomic<int> allowed[64];
     cudaError_t e = launch_queries8<D>(a, s);
     if (e != cudaSuccess) return e;
     e = allow_shared(kv8_wide_kernel<D, NP>, int(smem), allowed);
     if (e != cudaSuccess) return e;
-    e = launch_after(kv8_wide_kernel<D, NP>, unsigned(grid), unsigned(kWideThreads8), smem, s, a);
+    e = launch_after(kv8_wide_kernel<D, NP>, unsigned(grid), unsigned(wide8_threads(D)), smem, s, a);
     if (e != cudaSuccess) return e;
     return launch_join<D>(a, grid, kWideRows8, s);
 }
