@@ -33,10 +33,12 @@ __device__ __forceinline__ int kv8_exponent(uint32_t word) {
 }
 __device__ __forceinline__ float kv8_power(int e) { return __int_as_float((127 + e) << 23); }  // -126 <= e <= 127
 
-// Codes nearest to two numbers (ties to even, at most 448 in magnitude): x in the low byte.
-__device__ __forceinline__ uint32_t kv8_codes(float x, float y) {
-    uint16_t c;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(y), "f"(x));
+// Codes nearest to four numbers (ties to even, at most 448 in magnitude), x in the lowest byte.
+__device__ __forceinline__ uint32_t kv8_codes(float x, float y, float z, float w) {
+    uint32_t c;
+    asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\tmov.b32 %0, {a, b};\n\t}"
+        : "=r"(c)
+        : "f"(x), "f"(y), "f"(z), "f"(w));
     return c;
 }
 // What the two codes in the low half of w stand for.

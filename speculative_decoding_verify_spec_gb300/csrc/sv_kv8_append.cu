@@ -266,9 +266,9 @@ __global__ void __launch_bounds__(kApp8Threads) kv8_append_kernel(const Append8A
                     const int d = piece * 16 + 4 * j;
                     const bool turned = rot.cos && d < 2 * rot.pairs;
                     const float o = turned ? doff : 0.f;
-                    uint32_t w = kv8_codes(y[0] - o, y[1] - o) | kv8_codes(y[2] - o, y[3] - o) << 16;
+                    uint32_t w = kv8_codes(y[0] - o, y[1] - o, y[2] - o, y[3] - o);
                     if (turned) {
-                        const uint32_t u = kv8_codes(y[0] + o, y[1] + o) | kv8_codes(y[2] + o, y[3] + o) << 16;
+                        const uint32_t u = kv8_codes(y[0] + o, y[1] + o, y[2] + o, y[3] + o);
                         if (w != u || odd) {
                             uint32_t r = 0;
 #pragma unroll 1
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kApp8Threads) kv8_append_kernel(const Append8A
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 u = kv8_numbers(w[j]), v = kv8_numbers(w[j] >> 16);
-                w[j] = kv8_no_minus_zero(kv8_codes(u.x * shrink, u.y * shrink) | kv8_codes(v.x * shrink, v.y * shrink) << 16);
+                w[j] = kv8_no_minus_zero(kv8_codes(u.x * shrink, u.y * shrink, v.x * shrink, v.y * shrink));
             }
             *at = make_uint4(w[0], w[1], w[2], w[3]);
         }

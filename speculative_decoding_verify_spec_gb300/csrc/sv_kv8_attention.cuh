@@ -149,20 +149,20 @@ __device__ __forceinline__ bool group_or(bool x) {
     return r != 0;
 }
 
-// The parts of a pair of numbers, NP times two codes (the first number's in the low byte).  A part is the number rounded to 4 bits, by the
-// difference with a multiple of it (Dekker's splitting): the conversion to a code then rounds only what is below 2^-6, and a conversion back
-// would cost four times a conversion there.
+// The parts of two pairs of numbers, NP times four codes (the first number's in the lowest byte).  A part is the number rounded to 4 bits, by
+// the difference with a multiple of it (Dekker's splitting): the conversion to a code then rounds only what is below 2^-6, and a
+// conversion back would cost four times a conversion there.
 template <int NP>
-__device__ __forceinline__ void parts8(float x, float y, uint32_t (&c)[NP]) {
+__device__ __forceinline__ void parts8(Two v, Two w, uint32_t (&c)[NP]) {
     const Two minus = two(-1.f, -1.f), split4 = two(1048577.f, 1048577.f);  // 2^20 + 1
-    Two v = two(x, y);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        const float2 f = split(v);
-        c[i] = kv8_codes(f.x, f.y);
+        const float2 f = split(v), g = split(w);
+        c[i] = kv8_codes(f.x, f.y, g.x, g.y);
         if (i + 1 < NP) {
-            const Two m = mul2(v, split4), top = fma2(fma2(v, minus, m), minus, m);  // m - (m - v)
-            v = fma2(top, minus, v);
+            const Two m = mul2(v, split4), o = mul2(w, split4);
+            v = fma2(fma2(fma2(v, minus, m), minus, m), minus, v);  // v - (m - (m - v))
+            w = fma2(fma2(fma2(w, minus, o), minus, o), minus, w);
         }
     }
 }
@@ -473,18 +473,15 @@ __global__ void __launch_bounds__(kQueryThreads8) kv8_queries_kernel(const Att8A
     const int e2 = top == 0 ? 0 : max(int(top >> 23) - 127 - 7, -110);
     const bool odd = top >= 0x7F800000u;
     const float shrink = power2(odd ? 0 : -e2);
-    uint32_t code[3][2] = {};
+    uint32_t code[2][3];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t p[3];
-        parts8(odd ? NAN : x[2 * i] * shrink, odd ? NAN : x[2 * i + 1] * shrink, p);
+    for (int i = 0; i < 8; ++i) x[i] = odd ? NAN : x[i] * shrink;
 #pragma unroll
-        for (int k = 0; k < 3; ++k) code[k][i / 2] |= p[k] << (16 * (i & 1));
-    }
+    for (int i = 0; i < 2; ++i) parts8(two(x[4 * i], x[4 * i + 1]), two(x[4 * i + 2], x[4 * i + 3]), code[i]);
     uint8_t *q = a.parts + tile * query_bytes8(D, a.nr);
 #pragma unroll
     for (int k = 0; k < 3; ++k)
-        if (k < a.nq) *reinterpret_cast<uint2 *>(q + kv8_code_byte(D, k * a.nr + r, d0)) = make_uint2(code[k][0], code[k][1]);
+        if (k < a.nq) *reinterpret_cast<uint2 *>(q + kv8_code_byte(D, k * a.nr + r, d0)) = make_uint2(code[0][k], code[1][k]);
     if (c == 0) reinterpret_cast<float *>(q + 3 * a.nr * D)[r] =
             a.scale == 0.f ? 1.f : fmaxf(fabsf(a.scale) * 1.4426950408889634f * power2(odd ? 0 : e2), 1.2e-38f);
 }
@@ -715,23 +712,23 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                 __syncwarp();
             }
             // the weights
-            uint32_t code[NP][4];
+            uint32_t code[4][NP] = {};
             const Two inv2 = two(inv, inv);
 #pragma unroll
             for (int c = 0; c < RW / 8; ++c) {
-#pragma unroll
-                for (int k = 0; k < NP; ++k) code[k][2 * c] = code[k][2 * c + 1] = 0;
                 if (8 * c >= live) continue;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 mv = sh.move[wg][quarter][n & 1][4 * c + j];
-                    const float2 x = split(add2(two(t[8 * c + 2 * j], t[8 * c + 2 * j + 1]), two(mv.x, mv.y)));
-                    const float w0 = ex2(x.x), w1 = ex2(x.y);
-                    l[4 * c + j] = fma2(mul2(two(w0, w1), inv2), two(mv.z, mv.w), l[4 * c + j]);
-                    uint32_t p[NP];
-                    parts8(w0, w1, p);
+                for (int j = 0; j < 4; j += 2) {
+                    Two w[2];
 #pragma unroll
-                    for (int k = 0; k < NP; ++k) code[k][2 * c + j / 2] |= p[k] << (16 * (j & 1));
+                    for (int i = 0; i < 2; ++i) {
+                        const int at = 4 * c + j + i;  // the pair of rows
+                        const float4 mv = sh.move[wg][quarter][n & 1][at];
+                        const float2 x = split(add2(two(t[2 * at], t[2 * at + 1]), two(mv.x, mv.y)));
+                        w[i] = two(ex2(x.x), ex2(x.y));
+                        l[at] = fma2(mul2(w[i], inv2), two(mv.z, mv.w), l[at]);
+                    }
+                    parts8(w[0], w[1], code[2 * c + j / 2]);
                 }
             }
             const bool first = (flags & kFirst8) != 0, last = (flags & kLast8) != 0;
@@ -740,7 +737,7 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                 uint8_t *to = sh.w[n % Sh::kP] + wg * 2048 + token * 16;
                 if (live > 0) {
 #pragma unroll
-                    for (int k = 0; k < NP; ++k) *reinterpret_cast<uint4 *>(to + k * NR * kTile8) = make_uint4(code[k][0], code[k][1], code[k][2], code[k][3]);
+                    for (int k = 0; k < NP; ++k) *reinterpret_cast<uint4 *>(to + k * NR * kTile8) = make_uint4(code[0][k], code[1][k], code[2][k], code[3][k]);
                 }
                 if ((flags & kRagged8) && wg == 0 && inv == 0.f) {  // a code that is not there may be a NaN, which no weight of 0 takes away
                     uint8_t *v = sh.v[n % kValues];

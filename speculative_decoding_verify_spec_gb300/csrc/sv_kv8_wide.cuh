@@ -313,20 +313,21 @@ __global__ void __launch_bounds__(wide8_threads(D), wide8_occupancy(D)) kv8_wide
                     scores(b, s, scale, shift, inv);
                     const Two a2 = two(scale, scale), b2 = two(shift + minus, shift + minus);
                     Two sum = 0;
-                    uint32_t code[NP][4];
+                    uint32_t code[4][NP];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 x = split(fma2(two(s[2 * j], s[2 * j + 1]), a2, b2));
-                        const float w0 = ex2(x.x), w1 = ex2(x.y);
-                        sum = add2(sum, two(w0, w1));
-                        uint32_t p[NP];
-                        parts8(w0, w1, p);
+                    for (int j = 0; j < 4; ++j) {
+                        Two w[2];
 #pragma unroll
-                        for (int k = 0; k < NP; ++k) code[k][j / 2] = j & 1 ? code[k][j / 2] | p[k] << 16 : p[k];
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 x = split(fma2(two(s[4 * j + 2 * i], s[4 * j + 2 * i + 1]), a2, b2));
+                            w[i] = two(ex2(x.x), ex2(x.y));
+                            sum = add2(sum, w[i]);
+                        }
+                        parts8(w[0], w[1], code[j]);
                     }
 #pragma unroll
                     for (int k = 0; k < NP; ++k)
-                        *reinterpret_cast<uint4 *>(sh.w[k] + (group * (TW / 16) + b) * 2048 + r * 16) = make_uint4(code[k][0], code[k][1], code[k][2], code[k][3]);
+                        *reinterpret_cast<uint4 *>(sh.w[k] + (group * (TW / 16) + b) * 2048 + r * 16) = make_uint4(code[0][k], code[1][k], code[2][k], code[3][k]);
                     const float2 both = split(sum);
                     l = fmaf((both.x + both.y) * inv, f, l);
                 }
