@@ -8,9 +8,9 @@
 // once for both.  The rotated numbers stay in registers from the reduction to the codes.
 //
 // The result is that of the exact rule.  fp32 leaves a rotated key off by at most 2^-23 (|a cos| + |b sin|), and with D the
-// largest such bound of the block, a scale or a code is settled if x - D and x + D have the same one.  What is left (a code in
-// some ten thousand, a scale in a million) is computed in 64 bits, where a 16-bit number times an fp32 angle is exact and one
-// subtraction rounds.
+// largest such bound of the block (for its scale) or of a lane's numbers (for their codes), a scale or a code is settled if x - D and x + D
+// have the same one.  What is left (a code in some ten thousand, a scale in a million) is computed in 64 bits, where a 16-bit number
+// times an fp32 angle is exact and one subtraction rounds; a lane collects its codes in doubt first, so that the lanes' ones go side by side.
 //
 // Everything is read once and written once; 16 bits in, 8 out (and 16 where the values held are wanted).
 #include <cstdint>
@@ -225,10 +225,9 @@ __global__ void __launch_bounds__(kApp8Threads) kv8_append_kernel(const Append8A
         for (int i = 0; i < W; ++i) top = max(top, red[mine][0][i]), bound = max(bound, red[mine][1][i]);
     }
     const float off = __uint_as_float(bound) * 2.4e-7f;  // 2^-22 and a little: two roundings, and those of the sums that make `most`
-    int e = ceil_exponent(fmaxf(__uint_as_float(top) - off, 0.f));
+    int e = ceil_exponent(fmaxf(__uint_as_float(top) - off, 0.f));  // (if !odd) that of the largest magnitude, or less
     uint32_t bad = 0;  // slots with a NaN or an infinity
-    if (__syncthreads_or(odd || e != ceil_exponent(__uint_as_float(top) + off))) {
-        // in 64 bits: first which vectors are to be left out, then the largest magnitude of the others
+    if (odd) {  // first which vectors are to be left out, then the largest magnitude of the others
         for (int round = 0; round < 2; ++round) {
             e = -1022;
             if (live && !(bad >> slot & 1u)) {
@@ -246,51 +245,73 @@ __global__ void __launch_bounds__(kApp8Threads) kv8_append_kernel(const Append8A
             bad = bad_s[mine];
         }
         e = e_s[mine];
+    } else if (__syncthreads_or(e != ceil_exponent(__uint_as_float(top) + off))) {
+        // the numbers that may be above 2^e, in 64 bits.  (A power of two itself, not turned, is in doubt: one largest magnitude in 200.)
+        uint32_t doubt = 0;
+        if (live) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) doubt |= uint32_t(fabsf(x[j / 16][j % 16]) + off > kv8_power(e)) << j;
+        }
+#pragma unroll 1
+        while (doubt) {
+            const int j = __ffs(doubt) - 1;
+            doubt &= doubt - 1;
+            atomicMax(&e_s[mine], ceil_exponent(rotated_exactly<kBF16>(rot, row, angles, (j < 16 ? p : q) * 16 + j % 16)));
+        }
+        __syncthreads();
+        e = max(e, e_s[mine]);
     }
     e = min(max(e - kKv8Top, kKv8Least), kKv8Most);
     if (here && lo > 0) e = max(e, kv8_exponent(old));
-    const float inv = kv8_power(-e), scale = kv8_power(e), doff = off * inv;
+    const float inv = kv8_power(-e), scale = kv8_power(e);
+    // this lane's numbers are off by 2^-23 of its own `most`, and the sums below by half of that
+    const float o_turned = most * 1.85e-7f * inv;
 
     if (slot >= lo && t < a.T) {
         const bool nan = bad >> slot & 1u;
+        uint32_t c[2][4] = {}, doubt = 0;  // bit 16 k + i: element i of piece k
+        if (live && !nan) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t c[4] = {0, 0, 0, 0};
-            const int piece = k ? q : p;
-            if (live && !nan) {
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float y[4];
 #pragma unroll
                     for (int n = 0; n < 4; ++n) y[n] = x[k][4 * j + n] * inv;
-                    const int d = piece * 16 + 4 * j;
-                    const bool turned = rot.cos && d < 2 * rot.pairs;
-                    const float o = turned ? doff : 0.f;
-                    uint32_t w = kv8_codes(y[0] - o, y[1] - o, y[2] - o, y[3] - o);
+                    const bool turned = rot.cos && (k ? q : p) * 16 + 4 * j < 2 * rot.pairs;
+                    const float o = turned ? o_turned : 0.f;
+                    c[k][j] = kv8_codes(y[0] - o, y[1] - o, y[2] - o, y[3] - o);
                     if (turned) {
-                        const uint32_t u = kv8_codes(y[0] + o, y[1] + o, y[2] + o, y[3] + o);
-                        if (w != u || odd) {
-                            uint32_t r = 0;
-#pragma unroll 1
-                            for (int n = 0; n < 4; ++n) {
-                                uint32_t one = w >> (8 * n) & 255u;
-                                if (odd || one != (u >> (8 * n) & 255u))
-                                    one = code_exactly(rotated_exactly<kBF16>(rot, row, angles, d + n) * double(inv));
-                                r |= one << (8 * n);
-                            }
-                            w = r;
+                        const uint32_t u = kv8_codes(y[0] + o, y[1] + o, y[2] + o, y[3] + o) ^ c[k][j];
+                        if (u || odd) {
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) doubt |= uint32_t(odd || (u >> (8 * n) & 255u)) << (16 * k + 4 * j + n);
                         }
                     }
-                    c[j] = kv8_no_minus_zero(w);
                 }
+#pragma unroll 1
+            while (doubt) {  // (the lanes' ones side by side)
+                const int i = __ffs(doubt) - 1, d = (i < 16 ? p : q) * 16 + (i & 15), shift = 8 * (i & 3);
+                doubt &= doubt - 1;
+                const uint32_t one = code_exactly(rotated_exactly<kBF16>(rot, row, angles, d) * double(inv));
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (i / 4 == k) c[k / 4][k % 4] = (c[k / 4][k % 4] & ~(255u << shift)) | one << shift;
             }
-            if (live && here) *reinterpret_cast<uint4 *>(codes + kv8_code_byte(D, s0 + slot, piece * 16)) = make_uint4(c[0], c[1], c[2], c[3]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int piece = k ? q : p;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[k][j] = kv8_no_minus_zero(c[k][j]);
+            if (live && here)
+                *reinterpret_cast<uint4 *>(codes + kv8_code_byte(D, s0 + slot, piece * 16)) = make_uint4(c[k][0], c[k][1], c[k][2], c[k][3]);
             if (held) {
                 const float s = nan ? NAN : scale;
                 uint32_t o[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 u = kv8_numbers(c[j]), v = kv8_numbers(c[j] >> 16);
+                    const float2 u = kv8_numbers(c[k][j]), v = kv8_numbers(c[k][j] >> 16);
                     o[2 * j] = kv8_pack<kBF16>(u.x * s, u.y * s), o[2 * j + 1] = kv8_pack<kBF16>(v.x * s, v.y * s);
                 }
                 uint4 *to = reinterpret_cast<uint4 *>(held + ((int64_t(b) * a.T + t) * a.H + h) * D + piece * 16);
