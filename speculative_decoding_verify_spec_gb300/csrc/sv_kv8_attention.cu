@@ -31,8 +31,10 @@ cudaError_t launch_wide8_of<256, 3>(const Att8Args &a, int grid, cudaStream_t s)
 
 namespace {
 
-// More rows than this a kv head go to the kernel for many rows.
-constexpr int kNarrowRows8 = 64;
+// More rows than this a kv head go to the kernel for many rows.  64 sequences of up to 2047 cached tokens (1500 of 256 dimensions), 4 kv heads, us
+// in tiles of up to 64 (48) rows and in one of 128: 64 dimensions, bf16, 48 rows 51 and 58, 64 rows 62 and 59; 128 dimensions, rotated
+// bf16, 64 rows 71 and 84, 72 rows 90 and 81, 96 rows 97 and 86; 256 dimensions, rotated bf16, 96 rows 118 and 165, 112 rows 197 and 175.
+constexpr int narrow_rows8(int D) { return D == 256 ? 96 : 64; }
 
 struct Att8Layout {
     size_t desc, ml, acc, parts, see, total;
@@ -41,8 +43,8 @@ struct Att8Layout {
 };
 Att8Layout att8_layout(int B, int T, int H, int64_t rows, int D) {
     Att8Layout L;
-    L.wide = rows > kNarrowRows8;
-    L.nr = L.wide ? kWideRows8 : att8_rows(rows);
+    L.wide = rows > narrow_rows8(D);
+    L.nr = L.wide ? kWideRows8 : att8_rows(rows, D);
     L.tile = L.wide ? wide8_tile(D) : kTile8;
     L.grid = kAttSMs * (L.wide ? wide8_occupancy(D) : att8_occupancy(D, L.nr));
     L.see_words = L.wide ? (T + 31) / 32 : (L.nr + 31) / 32;

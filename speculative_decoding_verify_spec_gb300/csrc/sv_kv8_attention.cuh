@@ -42,12 +42,14 @@ __host__ __device__ constexpr int att8_stages(int D, int NR) { return D == 64 ? 
 __host__ __device__ constexpr int att8_value_stages(int D, int NR) {
     return D == 256 ? (NR == 32 ? 3 : NR == 16 ? 3 : 2) : D == 128 && NR == 16 ? 3 : att8_stages(D, NR);
 }
-__host__ __device__ constexpr int att8_q_places(int D, int NR) { return D == 256 && NR >= 48 ? 1 : 2; }
+__host__ __device__ constexpr int att8_q_places(int D, int NR) { return D == 256 && NR == 48 ? 1 : 2; }
 __host__ __device__ constexpr int att8_w_places(int D, int NR) { return NR >= 48 || D == 256 || (D == 128 && NR == 32) ? 1 : 2; }
 __host__ __device__ constexpr int att8_occupancy(int D, int NR) { return D == 256 || NR >= 48 ? 1 : 2; }
-// Rows a tile, by the rows that share a kv head: as few tiles of up to 64 as there have to be, and no larger than they need be.
-inline int att8_rows(int64_t rows) {
-    const int64_t tiles = (rows + 63) / 64;
+// Rows a tile, by the rows that share a kv head: as few tiles as there have to be, and no larger than they need be.  At most 64; 48 of 256
+// dimensions, where 64 rows took 114 us in one tile and 72 rows 111 us in two (64 sequences of up to 1500 tokens, 4 kv heads, bf16).
+constexpr int att8_cap(int D) { return D == 256 ? 48 : 64; }
+inline int att8_rows(int64_t rows, int D) {
+    const int64_t tiles = (rows + att8_cap(D) - 1) / att8_cap(D);
     return int((rows + tiles * kGroupRows8 - 1) / (tiles * kGroupRows8)) * kGroupRows8;
 }
 
@@ -837,10 +839,12 @@ cudaError_t launch_attention8_rows(const Att8Args &a, int grid, cudaStream_t s);
     cudaError_t launch_attention8_rows<D, NP>(const Att8Args &a, int grid, cudaStream_t s) {    \
         cudaError_t e = launch_queries8<D>(a, s);                                                              \
         if (e != cudaSuccess) return e;                                                                       \
+        if constexpr (att8_cap(D) >= 64) {                                                                    \
+            if (a.nr == 64) return launch_attention8<D, 64, NP>(a, grid, s);                                   \
+        }                                                                                                     \
         return a.nr == 16   ? launch_attention8<D, 16, NP>(a, grid, s)                                         \
                : a.nr == 32 ? launch_attention8<D, 32, NP>(a, grid, s)                                         \
-               : a.nr == 48 ? launch_attention8<D, 48, NP>(a, grid, s)                                         \
-                            : launch_attention8<D, 64, NP>(a, grid, s);                                        \
+                            : launch_attention8<D, 48, NP>(a, grid, s);                                        \
     }
 
 }  // namespace sv
