@@ -162,7 +162,8 @@ size_t spec_kv8_page_bytes(int page_size, int head_dim);
 
 /*
  * Appends T new tokens per sequence.  Arguments as for spec_kv_append.  Tokens of k_values, v_values that are dropped
- * get what they would have been held as in a block without older tokens.
+ * get what they would have been held as in a block without older tokens.  Two sequences must not append to the same block
+ * of 16 slots (its scale is theirs together).  No workspace.
  */
 sv_status spec_kv8_append(const void *k, int64_t k_batch_stride, int64_t k_token_stride, int64_t k_head_stride,
                           const void *v, int64_t v_batch_stride, int64_t v_token_stride, int64_t v_head_stride,
@@ -185,7 +186,8 @@ sv_status spec_kv8_read(const void *cache, int num_pages, int page_size, int B, 
 
 /*
  * Attention of the T new tokens over the cache, which holds them already.  Arguments, workspace and status as for
- * spec_kv_attention.  A row that sees a token whose key or value is held as NaN is NaN.
+ * spec_kv_attention.  A row that sees a token whose key or value is held as NaN is NaN, and so is one whose query has a NaN or
+ * an infinity.  The workspace grows with the batch: the queries are kept there in parts.
  */
 size_t spec_kv8_attention_workspace_size(int B, int T, int heads, int kv_heads, int head_dim);
 sv_status spec_kv8_attention(const void *q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,

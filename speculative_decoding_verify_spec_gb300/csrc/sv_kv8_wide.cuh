@@ -9,6 +9,10 @@
 // multiplication that scales a score.  Two or four groups of 128 threads have the 128 rows each, and their share of
 // the tile's tokens and of the output's dimensions.  The scores are read from tensor memory twice, for the maximum and for the weights, 16 tokens
 // at a time, instead of kept.  As there, every tile has its own m and output, which is added up in registers.
+//
+// Measured: 64 x 64 tree nodes with 4 query heads a kv head over up to 2047 tokens, us: 64 dimensions, bf16 114, fp16 128; 128 dimensions, rotated, bf16
+// 158, fp16 174; 256 dimensions, rotated, 367 and 417.  At 64 dimensions that is 2.1 instructions a clock (of 4), the tensor pipe at 24 %: a tile's path
+// through a block (scores, maximum, barrier, weights, product) is covered by the other block of the SM only in part.
 #pragma once
 
 #include "sv_kv8_attention.cuh"
