@@ -13,9 +13,9 @@
 // times an fp32 angle is exact and one subtraction rounds; a lane collects its codes in doubt first, so that the lanes' ones go side by side.
 //
 // Everything is read once and written once; 16 bits in, 8 out (and 16 where the values held are wanted).  Measured, with the values held:
-// 8 prompts of up to 2001 tokens, 16 heads of 64, fp16, 49 us (2.9 TB/s); one of 16384 tokens, 4 heads of 256, bf16, 59 us (3.1 TB/s), 47
-// without a rotation; 256 x 9 drafts, 8 heads of 128, 16 us.  It waits for loads (a block's lengths, then its page and rows, then its angles)
-// with 18 and 25 warps an SM under way, and issues 1.7 instructions a clock.  Blocks that take several items in turn were slower (88 us for 59).
+// 8 prompts of up to 2001 tokens, 16 heads of 64, fp16, 41 us (3.5 TB/s); one of 16384 tokens, 4 heads of 256, bf16, 50 us (3.7 TB/s);
+// 256 x 9 drafts, 8 heads of 128, 16 us.  It waits for loads (a block's lengths, then its page and rows, then its angles) with 18 and 25 warps
+// an SM under way, and issues 2 instructions a clock.  Blocks that take several items in turn were slower (88 us for 59, before rows went in 32 bytes).
 #include <cstdint>
 
 #include "sv_checks.cuh"
@@ -37,6 +37,7 @@ struct Append8Args {
     const int32_t *table, *start, *new_lens;
     Rotation rot;
     uint16_t *k_values, *v_values;
+    bool whole_in, whole;  // all rows of k and v, of k_values and v_values are on the 32-byte grid
 };
 
 // How rows and rotation lie: any way; on the 16-byte grid, and the rotation's partners whole pieces apart (or no rotation);
@@ -55,10 +56,9 @@ __device__ __forceinline__ void pieces_of(int pairs, int unit, int &lo, int &hi)
 }
 
 template <Layout8 kLayout>
-__device__ __forceinline__ void load_piece(const uint16_t *p, uint32_t (&w)[8]) {
+__device__ __forceinline__ void load_piece(const uint16_t *p, uint32_t (&w)[8], bool whole) {
     if (kLayout != kAny8) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p)), y = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+        kv8_load_row(p, w, whole);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = uint32_t(__ldg(p + 2 * i)) | uint32_t(__ldg(p + 2 * i + 1)) << 16;
@@ -158,6 +158,13 @@ __device__ __noinline__ uint32_t code_exactly(double x) {
     return uint32_t(n >= 8 ? (e + 6) * 8 + n : n) | (x < 0 ? 128u : 0u);                    // (16: the next exponent's first)
 }
 
+// The larger one, NaN if there is one.
+__device__ __forceinline__ float max_or_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
 template <int D, Layout8 kLayout, bool kBF16>
 __global__ void __launch_bounds__(kApp8Threads) kv8_append_kernel(const Append8Args a) {
     constexpr int W = D / 64, kItems = kApp8Threads / 32 / W;  // warps of a block of slots, and those blocks of a thread block
@@ -200,15 +207,12 @@ __global__ void __launch_bounds__(kApp8Threads) kv8_append_kernel(const Append8A
     bool fine = true;
     if (live) {
         uint32_t raw[2][8];
-        load_piece<kLayout>(row + p * 16, raw[0]), load_piece<kLayout>(row + q * 16, raw[1]);
+        load_piece<kLayout>(row + p * 16, raw[0], a.whole_in), load_piece<kLayout>(row + q * 16, raw[1], a.whole_in);
         if (rot.cos) angles = kv_rotation_row(rot, int64_t(b) * a.T + t, before, int(t));
         rotated<kLayout, kBF16>(rot, row, angles, p, q, raw, x, most);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) largest = fmaxf(largest, fmaxf(fabsf(x[0][j]), fabsf(x[1][j])));
-        float sum = 0.f;  // finite if every number is
-#pragma unroll
-        for (int j = 0; j < 16; ++j) sum += fabsf(x[0][j]) * 0.f + fabsf(x[1][j]) * 0.f;
-        fine = sum == 0.f && most < INFINITY;
+        for (int j = 0; j < 16; ++j) largest = max_or_nan(max_or_nan(largest, fabsf(x[0][j])), fabsf(x[1][j]));
+        fine = largest < INFINITY && most < INFINITY;
     }
     const bool here = pg >= 0 && pg < a.num_pages && SV_IN(kv8_code_byte(D, s0 + kKv8Block - 1, D - 1), a.page * D);
     uint8_t *base = here ? a.cache + (int64_t(pg) * a.H + h) * kv8_page_bytes(a.page, D) : nullptr;
@@ -317,8 +321,7 @@ __global__ void __launch_bounds__(kApp8Threads) kv8_append_kernel(const Append8A
                     const float2 u = kv8_numbers(c[k][j]), v = kv8_numbers(c[k][j] >> 16);
                     o[2 * j] = kv8_pack<kBF16>(u.x * s, u.y * s), o[2 * j + 1] = kv8_pack<kBF16>(v.x * s, v.y * s);
                 }
-                uint4 *to = reinterpret_cast<uint4 *>(held + ((int64_t(b) * a.T + t) * a.H + h) * D + piece * 16);
-                to[0] = make_uint4(o[0], o[1], o[2], o[3]), to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                kv8_store_row(held + ((int64_t(b) * a.T + t) * a.H + h) * D + piece * 16, o, a.whole);
             }
         }
     }
@@ -397,6 +400,8 @@ extern "C" sv_status spec_kv8_append(const void *k, int64_t k_batch_stride, int6
     a.table = page_table, a.start = start, a.new_lens = new_lens;
     a.rot = sv::Rotation{cos, sin, table_len, cos ? pairs : 0, interleaved != 0, positions};
     a.k_values = static_cast<uint16_t *>(k_values), a.v_values = static_cast<uint16_t *>(v_values);
+    a.whole = (reinterpret_cast<uintptr_t>(k_values) | reinterpret_cast<uintptr_t>(v_values)) % 32 == 0;
+    a.whole_in = all % 16 == 0 && (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 32 == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == SV_KV_BF16;
     const cudaError_t e = head_dim == 64    ? sv::launch_append8<64>(a, layout, bf16, s)

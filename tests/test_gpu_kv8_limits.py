@@ -74,3 +74,32 @@ def test_a_query_that_is_no_number_is_its_own_row_only(T, G):
         assert torch.isnan(got[at]).all()
         got[at] = want[at] = 0
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("off", [8, 3])
+def test_rows_off_the_32_byte_grid(interleaved, off):
+    """Rows, angles and results on the 16-byte grid only (rows off that too) hold and give back what those on the 32-byte grid do."""
+    g = torch.Generator().manual_seed(off)
+    B, T, H, D, page = 2, 40, 2, 128, 16
+
+    def shifted(x, n):
+        room = torch.zeros(x.numel() + n, dtype=x.dtype, device=DEV)
+        room[n:] = x.reshape(-1)
+        return room[n:].view(x.shape)
+
+    k, v = (dev(torch.randn((B, T, H, D), generator=g).to(torch.float16)) for _ in range(2))
+    cos, sin = U.tables(T + 20, D // 2, DEV)
+    table = torch.arange(B * 4, dtype=torch.int32, device=DEV).view(B, 4)
+    results = []
+    for move in (0, 1):
+        cache = torch.zeros((B * 4, H, page * (2 * D + 1)), dtype=torch.uint8, device=DEV)
+        x, y, c, s = (shifted(t, move * n) for t, n in ((k, off), (v, off), (cos, 4), (sin, 4)))
+        hk, hv, rk, rv = (shifted(torch.zeros_like(k), move * 8) for _ in range(4))
+        assert all((t.data_ptr() % 32 != 0) == bool(move) for t in (x, y, c, s, hk, hv, rk, rv))
+        sv.spec_kv8_append(x, y, cache, table, int32(5, 20), cos=c, sin=s, interleaved=interleaved, return_values=True, k_values=hk, v_values=hv)
+        sv.spec_kv8_read(cache, table, int32(5, 20), T, dtype=torch.float16, k=rk, v=rv)
+        results.append((cache, hk, hv, rk, rv))
+    assert results[0][1].any()
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
