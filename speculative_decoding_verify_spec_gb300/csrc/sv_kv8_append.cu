@@ -13,8 +13,8 @@
 // times an fp32 angle is exact and one subtraction rounds; a lane collects its codes in doubt first, so that the lanes' ones go side by side.
 //
 // Everything is read once and written once; 16 bits in, 8 out (and 16 where the values held are wanted).  Measured, with the values held:
-// 8 prompts of up to 2001 tokens, 16 heads of 64, fp16, 41 us (3.5 TB/s); one of 16384 tokens, 4 heads of 256, bf16, 50 us (3.7 TB/s);
-// 256 x 9 drafts, 8 heads of 128, 16 us.  It waits for loads (a block's lengths, then its page and rows, then its angles) with 18 and 25 warps
+// 8 prompts of up to 2001 tokens, 16 heads of 64, fp16, 41 us (3.5 TB/s); one of 16384 tokens, 4 heads of 256, bf16, 46 us (4.0 TB/s), 38 without a rotation;
+// 256 x 9 drafts, 8 heads of 128, 16 us.  It waits for loads (a block's lengths, then its page and rows, then its angles) with 18 and 24 warps
 // an SM under way, and issues 2 instructions a clock.  Blocks that take several items in turn were slower (88 us for 59, before rows went in 32 bytes).
 #include <cstdint>
 
@@ -37,7 +37,7 @@ struct Append8Args {
     const int32_t *table, *start, *new_lens;
     Rotation rot;
     uint16_t *k_values, *v_values;
-    bool whole_in, whole;  // all rows of k and v, of k_values and v_values are on the 32-byte grid
+    bool whole_in, whole, whole_angles;  // all rows of k and v, of k_values and v_values, of the angles are on the 32-byte grid
 };
 
 // How rows and rotation lie: any way; on the 16-byte grid, and the rotation's partners whole pieces apart (or no rotation);
@@ -70,10 +70,18 @@ __device__ __forceinline__ float2 widen2(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
+// Eight angles.  (Those of neighbours are taken by fours: by eights, prompts of 64 dimensions took 41.9 us for 41.0.)
+__device__ __forceinline__ void load_angles(const float *p, bool whole, float (&x)[8]) {
+    uint32_t w[8];
+    kv8_load_row(reinterpret_cast<const uint16_t *>(p), w, whole);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+}
+
 // The raw pair w (piece lo, piece hi) as floats, rotated; `most` takes the largest |a cos| + |b sin|.
 template <Layout8 kLayout, bool kBF16>
 __device__ __forceinline__ void rotated(const Rotation &rot, const uint16_t *row, int64_t angles, int lo, int hi, const uint32_t (&w)[2][8],
-                                        float (&x)[2][16], float &most) {
+                                        float (&x)[2][16], float &most, bool whole) {
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -86,11 +94,11 @@ __device__ __forceinline__ void rotated(const Rotation &rot, const uint16_t *row
     if constexpr (kLayout == kHalves8) {
         if (lo * 16 >= rot.pairs) return;
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            const float4 cv = __ldg(reinterpret_cast<const float4 *>(cp + lo * 16 + i)), sv = __ldg(reinterpret_cast<const float4 *>(sp + lo * 16 + i));
-            const float c[4] = {cv.x, cv.y, cv.z, cv.w}, s[4] = {sv.x, sv.y, sv.z, sv.w};
+        for (int i = 0; i < 16; i += 8) {
+            float c[8], s[8];
+            load_angles(cp + lo * 16 + i, whole, c), load_angles(sp + lo * 16 + i, whole, s);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 const float a = x[0][i + j], b = x[1][i + j];
                 most = fmaxf(most, (fabsf(a) + fabsf(b)) * fmaxf(fabsf(c[j]), fabsf(s[j])));
                 x[0][i + j] = fmaf(a, c[j], -b * s[j]), x[1][i + j] = fmaf(b, c[j], a * s[j]);
@@ -209,7 +217,7 @@ __global__ void __launch_bounds__(kApp8Threads) kv8_append_kernel(const Append8A
         uint32_t raw[2][8];
         load_piece<kLayout>(row + p * 16, raw[0], a.whole_in), load_piece<kLayout>(row + q * 16, raw[1], a.whole_in);
         if (rot.cos) angles = kv_rotation_row(rot, int64_t(b) * a.T + t, before, int(t));
-        rotated<kLayout, kBF16>(rot, row, angles, p, q, raw, x, most);
+        rotated<kLayout, kBF16>(rot, row, angles, p, q, raw, x, most, a.whole_angles);
 #pragma unroll
         for (int j = 0; j < 16; ++j) largest = max_or_nan(max_or_nan(largest, fabsf(x[0][j])), fabsf(x[1][j]));
         fine = largest < INFINITY && most < INFINITY;
@@ -401,6 +409,7 @@ extern "C" sv_status spec_kv8_append(const void *k, int64_t k_batch_stride, int6
     a.rot = sv::Rotation{cos, sin, table_len, cos ? pairs : 0, interleaved != 0, positions};
     a.k_values = static_cast<uint16_t *>(k_values), a.v_values = static_cast<uint16_t *>(v_values);
     a.whole = (reinterpret_cast<uintptr_t>(k_values) | reinterpret_cast<uintptr_t>(v_values)) % 32 == 0;
+    a.whole_angles = pairs % 8 == 0 && (reinterpret_cast<uintptr_t>(cos) | reinterpret_cast<uintptr_t>(sin)) % 32 == 0;
     a.whole_in = all % 16 == 0 && (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 32 == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == SV_KV_BF16;
