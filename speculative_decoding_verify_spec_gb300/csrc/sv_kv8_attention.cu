@@ -4,17 +4,17 @@
 namespace sv {
 
 template <>
-cudaError_t launch_attention8_rows<64, 2>(const Att8Args &a, int grid, cudaStream_t s);
-template <>
 cudaError_t launch_attention8_rows<64, 3>(const Att8Args &a, int grid, cudaStream_t s);
 template <>
-cudaError_t launch_attention8_rows<128, 2>(const Att8Args &a, int grid, cudaStream_t s);
+cudaError_t launch_attention8_rows<64, 4>(const Att8Args &a, int grid, cudaStream_t s);
 template <>
 cudaError_t launch_attention8_rows<128, 3>(const Att8Args &a, int grid, cudaStream_t s);
 template <>
-cudaError_t launch_attention8_rows<256, 2>(const Att8Args &a, int grid, cudaStream_t s);
+cudaError_t launch_attention8_rows<128, 4>(const Att8Args &a, int grid, cudaStream_t s);
 template <>
 cudaError_t launch_attention8_rows<256, 3>(const Att8Args &a, int grid, cudaStream_t s);
+template <>
+cudaError_t launch_attention8_rows<256, 4>(const Att8Args &a, int grid, cudaStream_t s);
 
 template <>
 cudaError_t launch_wide8_of<64, 2>(const Att8Args &a, int grid, cudaStream_t s);
@@ -135,11 +135,11 @@ sv_status spec_kv8_attention(const void *q, int64_t q_batch_stride, int64_t q_to
             : a.bf16          ? sv::launch_wide8_of<256, 2>(a, grid, s)
                               : sv::launch_wide8_of<256, 3>(a, grid, s);
     else if (head_dim == 64)
-        e = a.bf16 ? sv::launch_attention8_rows<64, 2>(a, grid, s) : sv::launch_attention8_rows<64, 3>(a, grid, s);
+        e = a.bf16 ? sv::launch_attention8_rows<64, 3>(a, grid, s) : sv::launch_attention8_rows<64, 4>(a, grid, s);
     else if (head_dim == 128)
-        e = a.bf16 ? sv::launch_attention8_rows<128, 2>(a, grid, s) : sv::launch_attention8_rows<128, 3>(a, grid, s);
+        e = a.bf16 ? sv::launch_attention8_rows<128, 3>(a, grid, s) : sv::launch_attention8_rows<128, 4>(a, grid, s);
     else
-        e = a.bf16 ? sv::launch_attention8_rows<256, 2>(a, grid, s) : sv::launch_attention8_rows<256, 3>(a, grid, s);
+        e = a.bf16 ? sv::launch_attention8_rows<256, 3>(a, grid, s) : sv::launch_attention8_rows<256, 4>(a, grid, s);
     return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 

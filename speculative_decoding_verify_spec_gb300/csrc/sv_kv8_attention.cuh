@@ -8,13 +8,17 @@
 //   S [128 tokens x rows]     = K codes [128 x D]  times  q^T          D / 32 steps a part of q
 //   O [D (128) x rows]        = V codes^T [D x 128]  times  w          4 steps a part of w
 // The other operands are 8-bit floats too, so a query and a weight are held as sums of parts, each the rounding of what the parts
-// before it left: two have the 8 bits of a bfloat16, three 12.  A part's products are summed in fp32 with the others', which
+// before it left.  A query's have 4 bits each: two hold the 8 bits of a bfloat16, three 12.  A part's products are summed in fp32 with the others', which
 // costs no more than one product in 16 bits would.
 //
-// Weights of 8 bits reach down to 2^-18 of the largest at most.  So every tile of 128 tokens has its own m, a whole number (the rounded
-// largest t of the row's tokens that it sees, less 8), and its own O, which is added to the row's sums in registers times 2^(m -
-// M), with M the row's first m; M moves only when a later m is 60 above it.  Hidden or far heavier tokens of other
-// tiles take no bits from a tile's weights.
+// Weights span far more than such floats do: next to a token with nearly all of the probability, or in a tile with a block whose scale is
+// 2^30 above its neighbours', it is the small ones that may make the result, for nothing says that the large one's value is not 0.  So
+// their parts have 5 bits of exponent and 3 bits each (three hold 11 bits, for bf16 outputs, four 15, for fp16 ones), and two ranges: weights from
+// 2^-23 of the tile's largest on (2^-20 with four parts), and those below, times 2^23 (2^20), in columns of their own, whose sums come back times
+// 2^-23.  A weight is off by 2^-11 of itself (2^-15), near a range's lower end by 2^-8.6 (2^-12), and below both by 2^-51.5 of the largest at most.
+//
+// Every tile of 128 tokens has its own m, a whole number (the rounded largest t of the row's tokens that it sees, less 15), and its own O, which is added
+// to the row's sums in registers times 2^(m - M), with M the row's first m; M moves only when a later m is 60 above it.
 //
 // The queries' parts come from a kernel of their own.  A block of the attention has a warp that copies tiles and queries into rings in
 // shared memory (keys and values apart: a key's place is free once its scores are there), a thread that issues the
@@ -27,11 +31,11 @@
 // Work: all tiles of the batch form one list that is cut into equal shares, as in sv_kv_attention.cuh, whose list, descriptors
 // and join of split segments these are.
 //
-// Measured, and what bounds it.  256 single tokens with 8 heads a kv head over 4600 cached ones on average: 372 us in a graph, 6.5 TB/s, 97 % of
-// a plain copy's rate.  6 drafts over 200001 tokens, 256 dimensions: 85 us, 4.8 TB/s; there and with more rows the path of a
-// tile through a block counts, which one block an SM does not cover: 64 x 9 drafts with 4 heads a kv head (36 rows) take 128 us, 2.1 us a
-// tile, with 2.0 instructions a clock, the tensor pipe at 41 % and the memory at 33 %.  A product of 128 x N x 32 takes 48 clocks or less up to
-// N = 64 and N / 2 from there, measured, so that parts cost little.
+// Measured, and what bounds it.  256 single tokens with 8 heads a kv head over 4600 cached ones on average: 392 us in a graph, 6.2 TB/s, 92 % of
+// a plain copy's rate.  6 drafts over 200001 tokens, 256 dimensions: 99 us, 4.1 TB/s; there and with more rows the path of a
+// tile through a block counts, which one block an SM does not cover: 64 x 9 drafts with 4 heads a kv head (36 rows) take 147 us, 2.4 us a
+// tile.  (With two parts of 4 bits a weight and one range, which lost weights of 2^-18 of the largest, these took 372, 85 and 128 us.)  A product of 128 x N x 32
+// takes 45 clocks up to N = 48, 48 for 64, 56 for 96 and 65 for 128 columns, measured, so that parts and ranges cost little there.
 #pragma once
 
 #include "sv_kv8.cuh"
@@ -43,13 +47,12 @@ constexpr int kTile8 = 128;
 constexpr int kGroupRows8 = 16;  // query rows of a softmax group
 __host__ __device__ constexpr int att8_groups(int NR) { return NR / kGroupRows8; }
 __host__ __device__ constexpr int att8_threads(int NR) { return 64 + 128 * att8_groups(NR); }
-// Tiles in the rings, places for queries and weights, and blocks an SM: by shared memory and registers.
+// Tiles in the rings, places for queries, and blocks an SM: by shared memory and registers.
 __host__ __device__ constexpr int att8_stages(int D, int NR) { return D == 64 ? (NR == 16 ? 5 : NR == 32 ? 4 : 6) : D == 128 ? (NR <= 32 ? 2 : 3) : (NR == 16 ? 3 : 2); }
 __host__ __device__ constexpr int att8_value_stages(int D, int NR) {
-    return D == 256 ? (NR == 32 ? 3 : NR == 16 ? 3 : 2) : D == 128 && NR == 16 ? 3 : att8_stages(D, NR);
+    return D == 256 ? (NR == 48 ? 2 : 3) : D == 128 && NR == 16 ? 3 : D == 64 && NR == 32 ? 3 : att8_stages(D, NR);
 }
-__host__ __device__ constexpr int att8_q_places(int D, int NR) { return D == 256 && NR == 48 ? 1 : 2; }
-__host__ __device__ constexpr int att8_w_places(int D, int NR) { return NR >= 48 || D == 256 || (D == 128 && NR == 32) ? 1 : 2; }
+__host__ __device__ constexpr int att8_q_places(int D, int NR) { return D == 256 || (D == 128 && NR == 32) ? 1 : 2; }
 __host__ __device__ constexpr int att8_occupancy(int D, int NR) { return D == 256 || NR >= 48 ? 1 : 2; }
 // Rows a tile, by the rows that share a kv head: as few tiles as there have to be, and no larger than they need be.  At most 64; 48 of 256
 // dimensions, where 64 rows took 114 us in one tile and 72 rows 111 us in two (64 sequences of up to 1500 tokens, 4 kv heads, bf16).
@@ -59,6 +62,7 @@ inline int att8_rows(int64_t rows, int D) {
     return int((rows + tiles * kGroupRows8 - 1) / (tiles * kGroupRows8)) * kGroupRows8;
 }
 
+constexpr float kTop8 = 15.f;  // log2 of the largest weight
 enum : int { kMasked8 = 1, kRagged8 = 2, kFirst8 = 4, kLast8 = 8 };  // in Unit::masked: not every row sees every token; not every token is there; of a segment
 
 // Bytes of a segment's queries: three parts, laid out as the keys, and the rows' factors.
@@ -81,15 +85,17 @@ struct alignas(16) Info8 {
 template <int D, int NR, int NP>
 struct Att8Shared {
     static constexpr int kDims = D, kRows = NR, kTile = kTile8, W = att8_groups(NR), RW = kGroupRows8, SW = (NR + 31) / 32, kStages = att8_stages(D, NR), kValues = att8_value_stages(D, NR), kInfos = kStages + 2;
-    static constexpr int kQ = att8_q_places(D, NR), kP = att8_w_places(D, NR), MB = D == 256 ? 2 : 1;
+    static constexpr int kQ = att8_q_places(D, NR), MB = D == 256 ? 2 : 1;
     // Few rows: a product reads the cache's operand at its full width whatever the columns, so the parts are columns of
     // one product and are added up afterwards.
-    static constexpr bool kStackQ = NR == 16 || (D == 256 && NR == 32), kStackP = NR == 16 || (D == 256 && NR == 32 && NP == 2);
-    static constexpr int kScoreCols = kStackQ ? (NR == 16 ? 64 : 96) : NR == 32 ? 32 : 64, kOutEach = NR >= 48 || (kStackP && NP * NR > 32) ? 64 : 32, kOutCols = MB * kOutEach;
+    static constexpr bool kStackQ = NR == 16 || (D == 256 && NR == 32);
+    // A part of the weights has the rows' columns twice (one of a weight's two is 0).  16 rows: the first two parts side by side.
+    static constexpr int kStackP = NR == 16 ? 2 : 1;
+    static constexpr int kScoreCols = kStackQ ? (NR == 16 ? 64 : 96) : NR == 32 ? 32 : 64, kOutEach = 2 * kStackP * NR, kOutCols = MB * kOutEach;
     static constexpr int kUsed = 2 * (kScoreCols + kOutCols), kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     alignas(128) uint8_t k[kStages][kTile8 * D];
     uint8_t v[kValues][kTile8 * D];       // (64 dimensions: a product's upper 64 rows read past the end, into w)
-    uint8_t w[kP][NP * NR * kTile8];      // [part][16 rows][token][16 bytes]
+    uint8_t w[NP][2][NR * kTile8];        // [part][of the upper range, of the lower one][16 rows][token][16 bytes]
     struct Queries {
         uint8_t part[3][NR * D];
         float factor[NR];                 // log2(e) scale times the power of two taken out of the row
@@ -110,8 +116,8 @@ struct Att8Shared {
 // first distance, and the second.  Later steps are sums with the first word (computed anew, a descriptor cost the issuing thread 150 clocks a product).
 __device__ __forceinline__ uint32_t operand8(uint32_t addr, uint32_t along_k) { return (addr & 0x3FFFF) >> 4 | along_k >> 4 << 16; }
 __host__ __device__ constexpr uint32_t operand8_high(uint32_t across) { return across >> 4 | 1u << 14; }
-// 8-bit floats (4 bits of exponent) into fp32, 128 rows, N columns; `turned`: both operands have their rows contiguous.
-__device__ __forceinline__ constexpr uint32_t kind8(int N, bool turned) { return 1u << 4 | (turned ? 3u << 15 : 0u) | uint32_t(N / 8) << 17 | 8u << 24; }
+// 8-bit floats (4 bits of exponent; `five`: 5 in the second operand) into fp32, 128 rows, N columns; `turned`: both operands have their rows contiguous.
+__device__ __forceinline__ constexpr uint32_t kind8(int N, bool turned, bool five = false) { return 1u << 4 | (five ? 1u << 10 : 0u) | (turned ? 3u << 15 : 0u) | uint32_t(N / 8) << 17 | 8u << 24; }
 __device__ __forceinline__ void mma8(uint32_t d, uint32_t a, uint32_t a_high, uint32_t b, uint32_t b_high, uint32_t kind, bool add) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tsetp.ne.u32 p, %6, 0;\n\t"
@@ -172,6 +178,63 @@ __device__ __forceinline__ void parts8(Two v, Two w, uint32_t (&c)[NP]) {
             v = fma2(fma2(fma2(v, minus, m), minus, m), minus, v);  // v - (m - (m - v))
             w = fma2(fma2(fma2(w, minus, o), minus, o), minus, w);
         }
+    }
+}
+
+// The parts of four weights, the first one's in the lowest byte, a word for a part in the upper range and one in the lower range.  Weights are at most 2^15.5; those of
+// 2^-kLow on are taken as they are, those below times 2^kLift, into the parts of the lower range; a weight's parts in the other range are 0.  A part has
+// 3 bits and 5 of exponent: the upper byte of a 16-bit float, so that a part is one addition (to the nearest) and the next ones' sum one
+// exact subtraction there.  Three parts hold the 11 bits of such a float; the fourth is what the float left of the weight.
+template <int NP>
+struct Weights8 {
+    static constexpr int kLow = NP == 3 ? 8 : 5, kLift = int(kTop8) + kLow;
+};
+__device__ __forceinline__ uint32_t half2_of(float2 x) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x.y), "f"(x.x));
+    return h;
+}
+__device__ __forceinline__ uint32_t half2_minus(uint32_t x, uint32_t y) {
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(y));
+    return x;
+}
+template <int NP>
+__device__ __forceinline__ void weight_parts8(const Two (&w)[2], uint32_t (&upper)[NP], uint32_t (&lower)[NP]) {
+    constexpr float lift = float(1 << Weights8<NP>::kLift);
+    constexpr uint32_t border = uint32_t(15 - Weights8<NP>::kLow) << 10 /* 2^-kLow */, nearest = 0x00800080u, high = 0xFF00FF00u;
+    uint32_t h[2], mask[2], part[2];
+    float2 rest[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const Two lifted = mul2(w[i], two(lift, lift));
+        const uint32_t up = half2_of(split(w[i])), low = half2_of(split(lifted));
+        asm("set.ge.u32.f16x2 %0, %1, %2;" : "=r"(mask[i]) : "r"(up), "r"(border << 16 | border));
+        h[i] = (up & mask[i]) | (low & ~mask[i]);
+        if (NP > 3) {
+            const __half2 h2 = *reinterpret_cast<const __half2 *>(&h[i]);
+            const float2 a = split(w[i]), b = split(lifted), f = __half22float2(h2);
+            rest[i] = make_float2((mask[i] & 1u ? a.x : b.x) - f.x, (mask[i] >> 16 ? a.y : b.y) - f.y);
+        }
+    }
+    const uint32_t which = __byte_perm(mask[0], mask[1], 0x7531);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        uint32_t round[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            round[i] = h[i] + nearest;
+            part[i] = round[i] & high;
+            if (k < 2) h[i] = half2_minus(h[i], part[i]);
+        }
+        const uint32_t code = __byte_perm(round[0], round[1], 0x7531);
+        upper[k] = code & which, lower[k] = code & ~which;
+    }
+    if (NP > 3) {
+        uint32_t code;
+        asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e5m2x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e5m2x2.f32 b, %4, %3;\n\tmov.b32 %0, {a, b};\n\t}"
+            : "=r"(code)
+            : "f"(rest[0].x), "f"(rest[0].y), "f"(rest[1].x), "f"(rest[1].y));
+        upper[NP - 1] = code & which, lower[NP - 1] = code & ~which;
     }
 }
 
@@ -383,17 +446,16 @@ __device__ __forceinline__ void issue_products8(const Att8Args &a, Att8Shared<D,
         if (!mbar_test(&sh.full_w[n & 1], uint32_t(n >> 1) & 1u) || !mbar_test(&sh.full_v[s], uint32_t(n / kValues) & 1u)) return false;
         if (n >= 2 && !mbar_test(&sh.free_o[n & 1], uint32_t((n >> 1) - 1) & 1u)) return false;
         fence_after();
-        constexpr int parts = Sh::kStackP ? 1 : NP, cols = Sh::kStackP ? NP * NR : NR;
         const uint32_t d = tmem + 2 * Sh::kScoreCols + (n & 1) * Sh::kOutCols;
-        const uint32_t v = operand8(smem_u32(sh.v[s]), 8 * D), w = operand8(smem_u32(sh.w[n % Sh::kP]), 128);
+        const uint32_t v = operand8(smem_u32(sh.v[s]), 8 * D), w = operand8(smem_u32(sh.w), 128);
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-            for (int p = 0; p < parts; ++p)
+            for (int p = 0; p < NP; p += Sh::kStackP)
 #pragma unroll
                 for (int i = 0; i < kTile8 / 32; ++i)
-                    mma8(d + mb * Sh::kOutEach, v + mb * 64 + i * 2 * D, operand8_high(128), w + p * NR * kTile8 / 16 + i * 32, operand8_high(2048),
-                         kind8(cols, true), p > 0 || i > 0);
+                    mma8(d + mb * Sh::kOutEach, v + mb * 64 + i * 2 * D, operand8_high(128), w + p * 2 * NR * kTile8 / 16 + i * 32, operand8_high(2048),
+                         kind8(2 * NR * (p + Sh::kStackP <= NP ? Sh::kStackP : 1), true, true), p > 0 || i > 0);
         wide_commit(&sh.empty_v[s]);
         wide_commit(&sh.full_o[n & 1]);
         return true;
@@ -570,29 +632,31 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
             if (failed) return;
             fence_after();
             if (writes) {
-                constexpr int parts = Sh::kStackP ? NP : 1;
+                constexpr int cols = 2 * Sh::kStackP;  // of a row: the ranges' parts
+                constexpr float lowered = 1.f / (1 << Weights8<NP>::kLift);
                 const uint32_t o_at = tmem_o + (n & 1) * Sh::kOutCols;
 #pragma unroll
                 for (int c = 0; c < RW / 8; ++c) {
                     if (8 * c >= live) continue;
-                    float o[MB][parts][8];
+                    float o[MB][cols][8];
 #pragma unroll
                     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-                        for (int p = 0; p < parts; ++p) tmem_get8(o[mb][p], o_at + mb * Sh::kOutEach + p * NR + 8 * c);
+                        for (int p = 0; p < cols; ++p) tmem_get8(o[mb][p], o_at + mb * Sh::kOutEach + p * NR + 8 * c);
                     tmem_loaded();
 #pragma unroll
                     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-                        for (int p = 0; p < parts; ++p) tmem_here(o[mb][p]);
+                        for (int p = 0; p < cols; ++p) tmem_here(o[mb][p]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float4 mv = sh.move[wg][quarter][n & 1][4 * c + j];
 #pragma unroll
                         for (int mb = 0; mb < MB; ++mb) {
-                            Two x = two(o[mb][0][2 * j], o[mb][0][2 * j + 1]);
-#pragma unroll
-                            for (int p = 1; p < parts; ++p) x = add2(x, two(o[mb][p][2 * j], o[mb][p][2 * j + 1]));
+                            Two x = two(o[mb][0][2 * j], o[mb][0][2 * j + 1]), y = two(o[mb][1][2 * j], o[mb][1][2 * j + 1]);
+                            if (Sh::kStackP == 2)
+                                x = add2(x, two(o[mb][cols - 2][2 * j], o[mb][cols - 2][2 * j + 1])), y = add2(y, two(o[mb][cols - 1][2 * j], o[mb][cols - 1][2 * j + 1]));
+                            x = fma2(y, two(lowered, lowered), x);
                             acc[mb][4 * c + j] = fma2(x, two(mv.z, mv.w), acc[mb][4 * c + j]);
                         }
                     }
@@ -703,7 +767,7 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                     if (M == -INFINITY) M = whole;
                     if (whole > M + 60.f) g = ex2(fmaxf(M - whole, -126.f)), M = whole;
                     f = ex2(fmaxf(whole - M, -127.f));
-                    minus = float(kKv8Top) - whole;
+                    minus = kTop8 - whole;
                 }
                 float *mv = reinterpret_cast<float *>(&sh.move[wg][quarter][n & 1][row / 2]);
                 if (lane < 16) mv[row & 1] = minus, mv[2 + (row & 1)] = f;
@@ -720,32 +784,33 @@ __global__ void __launch_bounds__(att8_threads(NR), att8_occupancy(D, NR)) kv8_a
                 __syncwarp();
             }
             // the weights
-            uint32_t code[4][NP] = {};
-            const Two inv2 = two(inv, inv);
-#pragma unroll
-            for (int c = 0; c < RW / 8; ++c) {
-                if (8 * c >= live) continue;
-#pragma unroll
-                for (int j = 0; j < 4; j += 2) {
-                    Two w[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int at = 4 * c + j + i;  // the pair of rows
-                        const float4 mv = sh.move[wg][quarter][n & 1][at];
-                        const float2 x = split(add2(two(t[2 * at], t[2 * at + 1]), two(mv.x, mv.y)));
-                        w[i] = two(ex2(x.x), ex2(x.y));
-                        l[at] = fma2(mul2(w[i], inv2), two(mv.z, mv.w), l[at]);
-                    }
-                    parts8(w[0], w[1], code[2 * c + j / 2]);
-                }
-            }
             const bool first = (flags & kFirst8) != 0, last = (flags & kLast8) != 0;
-            if (Sh::kP == 1 && !first) wait(&sh.full_o[(n & 1) ^ 1], uint32_t((n - 1) >> 1) & 1u);  // its weights are in this place
+            if (!first) wait(&sh.full_o[(n & 1) ^ 1], uint32_t((n - 1) >> 1) & 1u);  // the last unit's weights are in the place of these
             if (!failed) {
-                uint8_t *to = sh.w[n % Sh::kP] + wg * 2048 + token * 16;
-                if (live > 0) {
+                const Two inv2 = two(inv, inv);
+                uint8_t *to = sh.w[0][0] + wg * 2048 + token * 16;
 #pragma unroll
-                    for (int k = 0; k < NP; ++k) *reinterpret_cast<uint4 *>(to + k * NR * kTile8) = make_uint4(code[0][k], code[1][k], code[2][k], code[3][k]);
+                for (int c = 0; c < RW / 8; ++c) {
+                    if (8 * c >= live) continue;
+                    uint32_t upper[2][NP], lower[2][NP];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        Two w[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int at = 4 * c + 2 * j + i;  // the pair of rows
+                            const float4 mv = sh.move[wg][quarter][n & 1][at];
+                            const float2 x = split(add2(two(t[2 * at], t[2 * at + 1]), two(mv.x, mv.y)));
+                            w[i] = two(ex2(x.x), ex2(x.y));
+                            l[at] = fma2(mul2(w[i], inv2), two(mv.z, mv.w), l[at]);
+                        }
+                        weight_parts8<NP>(w, upper[j], lower[j]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < NP; ++k) {  // (both halves of 16 bytes at once were slower: their registers spill)
+                        *reinterpret_cast<uint2 *>(to + 2 * k * NR * kTile8 + 8 * c) = make_uint2(upper[0][k], upper[1][k]);
+                        *reinterpret_cast<uint2 *>(to + (2 * k + 1) * NR * kTile8 + 8 * c) = make_uint2(lower[0][k], lower[1][k]);
+                    }
                 }
                 if ((flags & kRagged8) && wg == 0 && inv == 0.f) {  // a code that is not there may be a NaN, which no weight of 0 takes away
                     uint8_t *v = sh.v[n % kValues];

@@ -1,6 +1,6 @@
-// sv_kv8_attention_128_exact.cu -- the attention kernels over the 8-bit cache for 128 dimensions, weights in three parts.
+// sv_kv8_attention_128_exact.cu -- the attention kernels over the 8-bit cache for 128 dimensions, weights in four parts.
 #include "sv_kv8_attention.cuh"
 
 namespace sv {
-SV_KV8_ATTENTION_INSTANTIATE(128, 3)
+SV_KV8_ATTENTION_INSTANTIATE(128, 4)
 }

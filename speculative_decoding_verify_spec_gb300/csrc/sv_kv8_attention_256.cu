@@ -1,6 +1,6 @@
-// sv_kv8_attention_256.cu -- the attention kernels over the 8-bit cache for 256 dimensions, weights in two parts.
+// sv_kv8_attention_256.cu -- the attention kernels over the 8-bit cache for 256 dimensions, weights in three parts.
 #include "sv_kv8_attention.cuh"
 
 namespace sv {
-SV_KV8_ATTENTION_INSTANTIATE(256, 2)
+SV_KV8_ATTENTION_INSTANTIATE(256, 3)
 }
