@@ -188,6 +188,10 @@ sv_status spec_kv8_read(const void *cache, int num_pages, int page_size, int B, 
  * Attention of the T new tokens over the cache, which holds them already.  Arguments, workspace and status as for
  * spec_kv_attention.  A row that sees a token whose key or value is held as NaN is NaN, and so is one whose query has a NaN or
  * an infinity.  The workspace grows with the batch: the queries are kept there in parts.
+ * What is rounded on the way, beside sums in fp32: a query's number by 2^-12 of itself (not at all if it is bf16 and not rotated) and by 2^-17 of
+ * its row's largest one; a token's weight (its probability times its value's scale) by 2^-8.6 of itself for bf16 results and by 2^-12
+ * for fp16 ones, and by 2^-51 of the largest weight that the row has among 128 neighbouring tokens.  So a token of nearly all of the probability, or
+ * a loud one in the same block, takes nothing from the others.  (More than 64 rows a kv head of 64 or 128 dimensions: 2^-17 of itself, and no more.)
  */
 size_t spec_kv8_attention_workspace_size(int B, int T, int heads, int kv_heads, int head_dim);
 sv_status spec_kv8_attention(const void *q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,

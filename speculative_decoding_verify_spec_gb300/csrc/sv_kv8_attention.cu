@@ -17,24 +17,18 @@ template <>
 cudaError_t launch_attention8_rows<256, 4>(const Att8Args &a, int grid, cudaStream_t s);
 
 template <>
-cudaError_t launch_wide8_of<64, 2>(const Att8Args &a, int grid, cudaStream_t s);
+cudaError_t launch_wide8_of<64>(const Att8Args &a, int grid, cudaStream_t s);
 template <>
-cudaError_t launch_wide8_of<64, 3>(const Att8Args &a, int grid, cudaStream_t s);
-template <>
-cudaError_t launch_wide8_of<128, 2>(const Att8Args &a, int grid, cudaStream_t s);
-template <>
-cudaError_t launch_wide8_of<128, 3>(const Att8Args &a, int grid, cudaStream_t s);
-template <>
-cudaError_t launch_wide8_of<256, 2>(const Att8Args &a, int grid, cudaStream_t s);
-template <>
-cudaError_t launch_wide8_of<256, 3>(const Att8Args &a, int grid, cudaStream_t s);
+cudaError_t launch_wide8_of<128>(const Att8Args &a, int grid, cudaStream_t s);
 
 namespace {
 
-// More rows than this a kv head go to the kernel for many rows.  64 sequences of up to 2047 cached tokens (1500 of 256 dimensions), 4 kv heads, us
-// in tiles of up to 64 (48) rows and in one of 128: 64 dimensions, bf16, 48 rows 51 and 58, 64 rows 62 and 59; 128 dimensions, rotated
-// bf16, 64 rows 71 and 84, 72 rows 90 and 81, 96 rows 97 and 86; 256 dimensions, rotated bf16, 96 rows 118 and 165, 112 rows 197 and 175.
-constexpr int narrow_rows8(int D) { return D == 256 ? 96 : 64; }
+// More rows than this a kv head go to the kernel for many rows.  4 kv heads, us in tiles of up to 64 rows and in one of 128; 64 sequences of up to 2047
+// cached tokens: 64 dimensions 48 rows 57 and 66, 64 rows 68 and 66, 80 rows 99 and 73 (fp16 72 and 65, 104 and 71 for the last two); 128 dimensions 64 rows
+// 75 and 90, 80 rows 107 and 91 (fp16 78 and 88, 115 and 89).  8 sequences of up to 8192: 64 dimensions 64 rows 38 and 41, 80 rows 48 and 45; 128 dimensions
+// 64 rows 40 and 49, 80 rows 50 and 50.  One of 16384 has too few segments for tiles of 128 rows, 22 and 33, 23 and 31 for 96 rows, but how
+// long the sequences are is on the GPU.  (bf16, rotated, unless it says fp16.)
+constexpr int64_t kNarrowRows8 = 64;
 
 struct Att8Layout {
     size_t desc, ml, acc, parts, see, total;
@@ -43,7 +37,7 @@ struct Att8Layout {
 };
 Att8Layout att8_layout(int B, int T, int H, int64_t rows, int D) {
     Att8Layout L;
-    L.wide = rows > narrow_rows8(D);
+    L.wide = wide8_has(D) && rows > kNarrowRows8;
     L.nr = L.wide ? kWideRows8 : att8_rows(rows, D);
     L.tile = L.wide ? wide8_tile(D) : kTile8;
     L.grid = kAttSMs * (L.wide ? wide8_occupancy(D) : att8_occupancy(D, L.nr));
@@ -130,10 +124,7 @@ sv_status spec_kv8_attention(const void *q, int64_t q_batch_stride, int64_t q_to
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (L.wide)
-        e = head_dim == 64    ? a.bf16 ? sv::launch_wide8_of<64, 2>(a, grid, s) : sv::launch_wide8_of<64, 3>(a, grid, s)
-            : head_dim == 128 ? a.bf16 ? sv::launch_wide8_of<128, 2>(a, grid, s) : sv::launch_wide8_of<128, 3>(a, grid, s)
-            : a.bf16          ? sv::launch_wide8_of<256, 2>(a, grid, s)
-                              : sv::launch_wide8_of<256, 3>(a, grid, s);
+        e = head_dim == 64 ? sv::launch_wide8_of<64>(a, grid, s) : sv::launch_wide8_of<128>(a, grid, s);
     else if (head_dim == 64)
         e = a.bf16 ? sv::launch_attention8_rows<64, 3>(a, grid, s) : sv::launch_attention8_rows<64, 4>(a, grid, s);
     else if (head_dim == 128)

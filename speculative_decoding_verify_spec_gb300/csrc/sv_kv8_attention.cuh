@@ -163,17 +163,16 @@ __device__ __forceinline__ bool group_or(bool x) {
     return r != 0;
 }
 
-// The parts of two pairs of numbers, NP times four codes (the first number's in the lowest byte).  A part is the number rounded to 4 bits, by
+// The three parts of two pairs of numbers, four codes each (the first number's in the lowest byte).  A part is the number rounded to 4 bits, by
 // the difference with a multiple of it (Dekker's splitting): the conversion to a code then rounds only what is below 2^-6, and a
 // conversion back would cost four times a conversion there.
-template <int NP>
-__device__ __forceinline__ void parts8(Two v, Two w, uint32_t (&c)[NP]) {
+__device__ __forceinline__ void parts8(Two v, Two w, uint32_t (&c)[3]) {
     const Two minus = two(-1.f, -1.f), split4 = two(1048577.f, 1048577.f);  // 2^20 + 1
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
+    for (int i = 0; i < 3; ++i) {
         const float2 f = split(v), g = split(w);
         c[i] = kv8_codes(f.x, f.y, g.x, g.y);
-        if (i + 1 < NP) {
+        if (i < 2) {
             const Two m = mul2(v, split4), o = mul2(w, split4);
             v = fma2(fma2(fma2(v, minus, m), minus, m), minus, v);  // v - (m - (m - v))
             w = fma2(fma2(fma2(w, minus, o), minus, o), minus, w);

@@ -1,13 +1,9 @@
-// sv_kv8_wide_64.cu -- the attention kernels over the 8-bit cache for many rows and 64 dimensions.
+// sv_kv8_wide_64.cu -- the attention kernel over the 8-bit cache for many rows and 64 dimensions.
 #include "sv_kv8_wide.cuh"
 
 namespace sv {
 template <>
-cudaError_t launch_wide8_of<64, 2>(const Att8Args &a, int grid, cudaStream_t s) {
-    return launch_wide8<64, 2>(a, grid, s);
-}
-template <>
-cudaError_t launch_wide8_of<64, 3>(const Att8Args &a, int grid, cudaStream_t s) {
-    return launch_wide8<64, 3>(a, grid, s);
+cudaError_t launch_wide8_of<64>(const Att8Args &a, int grid, cudaStream_t s) {
+    return launch_wide8<64>(a, grid, s);
 }
 }  // namespace sv

@@ -8,11 +8,13 @@ import torch
 import speculative_decoding_verify_spec_gb300 as sv
 from tests import kv8_bounds
 from tests import kv8_reference as R
+from tests import serve_util as U
 from tests.test_gpu_kv8 import DEV, DT, dev
+from tests.test_gpu_kv8_attention import filled
 
 pytestmark = pytest.mark.gpu
 
-ROWS = [(1, 4), (9, 4)]  # (new tokens, query heads a kv head)
+FEW, MANY = [(1, 4), (9, 4)], [(40, 4)]  # (new tokens, query heads a kv head): the two kernels
 
 
 def held(k, v, page):
@@ -35,7 +37,7 @@ def check(q, cache, table, start, page, cap, new=None, parent=None, cos=None, si
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("T,G", ROWS)
+@pytest.mark.parametrize("T,G", FEW + MANY)
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("L", [17, 100, 300])
 def test_a_sink_of_small_values(L, D, T, G, dtype):
@@ -55,7 +57,7 @@ def test_a_sink_of_small_values(L, D, T, G, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("G", [2])
+@pytest.mark.parametrize("G", [2, 16])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("L", [5, 120])
 def test_quiet_tokens_in_a_loud_block(L, D, G, dtype):
@@ -71,7 +73,7 @@ def test_quiet_tokens_in_a_loud_block(L, D, G, dtype):
         check(q, *held(k, v, page), start, page, 2.0**-6, parent=parent)
 
 
-@pytest.mark.parametrize("T,G", ROWS)
+@pytest.mark.parametrize("T,G", FEW + MANY)
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_blocks_of_all_loudnesses(D, T, G):
     """Every block of 16 has another loudness, 2^-36 to 2^36, and a probability as much smaller: all take part in the result."""
@@ -85,7 +87,7 @@ def test_blocks_of_all_loudnesses(D, T, G):
     check(q, *held(k, v, page), torch.tensor([n - T], dtype=torch.int32), page, 2.0**-5)
 
 
-@pytest.mark.parametrize("T,G", ROWS)
+@pytest.mark.parametrize("T,G", FEW + MANY)
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_dimensions_of_all_sizes(D, T, G):
     """Values whose dimensions differ by up to 2^16: codes down to the smallest, and those that are 0."""
@@ -95,3 +97,16 @@ def test_dimensions_of_all_sizes(D, T, G):
     k, v = torch.randn((2, 1, n, H, D), generator=g)
     check(q, *held(k, v * torch.exp2(-(torch.arange(D) % 17).float()), page), torch.tensor([150], dtype=torch.int32), page, 2.0**-6)
 
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D,T,G,L", [(64, 300, 1, 77), (64, 150, 4, 0), (128, 300, 1, 0), (128, 131, 2, 300), (256, 290, 1, 100), (256, 130, 3, 1)])
+def test_long_chains(D, T, G, L, dtype):
+    """More new tokens than a tile holds, over contexts that are no multiple of one: prompts taken in pieces."""
+    g = torch.Generator().manual_seed(D + T)
+    B, H, page = 2, 2, 48
+    start = torch.tensor([L, L // 2], dtype=torch.int32)
+    cache, table = filled(B, start + T, H, page, D, (L + T) // page + 1, g, 0.0)
+    q = 0.3 * torch.randn((B, T, H * G, D), generator=g)
+    check(q.to(DT[dtype]), cache, table, start, page, 2.0**-5, new=torch.tensor([T, T - 7], dtype=torch.int32))
+    cos, sin = U.tables(L + T, D // 2)
+    check(q.to(DT[dtype]), cache, table, start, page, 2.0**-5, cos=cos, sin=sin)
