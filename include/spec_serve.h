@@ -129,7 +129,7 @@ sv_status spec_kv_append(const void *k, int64_t k_batch_stride, int64_t k_token_
  * tokens from new_lens[b] on.
  * workspace  spec_kv_attention_workspace_size(...) bytes, 16-byte aligned, any contents.  Its first
  *            int32 is the call's status once the stream has completed: SV_OK, or SV_ERR_TIMEOUT if
- *            a bounded device wait (one second) gave up; `out` is then of no use.
+ *            a bounded device wait (one second) gave up; `out` is then NaN throughout.
  */
 size_t spec_kv_attention_workspace_size(int B, int T, int heads, int kv_heads, int head_dim);
 sv_status spec_kv_attention(const void *q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,
@@ -216,7 +216,7 @@ int64_t spec_kv_code_offset(int page_size, int head_dim, int values, int token, 
  * Test hook of the bounds-checked build: from now on no thread block of spec_kv_attention or spec_kv8_attention gets the
  * unit-th piece of the cache (from 0) that it is to read, or any after it; -1: all do.  The waits for
  * them run out after a second each, the call ends with SV_ERR_TIMEOUT in its workspace, and its output
- * is of no use.  SV_ERR_UNSUPPORTED in the normal build.
+ * is NaN.  SV_ERR_UNSUPPORTED in the normal build.
  */
 sv_status spec_kv_lose_unit(int unit);
 

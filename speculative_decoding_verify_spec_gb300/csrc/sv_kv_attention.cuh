@@ -1021,6 +1021,7 @@ __global__ void __launch_bounds__(att_threads(D, NR), att_occupancy(D, NR)) kv_a
 // Joins a segment that several CTAs share: out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c, in one pass with a
 // running M.  Block (c, y) acts if CTA c's share is the second one with a part of a segment; y takes the rows that 256
 // threads hold at four dimensions a thread.  What bounds it is the latency of three dependent reads.
+// If a wait gave up the call's result is NaN throughout, so that a caller who does not look at the status takes nothing wrong for right.
 constexpr int kJoinThreads = 256;
 __host__ __device__ constexpr int join_rows(int D) { return kJoinThreads * 4 / D; }
 
@@ -1030,7 +1031,14 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const A
     // all its places; 256 single tokens took 389 us so, and 299 without)
     griddep_wait();
     const int c = int(blockIdx.x) / groups + 1, r = int(blockIdx.x) % groups * join_rows(D) + threadIdx.x / (D / 4);
-    const AttDesc d = a.desc[c];
+    const int status = __ldcg(a.status);
+    const AttDesc d = c < ncta ? a.desc[c] : AttDesc{0, 0, 0, 0, 0, 0, 0, 0};  // (one block alone: only the status)
+    if (status != SV_OK) {
+        const int64_t words = int64_t(a.B) * a.T * a.H * a.G * (D / 2);
+        for (int64_t i = int64_t(blockIdx.x) * kJoinThreads + threadIdx.x; i < words; i += int64_t(gridDim.x) * kJoinThreads)
+            reinterpret_cast<uint32_t *>(a.out)[i] = 0xFFFFFFFFu;
+        return;
+    }
     if (!d.join || r >= R) return;
     const int d4 = threadIdx.x % (D / 4) * 4, row = d.rt * R + r, node = row / a.G;
     if (node >= a.T) return;
@@ -1080,8 +1088,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join_kernel(const A
 template <int D>
 cudaError_t launch_join(const AttArgs &a, int grid, int R, cudaStream_t s) {
     const int groups = (R + join_rows(D) - 1) / join_rows(D);
-    if (grid < 2) return cudaSuccess;  // nothing is shared
-    return launch_after(kv_attention_join_kernel<D>, unsigned((grid - 1) * groups), unsigned(kJoinThreads), 0, s, a, grid, R, groups);
+    return launch_after(kv_attention_join_kernel<D>, unsigned(grid > 1 ? (grid - 1) * groups : 1), unsigned(kJoinThreads), 0, s, a, grid, R, groups);
 }
 
 template <int D, int NR, bool kExact>

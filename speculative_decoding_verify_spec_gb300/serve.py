@@ -248,7 +248,7 @@ def spec_kv_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Te
     if `parent` [T] gives a tree.  scale defaults to head_dim ** -0.5.  Returns [B, T, heads, head_dim].
 
     The first int32 of `workspace` (spec_kv_attention_workspace_size bytes; one of the call's own unless given) is the call's status
-    once the stream has completed: 0, or 4 if a bounded wait on the device gave up and the result is of no use."""
+    once the stream has completed: 0, or 4 if a bounded wait on the device gave up; the result is then NaN throughout."""
     lib = _library()
     qs, dt, dev = _heads4(q, "q"), _kv_dtype(q, "q"), q.device
     B, T, Hq, D = q.shape
