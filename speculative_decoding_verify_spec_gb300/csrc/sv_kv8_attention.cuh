@@ -24,7 +24,7 @@
 // shared memory (keys and values apart: a key's place is free once its scores are there), a thread that issues the
 // products as their operands come, and a group of four warps for the softmax for each 16 rows.  A thread of those has one
 // token's scores for the group's rows, and one or two dimensions of their output: maxima are one reduction over the warp and one
-// barrier, the weights' sums stay in the thread until the segment ends, and a token's weights are stored in 16 bytes a part
+// barrier, the weights' sums stay in the thread until the segment ends, and a token's weights are stored in 16 bytes a part and range
 // (rows are the operand's contiguous axis).  Scores and outputs have two places each in tensor memory, so that the next tile's
 // scores are computed during this one's softmax, and its output is taken up after the next one's weights.
 //
@@ -34,7 +34,7 @@
 // Measured, and what bounds it.  256 single tokens with 8 heads a kv head over 4600 cached ones on average: 392 us in a graph, 6.2 TB/s, 92 % of
 // a plain copy's rate.  6 drafts over 200001 tokens, 256 dimensions: 99 us, 4.1 TB/s; there and with more rows the path of a
 // tile through a block counts, which one block an SM does not cover: 64 x 9 drafts with 4 heads a kv head (36 rows) take 147 us, 2.4 us a
-// tile.  (With two parts of 4 bits a weight and one range, which lost weights of 2^-18 of the largest, these took 372, 85 and 128 us.)  A product of 128 x N x 32
+// tile, 54 instructions for each row and token, 2.1 a clock, the tensor pipe at 44 %.  (With two parts of 4 bits a weight and one range, which lost weights of 2^-18 of the largest, these took 372, 85 and 128 us.)  A product of 128 x N x 32
 // takes 45 clocks up to N = 48, 48 for 64, 56 for 96 and 65 for 128 columns, measured, so that parts and ranges cost little there.
 #pragma once
 
@@ -55,7 +55,7 @@ __host__ __device__ constexpr int att8_value_stages(int D, int NR) {
 __host__ __device__ constexpr int att8_q_places(int D, int NR) { return D == 256 || (D == 128 && NR == 32) ? 1 : 2; }
 __host__ __device__ constexpr int att8_occupancy(int D, int NR) { return D == 256 || NR >= 48 ? 1 : 2; }
 // Rows a tile, by the rows that share a kv head: as few tiles as there have to be, and no larger than they need be.  At most 64; 48 of 256
-// dimensions, where 64 rows took 114 us in one tile and 72 rows 111 us in two (64 sequences of up to 1500 tokens, 4 kv heads, bf16).
+// dimensions, by tensor memory.
 constexpr int att8_cap(int D) { return D == 256 ? 48 : 64; }
 inline int att8_rows(int64_t rows, int D) {
     const int64_t tiles = (rows + att8_cap(D) - 1) / att8_cap(D);

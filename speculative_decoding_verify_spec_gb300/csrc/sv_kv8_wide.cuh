@@ -11,10 +11,11 @@
 // at a time, instead of kept.  As there, every tile has its own m and output, which is added up in registers.
 //
 // A weight is held in two bfloat16 parts: off by 2^-17 of itself however far below the tile's largest it is, for bfloat16 has the exponents of fp32.  The
-// value codes are widened for that once a tile, by the softmax's threads: once for 128 rows.  (As parts of 8 bits, of one range, as
-// the values were held before, two parts took 116 and three 130 us in the first case below, and lost weights of 2^-18 of the largest.)
+// value codes are widened for that once a tile, by the softmax's threads: once for 128 rows.  (In parts of 8 bits and one
+// range, against the codes as they lie, two parts took 116 and three 130 us in the first case below, and lost weights of 2^-18 of the largest.)
 //
-// Measured: 64 x 64 tree nodes with 4 query heads a kv head over up to 2047 tokens, us: 64 dimensions 129 to 132; 128 dimensions 167 to 174.  A tile's path
+// Measured: 64 x 64 tree nodes with 4 query heads a kv head over up to 2047 tokens, us: 64 dimensions 129 to 132, 27 instructions
+// for each row and token, 2.3 a clock, the tensor pipe at 33 %; 128 dimensions 165 to 174.  A tile's path
 // through a block (scores, maximum, barrier, weights, product) is covered by the other block of the SM only in part, and at 128 dimensions by none.
 // 256 dimensions, whose queries leave shared memory for a tile of 64 tokens and one place for all else, took 242, 435 and 457 us
 // for 128, 192 and 256 rows where tiles of 48 rows of the other kernel take 229, 296 and 435 (bf16, rotated): they go there.
@@ -25,8 +26,8 @@
 namespace sv {
 
 constexpr int kWideRows8 = 128;
+__host__ __device__ constexpr bool wide8_has(int D) { return D <= 128; }  // (256: above)
 // Softmax groups of a block and blocks an SM: two blocks hide each other's waits where registers and shared memory admit them.
-__host__ __device__ constexpr bool wide8_has(int D) { return D <= 128; }
 __host__ __device__ constexpr int wide8_groups(int D) { return D == 64 ? 2 : 4; }
 __host__ __device__ constexpr int wide8_occupancy(int D) { return D == 64 ? 2 : 1; }
 __host__ __device__ constexpr int wide8_threads(int D) { return 64 + 128 * wide8_groups(D); }
